@@ -66,7 +66,8 @@ typedef enum {
   DSPARK_ERR_CUDA = 4,        /* a CUDA runtime call failed */
   DSPARK_ERR_TIMEOUT = 5,     /* a bounded device-side wait ran out (device) */
   DSPARK_ERR_RANGE = 6,       /* a token id outside [0, V) was read (device) */
-  DSPARK_ERR_TOO_LARGE = 7    /* problem exceeds the fixed scratch of dspark_schedule_static */
+  DSPARK_ERR_TOO_LARGE = 7,   /* problem exceeds the fixed scratch of dspark_schedule_static */
+  DSPARK_ERR_CAPACITY = 8     /* free pages, block-table columns or token capacity ran out (device) */
 } dspark_status;
 
 typedef enum { DSPARK_FP32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
@@ -352,6 +353,114 @@ dspark_status dspark_sts_fit(int32_t N, int32_t gamma, const float* conf, const 
 dspark_status dspark_sts_status(const void* scratch, dspark_stream_t stream);
 dspark_status dspark_sts_apply(int32_t R, int32_t gamma, const float* conf, const float* temperature,
                                float* conf_out, dspark_stream_t stream);
+
+/*
+ * The target's side of a round in a serving engine: cache pages and slots of
+ * the round's tokens, their keys and values into the paged cache, attention
+ * over a shared prefix and each request's own pages, and the target's sampling
+ * rule. (After the LM head, the logits of dspark_truncate are the
+ * target_logits of dspark_verify.) These calls take any workspace of at least
+ * 256 bytes for the device status word; dspark_prefix_attention needs the size
+ * that dspark_attention_workspace_bytes gives.
+ *
+ * dspark_page_plan: pages and slots of new_len[r] tokens for every request r
+ * (a round: the anchor and the scheduled draft tokens, L_r + 1) that holds
+ * cached_len[r] tokens in ceil(cached_len / page_size) pages.
+ *   cached_len, new_len [R] int32   >= 0 (a negative one counts as 0, DSPARK_ERR_RANGE)
+ *   free_pages  [n_free] int32      ids of free pages, taken in order: request by request, each
+ *                                   request's missing pages by position
+ *   block_table [R, max_pages] int32 in/out  the new pages' entries are written (-1 where the
+ *                                   list has run out), all others left as they are
+ *   q_start     [R+1] int32 out     first new token of each request, and their number T
+ *   kv_len      [R] int32 out       cached_len + new_len
+ *   positions   [capacity] int32 out  position of each new token in its request; -1 past T
+ *   slots       [capacity] int64 out  page * page_size + offset; -1 where there is no page, and past T
+ *   used        [1] int32 out       free pages taken
+ * A list, a table row or a capacity that is too short sets DSPARK_ERR_CAPACITY
+ * (tokens past the capacity are not written, q_start stays within it).
+ */
+dspark_status dspark_page_plan(int32_t R, int32_t page_size, int32_t max_pages, int32_t n_free,
+                               int32_t capacity, const int32_t* cached_len, const int32_t* new_len,
+                               const int32_t* free_pages, int32_t* block_table, int32_t* q_start,
+                               int32_t* kv_len, int32_t* positions, int64_t* slots, int32_t* used,
+                               void* workspace, size_t workspace_bytes, dspark_stream_t stream);
+
+/*
+ * dspark_kv_append: k_cache[slots[t]] = k[t], v_cache[slots[t]] = v[t].
+ *   k, v              [T, n_kv_heads, head_dim] dtype
+ *   slots             [T] int64        distinct; a negative one is skipped, one >= n_slots too
+ *                                      (DSPARK_ERR_RANGE)
+ *   k_cache, v_cache  [n_slots, n_kv_heads, head_dim] dtype, n_slots = pages * page_size
+ */
+dspark_status dspark_kv_append(int32_t T, int32_t n_kv_heads, int32_t head_dim, int32_t dtype,
+                               const void* k, const void* v, const int64_t* slots, int64_t n_slots,
+                               void* k_cache, void* v_cache, void* workspace, size_t workspace_bytes,
+                               dspark_stream_t stream);
+
+/*
+ * dspark_prefix_attention: softmax attention of T query tokens over a prefix
+ * that every request shares and over each request's own pages. The queries of
+ * request r are tokens q_start[r] .. q_start[r+1] - 1, its last ones in order:
+ * token i of n stands at private position kv_len[r] - n + i and sees the whole
+ * prefix and the private positions up to its own. Query head h reads key head
+ * h / (n_heads / n_kv_heads).
+ *   q            [T, n_heads, head_dim] bf16
+ *   k_cache, v_cache [n_pages, page_size, n_kv_heads, head_dim] bf16 (the keys and values of
+ *                the new tokens are already there)
+ *   prefix_pages [ceil(prefix_len / page_size)] int32, the prefix's pages (NULL if prefix_len = 0)
+ *   block_table  [R, max_pages] int32, kv_len [R] int32, q_start [R+1] int32 as from dspark_page_plan
+ *   scale        > 0, the factor of the scores
+ *   out          [T, n_heads, head_dim] bf16 out
+ *   lse          [T, n_heads] float out or NULL, the natural log of the sum of e^score
+ * A query that sees no key gets out = 0 and lse = -inf. Cache entries that no
+ * query of the call sees are never part of a result, whatever bits they hold;
+ * those that one sees must be finite. Rows of q past q_start[R] are left out.
+ * Scores, softmax statistics and accumulators are float32; the weights that
+ * multiply v are rounded to bf16 (their sum is not).
+ * Requirements: bf16; head_dim 64 or 128; n_heads a multiple of n_kv_heads, at
+ * most 128 query heads a key head; page_size a power of two, 16 to 4096; q,
+ * k_cache, v_cache and out 16-byte aligned. A page id outside [0, n_pages), a
+ * kv_len outside [0, max_pages * page_size] or a q_start that falls or leaves
+ * [0, T] sets DSPARK_ERR_RANGE (the keys of such a page are left undefined but
+ * nothing outside the tensors is read; lengths are clamped).
+ */
+size_t dspark_attention_workspace_bytes(int32_t R, int32_t T, int32_t n_heads, int32_t n_kv_heads,
+                                        int32_t head_dim);
+dspark_status dspark_prefix_attention(int32_t R, int32_t T, int32_t n_heads, int32_t n_kv_heads,
+                                      int32_t head_dim, int32_t page_size, int32_t n_pages,
+                                      int32_t max_pages, int32_t prefix_len, const void* q,
+                                      const void* k_cache, const void* v_cache,
+                                      const int32_t* prefix_pages, const int32_t* block_table,
+                                      const int32_t* q_start, const int32_t* kv_len, float scale,
+                                      void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                      dspark_stream_t stream);
+
+/*
+ * The target's sampling rule on N rows of logits [N, V] dtype (V <= 2^20), its
+ * parameters one a row: temperature (0 = greedy: the first maximum alone),
+ * top_k (<= 0 or >= V: off), top_p (>= 1: off), min_p (<= 0: off, at most 1).
+ *   weights w = 2^((l - M) r) in float32, M the row's maximum, r = min(log2(e) / T, 1e30); masses
+ *   floor(w 2^40). With the row sorted by (logit descending, index ascending), top-k keeps the
+ *   first top_k entries; of these top-p keeps the ones whose mass before them is below
+ *   max(1, floor(top_p S)), S the mass of the top-k set; of these min-p keeps the ones with
+ *   w >= min_p. An entry of -inf is never kept.
+ * dspark_sample draws one token a row: the smallest v whose kept mass up to and
+ * including v exceeds floor(u Z), Z the kept mass, u [N] float64 in [0, 1).
+ *   tokens [N] int32 out, prob [N] float out or NULL: the token's mass / Z (1 if greedy)
+ * dspark_truncate writes out [N, V] dtype: the kept entries as they are, all
+ * others the lowest finite value of the type (weight 0 for every consumer;
+ * out may be logits itself).
+ * A row with a NaN or +inf, or with nothing above -inf, sets
+ * DSPARK_ERR_NONFINITE: its token is -1 with prob 0, dspark_truncate copies it.
+ */
+dspark_status dspark_sample(int32_t N, int32_t V, int32_t dtype, const void* logits,
+                            const float* temperature, const int32_t* top_k, const float* top_p,
+                            const float* min_p, const double* u, int32_t* tokens, float* prob,
+                            void* workspace, size_t workspace_bytes, dspark_stream_t stream);
+dspark_status dspark_truncate(int32_t N, int32_t V, int32_t dtype, const void* logits,
+                              const float* temperature, const int32_t* top_k, const float* top_p,
+                              const float* min_p, void* out, void* workspace, size_t workspace_bytes,
+                              dspark_stream_t stream);
 
 /* Synchronises `stream`, then returns the workspace's sticky device status
  * (DSPARK_OK if no device-side error was recorded). */

@@ -26,6 +26,10 @@ using namespace dspark;
 
 static thread_local int g_last_launches = 0;
 
+namespace dspark {
+void note_launches(int n) { g_last_launches = n; }
+}  // namespace dspark
+
 static bool dims_ok(int R, int gamma, int V, int rank, int dtype) {
   return R >= 1 && gamma >= 1 && gamma < 65535 && V >= 1 && rank >= 1 &&
          (dtype == DSPARK_FP32 || dtype == DSPARK_BF16) && (long long)R * (long long)gamma <= 65536 &&
@@ -335,6 +339,7 @@ const char* dspark_status_string(dspark_status status) {
     case DSPARK_ERR_TIMEOUT: return "bounded device wait ran out";
     case DSPARK_ERR_RANGE: return "token id outside [0, V)";
     case DSPARK_ERR_TOO_LARGE: return "R * gamma exceeds the 16384 candidates of the fixed scratch";
+    case DSPARK_ERR_CAPACITY: return "free pages, block-table columns or token capacity ran out";
   }
   return "unknown status";
 }

@@ -96,6 +96,9 @@ inline cudaError_t set_smem_limit_once(const void* fn, int bytes, std::atomic<un
   return e;
 }
 
+// Sets what dspark_last_launch_count() returns (entry points outside api.cu).
+void note_launches(int n);
+
 cudaError_t launch_draft(const DraftArgs& a, cudaStream_t s, int& launches);
 // The gated head runs only on the persistent tensor-core path: bf16, rank a
 // multiple of 64 up to 256, V a multiple of 8 and at least 64, 16-byte

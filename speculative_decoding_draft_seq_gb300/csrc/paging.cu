@@ -1,0 +1,223 @@
+// Paged key/value cache upkeep around a round: pages and slots of the tokens
+// that enter the cache (the anchor and the scheduled draft tokens of every
+// request), and the copy of their keys and values into it.
+//
+// page_plan_kernel  request r holds have = ceil(c / p) pages for its c cached
+//   tokens and needs ceil((c + n) / p) for n more (page size p). The missing
+//   ones are taken from the list of free pages in request order, so a request's
+//   first entry is the sum of the missing pages before it, and its first token's
+//   index the sum of n before it. Each CTA plans kPlanReqs requests and forms
+//   both sums over all earlier requests itself: at 8,192 requests that reads at
+//   most 64 KB from L2 in a CTA, and no CTA waits for another.
+// kv_append_kernel  one 16-byte piece of one token's key or value row a thread
+//   step; bound by bytes (each read once and written once).
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace dspark {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanReqs = 128;
+
+struct PlanParams {
+  int R, page, max_pages, n_free, capacity;
+  const int32_t* cached;
+  const int32_t* fresh;
+  const int32_t* free_pages;
+  int32_t* table;
+  int32_t* q_start;
+  int32_t* kv_len;
+  int32_t* positions;
+  long long* slots;
+  int32_t* used;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ long long block_sum_ll(long long v, long long* sh) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane == 0) sh[w] = v;
+  __syncthreads();
+  v = 0;
+  for (int i = 0; i < nw; ++i) v += sh[i];
+  return v;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
+  __shared__ long long sh[32];
+  __shared__ long long s_tok[kPlanReqs + 1], s_pg[kPlanReqs + 1];  // token / free-list starts of this CTA's requests
+  __shared__ int s_c[kPlanReqs], s_have[kPlanReqs];
+  const int tid = threadIdx.x, r0 = blockIdx.x * kPlanReqs, nr = min(kPlanReqs, p.R - r0);
+  bool bad = false;
+  auto lengths = [&](int r, int& c, int& n) {
+    c = __ldg(p.cached + r);
+    n = __ldg(p.fresh + r);
+    bad |= c < 0 || n < 0;
+    c = max(c, 0);
+    n = max(n, 0);
+  };
+  auto missing = [&](int c, int n) {
+    return ((long long)c + n + p.page - 1) / p.page - ((long long)c + p.page - 1) / p.page;
+  };
+  long long tok = 0, pg = 0;
+  for (int r = tid; r < r0; r += kPlanThreads) {
+    int c, n;
+    lengths(r, c, n);
+    tok += n;
+    pg += missing(c, n);
+  }
+  tok = block_sum_ll(tok, sh);
+  pg = block_sum_ll(pg, sh);
+  if (tid < nr) {
+    int c, n;
+    lengths(r0 + tid, c, n);
+    s_c[tid] = c;
+    s_have[tid] = (int)(((long long)c + p.page - 1) / p.page);
+    s_tok[tid + 1] = n;
+    s_pg[tid + 1] = missing(c, n);
+    const long long end = (long long)c + n;
+    bad |= end > 0x7fffffffll;
+    p.kv_len[r0 + tid] = (int)min(end, 0x7fffffffll);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    s_tok[0] = tok;
+    s_pg[0] = pg;
+    for (int i = 0; i < nr; ++i) { s_tok[i + 1] += s_tok[i]; s_pg[i + 1] += s_pg[i]; }
+  }
+  __syncthreads();
+  // new entries of the block table: -1 where the list has run out
+  bool full = false;
+  const int warp = tid >> 5, lane = tid & 31;
+  for (int i = warp; i < nr; i += kPlanThreads / 32) {
+    const int have = s_have[i];
+    const long long n_new = s_pg[i + 1] - s_pg[i];
+    full |= have + n_new > p.max_pages;
+    for (long long j = lane; j < n_new && have + j < p.max_pages; j += 32) {
+      const long long at = s_pg[i] + j;
+      full |= at >= p.n_free;
+      p.table[(size_t)(r0 + i) * p.max_pages + have + j] = at < p.n_free ? __ldg(p.free_pages + at) : -1;
+    }
+  }
+  if (tid < nr) p.q_start[r0 + tid] = (int)min(s_tok[tid], (long long)p.capacity);
+  const long long t_end = s_tok[nr];
+  full |= t_end > p.capacity;
+  // the tokens of this CTA's requests
+  for (long long t = s_tok[0] + tid; t < min(t_end, (long long)p.capacity); t += kPlanThreads) {
+    int lo = 0, hi = nr - 1;  // the last request that starts at or before t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_tok[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    const long long pos = s_c[lo] + (t - s_tok[lo]);
+    const long long col = pos / p.page;
+    int page = -1;
+    if (col < p.max_pages) {
+      if (col < s_have[lo]) {
+        page = __ldg(p.table + (size_t)(r0 + lo) * p.max_pages + col);
+      } else {
+        const long long at = s_pg[lo] + col - s_have[lo];
+        if (at < p.n_free) page = __ldg(p.free_pages + at);
+      }
+    }
+    p.positions[t] = (int)pos;
+    p.slots[t] = page < 0 ? -1ll : (long long)page * p.page + pos % p.page;
+  }
+  if (r0 + nr == p.R) {
+    if (tid == 0) {
+      p.q_start[p.R] = (int)min(t_end, (long long)p.capacity);
+      p.used[0] = (int)min(s_pg[nr], (long long)p.n_free);
+    }
+    for (long long t = t_end + tid; t < p.capacity; t += kPlanThreads) {
+      p.positions[t] = -1;
+      p.slots[t] = -1ll;
+    }
+  }
+  if (bad) set_status(p.status, DSPARK_ERR_RANGE);
+  if (full) set_status(p.status, DSPARK_ERR_CAPACITY);
+}
+
+// ---------------------------------------------------------------------------
+template <class Tv>
+__global__ void __launch_bounds__(256)
+    kv_append_kernel(long long n_vec, int per_row, const Tv* __restrict__ k, const Tv* __restrict__ v,
+                     const long long* __restrict__ slots, long long n_slots, Tv* __restrict__ k_cache,
+                     Tv* __restrict__ v_cache, uint32_t* status) {
+  const long long step = (long long)gridDim.x * blockDim.x;
+  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n_vec; i += step) {
+    const long long t = i / per_row;
+    const long long slot = __ldg(slots + t);
+    if (slot < 0) continue;
+    if (slot >= n_slots) {
+      set_status(status, DSPARK_ERR_RANGE);
+      continue;
+    }
+    const long long at = slot * per_row + (i - t * per_row);
+    const Tv a = k[i], b = v[i];
+    k_cache[at] = a;
+    v_cache[at] = b;
+  }
+}
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" dspark_status dspark_page_plan(int32_t R, int32_t page_size, int32_t max_pages, int32_t n_free,
+                                          int32_t capacity, const int32_t* cached_len, const int32_t* new_len,
+                                          const int32_t* free_pages, int32_t* block_table, int32_t* q_start,
+                                          int32_t* kv_len, int32_t* positions, int64_t* slots, int32_t* used,
+                                          void* workspace, size_t workspace_bytes, dspark_stream_t stream) {
+  note_launches(0);
+  if (R < 1 || page_size < 1 || max_pages < 1 || n_free < 0 || capacity < 0 || !cached_len || !new_len ||
+      (n_free > 0 && !free_pages) || !block_table || !q_start || !kv_len || (capacity > 0 && (!positions || !slots)) ||
+      !used)
+    return DSPARK_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < 256)
+    return DSPARK_ERR_WORKSPACE;
+  PlanParams p{R, page_size, max_pages, n_free, capacity, cached_len, new_len, free_pages, block_table, q_start,
+               kv_len, positions, reinterpret_cast<long long*>(slots), used, static_cast<uint32_t*>(workspace)};
+  page_plan_kernel<<<ceil_div(R, kPlanReqs), kPlanThreads, 0, (cudaStream_t)stream>>>(p);
+  note_launches(1);
+  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}
+
+extern "C" dspark_status dspark_kv_append(int32_t T, int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* k,
+                                          const void* v, const int64_t* slots, int64_t n_slots, void* k_cache,
+                                          void* v_cache, void* workspace, size_t workspace_bytes,
+                                          dspark_stream_t stream) {
+  note_launches(0);
+  if (T < 0 || n_kv_heads < 1 || head_dim < 1 || (long long)n_kv_heads * head_dim > (1 << 24) ||
+      (dtype != DSPARK_FP32 && dtype != DSPARK_BF16) || n_slots < 0 || n_slots > (1ll << 40))
+    return DSPARK_ERR_INVALID_ARG;
+  if (T > 0 && (!k || !v || !slots || !k_cache || !v_cache)) return DSPARK_ERR_INVALID_ARG;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < 256)
+    return DSPARK_ERR_WORKSPACE;
+  if (T == 0) return DSPARK_OK;
+  const int elem = dtype == DSPARK_BF16 ? 2 : 4;
+  const int row = n_kv_heads * head_dim * elem;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) |
+                       reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache);
+  const int unit = ((at | (uintptr_t)row) & 15) == 0 ? 16 : elem;  // bytes a thread copies at a time
+  const long long n_vec = (long long)T * (row / unit);
+  const int grid = (int)std::min<long long>((n_vec + 255) / 256, 152 * 16);
+  uint32_t* status = static_cast<uint32_t*>(workspace);
+  const long long* sl = reinterpret_cast<const long long*>(slots);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (unit == 16)
+    kv_append_kernel<<<grid, 256, 0, s>>>(n_vec, row / unit, (const uint4*)k, (const uint4*)v, sl, (long long)n_slots,
+                                          (uint4*)k_cache, (uint4*)v_cache, status);
+  else if (unit == 4)
+    kv_append_kernel<<<grid, 256, 0, s>>>(n_vec, row / unit, (const uint32_t*)k, (const uint32_t*)v, sl,
+                                          (long long)n_slots, (uint32_t*)k_cache, (uint32_t*)v_cache, status);
+  else
+    kv_append_kernel<<<grid, 256, 0, s>>>(n_vec, row / unit, (const uint16_t*)k, (const uint16_t*)v, sl,
+                                          (long long)n_slots, (uint16_t*)k_cache, (uint16_t*)v_cache, status);
+  note_launches(1);
+  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+}

@@ -14,7 +14,8 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdspark.so")
 
-OK, ERR_INVALID_ARG, ERR_NONFINITE, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_RANGE, ERR_TOO_LARGE = range(8)
+OK, ERR_INVALID_ARG, ERR_NONFINITE, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_RANGE, ERR_TOO_LARGE, \
+    ERR_CAPACITY = range(9)
 FP32, BF16 = 0, 1
 CAUSAL, LAGGED, ALL = 0, 1, 2
 
@@ -70,6 +71,19 @@ def _load():
     lib.dspark_sts_status.argtypes = [vp, vp]
     lib.dspark_sts_apply.restype = i32
     lib.dspark_sts_apply.argtypes = [i32, i32, vp, vp, vp, vp]
+    i64 = ctypes.c_int64
+    lib.dspark_page_plan.restype = i32
+    lib.dspark_page_plan.argtypes = [i32] * 5 + [vp] * 9 + [vp, sz, vp]
+    lib.dspark_kv_append.restype = i32
+    lib.dspark_kv_append.argtypes = [i32] * 4 + [vp] * 3 + [i64] + [vp] * 2 + [vp, sz, vp]
+    lib.dspark_attention_workspace_bytes.restype = sz
+    lib.dspark_attention_workspace_bytes.argtypes = [i32] * 5
+    lib.dspark_prefix_attention.restype = i32
+    lib.dspark_prefix_attention.argtypes = [i32] * 9 + [vp] * 7 + [f32] + [vp] * 2 + [vp, sz, vp]
+    lib.dspark_sample.restype = i32
+    lib.dspark_sample.argtypes = [i32] * 3 + [vp] * 8 + [vp, sz, vp]
+    lib.dspark_truncate.restype = i32
+    lib.dspark_truncate.argtypes = [i32] * 3 + [vp] * 6 + [vp, sz, vp]
     lib.dspark_device_status.restype = i32
     lib.dspark_device_status.argtypes = [vp, vp]
     lib.dspark_status_string.restype = ctypes.c_char_p
@@ -91,6 +105,7 @@ def last_launch_count():
 
 
 _I32, _F32, _F64, _U8 = torch.int32, torch.float32, torch.float64, torch.uint8
+_I64, _BF16 = torch.int64, torch.bfloat16
 
 
 def _ptr(t, dtype=None, host=False):
@@ -130,14 +145,18 @@ def workspace_bytes(R, gamma, V, rank, dtype, n_table):
     return int(lib.dspark_workspace_bytes(R, gamma, V, rank, dtype, n_table))
 
 
-def new_workspace(R, gamma, V, rank, dtype, n_table, device="cuda", stream=None):
-    """Allocates (with PyTorch) and clears a workspace for these sizes."""
-    n = workspace_bytes(R, gamma, V, rank, dtype, n_table)
+def _aligned_workspace(n, device, stream):
     ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + n]
     _check(lib.dspark_workspace_init(_ptr(ws, _U8), n, _stream(stream)), "dspark_workspace_init")
     return ws
+
+
+def new_workspace(R, gamma, V, rank, dtype, n_table, device="cuda", stream=None):
+    """Allocates (with PyTorch) and clears a workspace for these sizes."""
+    n = workspace_bytes(R, gamma, V, rank, dtype, n_table)
+    return _aligned_workspace(n, device, stream)
 
 
 def draft_sequential(base, anchor, W1, W2, temperature, seed, tokens, q_tok, q_stats, ws, stream=None):
@@ -277,6 +296,108 @@ def copy_scheduled_rows(host_target, device_target, host_sched_len, stream=None)
                                           _ptr(host_target, host=True), _ptr(device_target),
                                           _ptr(host_sched_len, _I32, host=True), _stream(stream)),
            "dspark_copy_scheduled_rows")
+
+
+def _shape(t, *want, name):
+    """Refuses a tensor whose shape is not `want` (None: any size)."""
+    if len(t.shape) != len(want) or any(w is not None and w != n for n, w in zip(t.shape, want)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('any' if w is None else w for w in want)}")
+
+
+def page_plan(cached_len, new_len, free_pages, page_size, block_table, q_start, kv_len, positions, slots, used, ws,
+              stream=None):
+    """Cache pages and slots of new_len[r] tokens a request: fills the new entries of block_table
+    [R, max_pages] from free_pages, and q_start [R+1], kv_len [R], positions and slots [capacity]
+    (int32, int64) and used [1]."""
+    R, max_pages = block_table.shape
+    _shape(cached_len, R, name="cached_len")
+    _shape(new_len, R, name="new_len")
+    _shape(q_start, R + 1, name="q_start")
+    _shape(kv_len, R, name="kv_len")
+    _shape(slots, positions.numel(), name="slots")
+    _check(lib.dspark_page_plan(R, int(page_size), max_pages, free_pages.numel(), positions.numel(),
+                                _ptr(cached_len, _I32), _ptr(new_len, _I32), _ptr(free_pages, _I32),
+                                _ptr(block_table, _I32), _ptr(q_start, _I32), _ptr(kv_len, _I32),
+                                _ptr(positions, _I32), _ptr(slots, _I64), _ptr(used, _I32), _ptr(ws, _U8), ws.numel(),
+                                _stream(stream)), "dspark_page_plan")
+
+
+def kv_append(k, v, slots, k_cache, v_cache, ws, stream=None):
+    """k_cache[slots[t]] = k[t] and the same for v: k, v [T, Hkv, D], caches
+    [pages, page_size, Hkv, D] (any leading dimensions), slots [T] int64; negative slots are skipped."""
+    T, Hkv, D = k.shape
+    _shape(v, T, Hkv, D, name="v")
+    _shape(slots, T, name="slots")
+    if k_cache.shape != v_cache.shape or k_cache.shape[-2:] != k.shape[-2:]:
+        raise ValueError("k_cache and v_cache must have one shape that ends in (Hkv, D)")
+    dt = k.dtype
+    _check(lib.dspark_kv_append(T, Hkv, D, _dtype_code(k), _ptr(k), _ptr(v, dt), _ptr(slots, _I64),
+                                k_cache.numel() // (Hkv * D), _ptr(k_cache, dt), _ptr(v_cache, dt), _ptr(ws, _U8),
+                                ws.numel(), _stream(stream)), "dspark_kv_append")
+
+
+def attention_workspace_bytes(R, T, Hq, Hkv, D):
+    return int(lib.dspark_attention_workspace_bytes(R, T, Hq, Hkv, D))
+
+
+def new_attention_workspace(R, T, Hq, Hkv, D, device="cuda", stream=None):
+    """Allocates (with PyTorch) and clears a workspace for prefix_attention calls of up to R
+    requests and T query tokens."""
+    n = attention_workspace_bytes(R, T, Hq, Hkv, D)
+    if n == 0:
+        raise DSparkError(ERR_INVALID_ARG, "dspark_attention_workspace_bytes")
+    return _aligned_workspace(n, device, stream)
+
+
+def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, q_start, kv_len, scale, out, ws,
+                     lse=None, stream=None):
+    """Attention of q [T, Hq, D] over the shared prefix and each request's own pages (caches
+    [n_pages, page_size, Hkv, D], block_table [R, max_pages]); writes out like q and, unless None,
+    lse [T, Hq] float32."""
+    T, Hq, D = q.shape
+    n_pages, page, Hkv = k_cache.shape[:3]
+    R, max_pages = block_table.shape
+    _shape(k_cache, None, None, None, D, name="k_cache")
+    _shape(v_cache, *k_cache.shape, name="v_cache")
+    _shape(out, T, Hq, D, name="out")
+    _shape(q_start, R + 1, name="q_start")
+    _shape(kv_len, R, name="kv_len")
+    if lse is not None:
+        _shape(lse, T, Hq, name="lse")
+    if prefix_len > 0 and prefix_pages.numel() * page < prefix_len:
+        raise ValueError("prefix_pages does not cover prefix_len")
+    _check(lib.dspark_prefix_attention(R, T, Hq, Hkv, D, page, n_pages, max_pages, int(prefix_len), _ptr(q, _BF16),
+                                       _ptr(k_cache, _BF16), _ptr(v_cache, _BF16),
+                                       _ptr(prefix_pages, _I32) if prefix_len > 0 else None, _ptr(block_table, _I32),
+                                       _ptr(q_start, _I32), _ptr(kv_len, _I32), float(scale), _ptr(out, _BF16),
+                                       _ptr(lse, _F32), _ptr(ws, _U8), ws.numel(), _stream(stream)),
+           "dspark_prefix_attention")
+
+
+def _rule(logits, temperature, top_k, top_p, min_p):
+    N, V = logits.shape
+    for t, name in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
+        _shape(t, N, name=name)
+    return (N, V, _dtype_code(logits), _ptr(logits), _ptr(temperature, _F32), _ptr(top_k, _I32), _ptr(top_p, _F32),
+            _ptr(min_p, _F32))
+
+
+def sample(logits, temperature, top_k, top_p, min_p, u, tokens, ws, prob=None, stream=None):
+    """One token a row of logits [N, V] by temperature, top-k, top-p and min-p (one of each a row)
+    from the uniforms u [N] float64; tokens [N] int32, prob [N] float32 or None."""
+    _shape(u, logits.shape[0], name="u")
+    _shape(tokens, logits.shape[0], name="tokens")
+    if prob is not None:
+        _shape(prob, logits.shape[0], name="prob")
+    _check(lib.dspark_sample(*_rule(logits, temperature, top_k, top_p, min_p), _ptr(u, _F64), _ptr(tokens, _I32),
+                             _ptr(prob, _F32), _ptr(ws, _U8), ws.numel(), _stream(stream)), "dspark_sample")
+
+
+def truncate(logits, temperature, top_k, top_p, min_p, out, ws, stream=None):
+    """out [N, V]: logits with every entry outside the rule's kept set at the type's lowest value."""
+    _shape(out, *logits.shape, name="out")
+    _check(lib.dspark_truncate(*_rule(logits, temperature, top_k, top_p, min_p), _ptr(out, logits.dtype), _ptr(ws, _U8),
+                               ws.numel(), _stream(stream)), "dspark_truncate")
 
 
 def wait_selftest(which, ws, stream=None):
