@@ -419,10 +419,11 @@ dspark_status dspark_kv_append(int32_t T, int32_t n_kv_heads, int32_t head_dim, 
  * multiply v are rounded to bf16 (their sum is not).
  * Requirements: bf16; head_dim 64 or 128; n_heads a multiple of n_kv_heads, at
  * most 128 query heads a key head; page_size a power of two, 16 to 4096; q,
- * k_cache, v_cache and out 16-byte aligned. A page id outside [0, n_pages), a
- * kv_len outside [0, max_pages * page_size] or a q_start that falls or leaves
- * [0, T] sets DSPARK_ERR_RANGE (the keys of such a page are left undefined but
- * nothing outside the tensors is read; lengths are clamped).
+ * k_cache, v_cache and out 16-byte aligned. DSPARK_ERR_RANGE is set by a page
+ * id outside [0, n_pages) (its keys and values read as zeros), by a kv_len
+ * outside [0, max_pages * page_size] (clamped), and by a q_start that does not
+ * begin at 0, falls or passes T (nothing is written then). Nothing outside the
+ * tensors is read. Three launches.
  */
 size_t dspark_attention_workspace_bytes(int32_t R, int32_t T, int32_t n_heads, int32_t n_kv_heads,
                                         int32_t head_dim);

@@ -3,18 +3,71 @@
 //   x_j = scale q . k_j over the prefix's keys and the request's keys up to the
 //   token's own position, out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),
 //   lse = m + ln sum_j e^(x_j - m), m = max_j x_j.
+//
+// The softmax of a row is joined from parts over disjoint key ranges: a part
+// gives (m, z = sum 2^(x log2(e) - m), o = sum 2^(x log2(e) - m) v), and parts
+// add up after scaling by 2^(m - max m). The prefix is one key range for the
+// rows of all requests (its keys are read once for 256 rows of the whole batch
+// instead of once a request), a request's own pages are another, and either is
+// split further when that makes enough work for every SM.
+//
+// Launches:
+//   attn_plan_kernel   one CTA: cuts the work into items (a key head, a block of
+//                      query tokens, a range of 128-key tiles), equal shares of
+//                      about 1/kPlanShare of an SM's work;
+//   attn_tiles_kernel  persistent, one CTA an SM, items b, b + grid, ...; odd
+//                      CTAs take them in reverse, so that the prefix items (bound
+//                      by the tensor cores) and the page items (bound by memory)
+//                      run at the same time;
+//   attn_join_kernel   adds a row's parts up.
+//
+// attn_tiles_kernel: rows are (token, query head of the key head), packed
+// floor(128 / group) tokens a 128-row half. Per 128-key tile and half: S = Q K^T
+// into TMEM (128 columns), a warpgroup turns S into bf16 weights in place (one
+// thread a row), O += P V with P read from TMEM. Two halves alternate, so one
+// half's softmax runs under the other's MMAs. The weights use a reference
+// maximum that is moved, and O rescaled, only when the row's maximum has risen
+// by more than 8 (2^8 fits every type on the way), so O is rarely rescaled.
+//   warps 0..3, 4..7  softmax and epilogue of half 0, 1
+//   warp 8            TMA loads: Q once an item, a ring of K and V tiles, one box
+//                     a page (or 128 rows of a longer one), 64 columns wide
+//   warp 9            MMA issue; zeroes the V rows of the last 16-key group that
+//                     lie past the keys (a weight of 0 times a NaN is a NaN)
+// Every wait is bounded: one that runs out records DSPARK_ERR_TIMEOUT, the
+// roles wind down, issued copies and MMAs land, and the TMEM is freed.
 #include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
+#include "tc_ptx.cuh"
+#include "verify_common.cuh"
 
 namespace dspark {
 
+constexpr int kATile = 128;        // keys a tile
+constexpr int kAThreads = 320;
+constexpr int kPlanShare = 4;      // items are at most about 1/4 of an SM's share of the work
+constexpr int kExtraSlots = 2048;  // token slots for splits beyond one part for the prefix and one for the pages
+constexpr int kMaxSms = 256;
+
+struct AttnItem {
+  int head;    // key head
+  int req;     // request, or -1: the prefix
+  int tok0;    // first query token
+  int n_tok;   // query tokens (at most two halves)
+  int key0;    // first key, a multiple of kATile
+  int n_keys;  // keys from key0 on that any row sees
+  int slot0;   // part slot of the first token; -1: the only part of its rows, written to out
+  int pos0;    // keys from key0 on that the first token sees (one more for each further token)
+};
+
+struct AttnHead {  // written by the plan
+  int n_items, prefix_splits, n_tokens, pad;
+};
+
 struct AttnParams {
-  int R, T, Hq, Hkv, page, n_pages, max_pages, prefix_len;
-  const __nv_bfloat16* q;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
+  int R, T, Hq, Hkv, G, TB, page, page_log2, n_pages, max_pages, prefix_len, sms;
+  long long cap_slots;
   const int32_t* prefix_pages;
   const int32_t* table;
   const int32_t* q_start;
@@ -23,65 +76,604 @@ struct AttnParams {
   __nv_bfloat16* out;
   float* lse;
   uint32_t* status;
+  AttnHead* head;
+  AttnItem* items;
+  int4* tokens;   // [T]: first page part slot, slots between parts, page parts (-1: nothing to join), unused
+  float2* stat;   // [slot][Hq]: (m, z)
+  float* acc;     // [slot][Hq][D]
 };
 
-// One warp a (token, query head): the running maximum and sum of the softmax over one key at a time.
-template <int D>
-__global__ void __launch_bounds__(256) attention_rows_kernel(AttnParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0)
-    for (int r = threadIdx.x; r < p.R; r += blockDim.x)
-      if (p.q_start[r] < 0 || p.q_start[r + 1] < p.q_start[r] || p.q_start[r + 1] > p.T || p.kv_len[r] < 0 ||
-          p.kv_len[r] > (long long)p.max_pages * p.page)
-        set_status(p.status, DSPARK_ERR_RANGE);
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (long long)p.T * p.Hq) return;
-  const int t = (int)(row / p.Hq), hq = (int)(row % p.Hq), h = hq / (p.Hq / p.Hkv);
-  int lo = 0, hi = p.R;
-  while (lo < hi) {  // the first request that ends after t
-    const int mid = (lo + hi) >> 1;
-    if (p.q_start[mid + 1] > t) hi = mid;
-    else lo = mid + 1;
+struct AttnLayout {
+  size_t head, tokens, items, stat, acc, total;
+  long long slots;
+};
+
+inline int attn_tokens_per_half(int G) { return 128 / G; }
+
+inline AttnLayout attn_layout(int R, int T, int Hq, int Hkv, int D) {
+  AttnLayout L;
+  const int TB = attn_tokens_per_half(Hq / Hkv);
+  const long long blocks = 2ll * ceil_div(T, 2 * TB) + R + 1;
+  const long long items = blocks * Hkv + (long long)kMaxSms * kPlanShare;
+  L.slots = 2ll * T + kExtraSlots;
+  size_t o = 256;
+  L.head = o;   o = align256(o + sizeof(AttnHead));
+  L.tokens = o; o = align256(o + (size_t)T * sizeof(int4));
+  L.items = o;  o = align256(o + (size_t)items * sizeof(AttnItem));
+  L.stat = o;   o = align256(o + (size_t)L.slots * Hq * sizeof(float2));
+  L.acc = o;    o = align256(o + (size_t)L.slots * Hq * D * sizeof(float));
+  L.total = o;
+  return L;
+}
+
+// ---------------------------------------------------------------------------
+// The plan. Request r's queries are cut into blocks of two halves; block b of
+// n tokens sees the first kv_len - n + (its last token) + 1 private keys.
+constexpr int kAPlanThreads = 1024;
+
+__device__ __forceinline__ long long scan_ll(long long v, long long* sh, long long& total) {  // exclusive
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  if (lo >= p.R || t < p.q_start[lo]) return;
-  const int r = lo, n = p.q_start[r + 1] - p.q_start[r];
-  const long long len = min((long long)p.kv_len[r], (long long)p.max_pages * p.page);
-  const long long seen = max(0ll, min(len, len - n + (t - p.q_start[r]) + 1));
-  float q[E], o[E] = {}, m = -INFINITY, z = 0.f;
+  __syncthreads();
+  if (lane == 31) sh[w] = x;
+  __syncthreads();
+  long long s = sh[lane];  // 32 warps
 #pragma unroll
-  for (int e = 0; e < E; ++e) q[e] = __bfloat162float(p.q[row * D + lane * E + e]);
-  for (int part = 0; part < 2; ++part) {
-    const long long keys = part ? seen : p.prefix_len;
-    const int32_t* pages = part ? p.table + (size_t)r * p.max_pages : p.prefix_pages;
-    for (long long j = 0; j < keys; ++j) {
-      const int pg = pages[j / p.page];
-      if (pg < 0 || pg >= p.n_pages) { set_status(p.status, DSPARK_ERR_RANGE); continue; }
-      const size_t at = (((size_t)pg * p.page + j % p.page) * p.Hkv + h) * D + lane * E;
-      float x = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) x = fmaf(q[e], __bfloat162float(p.k[at + e]), x);
-      x = warp_sum(x) * p.rate;
-      const float mn = fmaxf(m, x), a = exp2f(m - mn), w = exp2f(x - mn);
-      m = mn;
-      z = z * a + w;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * __bfloat162float(p.v[at + e]);
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  total = __shfl_sync(0xffffffffu, s, 31);
+  const long long before = __shfl_sync(0xffffffffu, s, w > 0 ? w - 1 : 0);
+  return x - v + (w > 0 ? before : 0ll);
+}
+
+__global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams p) {
+  __shared__ long long sh[32];
+  const int tid = threadIdx.x;
+  const int step = 2 * p.TB;  // tokens a block
+  bool bad = false;
+  auto request = [&](int r, int& start, int& n, int& len) {
+    const int a = __ldg(p.q_start + r), b = __ldg(p.q_start + r + 1), l = __ldg(p.kv_len + r);
+    const long long most = min((long long)p.max_pages * p.page, 0x7fffff00ll);
+    bad |= l < 0 || l > most;
+    start = a;
+    n = b - a;
+    len = (int)max(0ll, min((long long)l, most));
+  };
+  auto tiles_of = [&](int n, int len, int t0) {  // key tiles that the block of tokens t0.. of n sees
+    return ceil_div(max(0ll, (long long)len - n + min(t0 + step, n)), kATile);
+  };
+  // starts that fall or leave [0, T]: their blocks would not be bounded by T, so nothing is computed
+  bool broken = tid == 0 && __ldg(p.q_start) != 0;
+  for (int r = tid; r < p.R; r += kAPlanThreads) {
+    const int a = __ldg(p.q_start + r), b = __ldg(p.q_start + r + 1);
+    broken |= a < 0 || b < a || b > p.T;
+  }
+  if (__syncthreads_or(broken)) {
+    if (tid == 0) {
+      *p.head = AttnHead{0, 0, 0, 0};
+      set_status(p.status, DSPARK_ERR_RANGE);
+    }
+    return;
+  }
+  const int n_tokens = __ldg(p.q_start + p.R);
+  const int p_tiles = ceil_div(p.prefix_len, kATile), p_blocks = ceil_div(n_tokens, step);
+  long long units = 0;
+  for (int r = tid; r < p.R; r += kAPlanThreads) {
+    int start, n, len;
+    request(r, start, n, len);
+    for (int t0 = 0; t0 < n; t0 += step) units += tiles_of(n, len, t0);
+  }
+  long long total;
+  scan_ll(units, sh, total);
+  total = (total + (long long)p_blocks * p_tiles) * p.Hkv;
+  long long share = max(1ll, (total + (long long)p.sms * kPlanShare - 1) / ((long long)p.sms * kPlanShare));
+  int p_splits;
+  for (;;) {  // tiles an item: more where the parts would not fit
+    p_splits = ceil_div(p_tiles, share);
+    long long slots = 0, all;
+    for (int r = tid; r < p.R; r += kAPlanThreads) {
+      int start, n, len;
+      request(r, start, n, len);
+      for (int t0 = 0; t0 < n; t0 += step) slots += (long long)ceil_div(tiles_of(n, len, t0), share) * min(step, n - t0);
+    }
+    scan_ll(slots, sh, all);
+    if (all + (long long)p_splits * n_tokens <= p.cap_slots || share > (1 << 30)) break;
+    share *= 2;
+  }
+  const long long p_items = (long long)p_blocks * p.Hkv * p_splits;
+  for (long long i = tid; i < p_items; i += kAPlanThreads) {  // blocks that read the same keys next to one another
+    const int b = (int)(i % p_blocks), s = (int)((i / p_blocks) % p_splits), h = (int)(i / p_blocks / p_splits);
+    const int a = (int)((long long)s * p_tiles / p_splits), e = (int)((long long)(s + 1) * p_tiles / p_splits);
+    AttnItem it;
+    it.head = h;
+    it.req = -1;
+    it.tok0 = b * step;
+    it.n_tok = min(step, n_tokens - it.tok0);
+    it.key0 = a * kATile;
+    it.n_keys = min(p.prefix_len, e * kATile) - it.key0;
+    it.slot0 = s * n_tokens + it.tok0;
+    it.pos0 = it.n_keys;
+    p.items[i] = it;
+  }
+  long long item0 = p_items, slot0 = (long long)p_splits * n_tokens;
+  for (int r0 = 0; r0 < p.R; r0 += kAPlanThreads) {
+    const int r = r0 + tid;
+    int start = 0, n = 0, len = 0;
+    if (r < p.R) request(r, start, n, len);
+    long long items = 0, slots = 0;
+    for (int t0 = 0; t0 < n; t0 += step) {
+      const int ns = ceil_div(tiles_of(n, len, t0), share);
+      items += (long long)ns * p.Hkv;
+      slots += (long long)ns * min(step, n - t0);
+    }
+    long long n_items, n_slots;
+    long long item = item0 + scan_ll(items, sh, n_items), slot = slot0 + scan_ll(slots, sh, n_slots);
+    item0 += n_items;
+    slot0 += n_slots;
+    for (int t0 = 0; t0 < n; t0 += step) {
+      const int tiles = tiles_of(n, len, t0), ns = ceil_div(tiles, share), nt = min(step, n - t0);
+      const bool direct = p_splits == 0 && ns == 1;
+      for (int i = 0; i < nt; ++i)
+        p.tokens[start + t0 + i] = make_int4((int)slot + i, nt, direct ? -1 : ns, 0);
+      const int seen = max(0, min(len, len - n + t0 + nt));  // keys that the block's last token sees
+      for (int s = 0; s < ns; ++s) {
+        const int a = (int)((long long)s * tiles / ns), e = (int)((long long)(s + 1) * tiles / ns);
+        for (int h = 0; h < p.Hkv; ++h, ++item) {
+          AttnItem it;
+          it.head = h;
+          it.req = r;
+          it.tok0 = start + t0;
+          it.n_tok = nt;
+          it.key0 = a * kATile;
+          it.n_keys = min(seen, e * kATile) - it.key0;
+          it.slot0 = direct ? -1 : (int)slot + s * nt;
+          it.pos0 = len - n + t0 + 1 - it.key0;
+          p.items[item] = it;
+        }
+      }
+      slot += (long long)ns * nt;
     }
   }
+  if (tid == 0) {
+    p.head->n_items = (int)item0;
+    p.head->prefix_splits = p_splits;
+    p.head->n_tokens = n_tokens;
+  }
+  if (bad) set_status(p.status, DSPARK_ERR_RANGE);
+}
+
+// ---------------------------------------------------------------------------
+template <int D>
+struct AttnSmem {
+  static constexpr int kHalves = D / 64;               // 64-column boxes of a head
+  static constexpr uint32_t kBox = kATile * 128;       // 128 rows of 64 bf16
+  static constexpr uint32_t kTileBytes = kHalves * kBox;
+  static constexpr int kSlots = D == 128 ? 5 : 10;     // K and V tiles in the ring
+  static constexpr uint32_t kQ = 2 * kTileBytes;
+  static constexpr uint32_t kTotal = 1024 + kQ + kSlots * kTileBytes + 512;
+};
+
+// Items of this CTA in the order that it takes them.
+struct ItemWalk {
+  int n, b, grid, cnt;
+  __device__ ItemWalk(int n_items) : n(n_items), b(blockIdx.x), grid(gridDim.x) {
+    cnt = b < n ? (n - b + grid - 1) / grid : 0;
+  }
+  __device__ int at(int k) const { return b + ((b & 1) ? cnt - 1 - k : k) * grid; }
+};
+
+__device__ __forceinline__ AttnItem load_item(const AttnItem* p) {
+  const int4 a = __ldg(reinterpret_cast<const int4*>(p)), b = __ldg(reinterpret_cast<const int4*>(p) + 1);
+  AttnItem it;
+  it.head = a.x; it.req = a.y; it.tok0 = a.z; it.n_tok = a.w;
+  it.key0 = b.x; it.n_keys = b.y; it.slot0 = b.z; it.pos0 = b.w;
+  return it;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAThreads, 1)
+    attn_tiles_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
+                      const __grid_constant__ CUtensorMap mapV, AttnParams p, int q_rows, int box_rows) {
+  using S = AttnSmem<D>;
+  constexpr int kHalves = S::kHalves, kSlots = S::kSlots;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* sQ = smem;
+  unsigned char* sKV = smem + S::kQ;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sKV + kSlots * S::kTileBytes);
+  uint64_t* empty = full + kSlots;
+  uint64_t* qFull = empty + kSlots;
+  uint64_t* qEmpty = qFull + 1;
+  uint64_t* sFull = qEmpty + 1;   // [2] S of a half is in TMEM
+  uint64_t* pFull = sFull + 2;    // [2] P of a half is in TMEM
+  uint64_t* oFull = pFull + 2;    // [2] O of a half is complete
+  uint64_t* oEmpty = oFull + 2;   // [2] the epilogue has read O
+  uint64_t* drain = oEmpty + 2;
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* sAbort = reinterpret_cast<volatile int*>(sTmem + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    mbar_init(qFull, 1);
+    mbar_init(qEmpty, 1);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&sFull[g], 1);
+      mbar_init(&pFull[g], 4);
+      mbar_init(&oFull[g], 1);
+      mbar_init(&oEmpty[g], 4);
+    }
+    mbar_init(drain, 1);
+    *sAbort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) {
+    __syncwarp();
+    tmem_alloc(sTmem, 512);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sTmem;
+  const ItemWalk walk(p.head->n_items);
+
+  if (warp == 8) {
+    // ---- loads ----
+    if (lane == 0) {
+      prefetch_tensormap(&mapQ);
+      prefetch_tensormap(&mapK);
+      prefetch_tensormap(&mapV);
+    }
+    const uint64_t pol = l2_policy_evict_normal();
+    int n = 0, nq = 0;  // ring tiles and Q blocks issued
+    bool stop = false;
+    for (int k = 0; k < walk.cnt && !stop; ++k) {
+      const AttnItem it = load_item(p.items + walk.at(k));
+      const int nt = ceil_div(it.n_keys, kATile);
+      const int32_t* pages = it.req < 0 ? p.prefix_pages : p.table + (size_t)it.req * p.max_pages;
+      const int boxes = kATile / box_rows;
+      auto page_at = [&](int j) {  // lane i: the page of box i of tile j
+        const int pos = j * kATile + lane * box_rows;
+        return lane < boxes && pos < it.n_keys ? __ldg(pages + ((it.key0 + pos) >> p.page_log2)) : 0;
+      };
+      int pg = page_at(0);
+      for (int j = 0; j < nt && !stop; ++j) {
+        const int live = min(boxes, ceil_div(it.n_keys - j * kATile, box_rows));
+        const int row = (it.key0 + j * kATile + lane * box_rows) & (p.page - 1);
+        const int next = j + 1 < nt ? page_at(j + 1) : 0;
+        if (lane < live && (pg < 0 || pg >= p.n_pages)) set_status(p.status, DSPARK_ERR_RANGE);
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const int slot = n % kSlots;
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, sAbort, p.status))) { stop = true; break; }
+          if (lane == 0) mbar_expect_tx(&full[slot], (uint32_t)(live * box_rows * 128 * kHalves));
+          __syncwarp();
+          if (lane < live) {
+            unsigned char* dst = sKV + slot * S::kTileBytes + lane * box_rows * 128;
 #pragma unroll
-  for (int e = 0; e < E; ++e) p.out[row * D + lane * E + e] = __float2bfloat16_rn(z > 0.f ? o[e] / z : 0.f);
-  if (p.lse && lane == 0) p.lse[row] = z > 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+            for (int c = 0; c < kHalves; ++c)
+              tma_load_4d(dst + c * S::kBox, kv ? &mapV : &mapK, 64 * c, it.head, row, pg, &full[slot], pol);
+          }
+          if (j == 0 && kv == 0) {  // Q behind the first K tile: its buffer is free once the item before has no S left to form
+            if (!__all_sync(0xffffffffu, mbar_wait(qEmpty, (k & 1) ^ 1, sAbort, p.status))) { ++n; stop = true; break; }
+            if (lane == 0) {
+              const int groups = it.n_tok > p.TB ? 2 : 1;
+              mbar_expect_tx(qFull, (uint32_t)(groups * q_rows * 128 * kHalves));
+              for (int g = 0; g < groups; ++g)
+                for (int c = 0; c < kHalves; ++c)
+                  tma_load_4d(sQ + g * S::kTileBytes + c * S::kBox, &mapQ, 64 * c, 0, it.head, it.tok0 + g * p.TB, qFull, pol);
+            }
+            ++nq;
+          }
+        }
+        pg = next;
+      }
+    }
+    // no copy outlives the CTA: the last kSlots ring tiles and the last Q
+    if (nq > 0) mbar_wait_drain(qFull, (nq - 1) & 1, p.status);
+    for (int i = 1; i <= kSlots && n - i >= 0; ++i)
+      mbar_wait_drain(&full[(n - i) % kSlots], ((n - i) / kSlots) & 1, p.status);
+  } else if (warp == 9) {
+    // ---- MMA issue ----
+    const uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0), idesc_pv = idesc_bf16_f32(128, D, 1);
+    int n = 0;                // ring tiles consumed
+    uint32_t nP[2] = {0, 0};  // P tiles consumed of each half
+    uint32_t nO[2] = {0, 0};  // items finished by each half
+    bool stop = false;
+    auto ring_wait = [&]() {
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(&full[n % kSlots], (n / kSlots) & 1, sAbort, p.status));
+      tc_fence_after();
+      return ok;
+    };
+    auto issue_qk = [&](int g, int slot) {
+      if (lane == 0) {
+        const uint32_t q = smem_u32(sQ + g * S::kTileBytes), kk = smem_u32(sKV + slot * S::kTileBytes);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) {
+          const uint32_t off = (s / 4) * S::kBox + (s % 4) * 32;
+          tc_mma_bf16(tmem + 128u * g, smem_desc_sw128(q + off, 0, 1024), smem_desc_sw128(kk + off, 0, 1024), idesc_qk, s > 0);
+        }
+        tc_commit(&sFull[g]);
+      }
+    };
+    for (int k = 0; k < walk.cnt && !stop; ++k) {
+      const AttnItem it = load_item(p.items + walk.at(k));
+      const int nt = ceil_div(it.n_keys, kATile), groups = it.n_tok > p.TB ? 2 : 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(qFull, k & 1, sAbort, p.status))) { stop = true; break; }
+      if (!ring_wait()) { stop = true; break; }
+      for (int g = 0; g < groups; ++g) issue_qk(g, n % kSlots);
+      if (lane == 0) {
+        tc_commit(&empty[n % kSlots]);
+        if (nt == 1) tc_commit(qEmpty);
+      }
+      ++n;
+      for (int j = 0; j < nt && !stop; ++j) {
+        const int valid = min(kATile, it.n_keys - j * kATile), ksteps = (valid + 15) >> 4;
+        const int vslot = n % kSlots, kslot = (n + 1) % kSlots;
+        const bool more = j + 1 < nt;
+        for (int g = 0; g < groups; ++g) {
+          if (g == 0) {
+            if (!ring_wait()) { stop = true; break; }
+            if (valid & 15) {  // rows of the last group that lie past the keys
+              unsigned char* v = sKV + vslot * S::kTileBytes;
+              const int rows = 16 * ksteps - valid;
+              for (int i = lane; i < rows * 8 * kHalves; i += 32) {
+                const int c = i / (rows * 8), rest = i - c * rows * 8;
+                *reinterpret_cast<uint4*>(v + c * S::kBox + (valid + rest / 8) * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait(&pFull[g], nP[g] & 1, sAbort, p.status))) { stop = true; break; }
+          ++nP[g];
+          if (j == 0 && !__all_sync(0xffffffffu, mbar_wait(&oEmpty[g], (nO[g] & 1) ^ 1, sAbort, p.status))) { stop = true; break; }
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t v = smem_u32(sKV + vslot * S::kTileBytes);
+            for (int s = 0; s < ksteps; ++s)
+              tc_mma_bf16_ts(tmem + 256u + 128u * g, tmem + 128u * g + 8u * s, smem_desc_sw128(v + s * 2048, S::kBox, 1024),
+                             idesc_pv, (j | s) != 0);
+          }
+          if (more) {
+            if (g == 0) {
+              ++n;  // the V tile stays counted by vslot; the next K tile follows it in the ring
+              const bool ok = ring_wait();
+              if (!ok) { stop = true; break; }
+            }
+            issue_qk(g, kslot);
+          } else if (lane == 0) {
+            tc_commit(&oFull[g]);
+          }
+          if (!more) ++nO[g];
+        }
+        if (stop) break;
+        if (lane == 0) {
+          tc_commit(&empty[vslot]);
+          if (more) tc_commit(&empty[kslot]);
+          if (j + 2 == nt) tc_commit(qEmpty);
+        }
+        ++n;
+      }
+    }
+    if (lane == 0) {
+      tc_commit(drain);  // every MMA issued so far has completed
+      mbar_wait_drain(drain, 0, p.status);
+    }
+  } else {
+    // ---- softmax and epilogue: half g, one thread a row ----
+    const int g = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_base + 128u * g, tO = tmem + lane_base + 256u + 128u * g;
+    uint32_t nS = 0, nI = 0;
+    bool stop = false;
+    for (int k = 0; k < walk.cnt && !stop; ++k) {
+      const AttnItem it = load_item(p.items + walk.at(k));
+      if (g == 1 && it.n_tok <= p.TB) continue;
+      const int nt = ceil_div(it.n_keys, kATile);
+      const int tok = g * p.TB + row / p.G;
+      const bool valid = row < p.TB * p.G && tok < it.n_tok;
+      const int limit = !valid ? 0 : it.req < 0 ? it.n_keys : min(it.n_keys, it.pos0 + tok);  // keys the row sees
+      int clear = valid ? limit : 0x7fffffff;  // keys that every row of the warp sees
+      clear = warp_min_i(clear);
+      const bool any = clear != 0x7fffffff;
+      float m = -INFINITY, z = 0.f;
+      for (int j = 0; j < nt; ++j, ++nS) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sFull[g], nS & 1, sAbort, p.status))) { stop = true; break; }
+        tc_fence_after();
+        if (any) {
+          uint32_t a[64], b[64];
+          tmem_ld64_nowait(tS, a);
+          tmem_ld64_nowait(tS + 64u, b);
+          tmem_ld_wait64(a);
+          tmem_ld_wait64(b);
+          if ((j + 1) * kATile > clear) {
+            const int left = limit - j * kATile;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) {
+              if (c >= left) a[c] = 0xff800000u;
+              if (c + 64 >= left) b[c] = 0xff800000u;
+            }
+          }
+          float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 64; c += 4) {
+            x0 = max3(x0, __uint_as_float(a[c]), __uint_as_float(b[c]));
+            x1 = max3(x1, __uint_as_float(a[c + 1]), __uint_as_float(b[c + 1]));
+            x2 = max3(x2, __uint_as_float(a[c + 2]), __uint_as_float(b[c + 2]));
+            x3 = max3(x3, __uint_as_float(a[c + 3]), __uint_as_float(b[c + 3]));
+          }
+          const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * p.rate;
+          const bool rise = top > m + 8.f || (m == -INFINITY && top > m);
+          if (__any_sync(0xffffffffu, rise)) {
+            const float mn = rise ? top : m;
+            const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);  // mn >= m; 1 where m stays
+            m = mn;
+            z *= f;
+            if (j > 0) {
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                uint32_t u[32];
+                tmem_ld32(tO + c, o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
+                tmem_st32(tO + c, u);
+              }
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet: 2^(-inf) = 0
+          float z0 = 0.f, z1 = 0.f;
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float e0 = ex2_approx(fmaf(__uint_as_float(a[c]), p.rate, neg));
+            const float e1 = ex2_approx(fmaf(__uint_as_float(a[c + 1]), p.rate, neg));
+            z0 += e0;
+            z1 += e1;
+            w[c >> 1] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32(tS, w);
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            const float e0 = ex2_approx(fmaf(__uint_as_float(b[c]), p.rate, neg));
+            const float e1 = ex2_approx(fmaf(__uint_as_float(b[c + 1]), p.rate, neg));
+            z0 += e0;
+            z1 += e1;
+            w[c >> 1] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32(tS + 32u, w);
+          z += z0 + z1;
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pFull[g]);
+      }
+      if (stop) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&oFull[g], nI & 1, sAbort, p.status))) break;
+      ++nI;
+      tc_fence_after();
+      if (any) {
+        const int hq = it.head * p.G + row % p.G;
+        const size_t t = it.slot0 < 0 ? (size_t)it.tok0 + tok : (size_t)it.slot0 + tok;
+        const size_t at = valid ? t * p.Hq + hq : 0;
+        const float inv = z != 0.f ? 1.f / z : 0.f;
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          __syncwarp();
+          tmem_ld32(tO + c, o);
+          if (valid && it.slot0 < 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= inv;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(p.out + at * D + c + i) = pack_bf16x8(o + i);
+          } else if (valid) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              *reinterpret_cast<float4*>(p.acc + at * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        if (valid) {
+          if (it.slot0 >= 0) p.stat[at] = make_float2(m, z);
+          else if (p.lse) p.lse[at] = z != 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&oEmpty[g]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// One warp a (token, query head): the parts of the prefix, then those of the pages, in that order.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int np = p.head->prefix_splits;
+  if (row >= (long long)p.head->n_tokens * p.Hq) return;
+  const int t = (int)(row / p.Hq), hq = (int)(row % p.Hq);
+  const int4 map = __ldg(p.tokens + t);
+  if (map.z < 0) return;
+  const int n = np + map.z, n_tokens = p.head->n_tokens;
+  auto slot = [&](int i) {
+    return ((size_t)(i < np ? (long long)i * n_tokens + t : (long long)map.x + (long long)(i - np) * map.y)) * p.Hq + hq;
+  };
+  float M = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const float2 s = p.stat[slot(i)];
+    if (s.y != 0.f) M = fmaxf(M, s.x);
+  }
+  M = warp_max(M);
+  float o[E] = {}, Z = 0.f;
+  if (M > -INFINITY) {
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const size_t at = slot(i);
+      const float2 s = p.stat[at];
+      if (s.y == 0.f) continue;
+      const float f = ex2_approx(s.x - M);
+      Z = fmaf(s.y, f, Z);
+      const float* a = p.acc + at * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(a[e], f, o[e]);
+    }
+  }
+  const float inv = Z != 0.f ? 1.f / Z : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t*>(p.out + row * D + lane * E + e) = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+  if (p.lse && lane == 0) p.lse[row] = Z != 0.f ? (M + log2f(Z)) * 0.6931471805599453f : -INFINITY;
+}
+
+template <int D>
+static cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv,
+                                    int q_rows, int box_rows, cudaStream_t s) {
+  static std::atomic<unsigned long long> attr{0};
+  cudaError_t e = set_smem_limit_once((const void*)attn_tiles_kernel<D>, (int)AttnSmem<D>::kTotal, attr);
+  if (e != cudaSuccess) return e;
+  attn_plan_kernel<<<1, kAPlanThreads, 0, s>>>(p);
+  attn_tiles_kernel<D><<<p.sms, kAThreads, AttnSmem<D>::kTotal, s>>>(mq, mk, mv, p, q_rows, box_rows);
+  attn_join_kernel<D><<<ceil_div((long long)p.T * p.Hq, 8), 256, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace dspark
 
 using namespace dspark;
 
+static bool attn_heads_ok(int n_heads, int n_kv_heads, int head_dim) {
+  return n_heads >= 1 && n_kv_heads >= 1 && n_heads % n_kv_heads == 0 && n_heads / n_kv_heads <= 128 &&
+         (head_dim == 64 || head_dim == 128);
+}
+
 extern "C" size_t dspark_attention_workspace_bytes(int32_t R, int32_t T, int32_t n_heads, int32_t n_kv_heads,
                                                    int32_t head_dim) {
-  if (R < 1 || T < 0 || n_heads < 1 || n_kv_heads < 1 || head_dim < 1) return 0;
-  return 256;
+  if (R < 1 || T < 0 || !attn_heads_ok(n_heads, n_kv_heads, head_dim)) return 0;
+  return attn_layout(R, T, n_heads, n_kv_heads, head_dim).total;
 }
 
 extern "C" dspark_status dspark_prefix_attention(int32_t R, int32_t T, int32_t n_heads, int32_t n_kv_heads,
@@ -92,26 +684,60 @@ extern "C" dspark_status dspark_prefix_attention(int32_t R, int32_t T, int32_t n
                                                  const int32_t* kv_len, float scale, void* out, float* lse,
                                                  void* workspace, size_t workspace_bytes, dspark_stream_t stream) {
   note_launches(0);
-  if (R < 1 || T < 0 || n_heads < 1 || n_kv_heads < 1 || n_heads % n_kv_heads != 0 || n_heads / n_kv_heads > 128 ||
-      (head_dim != 64 && head_dim != 128) || page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)) != 0 ||
-      n_pages < 1 || max_pages < 1 || prefix_len < 0 || !(scale > 0.f) || !isfinite(scale))
+  if (R < 1 || T < 0 || !attn_heads_ok(n_heads, n_kv_heads, head_dim) || page_size < 16 || page_size > 4096 ||
+      (page_size & (page_size - 1)) != 0 || n_pages < 1 || max_pages < 1 || prefix_len < 0 || prefix_len > 0x7fffff00 ||
+      (long long)T * n_heads > (1ll << 30) || !(scale > 0.f) || !isfinite(scale))
     return DSPARK_ERR_INVALID_ARG;
   if (!q || !k_cache || !v_cache || (prefix_len > 0 && !prefix_pages) || !block_table || !q_start || !kv_len || !out)
     return DSPARK_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
        reinterpret_cast<uintptr_t>(out)) & 15)
     return DSPARK_ERR_INVALID_ARG;
-  const size_t need = dspark_attention_workspace_bytes(R, T, n_heads, n_kv_heads, head_dim);
-  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < need)
+  const AttnLayout L = attn_layout(R, T, n_heads, n_kv_heads, head_dim);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < L.total)
     return DSPARK_ERR_WORKSPACE;
   if (T == 0) return DSPARK_OK;
-  AttnParams p{R, T, n_heads, n_kv_heads, page_size, n_pages, max_pages, prefix_len,
-               (const __nv_bfloat16*)q, (const __nv_bfloat16*)k_cache, (const __nv_bfloat16*)v_cache, prefix_pages,
-               block_table, q_start, kv_len, scale * 1.4426950408889634f, (__nv_bfloat16*)out, lse,
-               static_cast<uint32_t*>(workspace)};
-  const int grid = ceil_div((long long)T * n_heads, 8);
-  if (head_dim == 128) attention_rows_kernel<128><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-  else attention_rows_kernel<64><<<grid, 256, 0, (cudaStream_t)stream>>>(p);
-  note_launches(1);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return DSPARK_ERR_CUDA;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (sms <= 0) return DSPARK_ERR_CUDA;
+  AttnParams p{};
+  p.R = R; p.T = T; p.Hq = n_heads; p.Hkv = n_kv_heads;
+  p.G = n_heads / n_kv_heads;
+  p.TB = attn_tokens_per_half(p.G);
+  p.page = page_size;
+  while ((1 << p.page_log2) < page_size) ++p.page_log2;
+  p.n_pages = n_pages; p.max_pages = max_pages; p.prefix_len = prefix_len;
+  p.sms = std::min(sms, kMaxSms);
+  p.cap_slots = L.slots;
+  p.prefix_pages = prefix_pages; p.table = block_table; p.q_start = q_start; p.kv_len = kv_len;
+  p.rate = scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.lse = lse;
+  p.status = static_cast<uint32_t*>(workspace);
+  p.head = ws_at<AttnHead>(workspace, L.head);
+  p.tokens = ws_at<int4>(workspace, L.tokens);
+  p.items = ws_at<AttnItem>(workspace, L.items);
+  p.stat = ws_at<float2>(workspace, L.stat);
+  p.acc = ws_at<float>(workspace, L.acc);
+  const uint64_t D = head_dim, e = 2;
+  CUtensorMap mq, mk, mv;
+  const int box_tokens = std::min(p.TB, T), box_rows = std::min(page_size, kATile);
+  {
+    const uint64_t dims[4] = {D, (uint64_t)p.G, (uint64_t)n_kv_heads, (uint64_t)T};
+    const uint64_t strides[3] = {D * e, D * e * p.G, D * e * n_heads};
+    const uint32_t box[4] = {64, (uint32_t)p.G, 1, (uint32_t)box_tokens};
+    if (!make_tmap_bf16(&mq, q, 4, dims, strides, box)) return DSPARK_ERR_CUDA;
+  }
+  const uint64_t dims[4] = {D, (uint64_t)n_kv_heads, (uint64_t)page_size, (uint64_t)n_pages};
+  const uint64_t strides[3] = {D * e, D * e * n_kv_heads, D * e * n_kv_heads * page_size};
+  const uint32_t box[4] = {64, 1, (uint32_t)box_rows, 1};
+  if (!make_tmap_bf16(&mk, k_cache, 4, dims, strides, box) || !make_tmap_bf16(&mv, v_cache, 4, dims, strides, box))
+    return DSPARK_ERR_CUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int q_rows = box_tokens * p.G;
+  const cudaError_t err = head_dim == 128 ? launch_attention<128>(p, mq, mk, mv, q_rows, box_rows, s)
+                                          : launch_attention<64>(p, mq, mk, mv, q_rows, box_rows, s);
+  note_launches(3);
+  return err == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
