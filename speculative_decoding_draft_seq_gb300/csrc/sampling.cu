@@ -11,19 +11,23 @@
 // of the top-k set; min-p keeps the entries with w >= min_p. All three are
 // prefixes of that order, so the kept set is "logit above x*, or equal to it
 // and index below cut": one threshold, found in three steps.
-//   1  the row streams in once from memory: maximum, and counts in 4096 bins of
-//      1/32 octave of weight (relative to an entry of the row, so that the
-//      maximum need not be known yet);
-//   2  the bins give the count, and within a few per mille the mass, at which
-//      top-k or top-p ends; a second pass (from L2) collects the entries of the
-//      bins in question, or of all bins from the top where they fit, in shared
-//      memory, and adds up the exact masses that the answer needs;
-//   3  radix selection on the collected entries' order-preserving integer keys
-//      (2048-bin histograms of counts and masses over a shrinking key range).
-// Where step 2 finds no set of bins that fits (thousands of equal entries, or
-// logits hundreds of octaves apart), the selection runs on the row itself.
-// One block a row: a row of 129,280 bf16 is 258 KB, and the rows in flight stay
-// in L2 between the passes.
+//   1  the row streams in once from memory: its maximum, and an estimate of its
+//      distribution in 4096 bins of 1/32 octave of weight. The largest entry of
+//      each 16-byte piece is counted once; for top-p the piece's first entry, if
+//      it is another one, stands for the rest of all pieces. (A shared-memory add
+//      for every entry bounds the pass: 15 us a row of 129,280 instead of 6.)
+//   2  the estimate says down to which logit top-k reaches (at least k pieces have
+//      a larger one), or between which two logits top-p ends, with a margin; a
+//      second pass (from L2) collects the entries of that range, or all from its
+//      lower end up where they fit, in shared memory, and forms exactly the masses
+//      that the answer needs. They prove the range right; a range that was not is
+//      moved by what they show, and collected again.
+//   3  exact selection among the collected entries: by comparing all pairs of a
+//      short list, else by radix selection on order-preserving integer keys
+//      (2048-bin histograms of counts or masses over a shrinking key range).
+// Where no range fits the list (thousands of equal entries, logits hundreds of
+// octaves apart), the radix selection runs on the row itself. One block a row: a
+// row of 129,280 bf16 is 258 KB, and the rows in flight stay in L2 between passes.
 #include <algorithm>
 
 #include "common.cuh"
@@ -34,8 +38,8 @@ namespace dspark {
 
 constexpr int kSBins = 2048;    // bins of a selection round
 constexpr int kWBins = 4096;    // weight bins, 32 an octave
-constexpr int kSList = 6144;    // collected entries
-constexpr uint32_t kSSmem = kWBins * 4 + kWBins * 8 + kSList * 8;
+constexpr int kSList = 2944;    // collected entries: four blocks of 256 threads fit an SM
+constexpr uint32_t kSSmem = kWBins * 4 + kWBins * 4 + kSList * 8;
 
 struct SampleParams {
   int V;
@@ -73,16 +77,62 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   return d;
 }
 
+__device__ __forceinline__ uint32_t bf16x2_max_nan(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long f32x2_add(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long f32x2_mul(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long f32x2_add_rz(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long f32x2_fma_rz(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // Sum of floor(w 2^40) over weights in [0, 1], as two sums of 20-bit halves: adding 8 with rounding
 // towards zero leaves floor(w 2^20) in the low mantissa bits, and what it cut off gives the other half.
 // Up to 2^11 weights fit.
+struct MassPair {  // the two halves of two masses
+  uint32_t hi[2], lo[2];
+  __device__ __forceinline__ MassPair(float w0, float w1) {
+    const unsigned long long w = f32x2_pack(w0, w1), eight = f32x2_pack(8.f, 8.f);
+    const unsigned long long a = f32x2_add_rz(w, eight);
+    const unsigned long long cut = f32x2_add(a, f32x2_pack(-8.f, -8.f));                  // exact
+    const unsigned long long rest = f32x2_fma(cut, f32x2_pack(-1.f, -1.f), w);             // exact
+    const unsigned long long b = f32x2_fma_rz(rest, f32x2_pack(0x1p20f, 0x1p20f), eight);
+    float x, y;
+    f32x2_unpack(a, x, y);
+    hi[0] = __float_as_uint(x);
+    hi[1] = __float_as_uint(y);
+    f32x2_unpack(b, x, y);
+    lo[0] = __float_as_uint(x);
+    lo[1] = __float_as_uint(y);
+  }
+};
 struct MassSum {
   uint32_t hi = 0, lo = 0, n = 0;
-  __device__ __forceinline__ void add(float w) {
-    const float a = __fadd_rz(w, 8.f);
-    const float b = __fmaf_rz(__fsub_rn(w, __fsub_rn(a, 8.f)), 0x1p20f, 8.f);
-    hi += __float_as_uint(a);
-    lo += __float_as_uint(b);
+  __device__ __forceinline__ void add(const MassPair& m) {
+    hi += m.hi[0] + m.hi[1];
+    lo += m.lo[0] + m.lo[1];
+    n += 2;
+  }
+  __device__ __forceinline__ void add(const MassPair& m, int i) {
+    hi += m.hi[i];
+    lo += m.lo[i];
     ++n;
   }
   __device__ __forceinline__ unsigned long long total() const {
@@ -125,8 +175,8 @@ __device__ __forceinline__ unsigned long long block_scan_u64(unsigned long long 
 }
 
 // A row in 16-byte pieces, the entries before the first and after the last aligned one on their own.
-// Plain loads: dspark_truncate may write the row in place.
-template <class Tin>
+// Plain loads: dspark_truncate may write the row in place. U pieces a thread are in flight.
+template <class Tin, int U>
 struct RowView {
   static constexpr int E = 16 / (int)sizeof(Tin);
   const Tin* row;
@@ -151,98 +201,157 @@ struct RowView {
       }
     }
   }
-  // f(x, v) for the entries of pieces g0 <= g < g1 (tid-th of nt threads) and, with `ends`, the loose ones
+  // The largest entry of a piece (NaN if there is one).
+  static __device__ __forceinline__ float largest(const uint4& q) {
+    if (E == 8) {
+      const uint32_t m = bf16x2_max_nan(bf16x2_max_nan(q.x, q.y), bf16x2_max_nan(q.z, q.w));
+      return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    }
+    return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)), max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
+  // f(piece, first index) for the pieces g0 <= g < g1, the tid-th of every nt
   template <class F>
-  __device__ __forceinline__ void each(int g0, int g1, int tid, int nt, bool ends, F f) const {
-    constexpr int U = 4;
+  __device__ __forceinline__ void pieces(int g0, int g1, int tid, int nt, F f) const {
     for (int g = g0 + tid; g < g1; g += U * nt) {
       uint4 q[U];
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (g + u * nt < g1) q[u] = piece(g + u * nt);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (g + u * nt >= g1) break;
-        float x[E];
-        split(q[u], x);
-        const int v = a0 + (g + u * nt) * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) f(x[e], v + e);
-      }
-    }
-    if (ends) {
-      const int loose = V - nv * E;
-      for (int i = tid; i < loose; i += nt) {
-        const int v = i < a0 ? i : i + nv * E;
-        f(at(v), v);
-      }
+      for (int u = 0; u < U; ++u)
+        if (g + u * nt < g1) f(q[u], a0 + (g + u * nt) * E);
     }
   }
+  // f(x, v) for the loose entries at both ends
   template <class F>
-  __device__ __forceinline__ void all(F f) const { each(0, nv, threadIdx.x, blockDim.x, true, f); }
+  __device__ __forceinline__ void loose(int tid, int nt, F f) const {
+    for (int i = tid; i < V - nv * E; i += nt) {
+      const int v = i < a0 ? i : i + nv * E;
+      f(at(v), v);
+    }
+  }
+  // f(x, v) for all entries
+  template <class F>
+  __device__ __forceinline__ void all(F f) const {
+    pieces(0, nv, threadIdx.x, blockDim.x, [&](const uint4& q, int v) {
+      float x[E];
+      split(q, x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) f(x[e], v + e);
+    });
+    loose(threadIdx.x, blockDim.x, f);
+  }
 };
 
-struct Threshold {
-  uint32_t key;             // the last kept key
-  unsigned long long ties;  // entries of this key that are kept, in index order
-  unsigned long long count, above;  // entries of this key; the mass of the larger keys
+// 64-bit sums of a selection round in two words: shared memory adds 32 bits natively (a 64-bit add is a
+// compare-and-swap loop, and equal logits all add to one bin).
+struct MassBin {
+  uint32_t lo, hi;
+  __device__ __forceinline__ unsigned long long value() const { return ((unsigned long long)hi << 32) | lo; }
 };
+__device__ __forceinline__ void add_mass(MassBin* b, unsigned long long m) {
+  const uint32_t lo = (uint32_t)m, old = atomicAdd(&b->lo, lo);
+  const uint32_t hi = (uint32_t)(m >> 32) + (old + lo < old ? 1u : 0u);
+  if (hi) atomicAdd(&b->hi, hi);
+}
+
+struct Threshold {
+  uint32_t key;   // the last kept key
+  uint32_t ties;  // entries of this key that are kept, in index order
+  uint32_t count; // entries of this key
+};
+
+__device__ __forceinline__ uint32_t block_scan_u32(uint32_t v, uint32_t* sh) {  // inclusive, over the block's threads
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh[w] = v;
+  __syncthreads();
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < w && lane < nw ? sh[lane] : 0u);
+  return v + before;
+}
+
+// The first of kSBins bins at which the running sum, from `above` on, reaches `target`: pick[0], and the sum
+// before it: pick[1]. A warp adds up neighbouring bins; the warp that the target falls to scans its own.
+template <class Value>
+__device__ __forceinline__ void find_bin(Value value, unsigned long long target, unsigned long long above, unsigned long long* sh,
+                                         unsigned long long* pick) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5, per = kSBins / nw;
+  unsigned long long v = 0;
+  for (int i = lane; i < per; i += 32) v += value(w * per + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0) sh[w] = v;
+  __syncthreads();
+  unsigned long long at = above;
+  for (int i = 0; i < w; ++i) at += sh[i];
+  if (at < target && at + v >= target) {
+    for (int i = lane; i < per; i += 32) {
+      const unsigned long long n = value(w * per + i);
+      unsigned long long x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (at + x - n < target && at + x >= target) {
+        pick[0] = w * per + i;
+        pick[1] = at + x - n;
+      }
+      at += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+}
 
 struct SelectScratch {
   uint32_t* cnt;              // [kSBins]
-  unsigned long long* mass;   // [kSBins]
+  MassBin* mass;              // [kSBins]
   unsigned long long* sh;     // [32]
   unsigned long long* pick;   // [4]
 };
 
-// The key at which the running count (by_mass = false) or mass in descending order first reaches
-// `target`, among the keys lo..hi of the entries that `source` enumerates; `above` is the mass of the
-// larger keys that it leaves out.
-template <class Source, class Mass>
-__device__ Threshold select_key(Source source, Mass mass_of, bool by_mass, unsigned long long target, unsigned long long c_above,
-                                unsigned long long m_above, uint32_t lo, uint32_t hi, const SelectScratch& s) {
-  const int tid = threadIdx.x, nt = blockDim.x, per = kSBins / nt;
+// The key at which the running count or (kByMass) mass in descending order first reaches `target`, among
+// the keys lo..hi of the entries that `source` enumerates; `above`: that of the larger keys it leaves out.
+template <bool kByMass, class Source, class Mass>
+__device__ Threshold select_key(Source source, Mass mass_of, unsigned long long target, unsigned long long above, uint32_t lo,
+                                uint32_t hi, const SelectScratch& s) {
+  const int tid = threadIdx.x, nt = blockDim.x;
   for (;;) {
     const uint32_t span = hi - lo;
     const int bits = 32 - __clz(span), shift = bits > 11 ? bits - 11 : 0;
     __syncthreads();
-    for (int b = tid; b < kSBins; b += nt) { s.cnt[b] = 0; s.mass[b] = 0; }
+    for (int b = tid; b < kSBins; b += nt) {
+      s.cnt[b] = 0;
+      if (kByMass) s.mass[b] = MassBin{0, 0};
+    }
     __syncthreads();
     source([&](uint32_t k) {
       if (k < lo || k > hi) return;
       const uint32_t b = (hi - k) >> shift;
       atomicAdd(&s.cnt[b], 1u);
-      atomicAdd(&s.mass[b], mass_of(k));
+      if (kByMass && shift > 0) add_mass(&s.mass[b], mass_of(k));
     });
     __syncthreads();
-    unsigned long long c = 0, m = 0;
-    for (int i = 0; i < per; ++i) { c += s.cnt[per * tid + i]; m += s.mass[per * tid + i]; }
-    unsigned long long ci = block_scan_u64(c, s.sh) - c + c_above, mi = block_scan_u64(m, s.sh) - m + m_above;
-    for (int i = 0; i < per; ++i) {
-      const unsigned long long cb = s.cnt[per * tid + i], mb = s.mass[per * tid + i];
-      const unsigned long long start = by_mass ? mi : ci, end = by_mass ? mi + mb : ci + cb;
-      if (start < target && end >= target) {
-        s.pick[0] = per * tid + i;
-        s.pick[1] = ci;
-        s.pick[2] = mi;
-        s.pick[3] = cb;
-      }
-      ci += cb;
-      mi += mb;
-    }
-    __syncthreads();
+    auto value = [&](int b) -> unsigned long long {
+      if (!kByMass) return s.cnt[b];
+      if (shift > 0) return s.mass[b].value();
+      const unsigned long long n = s.cnt[b];  // a bin of one key
+      return n ? n * mass_of(hi - (uint32_t)b) : 0ull;
+    };
+    find_bin(value, target, above, s.sh, s.pick);
     const uint32_t b = (uint32_t)s.pick[0];
-    c_above = s.pick[1];
-    m_above = s.pick[2];
-    const unsigned long long cnt = s.pick[3];
+    above = s.pick[1];
     if (shift == 0) {
       Threshold t;
       t.key = hi - b;
-      t.count = cnt;
-      t.above = m_above;
-      const unsigned long long w = mass_of(t.key);
-      t.ties = by_mass ? (target - m_above + w - 1) / w : target - c_above;
-      if (t.ties > cnt) t.ties = cnt;
+      t.count = s.cnt[b];
+      const unsigned long long w = kByMass ? mass_of(t.key) : 1ull;
+      t.ties = (uint32_t)min((unsigned long long)t.count, (target - above + w - 1) / w);
       __syncthreads();
       return t;
     }
@@ -250,6 +359,46 @@ __device__ Threshold select_key(Source source, Mass mass_of, bool by_mass, unsig
     lo = max(lo, top - ((1u << shift) - 1));
     hi = top;
   }
+}
+
+// Entry tid of a short list: how many entries come before it in an order, and their mass. All pairs are
+// compared, kRanked threads an entry's share each.
+constexpr int kRanked = 256;
+struct RankScratch {
+  unsigned long long* mass;  // [kRanked]
+  MassBin* before;           // [kRanked]
+  uint32_t* rank;            // [kRanked]
+};
+struct Ranked {
+  int rank;
+  unsigned long long mass, before;
+};
+template <class Mass, class First>
+__device__ Ranked rank_entries(const uint2* list, int n, Mass mass_of, First first, const RankScratch& s) {
+  const int tid = threadIdx.x, e = tid & (kRanked - 1), parts = blockDim.x / kRanked;
+  __syncthreads();
+  if (tid < n) {
+    s.mass[tid] = mass_of(list[tid].x);
+    s.before[tid] = MassBin{0, 0};
+    s.rank[tid] = 0;
+  }
+  __syncthreads();
+  if (e < n) {
+    const uint2 me = list[e];
+    uint32_t rank = 0;
+    unsigned long long m = 0;
+    for (int j = tid / kRanked; j < n; j += parts)
+      if (first(list[j], me)) {
+        ++rank;
+        m += s.mass[j];
+      }
+    atomicAdd(&s.rank[e], rank);
+    add_mass(&s.before[e], m);
+  }
+  __syncthreads();
+  Ranked r{0, 0, 0};
+  if (tid < n) r = Ranked{(int)s.rank[tid], s.mass[tid], s.before[tid].value()};
+  return r;
 }
 
 // Magic-number rounding to whole bins: float32 values from 2^23 on are integers.
@@ -262,19 +411,25 @@ struct WeightBins {
   static __device__ __forceinline__ float edge(int bin) { return 8388608.f + (float)bin; }
 };
 
-template <class Tin>
-__global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) {
+template <class Tin, int NT, int kBlocks>
+__global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams p) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ unsigned long long sh[32], s_pick[4];
   __shared__ float shf[32];
   __shared__ int shi[32], s_n;
-  uint32_t* cum_c = reinterpret_cast<uint32_t*>(s_raw);                               // [kWBins] from the top bin down
-  unsigned long long* cum_m = reinterpret_cast<unsigned long long*>(cum_c + kWBins);  // [kWBins] the same, estimated mass
-  uint2* list = reinterpret_cast<uint2*>(cum_m + kWBins);                             // [kSList] (key, index)
-  const SelectScratch scratch{reinterpret_cast<uint32_t*>(cum_m + kSBins), cum_m, sh, s_pick};
-  const int tid = threadIdx.x, nt = blockDim.x, V = p.V;
+  __shared__ uint2 s_range[32];
+  uint32_t* cum_c = reinterpret_cast<uint32_t*>(s_raw);        // [kWBins] estimated counts, from the top bin down
+  float* cum_m = reinterpret_cast<float*>(cum_c + kWBins);     // [kWBins] estimated masses, relative to the maximum's
+  uint2* list = reinterpret_cast<uint2*>(cum_m + kWBins);      // [kSList] (key, index)
+  // the selection's arrays, over the bins (no longer needed then)
+  MassBin* s_mass = reinterpret_cast<MassBin*>(s_raw);
+  const SelectScratch scratch{reinterpret_cast<uint32_t*>(s_mass + kSBins), s_mass, sh, s_pick};
+  unsigned long long* s_u64 = reinterpret_cast<unsigned long long*>(s_raw);
+  const RankScratch few{s_u64, reinterpret_cast<MassBin*>(s_u64 + kRanked), reinterpret_cast<uint32_t*>(s_u64 + 2 * kRanked)};
+  const int tid = threadIdx.x, V = p.V;
+  constexpr int nt = NT;
   const size_t r = blockIdx.x;
-  const RowView<Tin> row(static_cast<const Tin*>(p.logits) + r * V, V);
+  const RowView<Tin, (kBlocks > 1 ? 4 : 8)> row(static_cast<const Tin*>(p.logits) + r * V, V);
   const float T = __ldg(p.temperature + r), tp = __ldg(p.top_p + r);
   const float min_w = fminf(fmaxf(__ldg(p.min_p + r), 0.f), 1.f);
   const int k = __ldg(p.top_k + r);
@@ -282,11 +437,12 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
   const float rate = fminf(__fdiv_rn(1.4426950408889634f, T), 1e30f);
 
   // ---- 1: maximum and weight bins ----
+  using Row = RowView<Tin, (kBlocks > 1 ? 4 : 8)>;
   WeightBins bins{32.f * rate, 0.f};
   bool binned = by_k || by_p;
-  if (binned) {  // the bins' origin: the largest of the first entries
-    float m0 = -INFINITY;
-    for (int v = tid & 31; v < min(V, 256); v += 32) m0 = fmaxf(m0, row.at(v));
+  float m0 = -INFINITY;  // the largest of 256 spread entries: the bins' origin
+  if (binned) {
+    for (int i = tid & 31; i < 256; i += 32) m0 = fmaxf(m0, row.at((int)(((long long)i * V) >> 8)));
     m0 = warp_max(m0);
     if (!(fabsf(m0) < INFINITY)) m0 = 0.f;
     const float o = rintf(m0 * bins.c);
@@ -296,13 +452,25 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
     __syncthreads();
   }
   float M = -INFINITY;
-  if (binned)
-    row.all([&](float x, int) {
-      M = max_nan(M, x);
-      atomicAdd(&cum_c[kWBins - 1 - WeightBins::index(bins.pos(x))], 1u);
+  if (binned) {
+    auto count = [&](float x, uint32_t n) { atomicAdd(&cum_c[kWBins - 1 - WeightBins::index(bins.pos(x))], n); };
+    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int) {
+      const float g = Row::largest(q);
+      M = max_nan(M, g);
+      count(g, 1u);
+      if (!by_k) {  // of E entries that are not the largest with chance 1 - 1/E, E - 1 to stand for
+        const float x = Row::E == 8 ? __uint_as_float(q.x << 16) : __uint_as_float(q.x);
+        if (x < g) count(x, (uint32_t)Row::E);
+      }
     });
-  else
-    row.all([&](float x, int) { M = max_nan(M, x); });
+    row.loose(tid, nt, [&](float x, int) {
+      M = max_nan(M, x);
+      count(x, 1u);
+    });
+  } else {
+    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int) { M = max_nan(M, Row::largest(q)); });
+    row.loose(tid, nt, [&](float x, int) { M = max_nan(M, x); });
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
   if ((tid & 31) == 0) shf[tid >> 5] = M;
@@ -331,7 +499,17 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
   int n_list = 0;
   if (greedy) {
     int at = V;
-    row.all([&](float x, int v) { at = x == M ? min(at, v) : at; });
+    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v) {
+      if (Row::largest(q) != M || v >= at) return;
+      float x[Row::E];
+      Row::split(q, x);
+#pragma unroll
+      for (int e = Row::E - 1; e >= 0; --e)
+        if (x[e] == M) at = v + e;
+    });
+    row.loose(tid, nt, [&](float x, int v) {
+      if (x == M) at = min(at, v);
+    });
     at = block_min_i(at, shi);
     key = logit_key(M);
     cut = at + 1;
@@ -339,150 +517,265 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
     const uint32_t hi = logit_key(M), lowest = logit_key(-INFINITY);
     const float tm = __fmaf_rn(M, bins.c, bins.off - 8388608.f);  // the maximum's place on the bins' axis
     binned = binned && tm > 0.f && tm < kWBins - 1;
-    Threshold th;
+    Threshold th{0, 0, 0};
     bool found = false;
-    unsigned long long S = 0;
+    unsigned long long S = 0, want = 0, above = 0;  // top-p's whole, its limit, and what lies above the list
+    // the mass of the top-k set that ends at `th`
+    auto top_mass = [&](auto source) {
+      unsigned long long m = 0;
+      source([&](uint32_t q) { m += q > th.key ? mass_of(q) : 0ull; });
+      return block_sum_u64(m, sh) + th.ties * mass_of(th.key);
+    };
+    auto no_mass = [](uint32_t) { return 1ull; };
     // ---- 2: the bins in question ----
     if (binned) {
-      const int per = kWBins / nt;
-      unsigned long long c = 0, m = 0;
-      for (int i = 0; i < per; ++i) {
-        const int j = per * tid + i;
-        const unsigned long long n = cum_c[j];
+      // running sums from the top bin down, a stretch of neighbouring bins a warp
+      constexpr int per = kWBins / (NT / 32);
+      const int lane = tid & 31, w0 = (tid >> 5) * per;
+      auto weight = [&](int j) { return ex2_approx(((float)(kWBins - 1 - j) - tm) * 0.03125f); };
+      uint32_t c = 0;
+      float m = 0.f;
+#pragma unroll 4
+      for (int i = lane; i < per; i += 32) {
+        const uint32_t n = cum_c[w0 + i];
         c += n;
-        if (by_p && !by_k) m += n * fx40(ex2_approx(fminf(((float)(kWBins - 1 - j) - tm) * 0.03125f, 0.f)));
-        cum_c[j] = (uint32_t)c;
-        cum_m[j] = m;
+        if (!by_k) m += (float)n * weight(w0 + i);
       }
-      const unsigned long long c0 = block_scan_u64(c, sh) - c;
-      const unsigned long long m0 = by_p && !by_k ? block_scan_u64(m, sh) - m : 0ull;
-      for (int i = 0; i < per; ++i) {
-        cum_c[per * tid + i] += (uint32_t)c0;
-        cum_m[per * tid + i] += m0;
+      c = __reduce_add_sync(0xffffffffu, c);
+      m = warp_sum(m);
+      if (lane == 0) {
+        s_range[tid >> 5] = make_uint2(c, 0u);
+        shf[tid >> 5] = m;
       }
       __syncthreads();
-      auto first_c = [&](unsigned long long want) {  // the first bin (from the top) where the count reaches `want`
-        int a = 0, b = kWBins - 1;
-        while (a < b) {
-          const int mid = (a + b) >> 1;
-          if (cum_c[mid] >= want) b = mid;
-          else a = mid + 1;
-        }
-        return a;
-      };
-      auto first_m = [&](unsigned long long want) {
-        int a = 0, b = kWBins - 1;
-        while (a < b) {
-          const int mid = (a + b) >> 1;
-          if (cum_m[mid] >= want) b = mid;
-          else a = mid + 1;
-        }
-        return a;
-      };
-      auto count_in = [&](int a, int b) { return (int)(cum_c[b] - (a > 0 ? cum_c[a - 1] : 0u)); };
-      unsigned long long est = cum_m[kWBins - 1], want = 0;
-      long long shift = 0;  // exact minus estimated mass at the bins looked at
-      if (by_p && !by_k) want = scale_mass((double)fminf(tp, 1.f - 0x1p-24f), est);
-      for (int attempt = 0; attempt < 4 && !found; ++attempt) {
-        int ja, jb;  // bins, counted from the top
-        if (by_k) {
-          ja = jb = first_c((unsigned long long)k);
-        } else {
-          for (unsigned long long d = est >> (attempt == 0 ? 8 : 10);; d >>= 1) {
-            const long long w = (long long)want - shift;
-            ja = first_m(w > (long long)d ? (unsigned long long)(w - (long long)d) : 1ull);
-            jb = first_m(w + (long long)d > 0 ? (unsigned long long)(w + (long long)d) : 1ull);
-            if (d == 0 || count_in(ja, jb) <= kSList) break;
+      c = 0;
+      m = 0.f;
+      for (int i = 0; i < (tid >> 5); ++i) {
+        c += s_range[i].x;
+        m += shf[i];
+      }
+#pragma unroll 2
+      for (int i = lane; i < per; i += 32) {
+        const uint32_t n = cum_c[w0 + i];
+        uint32_t x = n;
+        float y = by_k ? 0.f : (float)n * weight(w0 + i);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t xo = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += xo;
+          if (!by_k) {
+            const float yo = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += yo;
           }
         }
-        headed = cum_c[jb] <= kSList;
-        if (headed) ja = 0;
-        n_list = count_in(ja, jb);
-        if (n_list > kSList) break;
-        const float f_lo = WeightBins::edge(kWBins - 1 - jb), f_hi = WeightBins::edge(kWBins - 1 - ja);
-        __syncthreads();
-        if (tid == 0) s_n = 0;
-        __syncthreads();
-        auto collect = [&](float t, float x, int v) {
-          if (t >= f_lo && t <= f_hi) list[atomicAdd(&s_n, 1)] = make_uint2(logit_key(x), (uint32_t)v);
-        };
-        unsigned long long above = 0;
-        if (by_p && !by_k) {
-          MassSum sum, over;
-          if (S == 0 && headed) {
-            row.all([&](float x, int v) {
-              sum.add(ex2_approx(__fmul_rn(__fsub_rn(x, M), rate)));
-              collect(bins.pos(x), x, v);
-            });
+        cum_c[w0 + i] = c + x;
+        c += __shfl_sync(0xffffffffu, x, 31);
+        if (!by_k) {
+          cum_m[w0 + i] = m + y;
+          m += __shfl_sync(0xffffffffu, y, 31);
+        }
+      }
+      __syncthreads();
+      // the first bin (from the top) whose sum reaches `goal` (warp-wide, 32 bins a step)
+      auto first = [&](const auto* cum, auto goal) {
+        int lo = 0, n = kWBins;
+        while (n > 1) {
+          n = (n + 31) / 32;
+          const int at = min(lo + ((tid & 31) + 1) * n - 1, kWBins - 1);
+          const uint32_t ok = __ballot_sync(0xffffffffu, cum[at] >= goal);
+          lo = min(lo + (ok ? __ffs(ok) - 1 : 31) * n, kWBins - 1);
+        }
+        return lo;
+      };
+      auto before_bin = [&](int j) { return j > 0 ? cum_c[j - 1] : 0u; };
+      const float origin = bins.off - 8388608.f;
+      auto lower_edge = [&](int j) { return j >= kWBins - 1 ? -INFINITY : ((float)(kWBins - 1 - j) - 0.5f - origin) / bins.c; };
+      const float est = by_k ? 0.f : cum_m[kWBins - 1];  // of the whole row
+      float goal = fminf(tp, 1.f) * est;  // top-p's limit in the estimate's measure
+      float slack = est * 0.0156f;
+      bool tight = false;
+      for (int attempt = 0; attempt < 4; ++attempt) {
+        if (tid < 32) {  // bins ja..jb, counted from the top
+          int ja = 0, jb;
+          if (by_k) {
+            jb = first(cum_c, (uint32_t)k);
           } else {
-            row.all([&](float x, int v) {
-              const float w = ex2_approx(__fmul_rn(__fsub_rn(x, M), rate)), t = bins.pos(x);
-              sum.add(w);
-              over.add(t > f_hi ? w : 0.f);
-              collect(t, x, v);
-            });
+            for (;; slack *= 0.5f) {
+              ja = first(cum_m, fmaxf(goal - slack, 0.f));
+              jb = first(cum_m, fmaxf(goal + slack, 0.f));
+              if (cum_c[jb] - before_bin(ja) <= kSList * 3 / 4 || ja == jb || slack < 1e-6f * goal) break;
+            }
           }
+          if (tid == 0) {
+            s_range[0] = make_uint2((uint32_t)ja, (uint32_t)jb);
+            shf[0] = slack;
+            s_n = 0;
+          }
+        }
+        __syncthreads();
+        const int ja = (int)s_range[0].x, jb = (int)s_range[0].y;
+        slack = shf[0];
+        headed = by_k || cum_c[jb] <= kSList * 3 / 4;
+        if (by_k && (cum_c[jb] < (uint32_t)k || k > kSList)) break;
+        const float x_lo = lower_edge(jb), x_hi = headed || ja == 0 ? INFINITY : lower_edge(ja - 1);
+        auto push = [&](float x, int v) {
+          const int i = atomicAdd(&s_n, 1);
+          if (i < kSList) list[i] = make_uint2(logit_key(x), (uint32_t)v);
+        };
+        auto collect = [&](float x, int v) {
+          if (x >= x_lo && x <= x_hi) push(x, v);
+        };
+        auto collect_piece = [&](const uint4& q, int v) {  // few entries of a piece, if any: one by one
+          float x[Row::E];
+          Row::split(q, x);
+          uint32_t in = 0;
+#pragma unroll
+          for (int e = 0; e < Row::E; ++e) in |= x[e] >= x_lo && x[e] <= x_hi ? 1u << e : 0u;
+          while (in) {
+            const int e = __ffs(in) - 1, i = Row::E == 8 ? e >> 1 : e;
+            in &= in - 1;
+            const uint32_t w = i & 2 ? i & 1 ? q.w : q.z : i & 1 ? q.y : q.x;
+            push(__uint_as_float(Row::E == 4 ? w : e & 1 ? w & 0xffff0000u : w << 16), v + e);
+          }
+        };
+        above = 0;
+        if (by_k) {
+          row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v) {
+            if (Row::largest(q) >= x_lo) collect_piece(q, v);
+          });
+          row.loose(tid, nt, collect);
+          __syncthreads();
+        } else {
+          MassSum sum, over;
+          const unsigned long long neg_m = f32x2_pack(-M, -M), rate2 = f32x2_pack(rate, rate);
+          auto pair = [&](float x0, float x1) {
+            float y0, y1;
+            f32x2_unpack(f32x2_mul(f32x2_add(f32x2_pack(x0, x1), neg_m), rate2), y0, y1);
+            return MassPair(ex2_approx(y0), ex2_approx(y1));
+          };
+          row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v) {
+            float x[Row::E];
+            Row::split(q, x);
+            const float g = Row::largest(q);
+            const bool some = g > x_hi;
+#pragma unroll
+            for (int e = 0; e < Row::E; e += 2) {
+              const MassPair m = pair(x[e], x[e + 1]);
+              sum.add(m);
+              if (some) {
+                if (x[e] > x_hi) over.add(m, 0);
+                if (x[e + 1] > x_hi) over.add(m, 1);
+              }
+            }
+            if (g >= x_lo) collect_piece(q, v);
+          });
+          row.loose(tid, nt, [&](float x, int v) {
+            const MassPair m = pair(x, x);
+            sum.add(m, 0);
+            if (x > x_hi) over.add(m, 0);
+            collect(x, v);
+          });
           S = block_sum_u64(sum.total(), sh);
           above = headed ? 0ull : block_sum_u64(over.total(), sh);
           want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
-        } else {
-          if (by_p && !headed) break;  // the top-k set's mass would not be known
-          row.all([&](float x, int v) { collect(bins.pos(x), x, v); });
+          __syncthreads();
         }
-        __syncthreads();
-        if (!by_k) {  // does the mass end among the list's entries?
+        n_list = s_n;
+        // does the rule end among the list's entries?
+        if (n_list > kSList) {
+          if (by_k || tight) break;
+          tight = slack < 1e-3f * goal;
+          slack *= 0.25f;
+        } else if (by_k) {
+          found = n_list >= k;
+        } else {
           unsigned long long in = 0;
           for (int i = tid; i < n_list; i += nt) in += mass_of(list[i].x);
           in = block_sum_u64(in, sh);
-          if (!(above < want && want <= above + in)) {
-            if (want > above) shift = (long long)(above + in) - (long long)cum_m[jb];
-            else shift = (long long)above - (long long)(ja > 0 ? cum_m[ja - 1] : 0ull);
-            continue;
-          }
+          found = above < want && want <= above + in;
+          // move the estimate to what is now known at the range's near end
+          const float at = want > above ? cum_m[jb] : ja > 0 ? cum_m[ja - 1] : 0.f;
+          const unsigned long long known = want > above ? above + in : above;
+          goal = at + ((float)want - (float)known) * 0x1p-40f;
+          slack = est * 0.004f;
         }
-        found = true;
+        if (found) break;
+        __syncthreads();
+      }
+      if (found) {
         // ---- 3: selection on the list ----
         auto from_list = [&](auto f) {
           for (int i = tid; i < n_list; i += nt) f(list[i].x);
         };
-        if (by_k) {
-          const unsigned long long before = ja > 0 ? cum_c[ja - 1] : 0u;
-          __syncthreads();
-          th = select_key(from_list, mass_of, false, (unsigned long long)k, before, 0ull, lowest, hi, scratch);
-          if (by_p) {
-            S = th.above + th.ties * mass_of(th.key);
-            want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
-            th = select_key(from_list, mass_of, true, want, 0ull, 0ull, th.key, hi, scratch);
+        if (n_list <= kRanked) {  // few entries: each one's place by comparing it with all
+          const Ranked e = rank_entries(list, n_list, mass_of, [](const uint2& a, const uint2& b) {
+            return a.x > b.x || (a.x == b.x && a.y < b.y);
+          }, few);
+          const int most = by_k ? min(k, n_list) : n_list;
+          if (by_k && by_p) {
+            if (tid < n_list && e.rank == most - 1) s_pick[2] = e.before + e.mass;
+            __syncthreads();
+            want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), s_pick[2]));
           }
+          const unsigned long long start = above + e.before, end = start + e.mass;
+          if (tid < n_list && e.rank < most && (!by_p || start < want) && !(e.rank + 1 < most && (!by_p || end < want))) {
+            s_pick[0] = list[tid].x;  // the last entry that both rules keep
+            s_pick[1] = list[tid].y;
+          }
+          __syncthreads();
+          th = Threshold{(uint32_t)s_pick[0], 0, 0};
+          cut = (int)s_pick[1] + 1;
         } else {
-          th = select_key(from_list, mass_of, true, want, 0ull, above, lowest, hi, scratch);
+          uint32_t k_lo = 0xffffffffu, k_hi = 0u;
+          for (int i = tid; i < n_list; i += nt) {
+            k_lo = min(k_lo, list[i].x);
+            k_hi = max(k_hi, list[i].x);
+          }
+          k_lo = __reduce_min_sync(0xffffffffu, k_lo);
+          k_hi = __reduce_max_sync(0xffffffffu, k_hi);
+          if ((tid & 31) == 0) s_range[tid >> 5] = make_uint2(k_lo, k_hi);
+          __syncthreads();
+          for (int i = 0; i < (nt >> 5); ++i) {
+            k_lo = min(k_lo, s_range[i].x);
+            k_hi = max(k_hi, s_range[i].y);
+          }
+          if (by_k) {
+            th = select_key<false>(from_list, no_mass, (unsigned long long)k, 0ull, k_lo, k_hi, scratch);
+            if (by_p) {
+              S = top_mass(from_list);
+              want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
+              th = select_key<true>(from_list, mass_of, want, 0ull, th.key, k_hi, scratch);
+            }
+          } else {
+            th = select_key<true>(from_list, mass_of, want, above, k_lo, k_hi, scratch);
+          }
         }
         if (th.ties < th.count) {  // the index of the last tie that is kept: the ties-th smallest
           auto tie_index = [&](auto f) {
             for (int i = tid; i < n_list; i += nt)
               if (list[i].x == th.key) f(~list[i].y);
           };
-          const Threshold at = select_key(tie_index, [](uint32_t) { return 1ull; }, false, th.ties, 0ull, 0ull,
-                                          ~(uint32_t)(V - 1), 0xffffffffu, scratch);
+          const Threshold at = select_key<false>(tie_index, no_mass, th.ties, 0ull, ~(uint32_t)(V - 1), 0xffffffffu, scratch);
           cut = (int)~at.key + 1;
         }
       }
     }
     if (!found) {  // the same selection on the row
       headed = false;
+      cut = V;
       uint32_t lo = lowest;
       if (by_k) {
-        th = select_key(from_row, mass_of, false, (unsigned long long)k, 0ull, 0ull, lo, hi, scratch);
+        th = select_key<false>(from_row, no_mass, (unsigned long long)k, 0ull, lo, hi, scratch);
         lo = th.key;
-        S = th.above + th.ties * mass_of(th.key);
+        if (by_p) S = top_mass(from_row);
       } else {
         MassSum sum;
-        row.all([&](float x, int) { sum.add(rule_weight(x, M, rate)); });
+        row.all([&](float x, int) { sum.add(MassPair(rule_weight(x, M, rate), 0.f), 0); });
         S = block_sum_u64(sum.total(), sh);
       }
       if (by_p) {
-        const unsigned long long want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
-        th = select_key(from_row, mass_of, true, want, 0ull, 0ull, lo, hi, scratch);
+        want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
+        th = select_key<true>(from_row, mass_of, want, 0ull, lo, hi, scratch);
       }
       if (th.ties < th.count) {
         const float xs = key_logit(th.key);
@@ -491,8 +784,7 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
             if (x == xs) f(~(uint32_t)v);
           });
         };
-        const Threshold at = select_key(tie_index, [](uint32_t) { return 1ull; }, false, th.ties, 0ull, 0ull,
-                                        ~(uint32_t)(V - 1), 0xffffffffu, scratch);
+        const Threshold at = select_key<false>(tie_index, no_mass, th.ties, 0ull, ~(uint32_t)(V - 1), 0xffffffffu, scratch);
         cut = (int)~at.key + 1;
       }
     }
@@ -520,35 +812,30 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
     const bool aligned = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.row)) & 15) == 0;
     const uint32_t low = sizeof(Tin) == 2 ? 0xff7fu : 0xff7fffffu;  // the lowest finite value
     if (aligned) {
-      constexpr int E = RowView<Tin>::E, U = 4;
-      for (int g = tid; g < row.nv; g += U * nt) {
-        uint4 q[U];
+      // two compares at a time against the threshold rounded up to bf16: it is a bf16 value unless min-p set
+      // it, and then x >= xs (cut = V) holds for the same bf16 values x
+      const __nv_bfloat16 t16 = __float2bfloat16_ru(xs);
+      const __nv_bfloat162 t2 = __halves2bfloat162(t16, t16);
+      row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v) {
+        uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        const bool whole = v + Row::E <= cut;  // ties of the whole piece are kept
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (g + u * nt < row.nv) q[u] = row.piece(g + u * nt);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (g + u * nt >= row.nv) break;
-          float x[E];
-          RowView<Tin>::split(q[u], x);
-          const int v = row.a0 + (g + u * nt) * E;
-          uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (E == 8) {
-              const uint32_t keep = (kept(x[(2 * i) % E], v + 2 * i) ? 0xffffu : 0u) | (kept(x[(2 * i + 1) % E], v + 2 * i + 1) ? 0xffff0000u : 0u);
-              w[i] = (w[i] & keep) | ((low | low << 16) & ~keep);
-            } else {
-              w[i] = kept(x[i % E], v + i) ? w[i] : low;
-            }
+        for (int i = 0; i < 4; ++i) {
+          if (Row::E == 8) {
+            const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+            uint32_t keep = __hge2_mask(x, t2);
+            if (!whole) keep = (kept(__low2float(x), v + 2 * i) ? 0xffffu : 0u) | (kept(__high2float(x), v + 2 * i + 1) ? 0xffff0000u : 0u);
+            w[i] = (w[i] & keep) | ((low | low << 16) & ~keep);
+          } else {
+            w[i] = kept(__uint_as_float(w[i]), v + i) ? w[i] : low;
           }
-          __stcs(reinterpret_cast<uint4*>(out + v), make_uint4(w[0], w[1], w[2], w[3]));
         }
-      }
+        __stcs(reinterpret_cast<uint4*>(out + v), make_uint4(w[0], w[1], w[2], w[3]));
+      });
     }
-    const int loose = aligned ? V - row.nv * RowView<Tin>::E : V;
+    const int loose = aligned ? V - row.nv * Row::E : V;
     for (int i = tid; i < loose; i += nt) {
-      const int v = aligned && i >= row.a0 ? i + row.nv * RowView<Tin>::E : i;
+      const int v = aligned && i >= row.a0 ? i + row.nv * Row::E : i;
       const Tin raw = row.row[v];
       if (kept(row.at(v), v)) out[v] = raw;
       else if (sizeof(Tin) == 2) *reinterpret_cast<uint16_t*>(out + v) = (uint16_t)low;
@@ -563,6 +850,19 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
     }
     return;
   }
+  if (headed && n_list <= kRanked) {  // every kept entry is on a short list: places by index
+    auto kept_mass = [&](const uint2& a) { return kept(key_logit(a.x), (int)a.y) ? mass_of(a.x) : 0ull; };
+    unsigned long long m = tid < n_list ? kept_mass(list[tid]) : 0ull;
+    const unsigned long long Z = block_sum_u64(m, sh), t = scale_mass(p.u[r], Z);
+    const Ranked e = rank_entries(list, n_list, mass_of, [&](const uint2& a, const uint2& b) {
+      return a.y < b.y && kept(key_logit(a.x), (int)a.y);
+    }, few);
+    if (m > 0 && e.before <= t && e.before + m > t) {
+      p.tokens[r] = (int)list[tid].y;
+      if (p.prob) p.prob[r] = (float)((double)m / (double)Z);
+    }
+    return;
+  }
   if (headed) {  // every kept entry is on the list: the draw selects an index by mass
     unsigned long long Z = 0;
     for (int i = tid; i < n_list; i += nt)
@@ -573,23 +873,14 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
     while (lo_i < hi_i) {
       const int bits = 32 - __clz((uint32_t)(hi_i - lo_i)), shift = bits > 11 ? bits - 11 : 0;
       __syncthreads();
-      for (int b = tid; b < kSBins; b += nt) scratch.mass[b] = 0;
+      for (int b = tid; b < kSBins; b += nt) scratch.mass[b] = MassBin{0, 0};
       __syncthreads();
       for (int i = tid; i < n_list; i += nt) {
         const uint2 e = list[i];
-        if (e.y >= lo_i && e.y <= hi_i && kept(key_logit(e.x), (int)e.y)) atomicAdd(&scratch.mass[(e.y - lo_i) >> shift], mass_of(e.x));
+        if (e.y >= lo_i && e.y <= hi_i && kept(key_logit(e.x), (int)e.y)) add_mass(&scratch.mass[(e.y - lo_i) >> shift], mass_of(e.x));
       }
       __syncthreads();
-      const int per = kSBins / nt;
-      unsigned long long m = 0;
-      for (int i = 0; i < per; ++i) m += scratch.mass[per * tid + i];
-      unsigned long long at = block_scan_u64(m, sh) - m + c_above;
-      for (int i = 0; i < per; ++i) {
-        const unsigned long long mb = scratch.mass[per * tid + i];
-        if (at <= t && at + mb > t) { s_pick[0] = per * tid + i; s_pick[1] = at; }
-        at += mb;
-      }
-      __syncthreads();
+      find_bin([&](int b) { return scratch.mass[b].value(); }, t + 1, c_above, sh, s_pick);
       const unsigned long long b = s_pick[0];
       c_above = s_pick[1];
       lo_i += b << shift;
@@ -601,23 +892,37 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
     }
     return;
   }
-  // the draw on the row: masses of one stretch of entries a warp, then the entries of the stretch
-  const int warp = tid >> 5, lane = tid & 31, nw = nt >> 5;
-  const int len = ((V + nw - 1) / nw + 31) & ~31, b0 = min(warp * len, V), b1 = min(b0 + len, V);
-  unsigned long long m = 0;
-  for (int v = b0 + lane; v < b1; v += 32) {
-    const float x = row.at(v);
-    if (kept(x, v)) m += fx40(rule_weight(x, M, rate));
-  }
+  // the draw on the row: masses of one stretch of pieces a warp (the loose entries before the first piece go
+  // with the first stretch, those after the last with the last), then the entries of the stretch
+  const int warp = tid >> 5, nw = nt >> 5, stretch = (row.nv + nw - 1) / nw;
+  const int g0 = min(warp * stretch, row.nv), g1 = min(g0 + stretch, row.nv);
+  auto first_of = [&](int w) { return w == 0 ? 0 : row.a0 + min(w * stretch, row.nv) * Row::E; };
+  auto end_of = [&](int w) { return w == nw - 1 ? V : first_of(w + 1); };
+  MassSum part;
+  auto weigh = [&](float x, int v) { part.add(MassPair(kept(x, v) ? rule_weight(x, M, rate) : 0.f, 0.f), 0); };
+  row.pieces(g0, g1, tid & 31, 32, [&](const uint4& q, int v) {
+    if (Row::largest(q) < xs) return;
+    float x[Row::E];
+    Row::split(q, x);
+#pragma unroll
+    for (int e = 0; e < Row::E; e += 2)
+      part.add(MassPair(kept(x[e], v + e) ? rule_weight(x[e], M, rate) : 0.f,
+                        kept(x[e + 1], v + e + 1) ? rule_weight(x[e + 1], M, rate) : 0.f));
+  });
+  if (warp == 0)
+    for (int v = tid; v < row.a0; v += 32) weigh(row.at(v), v);
+  if (warp == nw - 1)
+    for (int v = row.a0 + row.nv * Row::E + (tid & 31); v < V; v += 32) weigh(row.at(v), v);
+  unsigned long long m = part.total();
   const unsigned long long end = block_scan_u64(m, sh), Z = block_sum_u64(m, sh);
   const unsigned long long t = scale_mass(p.u[r], Z);
   unsigned long long start = __shfl_sync(0xffffffffu, end - m, 0);
   const unsigned long long stop = __shfl_sync(0xffffffffu, end, 31);
-  if (start <= t && stop > t && lane == 0) { s_pick[0] = b0; s_pick[1] = start; }
+  if (start <= t && stop > t && (tid & 31) == 0) { s_pick[0] = warp; s_pick[1] = start; }
   __syncthreads();
-  const int s0 = (int)s_pick[0], s1 = min(s0 + len, V);
+  const int s0 = first_of((int)s_pick[0]), s1 = end_of((int)s_pick[0]);
   start = s_pick[1];
-  const int each = (len + nt - 1) / nt, a = min(s0 + tid * each, s1), e = min(a + each, s1);
+  const int each = (s1 - s0 + nt - 1) / nt, a = min(s0 + tid * each, s1), e = min(a + each, s1);
   m = 0;
   for (int v = a; v < e; ++v) {
     const float x = row.at(v);
@@ -639,6 +944,15 @@ __global__ void __launch_bounds__(1024, 1) sampling_rule_kernel(SampleParams p) 
   }
 }
 
+template <class Tin, int NT, int kBlocks>
+static cudaError_t launch_rule(const SampleParams& p, int N, cudaStream_t s) {
+  static std::atomic<unsigned long long> attr{0};
+  const cudaError_t e = set_smem_limit_once((const void*)sampling_rule_kernel<Tin, NT, kBlocks>, (int)kSSmem, attr);
+  if (e != cudaSuccess) return e;
+  sampling_rule_kernel<Tin, NT, kBlocks><<<N, NT, kSSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
 static dspark_status sampling_entry(int32_t N, int32_t V, int32_t dtype, const void* logits, const float* temperature,
                                     const int32_t* top_k, const float* top_p, const float* min_p, const double* u,
                                     int32_t* tokens, float* prob, void* out, void* workspace, size_t workspace_bytes,
@@ -650,18 +964,16 @@ static dspark_status sampling_entry(int32_t N, int32_t V, int32_t dtype, const v
     return DSPARK_ERR_WORKSPACE;
   if (N == 0) return DSPARK_OK;
   SampleParams p{V, logits, temperature, top_k, top_p, min_p, u, tokens, prob, out, static_cast<uint32_t*>(workspace)};
-  static std::atomic<unsigned long long> attr_bf16{0}, attr_f32{0};
-  const bool bf16 = dtype == DSPARK_BF16;
-  const void* fn = bf16 ? (const void*)sampling_rule_kernel<__nv_bfloat16> : (const void*)sampling_rule_kernel<float>;
-  if (set_smem_limit_once(fn, (int)kSSmem, bf16 ? attr_bf16 : attr_f32) != cudaSuccess) return DSPARK_ERR_CUDA;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSPARK_ERR_CUDA;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int threads = N <= sms ? 1024 : 512;  // a block an SM for few rows, two for many (their phases overlap)
-  if (bf16) sampling_rule_kernel<__nv_bfloat16><<<N, threads, kSSmem, (cudaStream_t)stream>>>(p);
-  else sampling_rule_kernel<float><<<N, threads, kSSmem, (cudaStream_t)stream>>>(p);
+  const bool wide = N <= sms;
+  const cudaError_t e = dtype == DSPARK_BF16 ? wide ? launch_rule<__nv_bfloat16, 512, 1>(p, N, (cudaStream_t)stream)
+                                                    : launch_rule<__nv_bfloat16, 512, 2>(p, N, (cudaStream_t)stream)
+                                             : wide ? launch_rule<float, 512, 1>(p, N, (cudaStream_t)stream)
+                                                    : launch_rule<float, 512, 2>(p, N, (cudaStream_t)stream);
   note_launches(1);
-  return cudaGetLastError() == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
+  return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
 
 }  // namespace dspark
