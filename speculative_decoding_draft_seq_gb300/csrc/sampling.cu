@@ -12,7 +12,7 @@
 // prefixes of that order, so the kept set is "logit above x*, or equal to it
 // and index below cut": one threshold, found in three steps.
 //   1  the row streams in once from memory: its maximum, and an estimate of its
-//      distribution in 4096 bins of 1/32 octave of weight. The largest entry of
+//      distribution in 2048 bins of 1/16 octave of weight. The largest entry of
 //      each 16-byte piece is counted once; for top-p the piece's first entry, if
 //      it is another one, stands for the rest of all pieces. (A shared-memory add
 //      for every entry bounds the pass: 15 us a row of 129,280 instead of 6.)
@@ -24,7 +24,7 @@
 //      moved by what they show, and collected again.
 //   3  exact selection among the collected entries: by comparing all pairs of a
 //      short list, else by radix selection on order-preserving integer keys
-//      (2048-bin histograms of counts or masses over a shrinking key range).
+//      (1024-bin histograms of counts or masses over a shrinking key range).
 // Where no range fits the list (thousands of equal entries, logits hundreds of
 // octaves apart), the radix selection runs on the row itself. One block a row: a
 // row of 129,280 bf16 is 258 KB, and the rows in flight stay in L2 between passes.
@@ -36,10 +36,12 @@
 
 namespace dspark {
 
-constexpr int kSBins = 2048;    // bins of a selection round
-constexpr int kWBins = 4096;    // weight bins, 32 an octave
+constexpr int kSBits = 10;               // key bits that a selection round settles
+constexpr int kSBins = 1 << kSBits;
+constexpr int kWBins = 2048;    // weight bins, 16 an octave
 constexpr int kSList = 2944;    // collected entries: four blocks of 256 threads fit an SM
 constexpr uint32_t kSSmem = kWBins * 4 + kWBins * 4 + kSList * 8;
+static_assert(kSBins * 12 <= kWBins * 8, "the selection's arrays lie over the weight bins");
 
 struct SampleParams {
   int V;
@@ -106,7 +108,7 @@ __device__ __forceinline__ unsigned long long f32x2_fma_rz(unsigned long long a,
 // Sum of floor(w 2^40) over weights in [0, 1], as two sums of 20-bit halves: adding 8 with rounding
 // towards zero leaves floor(w 2^20) in the low mantissa bits, and what it cut off gives the other half.
 // Up to 2^11 weights fit.
-struct MassPair {  // the two halves of two masses
+struct MassPair {  // the two halves of two masses, above the bits of 8
   uint32_t hi[2], lo[2];
   __device__ __forceinline__ MassPair(float w0, float w1) {
     const unsigned long long w = f32x2_pack(w0, w1), eight = f32x2_pack(8.f, 8.f);
@@ -124,21 +126,18 @@ struct MassPair {  // the two halves of two masses
   }
 };
 struct MassSum {
-  uint32_t hi = 0, lo = 0, n = 0;
+  static constexpr uint32_t kBits = 0x7fffffu;
+  uint32_t hi = 0, lo = 0;
   __device__ __forceinline__ void add(const MassPair& m) {
-    hi += m.hi[0] + m.hi[1];
-    lo += m.lo[0] + m.lo[1];
-    n += 2;
+    hi += (m.hi[0] & kBits) + (m.hi[1] & kBits);
+    lo += (m.lo[0] & kBits) + (m.lo[1] & kBits);
   }
-  __device__ __forceinline__ void add(const MassPair& m, int i) {
-    hi += m.hi[i];
-    lo += m.lo[i];
-    ++n;
+  __device__ __forceinline__ void add_if(const MassPair& m, bool p0, bool p1) {
+    const uint32_t k0 = p0 ? kBits : 0u, k1 = p1 ? kBits : 0u;
+    hi += (m.hi[0] & k0) + (m.hi[1] & k1);
+    lo += (m.lo[0] & k0) + (m.lo[1] & k1);
   }
-  __device__ __forceinline__ unsigned long long total() const {
-    const uint32_t base = n * 0x41000000u;
-    return ((unsigned long long)(hi - base) << 20) + (lo - base);
-  }
+  __device__ __forceinline__ unsigned long long total() const { return ((unsigned long long)hi << 20) + lo; }
 };
 
 __device__ __forceinline__ unsigned long long block_sum_u64(unsigned long long v, unsigned long long* sh) {
@@ -178,7 +177,7 @@ __device__ __forceinline__ unsigned long long block_scan_u64(unsigned long long 
 // Plain loads: dspark_truncate may write the row in place. U pieces a thread are in flight.
 template <class Tin, int U>
 struct RowView {
-  static constexpr int E = 16 / (int)sizeof(Tin);
+  static constexpr int E = 16 / (int)sizeof(Tin), kInFlight = U;
   const Tin* row;
   int V, a0, nv;
   __device__ RowView(const Tin* r, int n) : row(r), V(n) {
@@ -209,17 +208,26 @@ struct RowView {
     }
     return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)), max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
   }
-  // f(piece, first index) for the pieces g0 <= g < g1, the tid-th of every nt
+  // A piece of -inf, in place of one past the end.
+  static __device__ __forceinline__ uint4 nothing() {
+    const uint32_t w = E == 8 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(w, w, w, w);
+  }
+  // f(piece, first index, is it one) for the pieces g0 <= g < g1, the tid-th of every nt; the lanes of a warp stay together
   template <class F>
   __device__ __forceinline__ void pieces(int g0, int g1, int tid, int nt, F f) const {
-    for (int g = g0 + tid; g < g1; g += U * nt) {
+    for (int b = g0; b < g1; b += U * nt) {
       uint4 q[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (g + u * nt < g1) q[u] = piece(g + u * nt);
+      for (int u = 0; u < U; ++u) {
+        const int g = b + tid + u * nt;
+        q[u] = g < g1 ? piece(g) : nothing();
+      }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (g + u * nt < g1) f(q[u], a0 + (g + u * nt) * E);
+      for (int u = 0; u < U; ++u) {
+        const int g = b + tid + u * nt;
+        f(q[u], a0 + g * E, g < g1);
+      }
     }
   }
   // f(x, v) for the loose entries at both ends
@@ -233,7 +241,8 @@ struct RowView {
   // f(x, v) for all entries
   template <class F>
   __device__ __forceinline__ void all(F f) const {
-    pieces(0, nv, threadIdx.x, blockDim.x, [&](const uint4& q, int v) {
+    pieces(0, nv, threadIdx.x, blockDim.x, [&](const uint4& q, int v, bool ok) {
+      if (!ok) return;
       float x[E];
       split(q, x);
 #pragma unroll
@@ -321,9 +330,9 @@ template <bool kByMass, class Source, class Mass>
 __device__ Threshold select_key(Source source, Mass mass_of, unsigned long long target, unsigned long long above, uint32_t lo,
                                 uint32_t hi, const SelectScratch& s) {
   const int tid = threadIdx.x, nt = blockDim.x;
-  for (;;) {
+  for (int round = 0;; ++round) {
     const uint32_t span = hi - lo;
-    const int bits = 32 - __clz(span), shift = bits > 11 ? bits - 11 : 0;
+    const int bits = 32 - __clz(span), shift = bits > kSBits ? bits - kSBits : 0;
     __syncthreads();
     for (int b = tid; b < kSBins; b += nt) {
       s.cnt[b] = 0;
@@ -346,7 +355,7 @@ __device__ Threshold select_key(Source source, Mass mass_of, unsigned long long 
     find_bin(value, target, above, s.sh, s.pick);
     const uint32_t b = (uint32_t)s.pick[0];
     above = s.pick[1];
-    if (shift == 0) {
+    if (shift == 0 || round == 32) {  // (a round settles kSBits of at most 32 bits)
       Threshold t;
       t.key = hi - b;
       t.count = s.cnt[b];
@@ -387,11 +396,12 @@ __device__ Ranked rank_entries(const uint2* list, int n, Mass mass_of, First fir
     const uint2 me = list[e];
     uint32_t rank = 0;
     unsigned long long m = 0;
-    for (int j = tid / kRanked; j < n; j += parts)
-      if (first(list[j], me)) {
-        ++rank;
-        m += s.mass[j];
-      }
+#pragma unroll 4
+    for (int j = tid / kRanked; j < n; j += parts) {
+      const bool b = first(list[j], me);
+      rank += b ? 1u : 0u;
+      m += b ? s.mass[j] : 0ull;
+    }
     atomicAdd(&s.rank[e], rank);
     add_mass(&s.before[e], m);
   }
@@ -416,7 +426,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ unsigned long long sh[32], s_pick[4];
   __shared__ float shf[32];
-  __shared__ int shi[32], s_n;
+  __shared__ int shi[32];
   __shared__ uint2 s_range[32];
   uint32_t* cum_c = reinterpret_cast<uint32_t*>(s_raw);        // [kWBins] estimated counts, from the top bin down
   float* cum_m = reinterpret_cast<float*>(cum_c + kWBins);     // [kWBins] estimated masses, relative to the maximum's
@@ -438,39 +448,47 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
 
   // ---- 1: maximum and weight bins ----
   using Row = RowView<Tin, (kBlocks > 1 ? 4 : 8)>;
-  WeightBins bins{32.f * rate, 0.f};
+  WeightBins bins{16.f * rate, 0.f};
   bool binned = by_k || by_p;
-  float m0 = -INFINITY;  // the largest of 256 spread entries: the bins' origin
-  if (binned) {
-    for (int i = tid & 31; i < 256; i += 32) m0 = fmaxf(m0, row.at((int)(((long long)i * V) >> 8)));
-    m0 = warp_max(m0);
-    if (!(fabsf(m0) < INFINITY)) m0 = 0.f;
-    const float o = rintf(m0 * bins.c);
-    binned = fabsf(o) <= 524288.f && rate > 0.f;  // else too far for bins of 1/32 octave in float32
-    bins.off = 8388608.f + (kWBins / 2) - o;
-    for (int b = tid; b < kWBins; b += nt) cum_c[b] = 0;
-    __syncthreads();
-  }
   float M = -INFINITY;
   if (binned) {
+    for (int b = tid; b < kWBins; b += nt) cum_c[b] = 0;
+    // the bins' origin: the largest entry of the first stretch, which stays in registers
+    constexpr int U = Row::kInFlight;
+    uint4 q0[U];
+    float m0 = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) q0[u] = tid + u * nt < row.nv ? row.piece(tid + u * nt) : Row::nothing();
+    row.loose(tid, nt, [&](float x, int) { m0 = fmaxf(m0, x); });
+#pragma unroll
+    for (int u = 0; u < U; ++u) m0 = fmaxf(m0, Row::largest(q0[u]));
+    m0 = block_max(m0, shf);
+    if (!(fabsf(m0) < INFINITY)) m0 = 0.f;
+    const float o = rintf(m0 * bins.c);
+    binned = fabsf(o) <= 524288.f && rate > 0.f;  // else too far for bins of 1/16 octave in float32
+    bins.off = 8388608.f + (kWBins / 2) - o;
     auto count = [&](float x, uint32_t n) { atomicAdd(&cum_c[kWBins - 1 - WeightBins::index(bins.pos(x))], n); };
-    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int) {
+    auto visit = [&](const uint4& q, int, bool ok) {
       const float g = Row::largest(q);
       M = max_nan(M, g);
-      count(g, 1u);
+      if (ok) count(g, 1u);
       if (!by_k) {  // of E entries that are not the largest with chance 1 - 1/E, E - 1 to stand for
         const float x = Row::E == 8 ? __uint_as_float(q.x << 16) : __uint_as_float(q.x);
         if (x < g) count(x, (uint32_t)Row::E);
       }
-    });
+    };
+#pragma unroll
+    for (int u = 0; u < U; ++u) visit(q0[u], 0, tid + u * nt < row.nv);
+    row.pieces(U * nt, row.nv, tid, nt, visit);
     row.loose(tid, nt, [&](float x, int) {
       M = max_nan(M, x);
       count(x, 1u);
     });
   } else {
-    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int) { M = max_nan(M, Row::largest(q)); });
+    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int, bool) { M = max_nan(M, Row::largest(q)); });
     row.loose(tid, nt, [&](float x, int) { M = max_nan(M, x); });
   }
+  __syncthreads();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
   if ((tid & 31) == 0) shf[tid >> 5] = M;
@@ -499,7 +517,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   int n_list = 0;
   if (greedy) {
     int at = V;
-    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v) {
+    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool) {
       if (Row::largest(q) != M || v >= at) return;
       float x[Row::E];
       Row::split(q, x);
@@ -532,7 +550,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       // running sums from the top bin down, a stretch of neighbouring bins a warp
       constexpr int per = kWBins / (NT / 32);
       const int lane = tid & 31, w0 = (tid >> 5) * per;
-      auto weight = [&](int j) { return ex2_approx(((float)(kWBins - 1 - j) - tm) * 0.03125f); };
+      auto weight = [&](int j) { return ex2_approx(((float)(kWBins - 1 - j) - tm) * 0.0625f); };
       uint32_t c = 0;
       float m = 0.f;
 #pragma unroll 4
@@ -543,16 +561,13 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       }
       c = __reduce_add_sync(0xffffffffu, c);
       m = warp_sum(m);
-      if (lane == 0) {
-        s_range[tid >> 5] = make_uint2(c, 0u);
-        shf[tid >> 5] = m;
-      }
+      if (lane == 0) s_range[tid >> 5] = make_uint2(c, __float_as_uint(m));
       __syncthreads();
       c = 0;
       m = 0.f;
       for (int i = 0; i < (tid >> 5); ++i) {
         c += s_range[i].x;
-        m += shf[i];
+        m += __uint_as_float(s_range[i].y);
       }
 #pragma unroll 2
       for (int i = lane; i < per; i += 32) {
@@ -587,64 +602,90 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
         }
         return lo;
       };
-      auto before_bin = [&](int j) { return j > 0 ? cum_c[j - 1] : 0u; };
       const float origin = bins.off - 8388608.f;
-      auto lower_edge = [&](int j) { return j >= kWBins - 1 ? -INFINITY : ((float)(kWBins - 1 - j) - 0.5f - origin) / bins.c; };
+      // the logit `j` bins down from the top of the first one
+      auto logit_at = [&](float j) { return j >= (float)kWBins ? -INFINITY : ((float)kWBins - 0.5f - j - origin) / bins.c; };
+      // how many bins down the mass reaches g, and the count there (straight between the bins' ends)
+      auto mass_at = [&](float g, float& n) {
+        const int j = first(cum_m, g);
+        const float a = j > 0 ? cum_m[j - 1] : 0.f, z = cum_m[j], na = j > 0 ? (float)cum_c[j - 1] : 0.f;
+        const float f = z > a ? fminf(fmaxf((g - a) / (z - a), 0.f), 1.f) : 1.f;
+        n = na + f * ((float)cum_c[j] - na);
+        return g >= cum_m[kWBins - 1] ? (float)kWBins : (float)j + f;
+      };
+      auto est_at = [&](float x) {  // the estimated mass above a logit
+        const float j = fminf(fmaxf((float)kWBins - 0.5f - (x * bins.c + origin), 0.f), (float)kWBins);
+        const int i = min((int)j, kWBins - 1);
+        const float a = i > 0 ? cum_m[i - 1] : 0.f;
+        return a + (j - (float)i) * (cum_m[i] - a);
+      };
       const float est = by_k ? 0.f : cum_m[kWBins - 1];  // of the whole row
       float goal = fminf(tp, 1.f) * est;  // top-p's limit in the estimate's measure
       float slack = est * 0.0156f;
       bool tight = false;
       for (int attempt = 0; attempt < 4; ++attempt) {
-        if (tid < 32) {  // bins ja..jb, counted from the top
-          int ja = 0, jb;
+        if (tid < 32) {
+          float lo, hi = INFINITY, head = 1.f;
           if (by_k) {
-            jb = first(cum_c, (uint32_t)k);
+            const int j = first(cum_c, (uint32_t)k);
+            lo = logit_at((float)(j + 1));
+            if (cum_c[j] < (uint32_t)k || k > kSList) head = 0.f;
           } else {
-            for (;; slack *= 0.5f) {
-              ja = first(cum_m, fmaxf(goal - slack, 0.f));
-              jb = first(cum_m, fmaxf(goal + slack, 0.f));
-              if (cum_c[jb] - before_bin(ja) <= kSList * 3 / 4 || ja == jb || slack < 1e-6f * goal) break;
+            float na, nb, ja, jb;
+            for (int step = 0;; ++step, slack *= 0.5f) {
+              ja = mass_at(fmaxf(goal - slack, 0.f), na);
+              jb = mass_at(goal + slack, nb);
+              if (nb - na <= kSList * 0.75f || step == 20) break;
             }
+            head = nb <= kSList * 0.75f ? 1.f : 0.f;
+            lo = logit_at(jb);
+            if (head == 0.f) hi = logit_at(ja);
           }
           if (tid == 0) {
-            s_range[0] = make_uint2((uint32_t)ja, (uint32_t)jb);
-            shf[0] = slack;
-            s_n = 0;
+            shf[0] = lo;
+            shf[1] = hi;
+            shf[2] = head;
+            shf[3] = slack;
           }
         }
         __syncthreads();
-        const int ja = (int)s_range[0].x, jb = (int)s_range[0].y;
-        slack = shf[0];
-        headed = by_k || cum_c[jb] <= kSList * 3 / 4;
-        if (by_k && (cum_c[jb] < (uint32_t)k || k > kSList)) break;
-        const float x_lo = lower_edge(jb), x_hi = headed || ja == 0 ? INFINITY : lower_edge(ja - 1);
-        auto push = [&](float x, int v) {
-          const int i = atomicAdd(&s_n, 1);
-          if (i < kSList) list[i] = make_uint2(logit_key(x), (uint32_t)v);
+        const float x_lo = shf[0], x_hi = shf[1];
+        headed = shf[2] != 0.f;
+        slack = shf[3];
+        if (by_k && !headed) break;
+        const float nan = __uint_as_float(0x7fc00000u);  // in no range
+        const uint32_t nan_w = Row::E == 8 ? 0x7fc07fc0u : __float_as_uint(nan);
+        const uint4 none = make_uint4(nan_w, nan_w, nan_w, nan_w);
+        // each warp fills a part of the list of its own (no atomics), the parts move together afterwards
+        constexpr int kPart = kSList / (NT / 32);
+        uint2* part = list + (tid >> 5) * kPart;
+        int n_part = 0;  // of the whole warp
+        const uint32_t below = (1u << (tid & 31)) - 1u;
+        auto collect = [&](float x, int v) {  // by whole warps
+          const bool in = x >= x_lo && x <= x_hi;
+          const uint32_t all = __ballot_sync(0xffffffffu, in);
+          if (all == 0) return;
+          const int at = n_part + __popc(all & below);
+          if (in && at < kPart) part[at] = make_uint2(logit_key(x), (uint32_t)v);
+          n_part += __popc(all);
         };
-        auto collect = [&](float x, int v) {
-          if (x >= x_lo && x <= x_hi) push(x, v);
-        };
-        auto collect_piece = [&](const uint4& q, int v) {  // few entries of a piece, if any: one by one
+        auto collect_piece = [&](const uint4& q, int v) {
           float x[Row::E];
           Row::split(q, x);
-          uint32_t in = 0;
 #pragma unroll
-          for (int e = 0; e < Row::E; ++e) in |= x[e] >= x_lo && x[e] <= x_hi ? 1u << e : 0u;
-          while (in) {
-            const int e = __ffs(in) - 1, i = Row::E == 8 ? e >> 1 : e;
-            in &= in - 1;
-            const uint32_t w = i & 2 ? i & 1 ? q.w : q.z : i & 1 ? q.y : q.x;
-            push(__uint_as_float(Row::E == 4 ? w : e & 1 ? w & 0xffff0000u : w << 16), v + e);
-          }
+          for (int e = 0; e < Row::E; ++e) collect(x[e], v + e);
+        };
+        auto collect_loose = [&]() {  // at most 2 E entries: the first warp takes them
+          if (tid >= 32) return;
+          const int n = V - row.nv * Row::E, v = tid < row.a0 ? tid : tid + row.nv * Row::E;
+          collect(tid < n ? row.at(v) : nan, v);
         };
         above = 0;
         if (by_k) {
-          row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v) {
-            if (Row::largest(q) >= x_lo) collect_piece(q, v);
+          row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
+            if (__any_sync(0xffffffffu, ok && Row::largest(q) >= x_lo)) collect_piece(ok ? q : none, v);
           });
-          row.loose(tid, nt, collect);
-          __syncthreads();
+          collect_loose();
         } else {
           MassSum sum, over;
           const unsigned long long neg_m = f32x2_pack(-M, -M), rate2 = f32x2_pack(rate, rate);
@@ -653,38 +694,54 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
             f32x2_unpack(f32x2_mul(f32x2_add(f32x2_pack(x0, x1), neg_m), rate2), y0, y1);
             return MassPair(ex2_approx(y0), ex2_approx(y1));
           };
-          row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v) {
+          row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
             float x[Row::E];
             Row::split(q, x);
             const float g = Row::largest(q);
-            const bool some = g > x_hi;
+            const bool some = __any_sync(0xffffffffu, g > x_hi);
 #pragma unroll
             for (int e = 0; e < Row::E; e += 2) {
               const MassPair m = pair(x[e], x[e + 1]);
               sum.add(m);
-              if (some) {
-                if (x[e] > x_hi) over.add(m, 0);
-                if (x[e + 1] > x_hi) over.add(m, 1);
-              }
+              if (some) over.add_if(m, x[e] > x_hi, x[e + 1] > x_hi);
             }
-            if (g >= x_lo) collect_piece(q, v);
+            if (__any_sync(0xffffffffu, ok && g >= x_lo)) collect_piece(ok ? q : none, v);
           });
-          row.loose(tid, nt, [&](float x, int v) {
+          row.loose(tid, nt, [&](float x, int) {
             const MassPair m = pair(x, x);
-            sum.add(m, 0);
-            if (x > x_hi) over.add(m, 0);
-            collect(x, v);
+            sum.add_if(m, true, false);
+            over.add_if(m, x > x_hi, false);
           });
+          collect_loose();
           S = block_sum_u64(sum.total(), sh);
           above = headed ? 0ull : block_sum_u64(over.total(), sh);
           want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
           __syncthreads();
         }
-        n_list = s_n;
+        {
+          if ((tid & 31) == 0) s_range[tid >> 5] = make_uint2((uint32_t)n_part, 0u);
+          constexpr int kMine = (kPart + 31) / 32;
+          uint2 mine[kMine];
+#pragma unroll
+          for (int i = 0; i < kMine; ++i)
+            if (32 * i + (tid & 31) < min(n_part, kPart)) mine[i] = part[32 * i + (tid & 31)];
+          __syncthreads();
+          int at = 0;
+          n_list = 0;
+          for (int i = 0; i < NT / 32; ++i) {
+            const int n = (int)s_range[i].x;
+            if (i < (tid >> 5)) at += min(n, kPart);
+            n_list = n > kPart ? kSList + 1 : n_list > kSList ? n_list : n_list + n;
+          }
+#pragma unroll
+          for (int i = 0; i < kMine; ++i)
+            if (32 * i + (tid & 31) < min(n_part, kPart)) list[at + 32 * i + (tid & 31)] = mine[i];
+          __syncthreads();
+        }
         // does the rule end among the list's entries?
         if (n_list > kSList) {
           if (by_k || tight) break;
-          tight = slack < 1e-3f * goal;
+          tight = slack < 1e-3f * est;
           slack *= 0.25f;
         } else if (by_k) {
           found = n_list >= k;
@@ -693,10 +750,9 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
           for (int i = tid; i < n_list; i += nt) in += mass_of(list[i].x);
           in = block_sum_u64(in, sh);
           found = above < want && want <= above + in;
-          // move the estimate to what is now known at the range's near end
-          const float at = want > above ? cum_m[jb] : ja > 0 ? cum_m[ja - 1] : 0.f;
+          // the estimate holds between two logits near one another: from what is now known at the nearer end on
           const unsigned long long known = want > above ? above + in : above;
-          goal = at + ((float)want - (float)known) * 0x1p-40f;
+          goal = est_at(want > above ? x_lo : x_hi) + ((float)want - (float)known) * 0x1p-40f;
           slack = est * 0.004f;
         }
         if (found) break;
@@ -709,7 +765,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
         };
         if (n_list <= kRanked) {  // few entries: each one's place by comparing it with all
           const Ranked e = rank_entries(list, n_list, mass_of, [](const uint2& a, const uint2& b) {
-            return a.x > b.x || (a.x == b.x && a.y < b.y);
+            return a.x > b.x | (a.x == b.x & a.y < b.y);
           }, few);
           const int most = by_k ? min(k, n_list) : n_list;
           if (by_k && by_p) {
@@ -770,7 +826,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
         if (by_p) S = top_mass(from_row);
       } else {
         MassSum sum;
-        row.all([&](float x, int) { sum.add(MassPair(rule_weight(x, M, rate), 0.f), 0); });
+        row.all([&](float x, int) { sum.add(MassPair(rule_weight(x, M, rate), 0.f)); });
         S = block_sum_u64(sum.total(), sh);
       }
       if (by_p) {
@@ -793,7 +849,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   }
   if (!greedy && min_w > 0.f) {  // the smallest key whose weight reaches min_p, by 32-way search
     uint32_t lo = key, hi = logit_key(M);  // the weight of hi is 1
-    while (lo < hi) {
+    for (int round = 0; lo < hi && round < 32; ++round) {
       const uint32_t step = (hi - lo) / 32 + 1;
       const uint32_t at = (uint32_t)min((unsigned long long)hi, lo + (unsigned long long)step * (tid & 31));
       const uint32_t ok = __ballot_sync(0xffffffffu, rule_weight(key_logit(at), M, rate) >= min_w);
@@ -816,7 +872,8 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       // it, and then x >= xs (cut = V) holds for the same bf16 values x
       const __nv_bfloat16 t16 = __float2bfloat16_ru(xs);
       const __nv_bfloat162 t2 = __halves2bfloat162(t16, t16);
-      row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v) {
+      row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
+        if (!ok) return;
         uint32_t w[4] = {q.x, q.y, q.z, q.w};
         const bool whole = v + Row::E <= cut;  // ties of the whole piece are kept
 #pragma unroll
@@ -855,7 +912,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
     unsigned long long m = tid < n_list ? kept_mass(list[tid]) : 0ull;
     const unsigned long long Z = block_sum_u64(m, sh), t = scale_mass(p.u[r], Z);
     const Ranked e = rank_entries(list, n_list, mass_of, [&](const uint2& a, const uint2& b) {
-      return a.y < b.y && kept(key_logit(a.x), (int)a.y);
+      return a.y < b.y & kept(key_logit(a.x), (int)a.y);
     }, few);
     if (m > 0 && e.before <= t && e.before + m > t) {
       p.tokens[r] = (int)list[tid].y;
@@ -870,8 +927,8 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
     Z = block_sum_u64(Z, sh);
     const unsigned long long t = scale_mass(p.u[r], Z);
     unsigned long long c_above = 0, lo_i = 0, hi_i = (unsigned long long)V - 1;  // index range that holds the token
-    while (lo_i < hi_i) {
-      const int bits = 32 - __clz((uint32_t)(hi_i - lo_i)), shift = bits > 11 ? bits - 11 : 0;
+    for (int round = 0; lo_i < hi_i && round < 32; ++round) {
+      const int bits = 32 - __clz((uint32_t)(hi_i - lo_i)), shift = bits > kSBits ? bits - kSBits : 0;
       __syncthreads();
       for (int b = tid; b < kSBins; b += nt) scratch.mass[b] = MassBin{0, 0};
       __syncthreads();
@@ -899,9 +956,9 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   auto first_of = [&](int w) { return w == 0 ? 0 : row.a0 + min(w * stretch, row.nv) * Row::E; };
   auto end_of = [&](int w) { return w == nw - 1 ? V : first_of(w + 1); };
   MassSum part;
-  auto weigh = [&](float x, int v) { part.add(MassPair(kept(x, v) ? rule_weight(x, M, rate) : 0.f, 0.f), 0); };
-  row.pieces(g0, g1, tid & 31, 32, [&](const uint4& q, int v) {
-    if (Row::largest(q) < xs) return;
+  auto weigh = [&](float x, int v) { part.add(MassPair(kept(x, v) ? rule_weight(x, M, rate) : 0.f, 0.f)); };
+  row.pieces(g0, g1, tid & 31, 32, [&](const uint4& q, int v, bool ok) {
+    if (!ok || Row::largest(q) < xs) return;
     float x[Row::E];
     Row::split(q, x);
 #pragma unroll
