@@ -39,7 +39,7 @@ namespace dspark {
 constexpr int kSBits = 10;               // key bits that a selection round settles
 constexpr int kSBins = 1 << kSBits;
 constexpr int kWBins = 2048;    // weight bins, 16 an octave
-constexpr int kSList = 2944;    // collected entries: four blocks of 256 threads fit an SM
+constexpr int kSList = 6144;    // collected entries (64 KB with the bins: two blocks an SM leave 96 KB to L1)
 constexpr uint32_t kSSmem = kWBins * 4 + kWBins * 4 + kSList * 8;
 static_assert(kSBins * 12 <= kWBins * 8, "the selection's arrays lie over the weight bins");
 
@@ -67,11 +67,14 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 __device__ __forceinline__ float rule_weight(float x, float M, float rate) {
   return x == -INFINITY ? 0.f : exp2f(__fmul_rn(__fsub_rn(x, M), rate));
 }
-// floor(x S) for x in [0, 1), x to 53 bits
+// floor(x S) for x in [0, 1), x to 53 bits, from the bits of x (FP64 instructions are slow here)
 __device__ __forceinline__ unsigned long long scale_mass(double x, unsigned long long S) {
-  if (!(x > 0.0)) x = 0.0;
-  if (x > 1.0 - 0x1p-53) x = 1.0 - 0x1p-53;
-  return scale_u53((unsigned long long)__double2ull_rz(x * 0x1p53), S);
+  const unsigned long long b = (unsigned long long)__double_as_longlong(x), one = 1ull << 53;
+  const int e = (int)(b >> 52);  // sign and exponent
+  const unsigned long long m = (b & ((1ull << 52) - 1)) | (1ull << 52);
+  // negative, NaN: 0; 1 and above: the largest below 1
+  const unsigned long long k = e >= 0x7ff ? 0ull : e >= 1023 ? one - 1 : e < 1023 - 54 ? 0ull : m >> (1022 - e);
+  return scale_u53(k, S);
 }
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
   float d;
@@ -216,18 +219,27 @@ struct RowView {
   // f(piece, first index, is it one) for the pieces g0 <= g < g1, the tid-th of every nt; the lanes of a warp stay together
   template <class F>
   __device__ __forceinline__ void pieces(int g0, int g1, int tid, int nt, F f) const {
-    for (int b = g0; b < g1; b += U * nt) {
-      uint4 q[U];
+    if (g0 >= g1) return;
+    uint4 q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int g = g0 + tid + u * nt;
+      q[u] = g < g1 ? piece(g) : nothing();
+    }
+    for (int b = g0; b < g1; b += U * nt) {  // the next loads are on their way while these are looked at
+      uint4 next[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int g = b + tid + u * nt;
-        q[u] = g < g1 ? piece(g) : nothing();
+        const int g = b + tid + (U + u) * nt;
+        next[u] = g < g1 ? piece(g) : nothing();
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int g = b + tid + u * nt;
         f(q[u], a0 + g * E, g < g1);
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) q[u] = next[u];
     }
   }
   // f(x, v) for the loose entries at both ends
@@ -436,6 +448,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   const SelectScratch scratch{reinterpret_cast<uint32_t*>(s_mass + kSBins), s_mass, sh, s_pick};
   unsigned long long* s_u64 = reinterpret_cast<unsigned long long*>(s_raw);
   const RankScratch few{s_u64, reinterpret_cast<MassBin*>(s_u64 + kRanked), reinterpret_cast<uint32_t*>(s_u64 + 2 * kRanked)};
+  uint2* few_list = reinterpret_cast<uint2*>(s_u64 + 3 * kRanked);
   const int tid = threadIdx.x, V = p.V;
   constexpr int nt = NT;
   const size_t r = blockIdx.x;
@@ -450,7 +463,8 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   using Row = RowView<Tin, (kBlocks > 1 ? 4 : 8)>;
   WeightBins bins{16.f * rate, 0.f};
   bool binned = by_k || by_p;
-  float M = -INFINITY;
+  float M = -INFINITY, mine = -INFINITY;  // the row's maximum; a greedy row: this thread's, and the piece it is in
+  int first_at = V;
   if (binned) {
     for (int b = tid; b < kWBins; b += nt) cum_c[b] = 0;
     // the bins' origin: the largest entry of the first stretch, which stays in registers
@@ -485,8 +499,17 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       count(x, 1u);
     });
   } else {
-    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int, bool) { M = max_nan(M, Row::largest(q)); });
-    row.loose(tid, nt, [&](float x, int) { M = max_nan(M, x); });
+    float best = -INFINITY;
+    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool) {
+      const float g = Row::largest(q);
+      M = max_nan(M, g);
+      if (g > best) { best = g; first_at = v; }
+    });
+    row.loose(tid, nt, [&](float x, int v) {
+      M = max_nan(M, x);
+      if (x > best || (x == best && v < first_at)) { best = x; first_at = v; }
+    });
+    mine = best;
   }
   __syncthreads();
 #pragma unroll
@@ -514,21 +537,13 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   uint32_t key = logit_key(-INFINITY) + 1;
   int cut = V;
   bool headed = false;  // the list holds every kept entry
-  int n_list = 0;
+  // each warp fills a part of the list of its own (no atomics)
+  constexpr int kPart = kSList / (NT / 32);
+  uint2* part = list + (tid >> 5) * kPart;
+  int n_part = 0, n_list = 0;  // entries of the warp's part, and of all
   if (greedy) {
-    int at = V;
-    row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool) {
-      if (Row::largest(q) != M || v >= at) return;
-      float x[Row::E];
-      Row::split(q, x);
-#pragma unroll
-      for (int e = Row::E - 1; e >= 0; --e)
-        if (x[e] == M) at = v + e;
-    });
-    row.loose(tid, nt, [&](float x, int v) {
-      if (x == M) at = min(at, v);
-    });
-    at = block_min_i(at, shi);
+    int at = block_min_i(mine == M ? first_at : V, shi);
+    while (at < V - 1 && row.at(at) != M) ++at;  // within the piece
     key = logit_key(M);
     cut = at + 1;
   } else if (by_k || by_p) {
@@ -538,6 +553,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
     Threshold th{0, 0, 0};
     bool found = false;
     unsigned long long S = 0, want = 0, above = 0;  // top-p's whole, its limit, and what lies above the list
+    unsigned long long below_before = 0;                // the mass down to the end of the range before
     // the mass of the top-k set that ends at `th`
     auto top_mass = [&](auto source) {
       unsigned long long m = 0;
@@ -605,14 +621,6 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       const float origin = bins.off - 8388608.f;
       // the logit `j` bins down from the top of the first one
       auto logit_at = [&](float j) { return j >= (float)kWBins ? -INFINITY : ((float)kWBins - 0.5f - j - origin) / bins.c; };
-      // how many bins down the mass reaches g, and the count there (straight between the bins' ends)
-      auto mass_at = [&](float g, float& n) {
-        const int j = first(cum_m, g);
-        const float a = j > 0 ? cum_m[j - 1] : 0.f, z = cum_m[j], na = j > 0 ? (float)cum_c[j - 1] : 0.f;
-        const float f = z > a ? fminf(fmaxf((g - a) / (z - a), 0.f), 1.f) : 1.f;
-        n = na + f * ((float)cum_c[j] - na);
-        return g >= cum_m[kWBins - 1] ? (float)kWBins : (float)j + f;
-      };
       auto est_at = [&](float x) {  // the estimated mass above a logit
         const float j = fminf(fmaxf((float)kWBins - 0.5f - (x * bins.c + origin), 0.f), (float)kWBins);
         const int i = min((int)j, kWBins - 1);
@@ -622,44 +630,47 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       const float est = by_k ? 0.f : cum_m[kWBins - 1];  // of the whole row
       float goal = fminf(tp, 1.f) * est;  // top-p's limit in the estimate's measure
       float slack = est * 0.0156f;
-      bool tight = false;
-      for (int attempt = 0; attempt < 4; ++attempt) {
+      float r_lo = 0.f, r_hi = 0.f;  // the range before
+      int move = 0;                  // 1: further down than it, -1: further up
+      int half = kSList / 6;         // entries either side of the goal
+      for (int attempt = 0; attempt < 6; ++attempt) {
         if (tid < 32) {
-          float lo, hi = INFINITY, head = 1.f;
+          int ja = 0, jb;
+          bool head = true;
           if (by_k) {
-            const int j = first(cum_c, (uint32_t)k);
-            lo = logit_at((float)(j + 1));
-            if (cum_c[j] < (uint32_t)k || k > kSList) head = 0.f;
+            jb = first(cum_c, (uint32_t)k);
+            head = cum_c[jb] >= (uint32_t)k && k <= kSList;
           } else {
-            float na, nb, ja, jb;
-            for (int step = 0;; ++step, slack *= 0.5f) {
-              ja = mass_at(fmaxf(goal - slack, 0.f), na);
-              jb = mass_at(goal + slack, nb);
-              if (nb - na <= kSList * 0.75f || step == 20) break;
-            }
-            head = nb <= kSList * 0.75f ? 1.f : 0.f;
-            lo = logit_at(jb);
-            if (head == 0.f) hi = logit_at(ja);
+            const int jg = first(cum_m, goal);
+            ja = first(cum_m, fmaxf(goal - slack, 0.f));
+            jb = first(cum_m, goal + slack);
+            const int at = (int)cum_c[jg];  // well within what the list holds
+            ja = max(ja, min(first(cum_c, (uint32_t)max(at - half, 1)), jg));
+            jb = min(jb, max(first(cum_c, (uint32_t)(at + half)) - 1, jg));
+            head = move == 0 && cum_c[jb] <= kSList / 2;
+          }
+          float lo = logit_at((float)(jb + 1)), hi = head ? INFINITY : logit_at((float)ja);
+          if (move > 0) {  // no entry of the range before is in this one
+            hi = fminf(hi, key_logit(logit_key(r_lo) - 1));
+            lo = fminf(lo, hi);
+          } else if (move < 0) {
+            lo = fmaxf(lo, key_logit(logit_key(r_hi) + 1));
+            hi = fmaxf(lo, hi);
           }
           if (tid == 0) {
             shf[0] = lo;
             shf[1] = hi;
-            shf[2] = head;
-            shf[3] = slack;
+            shf[2] = head ? 1.f : 0.f;
           }
         }
         __syncthreads();
         const float x_lo = shf[0], x_hi = shf[1];
         headed = shf[2] != 0.f;
-        slack = shf[3];
         if (by_k && !headed) break;
         const float nan = __uint_as_float(0x7fc00000u);  // in no range
         const uint32_t nan_w = Row::E == 8 ? 0x7fc07fc0u : __float_as_uint(nan);
         const uint4 none = make_uint4(nan_w, nan_w, nan_w, nan_w);
-        // each warp fills a part of the list of its own (no atomics), the parts move together afterwards
-        constexpr int kPart = kSList / (NT / 32);
-        uint2* part = list + (tid >> 5) * kPart;
-        int n_part = 0;  // of the whole warp
+        n_part = 0;
         const uint32_t below = (1u << (tid & 31)) - 1u;
         auto collect = [&](float x, int v) {  // by whole warps
           const bool in = x >= x_lo && x <= x_hi;
@@ -670,30 +681,52 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
           n_part += __popc(all);
         };
         auto collect_piece = [&](const uint4& q, int v) {
-          float x[Row::E];
-          Row::split(q, x);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+          uint32_t in = 0;  // bit i: entry i (float32), or the low half of word i; bit 16 + i: the high half
+          if (Row::E == 8) {  // two compares at a time, against the ends rounded inwards to bf16
+            const __nv_bfloat16 a = __float2bfloat16_ru(x_lo), b = __float2bfloat16_rd(x_hi);
+            const __nv_bfloat162 a2 = __halves2bfloat162(a, a), b2 = __halves2bfloat162(b, b);
 #pragma unroll
-          for (int e = 0; e < Row::E; ++e) collect(x[e], v + e);
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w[i]);
+              in |= __hge2_mask(x, a2) & __hle2_mask(x, b2) & (0x10001u << i);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) in |= __uint_as_float(w[i]) >= x_lo && __uint_as_float(w[i]) <= x_hi ? 1u << i : 0u;
+          }
+          for (uint32_t any = __reduce_or_sync(0xffffffffu, in); any; any &= any - 1) {
+            const int bit = __ffs(any) - 1, i = bit & 3;
+            const bool mine = (in >> bit) & 1u;
+            const uint32_t all = __ballot_sync(0xffffffffu, mine);
+            const int at = n_part + __popc(all & below);
+            if (mine && at < kPart) {
+              const uint32_t x = i & 2 ? i & 1 ? w[3] : w[2] : i & 1 ? w[1] : w[0];
+              const float f = __uint_as_float(Row::E == 4 ? x : bit & 16 ? x & 0xffff0000u : x << 16);
+              part[at] = make_uint2(logit_key(f), (uint32_t)(v + (Row::E == 4 ? i : 2 * i + (bit >> 4))));
+            }
+            n_part += __popc(all);
+          }
         };
         auto collect_loose = [&]() {  // at most 2 E entries: the first warp takes them
           if (tid >= 32) return;
           const int n = V - row.nv * Row::E, v = tid < row.a0 ? tid : tid + row.nv * Row::E;
           collect(tid < n ? row.at(v) : nan, v);
         };
-        above = 0;
+        const unsigned long long neg_m = f32x2_pack(-M, -M), rate2 = f32x2_pack(rate, rate);
+        auto pair = [&](float x0, float x1) {
+          float y0, y1;
+          f32x2_unpack(f32x2_mul(f32x2_add(f32x2_pack(x0, x1), neg_m), rate2), y0, y1);
+          return MassPair(ex2_approx(y0), ex2_approx(y1));
+        };
+        unsigned long long gap_mass = 0;
         if (by_k) {
           row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
             if (__any_sync(0xffffffffu, ok && Row::largest(q) >= x_lo)) collect_piece(ok ? q : none, v);
           });
           collect_loose();
-        } else {
+        } else if (move == 0) {  // the row's mass, and what lies above the range
           MassSum sum, over;
-          const unsigned long long neg_m = f32x2_pack(-M, -M), rate2 = f32x2_pack(rate, rate);
-          auto pair = [&](float x0, float x1) {
-            float y0, y1;
-            f32x2_unpack(f32x2_mul(f32x2_add(f32x2_pack(x0, x1), neg_m), rate2), y0, y1);
-            return MassPair(ex2_approx(y0), ex2_approx(y1));
-          };
           row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
             float x[Row::E];
             Row::split(q, x);
@@ -716,55 +749,82 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
           S = block_sum_u64(sum.total(), sh);
           above = headed ? 0ull : block_sum_u64(over.total(), sh);
           want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
-          __syncthreads();
+        } else {  // another range: only what lies between the two counts
+          MassSum gap;
+          const float g_lo = move > 0 ? x_hi : r_hi, g_hi = move > 0 ? r_lo : x_lo, least = move > 0 ? x_lo : r_hi;
+          row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
+            if (!__any_sync(0xffffffffu, ok && Row::largest(q) >= least)) return;
+            const uint4 p = ok ? q : none;
+            float x[Row::E];
+            Row::split(p, x);
+            bool some = false;
+#pragma unroll
+            for (int e = 0; e < Row::E; ++e) some |= x[e] > g_lo && x[e] < g_hi;
+            if (__any_sync(0xffffffffu, some)) {
+#pragma unroll
+              for (int e = 0; e < Row::E; e += 2)
+                gap.add_if(pair(x[e], x[e + 1]), x[e] > g_lo && x[e] < g_hi, x[e + 1] > g_lo && x[e + 1] < g_hi);
+            }
+            collect_piece(p, v);
+          });
+          row.loose(tid, nt, [&](float x, int) { gap.add_if(pair(x, x), x > g_lo && x < g_hi, false); });
+          collect_loose();
+          gap_mass = block_sum_u64(gap.total(), sh);
         }
-        {
-          if ((tid & 31) == 0) s_range[tid >> 5] = make_uint2((uint32_t)n_part, 0u);
-          constexpr int kMine = (kPart + 31) / 32;
-          uint2 mine[kMine];
-#pragma unroll
-          for (int i = 0; i < kMine; ++i)
-            if (32 * i + (tid & 31) < min(n_part, kPart)) mine[i] = part[32 * i + (tid & 31)];
-          __syncthreads();
-          int at = 0;
-          n_list = 0;
-          for (int i = 0; i < NT / 32; ++i) {
-            const int n = (int)s_range[i].x;
-            if (i < (tid >> 5)) at += min(n, kPart);
-            n_list = n > kPart ? kSList + 1 : n_list > kSList ? n_list : n_list + n;
-          }
-#pragma unroll
-          for (int i = 0; i < kMine; ++i)
-            if (32 * i + (tid & 31) < min(n_part, kPart)) list[at + 32 * i + (tid & 31)] = mine[i];
-          __syncthreads();
+        __syncthreads();
+        if ((tid & 31) == 0) s_range[tid >> 5] = make_uint2((uint32_t)n_part, 0u);
+        __syncthreads();
+        n_list = 0;
+        for (int i = 0; i < NT / 32; ++i) {
+          const int n = (int)s_range[i].x;
+          n_list = n > kPart || n_list > kSList ? kSList + 1 : n_list + n;
         }
         // does the rule end among the list's entries?
-        if (n_list > kSList) {
-          if (by_k || tight) break;
-          tight = slack < 1e-3f * est;
-          slack *= 0.25f;
-        } else if (by_k) {
-          found = n_list >= k;
-        } else {
-          unsigned long long in = 0;
-          for (int i = tid; i < n_list; i += nt) in += mass_of(list[i].x);
-          in = block_sum_u64(in, sh);
-          found = above < want && want <= above + in;
-          // the estimate holds between two logits near one another: from what is now known at the nearer end on
-          const unsigned long long known = want > above ? above + in : above;
-          goal = est_at(want > above ? x_lo : x_hi) + ((float)want - (float)known) * 0x1p-40f;
-          slack = est * 0.004f;
+        if (n_list > kSList) {  // a smaller range, from the upper end of this one on
+          if (by_k || move < 0) break;
+          if (move > 0) above = below_before + gap_mass;
+          below_before = above;
+          r_lo = x_hi < INFINITY ? key_logit(logit_key(x_hi) + 1) : INFINITY;
+          move = 1;
+          half /= 4;
+          goal = est_at(x_hi) + ((float)want - (float)above) * 0x1p-40f;
+          headed = false;
+          __syncthreads();
+          continue;
         }
+        if (by_k) {
+          found = n_list >= k;
+          break;
+        }
+        unsigned long long in = 0;
+        for (int i = tid & 31; i < n_part; i += 32) in += mass_of(part[i].x);
+        in = block_sum_u64(in, sh);
+        if (move > 0) above = below_before + gap_mass;
+        else if (move < 0) above = above - gap_mass - in;
+        below_before = above + in;
+        found = above < want && want <= above + in;
         if (found) break;
+        // the estimate holds between two logits near one another: from what is now known at the nearer end on
+        move = want > above ? 1 : -1;
+        const unsigned long long known = move > 0 ? above + in : above;
+        r_lo = x_lo;
+        r_hi = x_hi;
+        if (headed && move < 0) break;
+        goal = est_at(move > 0 ? x_lo : x_hi) + ((float)want - (float)known) * 0x1p-40f;
+        slack = est * 0.004f;
         __syncthreads();
       }
       if (found) {
         // ---- 3: selection on the list ----
         auto from_list = [&](auto f) {
-          for (int i = tid; i < n_list; i += nt) f(list[i].x);
+          for (int i = tid & 31; i < n_part; i += 32) f(part[i].x);
         };
         if (n_list <= kRanked) {  // few entries: each one's place by comparing it with all
-          const Ranked e = rank_entries(list, n_list, mass_of, [](const uint2& a, const uint2& b) {
+          int at = 0;
+          for (int i = 0; i < (tid >> 5); ++i) at += (int)s_range[i].x;
+          __syncthreads();  // (the short list lies over the weight bins)
+          for (int i = tid & 31; i < n_part; i += 32) few_list[at + i] = part[i];
+          const Ranked e = rank_entries(few_list, n_list, mass_of, [](const uint2& a, const uint2& b) {
             return a.x > b.x | (a.x == b.x & a.y < b.y);
           }, few);
           const int most = by_k ? min(k, n_list) : n_list;
@@ -775,20 +835,21 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
           }
           const unsigned long long start = above + e.before, end = start + e.mass;
           if (tid < n_list && e.rank < most && (!by_p || start < want) && !(e.rank + 1 < most && (!by_p || end < want))) {
-            s_pick[0] = list[tid].x;  // the last entry that both rules keep
-            s_pick[1] = list[tid].y;
+            s_pick[0] = few_list[tid].x;  // the last entry that both rules keep
+            s_pick[1] = few_list[tid].y;
           }
           __syncthreads();
           th = Threshold{(uint32_t)s_pick[0], 0, 0};
           cut = (int)s_pick[1] + 1;
         } else {
           uint32_t k_lo = 0xffffffffu, k_hi = 0u;
-          for (int i = tid; i < n_list; i += nt) {
-            k_lo = min(k_lo, list[i].x);
-            k_hi = max(k_hi, list[i].x);
+          for (int i = tid & 31; i < n_part; i += 32) {
+            k_lo = min(k_lo, part[i].x);
+            k_hi = max(k_hi, part[i].x);
           }
           k_lo = __reduce_min_sync(0xffffffffu, k_lo);
           k_hi = __reduce_max_sync(0xffffffffu, k_hi);
+          __syncthreads();
           if ((tid & 31) == 0) s_range[tid >> 5] = make_uint2(k_lo, k_hi);
           __syncthreads();
           for (int i = 0; i < (nt >> 5); ++i) {
@@ -808,8 +869,8 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
         }
         if (th.ties < th.count) {  // the index of the last tie that is kept: the ties-th smallest
           auto tie_index = [&](auto f) {
-            for (int i = tid; i < n_list; i += nt)
-              if (list[i].x == th.key) f(~list[i].y);
+            for (int i = tid & 31; i < n_part; i += 32)
+              if (part[i].x == th.key) f(~part[i].y);
           };
           const Threshold at = select_key<false>(tie_index, no_mass, th.ties, 0ull, ~(uint32_t)(V - 1), 0xffffffffu, scratch);
           cut = (int)~at.key + 1;
@@ -909,21 +970,21 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   }
   if (headed && n_list <= kRanked) {  // every kept entry is on a short list: places by index
     auto kept_mass = [&](const uint2& a) { return kept(key_logit(a.x), (int)a.y) ? mass_of(a.x) : 0ull; };
-    unsigned long long m = tid < n_list ? kept_mass(list[tid]) : 0ull;
+    unsigned long long m = tid < n_list ? kept_mass(few_list[tid]) : 0ull;
     const unsigned long long Z = block_sum_u64(m, sh), t = scale_mass(p.u[r], Z);
-    const Ranked e = rank_entries(list, n_list, mass_of, [&](const uint2& a, const uint2& b) {
+    const Ranked e = rank_entries(few_list, n_list, mass_of, [&](const uint2& a, const uint2& b) {
       return a.y < b.y & kept(key_logit(a.x), (int)a.y);
     }, few);
     if (m > 0 && e.before <= t && e.before + m > t) {
-      p.tokens[r] = (int)list[tid].y;
+      p.tokens[r] = (int)few_list[tid].y;
       if (p.prob) p.prob[r] = (float)((double)m / (double)Z);
     }
     return;
   }
   if (headed) {  // every kept entry is on the list: the draw selects an index by mass
     unsigned long long Z = 0;
-    for (int i = tid; i < n_list; i += nt)
-      if (kept(key_logit(list[i].x), (int)list[i].y)) Z += mass_of(list[i].x);
+    for (int i = tid & 31; i < n_part; i += 32)
+      if (kept(key_logit(part[i].x), (int)part[i].y)) Z += mass_of(part[i].x);
     Z = block_sum_u64(Z, sh);
     const unsigned long long t = scale_mass(p.u[r], Z);
     unsigned long long c_above = 0, lo_i = 0, hi_i = (unsigned long long)V - 1;  // index range that holds the token
@@ -932,8 +993,8 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       __syncthreads();
       for (int b = tid; b < kSBins; b += nt) scratch.mass[b] = MassBin{0, 0};
       __syncthreads();
-      for (int i = tid; i < n_list; i += nt) {
-        const uint2 e = list[i];
+      for (int i = tid & 31; i < n_part; i += 32) {
+        const uint2 e = part[i];
         if (e.y >= lo_i && e.y <= hi_i && kept(key_logit(e.x), (int)e.y)) add_mass(&scratch.mass[(e.y - lo_i) >> shift], mass_of(e.x));
       }
       __syncthreads();
@@ -955,22 +1016,22 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   const int g0 = min(warp * stretch, row.nv), g1 = min(g0 + stretch, row.nv);
   auto first_of = [&](int w) { return w == 0 ? 0 : row.a0 + min(w * stretch, row.nv) * Row::E; };
   auto end_of = [&](int w) { return w == nw - 1 ? V : first_of(w + 1); };
-  MassSum part;
-  auto weigh = [&](float x, int v) { part.add(MassPair(kept(x, v) ? rule_weight(x, M, rate) : 0.f, 0.f)); };
+  MassSum sum;
+  auto weigh = [&](float x, int v) { sum.add(MassPair(kept(x, v) ? rule_weight(x, M, rate) : 0.f, 0.f)); };
   row.pieces(g0, g1, tid & 31, 32, [&](const uint4& q, int v, bool ok) {
     if (!ok || Row::largest(q) < xs) return;
     float x[Row::E];
     Row::split(q, x);
 #pragma unroll
     for (int e = 0; e < Row::E; e += 2)
-      part.add(MassPair(kept(x[e], v + e) ? rule_weight(x[e], M, rate) : 0.f,
+      sum.add(MassPair(kept(x[e], v + e) ? rule_weight(x[e], M, rate) : 0.f,
                         kept(x[e + 1], v + e + 1) ? rule_weight(x[e + 1], M, rate) : 0.f));
   });
   if (warp == 0)
     for (int v = tid; v < row.a0; v += 32) weigh(row.at(v), v);
   if (warp == nw - 1)
     for (int v = row.a0 + row.nv * Row::E + (tid & 31); v < V; v += 32) weigh(row.at(v), v);
-  unsigned long long m = part.total();
+  unsigned long long m = sum.total();
   const unsigned long long end = block_scan_u64(m, sh), Z = block_sum_u64(m, sh);
   const unsigned long long t = scale_mass(p.u[r], Z);
   unsigned long long start = __shfl_sync(0xffffffffu, end - m, 0);
