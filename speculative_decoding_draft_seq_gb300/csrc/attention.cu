@@ -22,17 +22,24 @@
 //   attn_join_kernel   adds a row's parts up.
 //
 // attn_tiles_kernel: rows are (token, query head of the key head), packed
-// floor(128 / group) tokens a 128-row half. Per 128-key tile and half: S = Q K^T
-// into TMEM (128 columns), a warpgroup turns S into bf16 weights in place (one
-// thread a row), O += P V with P read from TMEM. Two halves alternate, so one
-// half's softmax runs under the other's MMAs. The weights use a reference
-// maximum that is moved, and O rescaled, only when the row's maximum has risen
-// by more than 8 (2^8 fits every type on the way), so O is rarely rescaled.
-//   warps 0..3, 4..7  softmax and epilogue of half 0, 1
+// floor(128 / group) tokens a 128-row half. Per 128-key tile: S = Q K^T into TMEM
+// (128 columns), a warpgroup turns S into bf16 weights in place (one thread a
+// row), O += P V with P read from TMEM. Two softmax warpgroups, each with an S / P
+// and an O of its own, keep two tiles in flight, so that one's softmax runs under
+// the other's MMAs: an item with more tokens than a half holds gives each one a
+// half of the rows (K and V tiles are read once for both); an item with fewer
+// gives them the even and the odd key tiles of the same rows (two parts). The
+// weights use a reference maximum that is moved, and O rescaled, only when the
+// row's maximum has risen by more than 8 (2^8 fits every type on the way), so O
+// is rarely rescaled.
+//   warps 0..3, 4..7  softmax and epilogue of warpgroup 0, 1; the V rows of the
+//                     last 16-key group that lie past the keys are zeroed here
+//                     (a weight of 0 times a NaN is a NaN)
 //   warp 8            TMA loads: Q once an item, a ring of K and V tiles, one box
 //                     a page (or 128 rows of a longer one), 64 columns wide
-//   warp 9            MMA issue; zeroes the V rows of the last 16-key group that
-//                     lie past the keys (a weight of 0 times a NaN is a NaN)
+//   warp 9            TMEM allocation; MMA issue by one thread, which forms a
+//                     descriptor word with one add a step (an MMA of 128 x 128 x 16
+//                     takes 64 cycles, little more than its issue)
 // Every wait is bounded: one that runs out records DSPARK_ERR_TIMEOUT, the
 // roles wind down, issued copies and MMAs land, and the TMEM is freed.
 #include <algorithm>
@@ -47,11 +54,11 @@ namespace dspark {
 constexpr int kATile = 128;        // keys a tile
 constexpr int kAThreads = 320;
 constexpr int kPlanShare = 4;      // items are at most about 1/4 of an SM's share of the work
-constexpr int kExtraSlots = 2048;  // token slots for splits beyond one part for the prefix and one for the pages
+constexpr int kExtraSlots = 2048;  // token slots beyond one part for the prefix and two for the pages
 constexpr int kMaxSms = 256;
 
 struct AttnItem {
-  int head;    // key head
+  int head;    // key head, and kAlternate
   int req;     // request, or -1: the prefix
   int tok0;    // first query token
   int n_tok;   // query tokens (at most two halves)
@@ -60,9 +67,12 @@ struct AttnItem {
   int slot0;   // part slot of the first token; -1: the only part of its rows, written to out
   int pos0;    // keys from key0 on that the first token sees (one more for each further token)
 };
+// An item of a block with at most one half's tokens: its warpgroups take the even and the odd tiles, and with two
+// tiles or more it has two parts, the second one n_tok slots on.
+constexpr int kAlternate = 1 << 30;
 
 struct AttnHead {  // written by the plan
-  int n_items, prefix_splits, n_tokens, pad;
+  int n_items, prefix_parts, n_tokens, pad;
 };
 
 struct AttnParams {
@@ -95,7 +105,7 @@ inline AttnLayout attn_layout(int R, int T, int Hq, int Hkv, int D) {
   const int TB = attn_tokens_per_half(Hq / Hkv);
   const long long blocks = 2ll * ceil_div(T, 2 * TB) + R + 1;
   const long long items = blocks * Hkv + (long long)kMaxSms * kPlanShare;
-  L.slots = 2ll * T + kExtraSlots;
+  L.slots = 3ll * T + kExtraSlots;
   size_t o = 256;
   L.head = o;   o = align256(o + sizeof(AttnHead));
   L.tokens = o; o = align256(o + (size_t)T * sizeof(int4));
@@ -163,6 +173,12 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
     return;
   }
   const int n_tokens = __ldg(p.q_start + p.R);
+  // how `tiles` key tiles of a block of `nt` tokens are split into items, and the parts that they leave
+  auto splits_of = [&](int tiles, int nt, long long share) {
+    const int ns = ceil_div(tiles, share);
+    return nt <= p.TB ? max(min(ns, tiles / 2), min(tiles, 1)) : ns;  // two tiles at least for the two warpgroups
+  };
+  auto parts_of = [&](int tiles, int nt, int ns) { return nt <= p.TB && tiles > 1 ? 2 * ns : ns; };
   const int p_tiles = ceil_div(p.prefix_len, kATile), p_blocks = ceil_div(n_tokens, step);
   long long units = 0;
   for (int r = tid; r < p.R; r += kAPlanThreads) {
@@ -174,17 +190,21 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
   scan_ll(units, sh, total);
   total = (total + (long long)p_blocks * p_tiles) * p.Hkv;
   long long share = max(1ll, (total + (long long)p.sms * kPlanShare - 1) / ((long long)p.sms * kPlanShare));
-  int p_splits;
+  int p_splits, p_parts;
   for (;;) {  // tiles an item: more where the parts would not fit
-    p_splits = ceil_div(p_tiles, share);
+    p_splits = splits_of(p_tiles, n_tokens, share);
+    p_parts = parts_of(p_tiles, n_tokens, p_splits);
     long long slots = 0, all;
     for (int r = tid; r < p.R; r += kAPlanThreads) {
       int start, n, len;
       request(r, start, n, len);
-      for (int t0 = 0; t0 < n; t0 += step) slots += (long long)ceil_div(tiles_of(n, len, t0), share) * min(step, n - t0);
+      for (int t0 = 0; t0 < n; t0 += step) {
+        const int tiles = tiles_of(n, len, t0), nt = min(step, n - t0);
+        slots += (long long)parts_of(tiles, nt, splits_of(tiles, nt, share)) * nt;
+      }
     }
     scan_ll(slots, sh, all);
-    if (all + (long long)p_splits * n_tokens <= p.cap_slots || share > (1 << 30)) break;
+    if (all + (long long)p_parts * n_tokens <= p.cap_slots || share > (1 << 30)) break;
     share *= 2;
   }
   const long long p_items = (long long)p_blocks * p.Hkv * p_splits;
@@ -192,58 +212,59 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
     const int b = (int)(i % p_blocks), s = (int)((i / p_blocks) % p_splits), h = (int)(i / p_blocks / p_splits);
     const int a = (int)((long long)s * p_tiles / p_splits), e = (int)((long long)(s + 1) * p_tiles / p_splits);
     AttnItem it;
-    it.head = h;
+    it.head = h | (n_tokens <= p.TB ? kAlternate : 0);
     it.req = -1;
     it.tok0 = b * step;
     it.n_tok = min(step, n_tokens - it.tok0);
     it.key0 = a * kATile;
     it.n_keys = min(p.prefix_len, e * kATile) - it.key0;
-    it.slot0 = s * n_tokens + it.tok0;
+    it.slot0 = (p_parts > p_splits ? 2 * s : s) * n_tokens + it.tok0;
     it.pos0 = it.n_keys;
     p.items[i] = it;
   }
-  long long item0 = p_items, slot0 = (long long)p_splits * n_tokens;
+  long long item0 = p_items, slot0 = (long long)p_parts * n_tokens;
   for (int r0 = 0; r0 < p.R; r0 += kAPlanThreads) {
     const int r = r0 + tid;
     int start = 0, n = 0, len = 0;
     if (r < p.R) request(r, start, n, len);
     long long items = 0, slots = 0;
     for (int t0 = 0; t0 < n; t0 += step) {
-      const int ns = ceil_div(tiles_of(n, len, t0), share);
+      const int tiles = tiles_of(n, len, t0), nt = min(step, n - t0), ns = splits_of(tiles, nt, share);
       items += (long long)ns * p.Hkv;
-      slots += (long long)ns * min(step, n - t0);
+      slots += (long long)parts_of(tiles, nt, ns) * nt;
     }
     long long n_items, n_slots;
     long long item = item0 + scan_ll(items, sh, n_items), slot = slot0 + scan_ll(slots, sh, n_slots);
     item0 += n_items;
     slot0 += n_slots;
     for (int t0 = 0; t0 < n; t0 += step) {
-      const int tiles = tiles_of(n, len, t0), ns = ceil_div(tiles, share), nt = min(step, n - t0);
-      const bool direct = p_splits == 0 && ns == 1;
+      const int tiles = tiles_of(n, len, t0), nt = min(step, n - t0), ns = splits_of(tiles, nt, share);
+      const int parts = parts_of(tiles, nt, ns);
+      const bool direct = p_splits == 0 && parts == 1;
       for (int i = 0; i < nt; ++i)
-        p.tokens[start + t0 + i] = make_int4((int)slot + i, nt, direct ? -1 : ns, 0);
+        p.tokens[start + t0 + i] = make_int4((int)slot + i, nt, direct ? -1 : parts, 0);
       const int seen = max(0, min(len, len - n + t0 + nt));  // keys that the block's last token sees
       for (int s = 0; s < ns; ++s) {
         const int a = (int)((long long)s * tiles / ns), e = (int)((long long)(s + 1) * tiles / ns);
         for (int h = 0; h < p.Hkv; ++h, ++item) {
           AttnItem it;
-          it.head = h;
+          it.head = h | (nt <= p.TB ? kAlternate : 0);
           it.req = r;
           it.tok0 = start + t0;
           it.n_tok = nt;
           it.key0 = a * kATile;
           it.n_keys = min(seen, e * kATile) - it.key0;
-          it.slot0 = direct ? -1 : (int)slot + s * nt;
+          it.slot0 = direct ? -1 : (int)slot + (parts > ns ? 2 * s : s) * nt;
           it.pos0 = len - n + t0 + 1 - it.key0;
           p.items[item] = it;
         }
       }
-      slot += (long long)ns * nt;
+      slot += (long long)parts * nt;
     }
   }
   if (tid == 0) {
     p.head->n_items = (int)item0;
-    p.head->prefix_splits = p_splits;
+    p.head->prefix_parts = p_parts;
     p.head->n_tokens = n_tokens;
   }
   if (bad) set_status(p.status, DSPARK_ERR_RANGE);
@@ -327,7 +348,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *sTmem;
+  const uint32_t tmem = *sTmem;  // 0: all 512 columns are this CTA's
   const ItemWalk walk(p.head->n_items);
 
   if (warp == 8) {
@@ -349,36 +370,47 @@ __global__ void __launch_bounds__(kAThreads, 1)
         const int pos = j * kATile + lane * box_rows;
         return lane < boxes && pos < it.n_keys ? __ldg(pages + ((it.key0 + pos) >> p.page_log2)) : 0;
       };
-      int pg = page_at(0);
-      for (int j = 0; j < nt && !stop; ++j) {
+      const int head = it.head & ~kAlternate, groups = it.head & kAlternate ? 1 : 2, ahead = groups == 2 ? 1 : 2;
+      // one K (kv = 0) or V tile into the ring
+      auto load = [&](int j, int kv, int pg) {
         const int live = min(boxes, ceil_div(it.n_keys - j * kATile, box_rows));
         const int row = (it.key0 + j * kATile + lane * box_rows) & (p.page - 1);
-        const int next = j + 1 < nt ? page_at(j + 1) : 0;
+        const int slot = n % kSlots;
         if (lane < live && (pg < 0 || pg >= p.n_pages)) set_status(p.status, DSPARK_ERR_RANGE);
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int slot = n % kSlots;
-          if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, sAbort, p.status))) { stop = true; break; }
-          if (lane == 0) mbar_expect_tx(&full[slot], (uint32_t)(live * box_rows * 128 * kHalves));
-          __syncwarp();
-          if (lane < live) {
-            unsigned char* dst = sKV + slot * S::kTileBytes + lane * box_rows * 128;
-#pragma unroll
-            for (int c = 0; c < kHalves; ++c)
-              tma_load_4d(dst + c * S::kBox, kv ? &mapV : &mapK, 64 * c, it.head, row, pg, &full[slot], pol);
-          }
-          if (j == 0 && kv == 0) {  // Q behind the first K tile: its buffer is free once the item before has no S left to form
-            if (!__all_sync(0xffffffffu, mbar_wait(qEmpty, (k & 1) ^ 1, sAbort, p.status))) { ++n; stop = true; break; }
-            if (lane == 0) {
-              const int groups = it.n_tok > p.TB ? 2 : 1;
-              mbar_expect_tx(qFull, (uint32_t)(groups * q_rows * 128 * kHalves));
-              for (int g = 0; g < groups; ++g)
-                for (int c = 0; c < kHalves; ++c)
-                  tma_load_4d(sQ + g * S::kTileBytes + c * S::kBox, &mapQ, 64 * c, 0, it.head, it.tok0 + g * p.TB, qFull, pol);
-            }
-            ++nq;
-          }
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, sAbort, p.status))) {
+          stop = true;
+          return;
         }
-        pg = next;
+        if (lane == 0) mbar_expect_tx(&full[slot], (uint32_t)(live * box_rows * 128 * kHalves));
+        __syncwarp();
+        if (lane < live) {
+          unsigned char* dst = sKV + slot * S::kTileBytes + lane * box_rows * 128;
+#pragma unroll
+          for (int c = 0; c < kHalves; ++c)
+            tma_load_4d(dst + c * S::kBox, kv ? &mapV : &mapK, 64 * c, head, row, pg, &full[slot], pol);
+        }
+        ++n;
+      };
+      // in the order of use: K of the first tiles, then V of a tile and K of the tile `ahead` on
+      int pgs[3] = {page_at(0), nt > 1 ? page_at(1) : 0, 0};  // pages of tiles j, j + 1, j + 2
+      load(0, 0, pgs[0]);
+      // Q behind the first K tile: its buffer is free once the item before has no S left to form
+      if (!stop && !__all_sync(0xffffffffu, mbar_wait(qEmpty, (k & 1) ^ 1, sAbort, p.status))) stop = true;
+      if (stop) break;
+      if (lane == 0) {
+        mbar_expect_tx(qFull, (uint32_t)(groups * q_rows * 128 * kHalves));
+        for (int g = 0; g < groups; ++g)
+          for (int c = 0; c < kHalves; ++c)
+            tma_load_4d(sQ + g * S::kTileBytes + c * S::kBox, &mapQ, 64 * c, 0, head, it.tok0 + g * p.TB, qFull, pol);
+      }
+      ++nq;
+      if (ahead == 2 && nt > 1) load(1, 0, pgs[1]);
+      for (int j = 0; j < nt && !stop; ++j) {
+        pgs[2] = j + 2 < nt ? page_at(j + 2) : 0;
+        load(j, 1, pgs[0]);
+        if (!stop && j + ahead < nt) load(j + ahead, 0, pgs[ahead]);
+        pgs[0] = pgs[1];
+        pgs[1] = pgs[2];
       }
     }
     // no copy outlives the CTA: the last kSlots ring tiles and the last Q
@@ -387,88 +419,116 @@ __global__ void __launch_bounds__(kAThreads, 1)
       mbar_wait_drain(&full[(n - i) % kSlots], ((n - i) / kSlots) & 1, p.status);
   } else if (warp == 9) {
     // ---- MMA issue ----
-    const uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0), idesc_pv = idesc_bf16_f32(128, D, 1);
-    int n = 0;                // ring tiles consumed
-    uint32_t nP[2] = {0, 0};  // P tiles consumed of each half
-    uint32_t nO[2] = {0, 0};  // items finished by each half
-    bool stop = false;
-    auto ring_wait = [&]() {
-      const bool ok = __all_sync(0xffffffffu, mbar_wait(&full[n % kSlots], (n / kSlots) & 1, sAbort, p.status));
-      tc_fence_after();
-      return ok;
-    };
-    auto issue_qk = [&](int g, int slot) {
-      if (lane == 0) {
-        const uint32_t q = smem_u32(sQ + g * S::kTileBytes), kk = smem_u32(sKV + slot * S::kTileBytes);
+    if (lane == 0) {
+      const uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0), idesc_pv = idesc_bf16_f32(128, D, 1);
+      int slot = 0, phase = 0;  // the next ring tile
+      uint32_t pPhase[2] = {0, 0}, oPhase[2] = {1, 1};
+      bool stop = false;
+      // descriptor words: start addresses in 16-byte units, the rest constant
+      const uint32_t q_lo = smem_u32(sQ) >> 4, kv_lo = smem_u32(sKV) >> 4;
+      constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 B, version 1, 128-byte swizzle
+      constexpr uint32_t kTileUnits = S::kTileBytes >> 4, kBoxUnits = S::kBox >> 4;
+      // waits for the next ring tile; its slot, or -1
+      auto next_tile = [&]() {
+        if (!mbar_wait(&full[slot], phase, sAbort, p.status)) {
+          stop = true;
+          return -1;
+        }
+        tc_fence_after();
+        const int s = slot;
+        if (++slot == kSlots) { slot = 0; phase ^= 1; }
+        return s;
+      };
+      auto issue_qk = [&](int g, int qg, int s0) {  // S of warpgroup g from Q half qg
+        const uint32_t q = q_lo + (uint32_t)qg * kTileUnits, kk = kv_lo + (uint32_t)s0 * kTileUnits;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s / 4) * S::kBox + (s % 4) * 32;
-          tc_mma_bf16(tmem + 128u * g, smem_desc_sw128(q + off, 0, 1024), smem_desc_sw128(kk + off, 0, 1024), idesc_qk, s > 0);
+          const uint32_t off = (s / 4) * kBoxUnits + (s % 4) * 2;
+          tc_mma_bf16_lo(128u * g, q + off, kHi, kk + off, kHi, idesc_qk, s > 0);
         }
         tc_commit(&sFull[g]);
-      }
-    };
-    for (int k = 0; k < walk.cnt && !stop; ++k) {
-      const AttnItem it = load_item(p.items + walk.at(k));
-      const int nt = ceil_div(it.n_keys, kATile), groups = it.n_tok > p.TB ? 2 : 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(qFull, k & 1, sAbort, p.status))) { stop = true; break; }
-      if (!ring_wait()) { stop = true; break; }
-      for (int g = 0; g < groups; ++g) issue_qk(g, n % kSlots);
-      if (lane == 0) {
-        tc_commit(&empty[n % kSlots]);
-        if (nt == 1) tc_commit(qEmpty);
-      }
-      ++n;
-      for (int j = 0; j < nt && !stop; ++j) {
-        const int valid = min(kATile, it.n_keys - j * kATile), ksteps = (valid + 15) >> 4;
-        const int vslot = n % kSlots, kslot = (n + 1) % kSlots;
-        const bool more = j + 1 < nt;
-        for (int g = 0; g < groups; ++g) {
-          if (g == 0) {
-            if (!ring_wait()) { stop = true; break; }
-            if (valid & 15) {  // rows of the last group that lie past the keys
-              unsigned char* v = sKV + vslot * S::kTileBytes;
-              const int rows = 16 * ksteps - valid;
-              for (int i = lane; i < rows * 8 * kHalves; i += 32) {
-                const int c = i / (rows * 8), rest = i - c * rows * 8;
-                *reinterpret_cast<uint4*>(v + c * S::kBox + (valid + rest / 8) * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-            }
-          }
-          if (!__all_sync(0xffffffffu, mbar_wait(&pFull[g], nP[g] & 1, sAbort, p.status))) { stop = true; break; }
-          ++nP[g];
-          if (j == 0 && !__all_sync(0xffffffffu, mbar_wait(&oEmpty[g], (nO[g] & 1) ^ 1, sAbort, p.status))) { stop = true; break; }
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t v = smem_u32(sKV + vslot * S::kTileBytes);
-            for (int s = 0; s < ksteps; ++s)
-              tc_mma_bf16_ts(tmem + 256u + 128u * g, tmem + 128u * g + 8u * s, smem_desc_sw128(v + s * 2048, S::kBox, 1024),
-                             idesc_pv, (j | s) != 0);
-          }
-          if (more) {
-            if (g == 0) {
-              ++n;  // the V tile stays counted by vslot; the next K tile follows it in the ring
-              const bool ok = ring_wait();
-              if (!ok) { stop = true; break; }
-            }
-            issue_qk(g, kslot);
-          } else if (lane == 0) {
-            tc_commit(&oFull[g]);
-          }
-          if (!more) ++nO[g];
+      };
+      auto issue_pv = [&](int g, int s0, int ksteps, bool first) {
+        const uint32_t v = (kv_lo + (uint32_t)s0 * kTileUnits) | (kBoxUnits << 16);  // MN-major: the leading offset is a box
+        const uint32_t d = 256u + 128u * g, a = 128u * g;
+        if (ksteps == 8) {
+#pragma unroll
+          for (int s = 0; s < 8; ++s) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
+        } else {
+          for (int s = 0; s < ksteps; ++s) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
         }
+      };
+      // waits for P of warpgroup g (and, at its first tile of an item, for the epilogue before to have read O)
+      auto p_ready = [&](int g, bool first) {
+        if (!mbar_wait(&pFull[g], pPhase[g], sAbort, p.status)) return false;
+        pPhase[g] ^= 1;
+        if (first) {
+          if (!mbar_wait(&oEmpty[g], oPhase[g], sAbort, p.status)) return false;
+          oPhase[g] ^= 1;
+        }
+        tc_fence_after();
+        return true;
+      };
+      for (int k = 0; k < walk.cnt && !stop; ++k) {
+        const AttnItem it = load_item(p.items + walk.at(k));
+        const int nt = ceil_div(it.n_keys, kATile), last_steps = (it.n_keys - (nt - 1) * kATile + 15) >> 4;
+        if (!mbar_wait(qFull, k & 1, sAbort, p.status)) break;
+        int ks = next_tile();
         if (stop) break;
-        if (lane == 0) {
-          tc_commit(&empty[vslot]);
-          if (more) tc_commit(&empty[kslot]);
-          if (j + 2 == nt) tc_commit(qEmpty);
+        issue_qk(0, 0, ks);
+        if (!(it.head & kAlternate)) {  // both halves of the rows, one after the other on each tile
+          issue_qk(1, 1, ks);
+          tc_commit(&empty[ks]);
+          if (nt == 1) tc_commit(qEmpty);
+          for (int j = 0; j < nt; ++j) {
+            const bool more = j + 1 < nt;
+            const int steps = more ? 8 : last_steps, vs = next_tile();
+            if (stop || !p_ready(0, j == 0)) { stop = true; break; }
+            issue_pv(0, vs, steps, j == 0);
+            if (more) {
+              ks = next_tile();
+              if (stop) break;
+              issue_qk(0, 0, ks);
+            } else {
+              tc_commit(&oFull[0]);
+            }
+            if (!p_ready(1, j == 0)) { stop = true; break; }
+            issue_pv(1, vs, steps, j == 0);
+            tc_commit(&empty[vs]);
+            if (more) {
+              issue_qk(1, 1, ks);
+              tc_commit(&empty[ks]);
+              if (j + 2 == nt) tc_commit(qEmpty);
+            } else {
+              tc_commit(&oFull[1]);
+            }
+          }
+        } else {  // even tiles to warpgroup 0, odd ones to 1
+          tc_commit(&empty[ks]);
+          if (nt > 1) {
+            ks = next_tile();
+            if (stop) break;
+            issue_qk(1, 0, ks);
+            tc_commit(&empty[ks]);
+          }
+          if (nt <= 2) tc_commit(qEmpty);
+          for (int j = 0; j < nt; ++j) {
+            const int g = j & 1, vs = next_tile();
+            if (stop || !p_ready(g, j < 2)) { stop = true; break; }
+            issue_pv(g, vs, j + 1 < nt ? 8 : last_steps, j < 2);
+            tc_commit(&empty[vs]);
+            if (j + 2 < nt) {
+              ks = next_tile();
+              if (stop) break;
+              issue_qk(g, 0, ks);
+              tc_commit(&empty[ks]);
+              if (j + 3 == nt) tc_commit(qEmpty);
+            } else {
+              tc_commit(&oFull[g]);
+            }
+          }
         }
-        ++n;
       }
-    }
-    if (lane == 0) {
       tc_commit(drain);  // every MMA issued so far has completed
       mbar_wait_drain(drain, 0, p.status);
     }
@@ -478,19 +538,23 @@ __global__ void __launch_bounds__(kAThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128u * g, tO = tmem + lane_base + 256u + 128u * g;
     uint32_t nS = 0, nI = 0;
+    int ring = 0;  // ring tiles of the items before
     bool stop = false;
     for (int k = 0; k < walk.cnt && !stop; ++k) {
       const AttnItem it = load_item(p.items + walk.at(k));
-      if (g == 1 && it.n_tok <= p.TB) continue;
       const int nt = ceil_div(it.n_keys, kATile);
-      const int tok = g * p.TB + row / p.G;
+      const bool halves = !(it.head & kAlternate);  // else the even tiles of all rows, or the odd ones
+      const int v_last = ring + 2 * nt - 1;  // the ring tile of the last V
+      ring += 2 * nt;
+      if (!halves && g >= nt) continue;
+      const int tok = (halves ? g * p.TB : 0) + row / p.G;
       const bool valid = row < p.TB * p.G && tok < it.n_tok;
       const int limit = !valid ? 0 : it.req < 0 ? it.n_keys : min(it.n_keys, it.pos0 + tok);  // keys the row sees
       int clear = valid ? limit : 0x7fffffff;  // keys that every row of the warp sees
       clear = warp_min_i(clear);
       const bool any = clear != 0x7fffffff;
       float m = -INFINITY, z = 0.f;
-      for (int j = 0; j < nt; ++j, ++nS) {
+      for (int j = halves ? 0 : g; j < nt; j += halves ? 1 : 2, ++nS) {
         if (!__all_sync(0xffffffffu, mbar_wait(&sFull[g], nS & 1, sAbort, p.status))) { stop = true; break; }
         tc_fence_after();
         if (any) {
@@ -522,7 +586,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);  // mn >= m; 1 where m stays
             m = mn;
             z *= f;
-            if (j > 0) {
+            if (j > (halves ? 0 : 1)) {
 #pragma unroll
               for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -558,6 +622,16 @@ __global__ void __launch_bounds__(kAThreads, 1)
           z += z0 + z1;
           tmem_st_wait();
         }
+        if (j + 1 == nt && (it.n_keys & 15) && (!halves || g == 0)) {  // V rows past the keys
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[v_last % kSlots], (v_last / kSlots) & 1, sAbort, p.status))) { stop = true; break; }
+          const int first = it.n_keys - j * kATile, rows = 16 - (it.n_keys & 15);
+          unsigned char* v = sKV + (v_last % kSlots) * S::kTileBytes;
+          for (int i = row; i < rows * 8 * kHalves; i += 128) {
+            const int c = i / (rows * 8), rest = i - c * rows * 8;
+            *reinterpret_cast<uint4*>(v + c * S::kBox + (first + rest / 8) * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pFull[g]);
@@ -567,8 +641,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
       ++nI;
       tc_fence_after();
       if (any) {
-        const int hq = it.head * p.G + row % p.G;
-        const size_t t = it.slot0 < 0 ? (size_t)it.tok0 + tok : (size_t)it.slot0 + tok;
+        const int hq = (it.head & ~kAlternate) * p.G + row % p.G;
+        const size_t t = it.slot0 < 0 ? (size_t)it.tok0 + tok : (size_t)it.slot0 + tok + (!halves && g ? it.n_tok : 0);
         const size_t at = valid ? t * p.Hq + hq : 0;
         const float inv = z != 0.f ? 1.f / z : 0.f;
 #pragma unroll
@@ -613,7 +687,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int np = p.head->prefix_splits;
+  const int np = p.head->prefix_parts;
   if (row >= (long long)p.head->n_tokens * p.Hq) return;
   const int t = (int)(row / p.Hq), hq = (int)(row % p.Hq);
   const int4 map = __ldg(p.tokens + t);
