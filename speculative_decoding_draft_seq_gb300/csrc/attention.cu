@@ -15,29 +15,32 @@
 //   attn_plan_kernel   one CTA: cuts the work into items (a key head, a block of
 //                      query tokens, a range of 128-key tiles), equal shares of
 //                      about 1/kPlanShare of an SM's work;
-//   attn_tiles_kernel  persistent, one CTA an SM, items b, b + grid, ...; odd
-//                      CTAs take them in reverse, so that the prefix items (bound
-//                      by the tensor cores) and the page items (bound by memory)
-//                      run at the same time;
+//   attn_tiles_kernel  persistent, one CTA an SM; a CTA takes the next item when it
+//                      is done with one. Prefix items (bound by the tensor cores)
+//                      and page items (bound by memory) alternate in their
+//                      numbers' ratio, so that both run at any time;
 //   attn_join_kernel   adds a row's parts up.
 //
 // attn_tiles_kernel: rows are (token, query head of the key head), packed
 // floor(128 / group) tokens a 128-row half. Per 128-key tile: S = Q K^T into TMEM
-// (128 columns), a warpgroup turns S into bf16 weights in place (one thread a
-// row), O += P V with P read from TMEM. Two softmax warpgroups, each with an S / P
-// and an O of its own, keep two tiles in flight, so that one's softmax runs under
-// the other's MMAs: an item with more tokens than a half holds gives each one a
-// half of the rows (K and V tiles are read once for both); an item with fewer
-// gives them the even and the odd key tiles of the same rows (two parts). The
-// weights use a reference maximum that is moved, and O rescaled, only when the
-// row's maximum has risen by more than 8 (2^8 fits every type on the way), so O
-// is rarely rescaled.
-//   warps 0..3, 4..7  softmax and epilogue of warpgroup 0, 1; the V rows of the
-//                     last 16-key group that lie past the keys are zeroed here
-//                     (a weight of 0 times a NaN is a NaN)
-//   warp 8            TMA loads: Q once an item, a ring of K and V tiles, one box
-//                     a page (or 128 rows of a longer one), 64 columns wide
-//   warp 9            TMEM allocation; MMA issue by one thread, which forms a
+// (128 columns), eight warps turn S into bf16 weights in place (two threads a row,
+// 64 columns each, that exchange their maxima), O += P V with P read from TMEM.
+// Two such groups of warps, each with an S / P and an O of its own, keep two tiles
+// in flight, so that one's softmax runs under the other's MMAs: an item with more
+// tokens than a half holds gives each one a half of the rows (K and V tiles are
+// read once for both); an item with fewer gives them the even and the odd key
+// tiles of the same rows (two parts). The weights use a reference maximum that is
+// moved, and O rescaled, only when the row's maximum has risen by more than 8
+// (2^8 fits every type on the way). The reference comes from the tiles before, so
+// that the weights need not wait for the maximum of their own tile (over both
+// warps of a row); a tile that exceeds it by more than 60 is weighted again.
+//   warps 0..7, 8..15 softmax and epilogue of group 0, 1; the V rows of the last
+//                     16-key group that lie past the keys are zeroed here (a weight
+//                     of 0 times a NaN is a NaN)
+//   warp 16           takes the items; TMA loads: Q once an item, a ring of K and V
+//                     tiles, one box a page (or 128 rows of a longer one), 64
+//                     columns wide
+//   warp 17           TMEM allocation; MMA issue by one thread, which forms a
 //                     descriptor word with one add a step (an MMA of 128 x 128 x 16
 //                     takes 64 cycles, little more than its issue)
 // Every wait is bounded: one that runs out records DSPARK_ERR_TIMEOUT, the
@@ -52,9 +55,10 @@
 namespace dspark {
 
 constexpr int kATile = 128;        // keys a tile
-constexpr int kAThreads = 320;
-constexpr int kPlanShare = 4;      // items are at most about 1/4 of an SM's share of the work
-constexpr int kExtraSlots = 2048;  // token slots beyond one part for the prefix and two for the pages
+constexpr int kASoftmaxWarps = 8;    // four a group: one thread a row
+constexpr int kAThreads = 32 * (kASoftmaxWarps + 2);
+constexpr int kPlanShare = 6;      // items are at most about 1/6 of an SM's share of the work
+constexpr int kExtraSlots = 8192;  // token slots beyond one part for the prefix and two for the pages
 constexpr int kMaxSms = 256;
 
 struct AttnItem {
@@ -72,7 +76,8 @@ struct AttnItem {
 constexpr int kAlternate = 1 << 30;
 
 struct AttnHead {  // written by the plan
-  int n_items, prefix_parts, n_tokens, pad;
+  int n_items, prefix_items, prefix_parts, n_tokens;
+  unsigned int next;  // items taken
 };
 
 struct AttnParams {
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
   }
   if (__syncthreads_or(broken)) {
     if (tid == 0) {
-      *p.head = AttnHead{0, 0, 0, 0};
+      *p.head = AttnHead{0, 0, 0, 0, 0u};
       set_status(p.status, DSPARK_ERR_RANGE);
     }
     return;
@@ -222,20 +227,35 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
     it.pos0 = it.n_keys;
     p.items[i] = it;
   }
-  long long item0 = p_items, slot0 = (long long)p_parts * n_tokens;
+  // page items of at least half a share first, then the smaller ones
+  auto small = [&](int tiles, int ns) { return 2ll * tiles < share * ns; };
+  long long n_large = 0;
+  for (int r = tid; r < p.R; r += kAPlanThreads) {
+    int start, n, len;
+    request(r, start, n, len);
+    for (int t0 = 0; t0 < n; t0 += step) {
+      const int tiles = tiles_of(n, len, t0), ns = splits_of(tiles, min(step, n - t0), share);
+      if (!small(tiles, ns)) n_large += (long long)ns * p.Hkv;
+    }
+  }
+  long long all_large;
+  scan_ll(n_large, sh, all_large);
+  long long large0 = p_items, small0 = p_items + all_large, slot0 = (long long)p_parts * n_tokens;
   for (int r0 = 0; r0 < p.R; r0 += kAPlanThreads) {
     const int r = r0 + tid;
     int start = 0, n = 0, len = 0;
     if (r < p.R) request(r, start, n, len);
-    long long items = 0, slots = 0;
+    long long larges = 0, smalls = 0, slots = 0;
     for (int t0 = 0; t0 < n; t0 += step) {
       const int tiles = tiles_of(n, len, t0), nt = min(step, n - t0), ns = splits_of(tiles, nt, share);
-      items += (long long)ns * p.Hkv;
+      (small(tiles, ns) ? smalls : larges) += (long long)ns * p.Hkv;
       slots += (long long)parts_of(tiles, nt, ns) * nt;
     }
-    long long n_items, n_slots;
-    long long item = item0 + scan_ll(items, sh, n_items), slot = slot0 + scan_ll(slots, sh, n_slots);
-    item0 += n_items;
+    long long n_l, n_s, n_slots;
+    long long large_at = large0 + scan_ll(larges, sh, n_l), small_at = small0 + scan_ll(smalls, sh, n_s);
+    long long slot = slot0 + scan_ll(slots, sh, n_slots);
+    large0 += n_l;
+    small0 += n_s;
     slot0 += n_slots;
     for (int t0 = 0; t0 < n; t0 += step) {
       const int tiles = tiles_of(n, len, t0), nt = min(step, n - t0), ns = splits_of(tiles, nt, share);
@@ -244,6 +264,7 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
       for (int i = 0; i < nt; ++i)
         p.tokens[start + t0 + i] = make_int4((int)slot + i, nt, direct ? -1 : parts, 0);
       const int seen = max(0, min(len, len - n + t0 + nt));  // keys that the block's last token sees
+      long long& item = small(tiles, ns) ? small_at : large_at;
       for (int s = 0; s < ns; ++s) {
         const int a = (int)((long long)s * tiles / ns), e = (int)((long long)(s + 1) * tiles / ns);
         for (int h = 0; h < p.Hkv; ++h, ++item) {
@@ -262,8 +283,11 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
       slot += (long long)parts * nt;
     }
   }
+  const long long item_end = small0;
   if (tid == 0) {
-    p.head->n_items = (int)item0;
+    p.head->n_items = (int)item_end;
+    p.head->prefix_items = (int)p_items;
+    p.head->next = 0;
     p.head->prefix_parts = p_parts;
     p.head->n_tokens = n_tokens;
   }
@@ -278,25 +302,9 @@ struct AttnSmem {
   static constexpr uint32_t kTileBytes = kHalves * kBox;
   static constexpr int kSlots = D == 128 ? 5 : 10;     // K and V tiles in the ring
   static constexpr uint32_t kQ = 2 * kTileBytes;
-  static constexpr uint32_t kTotal = 1024 + kQ + kSlots * kTileBytes + 512;
+  static constexpr uint32_t kTotal = kQ + kSlots * kTileBytes + 512;
+  static_assert(kTotal <= 227 * 1024, "shared memory of a CTA");
 };
-
-// Items of this CTA in the order that it takes them.
-struct ItemWalk {
-  int n, b, grid, cnt;
-  __device__ ItemWalk(int n_items) : n(n_items), b(blockIdx.x), grid(gridDim.x) {
-    cnt = b < n ? (n - b + grid - 1) / grid : 0;
-  }
-  __device__ int at(int k) const { return b + ((b & 1) ? cnt - 1 - k : k) * grid; }
-};
-
-__device__ __forceinline__ AttnItem load_item(const AttnItem* p) {
-  const int4 a = __ldg(reinterpret_cast<const int4*>(p)), b = __ldg(reinterpret_cast<const int4*>(p) + 1);
-  AttnItem it;
-  it.head = a.x; it.req = a.y; it.tok0 = a.z; it.n_tok = a.w;
-  it.key0 = b.x; it.n_keys = b.y; it.slot0 = b.z; it.pos0 = b.w;
-  return it;
-}
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t d;
@@ -310,38 +318,48 @@ __global__ void __launch_bounds__(kAThreads, 1)
                       const __grid_constant__ CUtensorMap mapV, AttnParams p, int q_rows, int box_rows) {
   using S = AttnSmem<D>;
   constexpr int kHalves = S::kHalves, kSlots = S::kSlots;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (no room to align by hand: the swizzled tiles need 1024 bytes, which the base has without static shared memory)
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_u32(smem) & 1023) {
+    if (threadIdx.x == 0) set_status(p.status, DSPARK_ERR_CUDA);
+    return;
+  }
   unsigned char* sQ = smem;
   unsigned char* sKV = smem + S::kQ;
   uint64_t* full = reinterpret_cast<uint64_t*>(sKV + kSlots * S::kTileBytes);
   uint64_t* empty = full + kSlots;
-  uint64_t* qFull = empty + kSlots;
-  uint64_t* qEmpty = qFull + 1;
-  uint64_t* sFull = qEmpty + 1;   // [2] S of a half is in TMEM
-  uint64_t* pFull = sFull + 2;    // [2] P of a half is in TMEM
-  uint64_t* oFull = pFull + 2;    // [2] O of a half is complete
+  uint64_t* qFull = empty + kSlots;  // [2] Q of a half
+  uint64_t* qEmpty = qFull + 2;      // [2]
+  uint64_t* sFull = qEmpty + 2;   // [2] S of a half is in TMEM
+  uint64_t* pFull = sFull + 2;    // [2][2] P of a group is in TMEM: its first 64 keys, the others
+  uint64_t* oFull = pFull + 4;    // [2] O of a half is complete
   uint64_t* oEmpty = oFull + 2;   // [2] the epilogue has read O
   uint64_t* drain = oEmpty + 2;
-  uint32_t* sTmem = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* iFull = drain + 1;    // [2] an item is there
+  uint64_t* iEmpty = iFull + 2;   // [2] every role has read it
+  uint32_t* sTmem = reinterpret_cast<uint32_t*>(iEmpty + 2);
   volatile int* sAbort = reinterpret_cast<volatile int*>(sTmem + 1);
+  int4* sItem = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(sTmem) + 31) & ~uintptr_t(15));  // [2][2] an AttnItem
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-    mbar_init(qFull, 1);
-    mbar_init(qEmpty, 1);
     for (int g = 0; g < 2; ++g) {
+      mbar_init(&qFull[g], 1);
+      mbar_init(&qEmpty[g], 1);
       mbar_init(&sFull[g], 1);
-      mbar_init(&pFull[g], 4);
+      mbar_init(&pFull[2 * g], kASoftmaxWarps / 2);
+      mbar_init(&pFull[2 * g + 1], kASoftmaxWarps / 2);
       mbar_init(&oFull[g], 1);
-      mbar_init(&oEmpty[g], 4);
+      mbar_init(&oEmpty[g], kASoftmaxWarps / 2);
+      mbar_init(&iFull[g], 1);
+      mbar_init(&iEmpty[g], kASoftmaxWarps + 1);
     }
     mbar_init(drain, 1);
     *sAbort = 0;
     mbar_fence_init();
   }
-  if (warp == 9) {
+  if (warp == kASoftmaxWarps + 1) {
     __syncwarp();
     tmem_alloc(sTmem, 512);
   }
@@ -349,9 +367,26 @@ __global__ void __launch_bounds__(kAThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *sTmem;  // 0: all 512 columns are this CTA's
-  const ItemWalk walk(p.head->n_items);
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, sAbort, p.status)) != 0;
+  };
+  // the k-th item of this CTA (n_keys 0: there is none); by whole warps
+  auto take = [&](int k) {
+    const int slot = k & 1;
+    AttnItem it;
+    it.n_keys = 0;
+    const bool ok = warp_wait(&iFull[slot], (k >> 1) & 1);
+    const int4 a = sItem[2 * slot], b = sItem[2 * slot + 1];
+    if (ok) {
+      it.head = a.x; it.req = a.y; it.tok0 = a.z; it.n_tok = a.w;
+      it.key0 = b.x; it.n_keys = b.y; it.slot0 = b.z; it.pos0 = b.w;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&iEmpty[slot]);
+    return it;
+  };
 
-  if (warp == 8) {
+  if (warp == kASoftmaxWarps) {
     // ---- loads ----
     if (lane == 0) {
       prefetch_tensormap(&mapQ);
@@ -359,10 +394,32 @@ __global__ void __launch_bounds__(kAThreads, 1)
       prefetch_tensormap(&mapV);
     }
     const uint64_t pol = l2_policy_evict_normal();
-    int n = 0, nq = 0;  // ring tiles and Q blocks issued
+    int n = 0, q_turn = 0;        // ring tiles issued; the Q buffer of the next item that needs one
+    uint32_t qPhase[2] = {1, 1};
     bool stop = false;
-    for (int k = 0; k < walk.cnt && !stop; ++k) {
-      const AttnItem it = load_item(p.items + walk.at(k));
+    const int n_items = p.head->n_items, n_prefix = p.head->prefix_items;
+    for (int k = 0; !stop; ++k) {
+      // the next item: prefix items and page items in their numbers' ratio
+      int item = 0;
+      if (lane == 0) {
+        const long long t = atomicAdd(&p.head->next, 1u);
+        const long long a = t * n_prefix / max(n_items, 1), b = (t + 1) * n_prefix / max(n_items, 1);
+        item = t >= n_items ? -1 : (int)(b > a ? a : n_prefix + t - a);
+      }
+      item = __shfl_sync(0xffffffffu, item, 0);
+      int4 half = make_int4(0, 0, 0, 0);  // lanes 0 and 1: the item's two halves
+      if (item >= 0 && lane < 2) half = __ldg(reinterpret_cast<const int4*>(p.items + item) + lane);
+      if (!warp_wait(&iEmpty[k & 1], ((k >> 1) & 1) ^ 1)) break;
+      if (lane < 2) sItem[2 * (k & 1) + lane] = half;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iFull[k & 1]);
+      if (item < 0) break;
+      AttnItem it;
+      it.head = __shfl_sync(0xffffffffu, half.x, 0);
+      it.req = __shfl_sync(0xffffffffu, half.y, 0);
+      it.tok0 = __shfl_sync(0xffffffffu, half.z, 0);
+      it.key0 = __shfl_sync(0xffffffffu, half.x, 1);
+      it.n_keys = __shfl_sync(0xffffffffu, half.y, 1);
       const int nt = ceil_div(it.n_keys, kATile);
       const int32_t* pages = it.req < 0 ? p.prefix_pages : p.table + (size_t)it.req * p.max_pages;
       const int boxes = kATile / box_rows;
@@ -377,7 +434,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         const int row = (it.key0 + j * kATile + lane * box_rows) & (p.page - 1);
         const int slot = n % kSlots;
         if (lane < live && (pg < 0 || pg >= p.n_pages)) set_status(p.status, DSPARK_ERR_RANGE);
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ((n / kSlots) & 1) ^ 1, sAbort, p.status))) {
+        if (!warp_wait(&empty[slot], ((n / kSlots) & 1) ^ 1)) {
           stop = true;
           return;
         }
@@ -394,16 +451,20 @@ __global__ void __launch_bounds__(kAThreads, 1)
       // in the order of use: K of the first tiles, then V of a tile and K of the tile `ahead` on
       int pgs[3] = {page_at(0), nt > 1 ? page_at(1) : 0, 0};  // pages of tiles j, j + 1, j + 2
       load(0, 0, pgs[0]);
-      // Q behind the first K tile: its buffer is free once the item before has no S left to form
-      if (!stop && !__all_sync(0xffffffffu, mbar_wait(qEmpty, (k & 1) ^ 1, sAbort, p.status))) stop = true;
-      if (stop) break;
-      if (lane == 0) {
-        mbar_expect_tx(qFull, (uint32_t)(groups * q_rows * 128 * kHalves));
-        for (int g = 0; g < groups; ++g)
+      // Q behind the first K tile: both halves, or one of the two buffers in turn, each free once the item that
+      // it held has no S left to form
+      for (int i = 0; i < groups && !stop; ++i) {
+        const int buf = groups == 2 ? i : q_turn;
+        if (!warp_wait(&qEmpty[buf], qPhase[buf])) { stop = true; break; }
+        qPhase[buf] ^= 1;
+        if (lane == 0) {
+          mbar_expect_tx(&qFull[buf], (uint32_t)(q_rows * 128 * kHalves));
           for (int c = 0; c < kHalves; ++c)
-            tma_load_4d(sQ + g * S::kTileBytes + c * S::kBox, &mapQ, 64 * c, 0, head, it.tok0 + g * p.TB, qFull, pol);
+            tma_load_4d(sQ + buf * S::kTileBytes + c * S::kBox, &mapQ, 64 * c, 0, head, it.tok0 + i * p.TB, &qFull[buf], pol);
+        }
       }
-      ++nq;
+      if (groups == 1) q_turn ^= 1;
+      if (stop) break;
       if (ahead == 2 && nt > 1) load(1, 0, pgs[1]);
       for (int j = 0; j < nt && !stop; ++j) {
         pgs[2] = j + 2 < nt ? page_at(j + 2) : 0;
@@ -414,134 +475,152 @@ __global__ void __launch_bounds__(kAThreads, 1)
       }
     }
     // no copy outlives the CTA: the last kSlots ring tiles and the last Q
-    if (nq > 0) mbar_wait_drain(qFull, (nq - 1) & 1, p.status);
+    for (int i = 0; i < 2; ++i) mbar_wait_drain(&qFull[i], qPhase[i] & 1, p.status);
     for (int i = 1; i <= kSlots && n - i >= 0; ++i)
       mbar_wait_drain(&full[(n - i) % kSlots], ((n - i) / kSlots) & 1, p.status);
-  } else if (warp == 9) {
-    // ---- MMA issue ----
-    if (lane == 0) {
-      const uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0), idesc_pv = idesc_bf16_f32(128, D, 1);
-      int slot = 0, phase = 0;  // the next ring tile
-      uint32_t pPhase[2] = {0, 0}, oPhase[2] = {1, 1};
-      bool stop = false;
-      // descriptor words: start addresses in 16-byte units, the rest constant
-      const uint32_t q_lo = smem_u32(sQ) >> 4, kv_lo = smem_u32(sKV) >> 4;
-      constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 B, version 1, 128-byte swizzle
-      constexpr uint32_t kTileUnits = S::kTileBytes >> 4, kBoxUnits = S::kBox >> 4;
-      // waits for the next ring tile; its slot, or -1
-      auto next_tile = [&]() {
-        if (!mbar_wait(&full[slot], phase, sAbort, p.status)) {
-          stop = true;
-          return -1;
-        }
-        tc_fence_after();
-        const int s = slot;
-        if (++slot == kSlots) { slot = 0; phase ^= 1; }
-        return s;
-      };
-      auto issue_qk = [&](int g, int qg, int s0) {  // S of warpgroup g from Q half qg
-        const uint32_t q = q_lo + (uint32_t)qg * kTileUnits, kk = kv_lo + (uint32_t)s0 * kTileUnits;
-#pragma unroll
+  } else if (warp == kASoftmaxWarps + 1) {
+    // ---- MMA issue: the whole warp goes through the waits, one elected lane issues ----
+    const uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0), idesc_pv = idesc_bf16_f32(128, D, 1);
+    uint32_t slot = 0, phase = 0;  // the next ring tile
+    uint32_t pPhase[2] = {0, 0}, oPhase[2] = {1, 1}, qPhase[2] = {0, 0}, q_turn = 0;
+    bool stop = false;
+    // descriptor words: start addresses in 16-byte units, the rest constant
+    const uint32_t q_lo = smem_u32(sQ) >> 4, kv_lo = smem_u32(sKV) >> 4;
+    constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 B, version 1, 128-byte swizzle
+    constexpr uint32_t kTileUnits = S::kTileBytes >> 4, kBoxUnits = S::kBox >> 4;
+    // waits for the next ring tile; its slot
+    auto next_tile = [&]() {
+      if (!warp_wait(&full[slot], phase)) stop = true;
+      tc_fence_after();
+      const uint32_t s = slot;
+      if (++slot == kSlots) { slot = 0; phase ^= 1; }
+      return s;
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) tc_commit(bar);
+    };
+    auto issue_qk = [&](uint32_t g, uint32_t qb, uint32_t s0) {  // S of group g from Q buffer qb
+      const uint32_t q = q_lo + qb * kTileUnits, kk = kv_lo + s0 * kTileUnits;
+      if (elect_one()) {
+#pragma unroll 1
         for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s / 4) * kBoxUnits + (s % 4) * 2;
+          const uint32_t off = (s >> 2) * kBoxUnits + (s & 3) * 2;
           tc_mma_bf16_lo(128u * g, q + off, kHi, kk + off, kHi, idesc_qk, s > 0);
         }
         tc_commit(&sFull[g]);
-      };
-      auto issue_pv = [&](int g, int s0, int ksteps, bool first) {
-        const uint32_t v = (kv_lo + (uint32_t)s0 * kTileUnits) | (kBoxUnits << 16);  // MN-major: the leading offset is a box
-        const uint32_t d = 256u + 128u * g, a = 128u * g;
-        if (ksteps == 8) {
-#pragma unroll
-          for (int s = 0; s < 8; ++s) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
-        } else {
-          for (int s = 0; s < ksteps; ++s) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
+      }
+    };
+    // k-steps from..to - 1 of O of group g
+    auto issue_pv = [&](uint32_t g, uint32_t s0, uint32_t from, uint32_t to, bool first) {
+      const uint32_t v = (kv_lo + s0 * kTileUnits + 128u * from) | (kBoxUnits << 16);  // MN-major: the leading offset is a box
+      const uint32_t d = 256u + 128u * g, a = 128u * g + 8u * from;
+      if (elect_one()) {
+#pragma unroll 1
+        for (uint32_t s = 0; s < to - from; ++s) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
+      }
+    };
+    // O += P V of group g's tile with `steps` groups of 16 keys, as P arrives (at the group's first tile of an
+    // item, once the epilogue before has read O)
+    auto pv = [&](uint32_t g, uint32_t vs, uint32_t steps, bool first_tile) {
+      if (!warp_wait(&pFull[2 * g], pPhase[g])) return false;
+      if (first_tile) {
+        if (!warp_wait(&oEmpty[g], oPhase[g])) return false;
+        oPhase[g] ^= 1;
+      }
+      tc_fence_after();
+      issue_pv(g, vs, 0, min(steps, 4u), first_tile);
+      if (!warp_wait(&pFull[2 * g + 1], pPhase[g])) return false;
+      pPhase[g] ^= 1;
+      tc_fence_after();
+      if (steps > 4) issue_pv(g, vs, 4, steps, false);
+      return true;
+    };
+    for (int k = 0; !stop; ++k) {
+      const AttnItem it = take(k);
+      // (through a warp-wide reduction: the result is in a uniform register)
+      const uint32_t n_keys = __reduce_max_sync(0xffffffffu, (uint32_t)it.n_keys);
+      const uint32_t halves = __reduce_max_sync(0xffffffffu, it.head & kAlternate ? 0u : 1u);
+      if (n_keys == 0) break;
+      const uint32_t nt = (n_keys + kATile - 1) / kATile, last_steps = (n_keys - (nt - 1) * kATile + 15) >> 4;
+      if (halves) {  // both halves of the rows, one after the other on each tile
+        for (uint32_t b = 0; b < 2; ++b) {
+          if (!warp_wait(&qFull[b], qPhase[b])) stop = true;
+          qPhase[b] ^= 1;
         }
-      };
-      // waits for P of warpgroup g (and, at its first tile of an item, for the epilogue before to have read O)
-      auto p_ready = [&](int g, bool first) {
-        if (!mbar_wait(&pFull[g], pPhase[g], sAbort, p.status)) return false;
-        pPhase[g] ^= 1;
-        if (first) {
-          if (!mbar_wait(&oEmpty[g], oPhase[g], sAbort, p.status)) return false;
-          oPhase[g] ^= 1;
-        }
-        tc_fence_after();
-        return true;
-      };
-      for (int k = 0; k < walk.cnt && !stop; ++k) {
-        const AttnItem it = load_item(p.items + walk.at(k));
-        const int nt = ceil_div(it.n_keys, kATile), last_steps = (it.n_keys - (nt - 1) * kATile + 15) >> 4;
-        if (!mbar_wait(qFull, k & 1, sAbort, p.status)) break;
-        int ks = next_tile();
+        if (stop) break;
+        uint32_t ks = next_tile();
         if (stop) break;
         issue_qk(0, 0, ks);
-        if (!(it.head & kAlternate)) {  // both halves of the rows, one after the other on each tile
-          issue_qk(1, 1, ks);
-          tc_commit(&empty[ks]);
-          if (nt == 1) tc_commit(qEmpty);
-          for (int j = 0; j < nt; ++j) {
-            const bool more = j + 1 < nt;
-            const int steps = more ? 8 : last_steps, vs = next_tile();
-            if (stop || !p_ready(0, j == 0)) { stop = true; break; }
-            issue_pv(0, vs, steps, j == 0);
-            if (more) {
-              ks = next_tile();
-              if (stop) break;
-              issue_qk(0, 0, ks);
-            } else {
-              tc_commit(&oFull[0]);
-            }
-            if (!p_ready(1, j == 0)) { stop = true; break; }
-            issue_pv(1, vs, steps, j == 0);
-            tc_commit(&empty[vs]);
-            if (more) {
-              issue_qk(1, 1, ks);
-              tc_commit(&empty[ks]);
-              if (j + 2 == nt) tc_commit(qEmpty);
-            } else {
-              tc_commit(&oFull[1]);
-            }
-          }
-        } else {  // even tiles to warpgroup 0, odd ones to 1
-          tc_commit(&empty[ks]);
-          if (nt > 1) {
+        issue_qk(1, 1, ks);
+        commit(&empty[ks]);
+        if (nt == 1) { commit(&qEmpty[0]); commit(&qEmpty[1]); }
+        for (uint32_t j = 0; j < nt; ++j) {
+          const bool more = j + 1 < nt;
+          const uint32_t steps = more ? 8 : last_steps, vs = next_tile();
+          if (stop || !pv(0, vs, steps, j == 0)) { stop = true; break; }
+          if (more) {
             ks = next_tile();
             if (stop) break;
-            issue_qk(1, 0, ks);
-            tc_commit(&empty[ks]);
+            issue_qk(0, 0, ks);
+          } else {
+            commit(&oFull[0]);
           }
-          if (nt <= 2) tc_commit(qEmpty);
-          for (int j = 0; j < nt; ++j) {
-            const int g = j & 1, vs = next_tile();
-            if (stop || !p_ready(g, j < 2)) { stop = true; break; }
-            issue_pv(g, vs, j + 1 < nt ? 8 : last_steps, j < 2);
-            tc_commit(&empty[vs]);
-            if (j + 2 < nt) {
-              ks = next_tile();
-              if (stop) break;
-              issue_qk(g, 0, ks);
-              tc_commit(&empty[ks]);
-              if (j + 3 == nt) tc_commit(qEmpty);
-            } else {
-              tc_commit(&oFull[g]);
-            }
+          if (!pv(1, vs, steps, j == 0)) { stop = true; break; }
+          commit(&empty[vs]);
+          if (more) {
+            issue_qk(1, 1, ks);
+            commit(&empty[ks]);
+            if (j + 2 == nt) { commit(&qEmpty[0]); commit(&qEmpty[1]); }
+          } else {
+            commit(&oFull[1]);
+          }
+        }
+      } else {  // even tiles to group 0, odd ones to 1
+        const uint32_t qb = q_turn;
+        q_turn ^= 1;
+        if (!warp_wait(&qFull[qb], qPhase[qb])) { stop = true; break; }
+        qPhase[qb] ^= 1;
+        uint32_t ks = next_tile();
+        if (stop) break;
+        issue_qk(0, qb, ks);
+        commit(&empty[ks]);
+        if (nt > 1) {
+          ks = next_tile();
+          if (stop) break;
+          issue_qk(1, qb, ks);
+          commit(&empty[ks]);
+        }
+        if (nt <= 2) commit(&qEmpty[qb]);
+        for (uint32_t j = 0; j < nt; ++j) {
+          const uint32_t g = j & 1, vs = next_tile();
+          if (stop || !pv(g, vs, j + 1 < nt ? 8 : last_steps, j < 2)) { stop = true; break; }
+          commit(&empty[vs]);
+          if (j + 2 < nt) {
+            ks = next_tile();
+            if (stop) break;
+            issue_qk(g, qb, ks);
+            commit(&empty[ks]);
+            if (j + 3 == nt) commit(&qEmpty[qb]);
+          } else {
+            commit(&oFull[g]);
           }
         }
       }
-      tc_commit(drain);  // every MMA issued so far has completed
-      mbar_wait_drain(drain, 0, p.status);
     }
+    commit(drain);  // every MMA issued so far has completed
+    mbar_wait_drain(drain, 0, p.status);
   } else {
-    // ---- softmax and epilogue: half g, one thread a row ----
+    // ---- softmax and epilogue: group g, one thread a row ----
     const int g = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128u * g, tO = tmem + lane_base + 256u + 128u * g;
+    const unsigned long long rate2 = f32x2_pack(p.rate, p.rate), one2 = f32x2_pack(1.f, 1.f);
     uint32_t nS = 0, nI = 0;
     int ring = 0;  // ring tiles of the items before
     bool stop = false;
-    for (int k = 0; k < walk.cnt && !stop; ++k) {
-      const AttnItem it = load_item(p.items + walk.at(k));
+    for (int k = 0; !stop; ++k) {
+      const AttnItem it = take(k);
+      if (it.n_keys == 0) break;
       const int nt = ceil_div(it.n_keys, kATile);
       const bool halves = !(it.head & kAlternate);  // else the even tiles of all rows, or the odd ones
       const int v_last = ring + 2 * nt - 1;  // the ring tile of the last V
@@ -555,10 +634,38 @@ __global__ void __launch_bounds__(kAThreads, 1)
       const bool any = clear != 0x7fffffff;
       float m = -INFINITY, z = 0.f;
       for (int j = halves ? 0 : g; j < nt; j += halves ? 1 : 2, ++nS) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&sFull[g], nS & 1, sAbort, p.status))) { stop = true; break; }
+        if (!warp_wait(&sFull[g], nS & 1)) { stop = true; break; }
         tc_fence_after();
+        if (j + 1 == nt && (it.n_keys & 15) && (!halves || g == 0)) {  // V rows past the keys
+          if (!warp_wait(&full[v_last % kSlots], (v_last / kSlots) & 1)) { stop = true; break; }
+          const int first = it.n_keys - j * kATile, rows = 16 - (it.n_keys & 15);
+          unsigned char* v = sKV + (v_last % kSlots) * S::kTileBytes;
+          for (int i = row; i < rows * 8 * kHalves; i += 128) {
+            const int c = i / (rows * 8), rest = i - c * rows * 8;
+            *reinterpret_cast<uint4*>(v + c * S::kBox + (first + rest / 8) * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        uint32_t a[64], b[64];
+        float neg = 0.f;
+        unsigned long long z2[4] = {0ull, 0ull, 0ull, 0ull};
+        // the weights of 64 keys, into the 32 columns at `to`
+        auto weights = [&](const uint32_t (&x)[64], uint32_t to) {
+          const unsigned long long neg2 = f32x2_pack(neg, neg);
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 64; c += 2) {
+            float e0, e1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), rate2, neg2), e0, e1);
+            e0 = ex2_approx(e0);
+            e1 = ex2_approx(e1);
+            z2[(c >> 1) & 3] = f32x2_fma(f32x2_pack(e0, e1), one2, z2[(c >> 1) & 3]);
+            w[c >> 1] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32(to, w);
+          tmem_st_wait();
+        };
         if (any) {
-          uint32_t a[64], b[64];
           tmem_ld64_nowait(tS, a);
           tmem_ld64_nowait(tS + 64u, b);
           tmem_ld_wait64(a);
@@ -571,73 +678,48 @@ __global__ void __launch_bounds__(kAThreads, 1)
               if (c + 64 >= left) b[c] = 0xff800000u;
             }
           }
-          float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+          float x[8];
 #pragma unroll
-          for (int c = 0; c < 64; c += 4) {
-            x0 = max3(x0, __uint_as_float(a[c]), __uint_as_float(b[c]));
-            x1 = max3(x1, __uint_as_float(a[c + 1]), __uint_as_float(b[c + 1]));
-            x2 = max3(x2, __uint_as_float(a[c + 2]), __uint_as_float(b[c + 2]));
-            x3 = max3(x3, __uint_as_float(a[c + 3]), __uint_as_float(b[c + 3]));
-          }
-          const float top = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * p.rate;
+          for (int i = 0; i < 8; ++i) x[i] = fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i]));
+#pragma unroll
+          for (int c = 8; c < 64; c += 8)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = max3(x[i], __uint_as_float(a[c + i]), __uint_as_float(b[c + i]));
+          const float top = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])) * p.rate;
           const bool rise = top > m + 8.f || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, rise)) {
             const float mn = rise ? top : m;
             const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);  // mn >= m; 1 where m stays
             m = mn;
             z *= f;
-            if (j > (halves ? 0 : 1)) {
+            if (j > (halves ? 0 : 1))
+              for (int c = 0; c < D; c += 8) {
+                uint32_t u[8];
+                tmem_ld8(tO + c, u);
 #pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                uint32_t u[32];
-                tmem_ld32(tO + c, o);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(o[i] * f);
-                tmem_st32(tO + c, u);
+                for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+                tmem_st8(tO + c, u);
               }
-            }
           }
-          const float neg = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet: 2^(-inf) = 0
-          float z0 = 0.f, z1 = 0.f;
-          uint32_t w[32];
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(a[c]), p.rate, neg));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(a[c + 1]), p.rate, neg));
-            z0 += e0;
-            z1 += e1;
-            w[c >> 1] = pack_bf16x2(e0, e1);
-          }
-          tmem_st32(tS, w);
-#pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(b[c]), p.rate, neg));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(b[c + 1]), p.rate, neg));
-            z0 += e0;
-            z1 += e1;
-            w[c >> 1] = pack_bf16x2(e0, e1);
-          }
-          tmem_st32(tS + 32u, w);
-          z += z0 + z1;
-          tmem_st_wait();
-        }
-        if (j + 1 == nt && (it.n_keys & 15) && (!halves || g == 0)) {  // V rows past the keys
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[v_last % kSlots], (v_last / kSlots) & 1, sAbort, p.status))) { stop = true; break; }
-          const int first = it.n_keys - j * kATile, rows = 16 - (it.n_keys & 15);
-          unsigned char* v = sKV + (v_last % kSlots) * S::kTileBytes;
-          for (int i = row; i < rows * 8 * kHalves; i += 128) {
-            const int c = i / (rows * 8), rest = i - c * rows * 8;
-            *reinterpret_cast<uint4*>(v + c * S::kBox + (first + rest / 8) * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+          neg = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet: 2^(-inf) = 0
+          weights(a, tS);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pFull[g]);
+        if (lane == 0) mbar_arrive(&pFull[2 * g]);
+        if (any) {
+          weights(b, tS + 32u);
+          float s0, s1, s2, s3;
+          f32x2_unpack(f32x2_fma(z2[0], one2, z2[1]), s0, s1);
+          f32x2_unpack(f32x2_fma(z2[2], one2, z2[3]), s2, s3);
+          z += (s0 + s1) + (s2 + s3);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pFull[2 * g + 1]);
       }
       if (stop) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(&oFull[g], nI & 1, sAbort, p.status))) break;
+      if (!warp_wait(&oFull[g], nI & 1)) break;
       ++nI;
       tc_fence_after();
       if (any) {
@@ -673,7 +755,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kASoftmaxWarps + 1) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, 512);
