@@ -23,26 +23,24 @@
 //
 // attn_tiles_kernel: rows are (token, query head of the key head), packed
 // floor(128 / group) tokens a 128-row half. Per 128-key tile: S = Q K^T into TMEM
-// (128 columns), eight warps turn S into bf16 weights in place (two threads a row,
-// 64 columns each, that exchange their maxima), O += P V with P read from TMEM.
-// Two such groups of warps, each with an S / P and an O of its own, keep two tiles
-// in flight, so that one's softmax runs under the other's MMAs: an item with more
+// (128 columns), four warps turn S into bf16 weights in place (one thread a row),
+// O += P V with P read from TMEM, the first 64 keys while the others' weights are
+// formed. Two such groups of warps, each with an S / P and an O of its own, keep two
+// tiles in flight, so that one's softmax runs under the other's MMAs: an item with more
 // tokens than a half holds gives each one a half of the rows (K and V tiles are
 // read once for both); an item with fewer gives them the even and the odd key
 // tiles of the same rows (two parts). The weights use a reference maximum that is
-// moved, and O rescaled, only when the row's maximum has risen by more than 8
-// (2^8 fits every type on the way). The reference comes from the tiles before, so
-// that the weights need not wait for the maximum of their own tile (over both
-// warps of a row); a tile that exceeds it by more than 60 is weighted again.
-//   warps 0..7, 8..15 softmax and epilogue of group 0, 1; the V rows of the last
-//                     16-key group that lie past the keys are zeroed here (a weight
-//                     of 0 times a NaN is a NaN)
-//   warp 16           takes the items; TMA loads: Q once an item, a ring of K and V
+// moved, and O rescaled, only when the row's maximum has risen by more than 8 (2^8
+// fits every type on the way), so O is rarely rescaled.
+//   warps 0..3, 4..7  softmax and epilogue of group 0, 1
+//   warp 8            takes the items; TMA loads: Q once an item, a ring of K and V
 //                     tiles, one box a page (or 128 rows of a longer one), 64
 //                     columns wide
-//   warp 17           TMEM allocation; MMA issue by one thread, which forms a
-//                     descriptor word with one add a step (an MMA of 128 x 128 x 16
-//                     takes 64 cycles, little more than its issue)
+//   warps 9, 10       MMA issue of group 0, 1 (and TMEM allocation). The waits and
+//                     commits of a tile take one warp longer than its MMAs (64
+//                     cycles each): one warp for both groups was the bound. The V
+//                     rows of the last 16-key group that lie past the keys are
+//                     zeroed here (a weight of 0 times a NaN is a NaN).
 // Every wait is bounded: one that runs out records DSPARK_ERR_TIMEOUT, the
 // roles wind down, issued copies and MMAs land, and the TMEM is freed.
 #include <algorithm>
@@ -56,7 +54,7 @@ namespace dspark {
 
 constexpr int kATile = 128;        // keys a tile
 constexpr int kASoftmaxWarps = 8;    // four a group: one thread a row
-constexpr int kAThreads = 32 * (kASoftmaxWarps + 2);
+constexpr int kAThreads = 32 * (kASoftmaxWarps + 3);
 constexpr int kPlanShare = 6;      // items are at most about 1/6 of an SM's share of the work
 constexpr int kExtraSlots = 8192;  // token slots beyond one part for the prefix and two for the pages
 constexpr int kMaxSms = 256;
@@ -343,19 +341,21 @@ __global__ void __launch_bounds__(kAThreads, 1)
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    // both issuing warps pass every phase of every tile and Q, in order, and sign every release: a warp that skipped
+    // some could get more than one phase apart from the other, where the parity of a wait means nothing
+    for (int i = 0; i < kSlots; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 2); }
     for (int g = 0; g < 2; ++g) {
       mbar_init(&qFull[g], 1);
-      mbar_init(&qEmpty[g], 1);
+      mbar_init(&qEmpty[g], 2);
       mbar_init(&sFull[g], 1);
       mbar_init(&pFull[2 * g], kASoftmaxWarps / 2);
       mbar_init(&pFull[2 * g + 1], kASoftmaxWarps / 2);
       mbar_init(&oFull[g], 1);
       mbar_init(&oEmpty[g], kASoftmaxWarps / 2);
       mbar_init(&iFull[g], 1);
-      mbar_init(&iEmpty[g], kASoftmaxWarps + 1);
+      mbar_init(&iEmpty[g], kASoftmaxWarps + 2);
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     *sAbort = 0;
     mbar_fence_init();
   }
@@ -478,28 +478,36 @@ __global__ void __launch_bounds__(kAThreads, 1)
     for (int i = 0; i < 2; ++i) mbar_wait_drain(&qFull[i], qPhase[i] & 1, p.status);
     for (int i = 1; i <= kSlots && n - i >= 0; ++i)
       mbar_wait_drain(&full[(n - i) % kSlots], ((n - i) / kSlots) & 1, p.status);
-  } else if (warp == kASoftmaxWarps + 1) {
-    // ---- MMA issue: the whole warp goes through the waits, one elected lane issues ----
+  } else if (warp > kASoftmaxWarps) {
+    // ---- MMA issue, a warp for each group: the whole warp goes through the waits, one elected lane issues ----
+    const uint32_t g = warp - (kASoftmaxWarps + 1);
     const uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0), idesc_pv = idesc_bf16_f32(128, D, 1);
-    uint32_t slot = 0, phase = 0;  // the next ring tile
-    uint32_t pPhase[2] = {0, 0}, oPhase[2] = {1, 1}, qPhase[2] = {0, 0}, q_turn = 0;
+    uint32_t pPhase = 0, oPhase = 1, qPhase[2] = {0, 0}, q_turn = 0;
+    uint32_t ring = 0, passed = 0;  // ring tiles of the items before; tiles whose arrival this warp has seen
     bool stop = false;
     // descriptor words: start addresses in 16-byte units, the rest constant
     const uint32_t q_lo = smem_u32(sQ) >> 4, kv_lo = smem_u32(sKV) >> 4;
     constexpr uint32_t kHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024 B, version 1, 128-byte swizzle
     constexpr uint32_t kTileUnits = S::kTileBytes >> 4, kBoxUnits = S::kBox >> 4;
-    // waits for the next ring tile; its slot
-    auto next_tile = [&]() {
-      if (!warp_wait(&full[slot], phase)) stop = true;
+    // passes the tiles before n, which are not this warp's: waits for each and signs it off
+    auto pass = [&](uint32_t n) {
+      for (; passed < n && !stop; ++passed) {
+        const uint32_t slot = passed % kSlots;
+        if (!warp_wait(&full[slot], (passed / kSlots) & 1)) stop = true;
+        else if (elect_one()) mbar_arrive(&empty[slot]);
+      }
+    };
+    // waits for ring tile n; its slot
+    auto tile = [&](uint32_t n) {
+      pass(n);
+      const uint32_t slot = n % kSlots;
+      if (!stop && !warp_wait(&full[slot], (n / kSlots) & 1)) stop = true;
+      ++passed;
       tc_fence_after();
-      const uint32_t s = slot;
-      if (++slot == kSlots) { slot = 0; phase ^= 1; }
-      return s;
+      return slot;
     };
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) tc_commit(bar);
-    };
-    auto issue_qk = [&](uint32_t g, uint32_t qb, uint32_t s0) {  // S of group g from Q buffer qb
+    // S of the group from Q buffer qb and the K tile in slot s0, which is signed off
+    auto qk = [&](uint32_t qb, uint32_t s0) {
       const uint32_t q = q_lo + qb * kTileUnits, kk = kv_lo + s0 * kTileUnits;
       if (elect_one()) {
 #pragma unroll 1
@@ -508,31 +516,47 @@ __global__ void __launch_bounds__(kAThreads, 1)
           tc_mma_bf16_lo(128u * g, q + off, kHi, kk + off, kHi, idesc_qk, s > 0);
         }
         tc_commit(&sFull[g]);
+        tc_commit(&empty[s0]);
       }
     };
-    // k-steps from..to - 1 of O of group g
-    auto issue_pv = [&](uint32_t g, uint32_t s0, uint32_t from, uint32_t to, bool first) {
+    // `steps` 16-key steps of O += P V from the `from`-th on
+    auto pv_steps = [&](uint32_t s0, uint32_t from, uint32_t steps, bool first) {
       const uint32_t v = (kv_lo + s0 * kTileUnits + 128u * from) | (kBoxUnits << 16);  // MN-major: the leading offset is a box
       const uint32_t d = 256u + 128u * g, a = 128u * g + 8u * from;
       if (elect_one()) {
 #pragma unroll 1
-        for (uint32_t s = 0; s < to - from; ++s) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
+        for (uint32_t s = 0; s < steps; ++s) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
       }
     };
-    // O += P V of group g's tile with `steps` groups of 16 keys, as P arrives (at the group's first tile of an
-    // item, once the epilogue before has read O)
-    auto pv = [&](uint32_t g, uint32_t vs, uint32_t steps, bool first_tile) {
-      if (!warp_wait(&pFull[2 * g], pPhase[g])) return false;
+    // O += P V with the V tile in slot s0 of `keys` keys, as P arrives (at the group's first tile of an item, once the
+    // epilogue before has read O); the tile is signed off, and O is complete with the last tile
+    auto pv = [&](uint32_t s0, uint32_t keys, bool first_tile, bool last_tile) {
+      const uint32_t steps = (keys + 15) >> 4;
+      if (keys & 15) {  // V rows past the keys: their weights are 0, but the rows may hold anything
+        unsigned char* v = sKV + s0 * S::kTileBytes;
+        const uint32_t rows = 16 - (keys & 15);
+        for (uint32_t i = lane; i < rows * 8 * kHalves; i += 32) {
+          const uint32_t c = i / (rows * 8), rest = i - c * rows * 8;
+          *reinterpret_cast<uint4*>(v + c * S::kBox + (keys + rest / 8) * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!warp_wait(&pFull[2 * g], pPhase)) return false;
       if (first_tile) {
-        if (!warp_wait(&oEmpty[g], oPhase[g])) return false;
-        oPhase[g] ^= 1;
+        if (!warp_wait(&oEmpty[g], oPhase)) return false;
+        oPhase ^= 1;
       }
       tc_fence_after();
-      issue_pv(g, vs, 0, min(steps, 4u), first_tile);
-      if (!warp_wait(&pFull[2 * g + 1], pPhase[g])) return false;
-      pPhase[g] ^= 1;
+      pv_steps(s0, 0, min(steps, 4u), first_tile);
+      if (!warp_wait(&pFull[2 * g + 1], pPhase)) return false;
+      pPhase ^= 1;
       tc_fence_after();
-      if (steps > 4) issue_pv(g, vs, 4, steps, false);
+      if (steps > 4) pv_steps(s0, 4, steps - 4, false);
+      if (elect_one()) {
+        tc_commit(&empty[s0]);
+        if (last_tile) tc_commit(&oFull[g]);
+      }
       return true;
     };
     for (int k = 0; !stop; ++k) {
@@ -541,73 +565,57 @@ __global__ void __launch_bounds__(kAThreads, 1)
       const uint32_t n_keys = __reduce_max_sync(0xffffffffu, (uint32_t)it.n_keys);
       const uint32_t halves = __reduce_max_sync(0xffffffffu, it.head & kAlternate ? 0u : 1u);
       if (n_keys == 0) break;
-      const uint32_t nt = (n_keys + kATile - 1) / kATile, last_steps = (n_keys - (nt - 1) * kATile + 15) >> 4;
-      if (halves) {  // both halves of the rows, one after the other on each tile
-        for (uint32_t b = 0; b < 2; ++b) {
+      const uint32_t nt = (n_keys + kATile - 1) / kATile, last_keys = n_keys - (nt - 1) * kATile;
+      if (halves) {  // half g of the rows over every tile: K0 V0 K1 V1 ... in the ring
+        for (uint32_t b = 0; b < 2 && !stop; ++b) {
           if (!warp_wait(&qFull[b], qPhase[b])) stop = true;
           qPhase[b] ^= 1;
         }
         if (stop) break;
-        uint32_t ks = next_tile();
+        if (elect_one()) mbar_arrive(&qEmpty[g ^ 1]);
+        uint32_t s0 = tile(ring);
         if (stop) break;
-        issue_qk(0, 0, ks);
-        issue_qk(1, 1, ks);
-        commit(&empty[ks]);
-        if (nt == 1) { commit(&qEmpty[0]); commit(&qEmpty[1]); }
+        qk(g, s0);
         for (uint32_t j = 0; j < nt; ++j) {
           const bool more = j + 1 < nt;
-          const uint32_t steps = more ? 8 : last_steps, vs = next_tile();
-          if (stop || !pv(0, vs, steps, j == 0)) { stop = true; break; }
+          if (!more && elect_one()) tc_commit(&qEmpty[g]);  // no S is left to form
+          s0 = tile(ring + 2 * j + 1);
+          if (stop || !pv(s0, more ? kATile : last_keys, j == 0, !more)) { stop = true; break; }
           if (more) {
-            ks = next_tile();
+            s0 = tile(ring + 2 * j + 2);
             if (stop) break;
-            issue_qk(0, 0, ks);
-          } else {
-            commit(&oFull[0]);
-          }
-          if (!pv(1, vs, steps, j == 0)) { stop = true; break; }
-          commit(&empty[vs]);
-          if (more) {
-            issue_qk(1, 1, ks);
-            commit(&empty[ks]);
-            if (j + 2 == nt) { commit(&qEmpty[0]); commit(&qEmpty[1]); }
-          } else {
-            commit(&oFull[1]);
+            qk(g, s0);
           }
         }
-      } else {  // even tiles to group 0, odd ones to 1
+      } else {  // tiles g, g + 2, ... of all rows: K0 K1 V0 K2 V1 K3 ... in the ring
         const uint32_t qb = q_turn;
         q_turn ^= 1;
-        if (!warp_wait(&qFull[qb], qPhase[qb])) { stop = true; break; }
+        if (!warp_wait(&qFull[qb], qPhase[qb])) break;
         qPhase[qb] ^= 1;
-        uint32_t ks = next_tile();
-        if (stop) break;
-        issue_qk(0, qb, ks);
-        commit(&empty[ks]);
-        if (nt > 1) {
-          ks = next_tile();
+        if (g < nt) {
+          uint32_t s0 = tile(ring + g);
           if (stop) break;
-          issue_qk(1, qb, ks);
-          commit(&empty[ks]);
-        }
-        if (nt <= 2) commit(&qEmpty[qb]);
-        for (uint32_t j = 0; j < nt; ++j) {
-          const uint32_t g = j & 1, vs = next_tile();
-          if (stop || !pv(g, vs, j + 1 < nt ? 8 : last_steps, j < 2)) { stop = true; break; }
-          commit(&empty[vs]);
-          if (j + 2 < nt) {
-            ks = next_tile();
-            if (stop) break;
-            issue_qk(g, qb, ks);
-            commit(&empty[ks]);
-            if (j + 3 == nt) commit(&qEmpty[qb]);
-          } else {
-            commit(&oFull[g]);
+          qk(qb, s0);
+          for (uint32_t j = g; j < nt; j += 2) {
+            const bool more = j + 2 < nt;
+            if (!more && elect_one()) tc_commit(&qEmpty[qb]);
+            s0 = tile(j + 1 < nt ? ring + 2 + 2 * j : ring + 2 * nt - 1);
+            if (stop || !pv(s0, j + 1 < nt ? kATile : last_keys, j == g, !more)) { stop = true; break; }
+            if (more) {
+              s0 = tile(ring + 2 * j + 3);
+              if (stop) break;
+              qk(qb, s0);
+            }
           }
+        } else if (elect_one()) {
+          mbar_arrive(&qEmpty[qb]);
         }
       }
+      ring += 2 * nt;
+      pass(ring);
     }
-    commit(drain);  // every MMA issued so far has completed
+    if (elect_one()) tc_commit(drain);  // every MMA issued so far by either warp has completed
+    __syncwarp();
     mbar_wait_drain(drain, 0, p.status);
   } else {
     // ---- softmax and epilogue: group g, one thread a row ----
@@ -616,15 +624,12 @@ __global__ void __launch_bounds__(kAThreads, 1)
     const uint32_t tS = tmem + lane_base + 128u * g, tO = tmem + lane_base + 256u + 128u * g;
     const unsigned long long rate2 = f32x2_pack(p.rate, p.rate), one2 = f32x2_pack(1.f, 1.f);
     uint32_t nS = 0, nI = 0;
-    int ring = 0;  // ring tiles of the items before
     bool stop = false;
     for (int k = 0; !stop; ++k) {
       const AttnItem it = take(k);
       if (it.n_keys == 0) break;
       const int nt = ceil_div(it.n_keys, kATile);
       const bool halves = !(it.head & kAlternate);  // else the even tiles of all rows, or the odd ones
-      const int v_last = ring + 2 * nt - 1;  // the ring tile of the last V
-      ring += 2 * nt;
       if (!halves && g >= nt) continue;
       const int tok = (halves ? g * p.TB : 0) + row / p.G;
       const bool valid = row < p.TB * p.G && tok < it.n_tok;
@@ -636,55 +641,33 @@ __global__ void __launch_bounds__(kAThreads, 1)
       for (int j = halves ? 0 : g; j < nt; j += halves ? 1 : 2, ++nS) {
         if (!warp_wait(&sFull[g], nS & 1)) { stop = true; break; }
         tc_fence_after();
-        if (j + 1 == nt && (it.n_keys & 15) && (!halves || g == 0)) {  // V rows past the keys
-          if (!warp_wait(&full[v_last % kSlots], (v_last / kSlots) & 1)) { stop = true; break; }
-          const int first = it.n_keys - j * kATile, rows = 16 - (it.n_keys & 15);
-          unsigned char* v = sKV + (v_last % kSlots) * S::kTileBytes;
-          for (int i = row; i < rows * 8 * kHalves; i += 128) {
-            const int c = i / (rows * 8), rest = i - c * rows * 8;
-            *reinterpret_cast<uint4*>(v + c * S::kBox + (first + rest / 8) * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        }
-        uint32_t a[64], b[64];
-        float neg = 0.f;
-        unsigned long long z2[4] = {0ull, 0ull, 0ull, 0ull};
-        // the weights of 64 keys, into the 32 columns at `to`
-        auto weights = [&](const uint32_t (&x)[64], uint32_t to) {
-          const unsigned long long neg2 = f32x2_pack(neg, neg);
-          uint32_t w[32];
+        // one copy of the code for both column halves: S is read from TMEM twice rather than kept (a body that
+        // is unrolled over the whole row overflows the instruction caches that the MMA and load warps share)
+        const bool masked = (j + 1) * kATile > clear;
+        auto load_half = [&](int h, uint32_t (&x)[64]) {
+          tmem_ld64_nowait(tS + 64u * h, x);
+          tmem_ld_wait64(x);
+          if (masked) {
+            const int left = limit - j * kATile - 64 * h;
 #pragma unroll
-          for (int c = 0; c < 64; c += 2) {
-            float e0, e1;
-            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), rate2, neg2), e0, e1);
-            e0 = ex2_approx(e0);
-            e1 = ex2_approx(e1);
-            z2[(c >> 1) & 3] = f32x2_fma(f32x2_pack(e0, e1), one2, z2[(c >> 1) & 3]);
-            w[c >> 1] = pack_bf16x2(e0, e1);
+            for (int c = 0; c < 64; ++c)
+              if (c >= left) x[c] = 0xff800000u;
           }
-          tmem_st32(to, w);
-          tmem_st_wait();
         };
+        float neg = 0.f;
         if (any) {
-          tmem_ld64_nowait(tS, a);
-          tmem_ld64_nowait(tS + 64u, b);
-          tmem_ld_wait64(a);
-          tmem_ld_wait64(b);
-          if ((j + 1) * kATile > clear) {
-            const int left = limit - j * kATile;
-#pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              if (c >= left) a[c] = 0xff800000u;
-              if (c + 64 >= left) b[c] = 0xff800000u;
-            }
-          }
           float x[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i]));
+          for (int i = 0; i < 8; ++i) x[i] = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t a[64];
+            load_half(h, a);
 #pragma unroll
-          for (int c = 8; c < 64; c += 8)
+            for (int c = 0; c < 64; c += 16)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = max3(x[i], __uint_as_float(a[c + i]), __uint_as_float(b[c + i]));
+              for (int i = 0; i < 8; ++i) x[i] = max3(x[i], __uint_as_float(a[c + i]), __uint_as_float(a[c + 8 + i]));
+          }
           const float top = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])) * p.rate;
           const bool rise = top > m + 8.f || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, rise)) {
@@ -693,6 +676,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             m = mn;
             z *= f;
             if (j > (halves ? 0 : 1))
+#pragma unroll 1
               for (int c = 0; c < D; c += 8) {
                 uint32_t u[8];
                 tmem_ld8(tO + c, u);
@@ -702,21 +686,34 @@ __global__ void __launch_bounds__(kAThreads, 1)
               }
           }
           neg = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet: 2^(-inf) = 0
-          weights(a, tS);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pFull[2 * g]);
-        if (any) {
-          weights(b, tS + 32u);
-          float s0, s1, s2, s3;
-          f32x2_unpack(f32x2_fma(z2[0], one2, z2[1]), s0, s1);
-          f32x2_unpack(f32x2_fma(z2[2], one2, z2[3]), s2, s3);
-          z += (s0 + s1) + (s2 + s3);
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {  // the weights of 64 keys, over the first quarters of S
+          if (any) {
+            uint32_t a[64], w[32];
+            load_half(h, a);
+            const unsigned long long neg2 = f32x2_pack(neg, neg);
+            unsigned long long z2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              float e0, e1;
+              f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(a[c]), __uint_as_float(a[c + 1])), rate2, neg2), e0, e1);
+              e0 = ex2_approx(e0);
+              e1 = ex2_approx(e1);
+              z2[(c >> 1) & 3] = f32x2_fma(f32x2_pack(e0, e1), one2, z2[(c >> 1) & 3]);
+              w[c >> 1] = pack_bf16x2(e0, e1);
+            }
+            tmem_st32(tS + 32u * h, w);
+            float s0, s1, s2, s3;
+            f32x2_unpack(f32x2_fma(z2[0], one2, z2[1]), s0, s1);
+            f32x2_unpack(f32x2_fma(z2[2], one2, z2[3]), s2, s3);
+            z += (s0 + s1) + (s2 + s3);
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pFull[2 * g + h]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pFull[2 * g + 1]);
       }
       if (stop) break;
       if (!warp_wait(&oFull[g], nI & 1)) break;

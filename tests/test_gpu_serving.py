@@ -211,6 +211,9 @@ SHAPES = [
     ([6, 4], [3, 0], 0, 6, 3, 64, 16),                  # more queries than keys: empty rows, then a request with none
     ([6, 4], [3, 0], 5, 6, 3, 128, 16),                 # the same with a prefix
     ([2, 2], [4500, 9], 9000, 8, 2, 64, 16),            # long: split over keys
+    # many more items than SMs, of one to five tiles, a half's rows and two halves' in turn
+    ([1 + i % 3 for i in range(220)], [3 + (i * 37) % 620 for i in range(220)], 300, 32, 8, 64, 16),
+    ([1 + (i * 7) % 40 for i in range(90)], [41 + (i * 53) % 500 for i in range(90)], 130, 16, 4, 128, 32),
 ]
 
 
