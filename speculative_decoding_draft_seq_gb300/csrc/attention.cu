@@ -310,6 +310,15 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return d;
 }
 
+// 32 bytes in one store (32-byte aligned).
+__device__ __forceinline__ void store32(float* to, const float* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(__float_as_uint(v[0])),
+               "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+               "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])),
+               "r"(__float_as_uint(v[7]))
+               : "memory");
+}
+
 template <int D>
 __global__ void __launch_bounds__(kAThreads, 1)
     attn_tiles_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
@@ -580,12 +589,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
           const bool more = j + 1 < nt;
           if (!more && elect_one()) tc_commit(&qEmpty[g]);  // no S is left to form
           s0 = tile(ring + 2 * j + 1);
+          const uint32_t s1 = more ? tile(ring + 2 * j + 2) : 0;  // (seen before P is, not between its MMAs)
           if (stop || !pv(s0, more ? kATile : last_keys, j == 0, !more)) { stop = true; break; }
-          if (more) {
-            s0 = tile(ring + 2 * j + 2);
-            if (stop) break;
-            qk(g, s0);
-          }
+          if (more) qk(g, s1);
         }
       } else {  // tiles g, g + 2, ... of all rows: K0 K1 V0 K2 V1 K3 ... in the ring
         const uint32_t qb = q_turn;
@@ -600,12 +606,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
             const bool more = j + 2 < nt;
             if (!more && elect_one()) tc_commit(&qEmpty[qb]);
             s0 = tile(j + 1 < nt ? ring + 2 + 2 * j : ring + 2 * nt - 1);
+            const uint32_t s1 = more ? tile(ring + 2 * j + 3) : 0;
             if (stop || !pv(s0, j + 1 < nt ? kATile : last_keys, j == g, !more)) { stop = true; break; }
-            if (more) {
-              s0 = tile(ring + 2 * j + 3);
-              if (stop) break;
-              qk(qb, s0);
-            }
+            if (more) qk(qb, s1);
           }
         } else if (elect_one()) {
           mbar_arrive(&qEmpty[qb]);
@@ -723,21 +726,54 @@ __global__ void __launch_bounds__(kAThreads, 1)
         const int hq = (it.head & ~kAlternate) * p.G + row % p.G;
         const size_t t = it.slot0 < 0 ? (size_t)it.tok0 + tok : (size_t)it.slot0 + tok + (!halves && g ? it.n_tok : 0);
         const size_t at = valid ? t * p.Hq + hq : 0;
-        const float inv = z != 0.f ? 1.f / z : 0.f;
+        if (it.slot0 < 0) {
+          const float inv = z != 0.f ? 1.f / z : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            __syncwarp();
+            tmem_ld32(tO + c, o);
+            if (valid) {
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          __syncwarp();
-          tmem_ld32(tO + c, o);
-          if (valid && it.slot0 < 0) {
+              for (int i = 0; i < 32; ++i) o[i] *= inv;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= inv;
+              for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(p.out + at * D + c + i) = pack_bf16x8(o + i);
+            }
+          }
+        } else {
+          // Four lanes trade 32-byte pieces of their rows, so that each store of theirs covers 128 bytes of one row: a
+          // lane that wrote its own row took a cache line a store (8,000 cycles an item of 256 rows)
+          const int i4 = lane & 3;
+          size_t to[4];
+          uint32_t have = 0;
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) *reinterpret_cast<uint4*>(p.out + at * D + c + i) = pack_bf16x8(o + i);
-          } else if (valid) {
+          for (int r = 0; r < 4; ++r) {
+            to[r] = __shfl_sync(0xffffffffu, (unsigned long long)at, (lane & ~3) + r);
+            have |= (__shfl_sync(0xffffffffu, valid, (lane & ~3) + r) ? 1u : 0u) << r;
+          }
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            __syncwarp();
+            tmem_ld32(tO + c, o);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(p.acc + at * D + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int step = 1; step <= 2; step <<= 1) {
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                if (u & step) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {  // pieces u and u + step of lanes that differ in `step`
+                  float& lo = o[8 * u + e];
+                  float& hi = o[8 * (u | step) + e];
+                  const float got = __shfl_xor_sync(0xffffffffu, i4 & step ? lo : hi, step);
+                  if (i4 & step) lo = got;
+                  else hi = got;
+                }
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if ((have >> r) & 1u) store32(p.acc + to[r] * D + c + 8 * i4, o + 8 * r);
           }
         }
         if (valid) {
