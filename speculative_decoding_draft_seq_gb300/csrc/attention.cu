@@ -119,36 +119,54 @@ inline AttnLayout attn_layout(int R, int T, int Hq, int Hkv, int D) {
   return L;
 }
 
+// Waits until the launch before this one in the stream is complete and its writes are visible; lets the launch
+// after this one be set up (it waits in turn).
+__device__ __forceinline__ void wait_for_launch_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // The plan. Request r's queries are cut into blocks of two halves; block b of
 // n tokens sees the first kv_len - n + (its last token) + 1 private keys.
-constexpr int kAPlanThreads = 1024;
+constexpr int kAPlanThreads = 1024;  // at most; a thread a request
 
-__device__ __forceinline__ long long scan_ll(long long v, long long* sh, long long& total) {  // exclusive
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  long long x = v;
+__device__ __forceinline__ long long plan_sum(long long v, long long* sh) {  // over the block
+  const int nw = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0;
+  for (int i = 0; i < nw; ++i) v += sh[i];
+  return v;
+}
+__device__ __forceinline__ longlong2 plan_scan(longlong2 v, longlong2* sh, longlong2& total) {  // exclusive, over the block
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+  longlong2 x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const long long a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
+    if (lane >= o) { x.x += a; x.y += b; }
   }
   __syncthreads();
   if (lane == 31) sh[w] = x;
   __syncthreads();
-  long long s = sh[lane];  // 32 warps
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += y;
+  longlong2 before = make_longlong2(0, 0);
+  total = before;
+  for (int i = 0; i < nw; ++i) {
+    const longlong2 s = sh[i];
+    if (i < w) { before.x += s.x; before.y += s.y; }
+    total.x += s.x;
+    total.y += s.y;
   }
-  total = __shfl_sync(0xffffffffu, s, 31);
-  const long long before = __shfl_sync(0xffffffffu, s, w > 0 ? w - 1 : 0);
-  return x - v + (w > 0 ? before : 0ll);
+  return make_longlong2(before.x + x.x - v.x, before.y + x.y - v.y);
 }
 
 __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams p) {
   __shared__ long long sh[32];
-  const int tid = threadIdx.x;
+  __shared__ longlong2 sh2[32];
+  const int tid = threadIdx.x, nthr = blockDim.x;
+  let_next_launch();
   const int step = 2 * p.TB;  // tokens a block
   bool bad = false;
   auto request = [&](int r, int& start, int& n, int& len) {
@@ -164,7 +182,7 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
   };
   // starts that fall or leave [0, T]: their blocks would not be bounded by T, so nothing is computed
   bool broken = tid == 0 && __ldg(p.q_start) != 0;
-  for (int r = tid; r < p.R; r += kAPlanThreads) {
+  for (int r = tid; r < p.R; r += nthr) {
     const int a = __ldg(p.q_start + r), b = __ldg(p.q_start + r + 1);
     broken |= a < 0 || b < a || b > p.T;
   }
@@ -179,39 +197,42 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
   // how `tiles` key tiles of a block of `nt` tokens are split into items, and the parts that they leave
   auto splits_of = [&](int tiles, int nt, long long share) {
     const int ns = ceil_div(tiles, share);
-    return nt <= p.TB ? max(min(ns, tiles / 2), min(tiles, 1)) : ns;  // two tiles at least for the two warpgroups
+    return nt <= p.TB ? max(min(ns, tiles / 2), min(tiles, 1)) : ns;  // two tiles at least for the two groups
   };
   auto parts_of = [&](int tiles, int nt, int ns) { return nt <= p.TB && tiles > 1 ? 2 * ns : ns; };
   const int p_tiles = ceil_div(p.prefix_len, kATile), p_blocks = ceil_div(n_tokens, step);
   long long units = 0;
-  for (int r = tid; r < p.R; r += kAPlanThreads) {
+  for (int r = tid; r < p.R; r += nthr) {
     int start, n, len;
     request(r, start, n, len);
     for (int t0 = 0; t0 < n; t0 += step) units += tiles_of(n, len, t0);
   }
-  long long total;
-  scan_ll(units, sh, total);
-  total = (total + (long long)p_blocks * p_tiles) * p.Hkv;
+  const long long total = (plan_sum(units, sh) + (long long)p_blocks * p_tiles) * p.Hkv;
   long long share = max(1ll, (total + (long long)p.sms * kPlanShare - 1) / ((long long)p.sms * kPlanShare));
+  // page items of at least half a share come first, then the smaller ones
+  auto small = [&](int tiles, int ns) { return 2ll * tiles < share * ns; };
   int p_splits, p_parts;
+  long long all_large;
   for (;;) {  // tiles an item: more where the parts would not fit
     p_splits = splits_of(p_tiles, n_tokens, share);
     p_parts = parts_of(p_tiles, n_tokens, p_splits);
-    long long slots = 0, all;
-    for (int r = tid; r < p.R; r += kAPlanThreads) {
+    long long slots = 0, larges = 0;  // (each below 2^31: summed in one word)
+    for (int r = tid; r < p.R; r += nthr) {
       int start, n, len;
       request(r, start, n, len);
       for (int t0 = 0; t0 < n; t0 += step) {
-        const int tiles = tiles_of(n, len, t0), nt = min(step, n - t0);
-        slots += (long long)parts_of(tiles, nt, splits_of(tiles, nt, share)) * nt;
+        const int tiles = tiles_of(n, len, t0), nt = min(step, n - t0), ns = splits_of(tiles, nt, share);
+        slots += (long long)parts_of(tiles, nt, ns) * nt;
+        if (!small(tiles, ns)) larges += (long long)ns * p.Hkv;
       }
     }
-    scan_ll(slots, sh, all);
-    if (all + (long long)p_parts * n_tokens <= p.cap_slots || share > (1 << 30)) break;
+    slots = plan_sum(slots, sh);
+    all_large = plan_sum(larges, sh);
+    if (slots + (long long)p_parts * n_tokens <= p.cap_slots || share > (1 << 30)) break;
     share *= 2;
   }
   const long long p_items = (long long)p_blocks * p.Hkv * p_splits;
-  for (long long i = tid; i < p_items; i += kAPlanThreads) {  // blocks that read the same keys next to one another
+  for (long long i = tid; i < p_items; i += nthr) {  // blocks that read the same keys next to one another
     const int b = (int)(i % p_blocks), s = (int)((i / p_blocks) % p_splits), h = (int)(i / p_blocks / p_splits);
     const int a = (int)((long long)s * p_tiles / p_splits), e = (int)((long long)(s + 1) * p_tiles / p_splits);
     AttnItem it;
@@ -225,21 +246,8 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
     it.pos0 = it.n_keys;
     p.items[i] = it;
   }
-  // page items of at least half a share first, then the smaller ones
-  auto small = [&](int tiles, int ns) { return 2ll * tiles < share * ns; };
-  long long n_large = 0;
-  for (int r = tid; r < p.R; r += kAPlanThreads) {
-    int start, n, len;
-    request(r, start, n, len);
-    for (int t0 = 0; t0 < n; t0 += step) {
-      const int tiles = tiles_of(n, len, t0), ns = splits_of(tiles, min(step, n - t0), share);
-      if (!small(tiles, ns)) n_large += (long long)ns * p.Hkv;
-    }
-  }
-  long long all_large;
-  scan_ll(n_large, sh, all_large);
   long long large0 = p_items, small0 = p_items + all_large, slot0 = (long long)p_parts * n_tokens;
-  for (int r0 = 0; r0 < p.R; r0 += kAPlanThreads) {
+  for (int r0 = 0; r0 < p.R; r0 += nthr) {
     const int r = r0 + tid;
     int start = 0, n = 0, len = 0;
     if (r < p.R) request(r, start, n, len);
@@ -249,12 +257,12 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
       (small(tiles, ns) ? smalls : larges) += (long long)ns * p.Hkv;
       slots += (long long)parts_of(tiles, nt, ns) * nt;
     }
-    long long n_l, n_s, n_slots;
-    long long large_at = large0 + scan_ll(larges, sh, n_l), small_at = small0 + scan_ll(smalls, sh, n_s);
-    long long slot = slot0 + scan_ll(slots, sh, n_slots);
-    large0 += n_l;
-    small0 += n_s;
-    slot0 += n_slots;
+    longlong2 all;
+    const longlong2 at = plan_scan(make_longlong2(larges | smalls << 32, slots), sh2, all);
+    long long large_at = large0 + (at.x & 0xffffffffll), small_at = small0 + (at.x >> 32), slot = slot0 + at.y;
+    large0 += all.x & 0xffffffffll;
+    small0 += all.x >> 32;
+    slot0 += all.y;
     for (int t0 = 0; t0 < n; t0 += step) {
       const int tiles = tiles_of(n, len, t0), nt = min(step, n - t0), ns = splits_of(tiles, nt, share);
       const int parts = parts_of(tiles, nt, ns);
@@ -281,13 +289,12 @@ __global__ void __launch_bounds__(kAPlanThreads, 1) attn_plan_kernel(AttnParams 
       slot += (long long)parts * nt;
     }
   }
-  const long long item_end = small0;
   if (tid == 0) {
-    p.head->n_items = (int)item_end;
+    p.head->n_items = (int)small0;
     p.head->prefix_items = (int)p_items;
-    p.head->next = 0;
     p.head->prefix_parts = p_parts;
     p.head->n_tokens = n_tokens;
+    p.head->next = 0;
   }
   if (bad) set_status(p.status, DSPARK_ERR_RANGE);
 }
@@ -376,6 +383,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *sTmem;  // 0: all 512 columns are this CTA's
+  wait_for_launch_before();      // (the set-up above runs under the plan)
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, sAbort, p.status)) != 0;
   };
@@ -417,7 +425,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
       }
       item = __shfl_sync(0xffffffffu, item, 0);
       int4 half = make_int4(0, 0, 0, 0);  // lanes 0 and 1: the item's two halves
-      if (item >= 0 && lane < 2) half = __ldg(reinterpret_cast<const int4*>(p.items + item) + lane);
+      if (item >= 0 && lane < 2) half = __ldcg(reinterpret_cast<const int4*>(p.items + item) + lane);
       if (!warp_wait(&iEmpty[k & 1], ((k >> 1) & 1) ^ 1)) break;
       if (lane < 2) sItem[2 * (k & 1) + lane] = half;
       __syncwarp();
@@ -483,6 +491,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         pgs[1] = pgs[2];
       }
     }
+    let_next_launch();
     // no copy outlives the CTA: the last kSlots ring tiles and the last Q
     for (int i = 0; i < 2; ++i) mbar_wait_drain(&qFull[i], qPhase[i] & 1, p.status);
     for (int i = 1; i <= kSlots && n - i >= 0; ++i)
@@ -644,34 +653,36 @@ __global__ void __launch_bounds__(kAThreads, 1)
       for (int j = halves ? 0 : g; j < nt; j += halves ? 1 : 2, ++nS) {
         if (!warp_wait(&sFull[g], nS & 1)) { stop = true; break; }
         tc_fence_after();
-        // one copy of the code for both column halves: S is read from TMEM twice rather than kept (a body that
-        // is unrolled over the whole row overflows the instruction caches that the MMA and load warps share)
-        const bool masked = (j + 1) * kATile > clear;
-        auto load_half = [&](int h, uint32_t (&x)[64]) {
-          tmem_ld64_nowait(tS + 64u * h, x);
-          tmem_ld_wait64(x);
-          if (masked) {
-            const int left = limit - j * kATile - 64 * h;
+        // Short loops over pieces of S, read from TMEM twice: what is unrolled further overflows the instruction
+        // caches, for which the softmax, MMA and load warps compete.
+        if (any && (j + 1) * kATile > clear) {  // scores of keys that the row does not see: -inf, in TMEM
+          const int left = limit - j * kATile;
+#pragma unroll 1
+          for (int c = 0; c < kATile; c += 8) {
+            uint32_t u[8];
+            tmem_ld8(tS + c, u);
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c >= left) x[c] = 0xff800000u;
+            for (int i = 0; i < 8; ++i) u[i] = c + i < left ? u[i] : 0xff800000u;
+            tmem_st8(tS + c, u);
           }
-        };
+          tmem_st_wait();
+        }
         float neg = 0.f;
         if (any) {
-          float x[8];
+          float x[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = -INFINITY;
+          for (int i = 0; i < 4; ++i) x[i] = -INFINITY;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t a[64];
-            load_half(h, a);
+          for (int c = 0; c < kATile; c += 64) {
+            uint32_t s[64];
+            tmem_ld64_nowait(tS + c, s);
+            tmem_ld_wait64(s);
 #pragma unroll
-            for (int c = 0; c < 64; c += 16)
+            for (int i = 0; i < 64; i += 8)
 #pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = max3(x[i], __uint_as_float(a[c + i]), __uint_as_float(a[c + 8 + i]));
+              for (int e = 0; e < 4; ++e) x[e] = max3(x[e], __uint_as_float(s[i + e]), __uint_as_float(s[i + 4 + e]));
           }
-          const float top = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])) * p.rate;
+          const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.rate;
           const bool rise = top > m + 8.f || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, rise)) {
             const float mn = rise ? top : m;
@@ -690,32 +701,37 @@ __global__ void __launch_bounds__(kAThreads, 1)
           }
           neg = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet: 2^(-inf) = 0
         }
+        const unsigned long long neg2 = f32x2_pack(neg, neg);
+        unsigned long long z2[2] = {0ull, 0ull};
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {  // the weights of 64 keys, over the first quarters of S
+        for (int c0 = 0; c0 < kATile; c0 += 64) {  // the weights of 64 keys, over columns of S that have been read
           if (any) {
-            uint32_t a[64], w[32];
-            load_half(h, a);
-            const unsigned long long neg2 = f32x2_pack(neg, neg);
-            unsigned long long z2[4] = {0ull, 0ull, 0ull, 0ull};
+            uint32_t s[64], w[64 / 2];
+            tmem_ld64_nowait(tS + c0, s);
+            tmem_ld_wait64(s);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
               float e0, e1;
-              f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(a[c]), __uint_as_float(a[c + 1])), rate2, neg2), e0, e1);
+              f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), rate2, neg2), e0, e1);
               e0 = ex2_approx(e0);
               e1 = ex2_approx(e1);
-              z2[(c >> 1) & 3] = f32x2_fma(f32x2_pack(e0, e1), one2, z2[(c >> 1) & 3]);
+              z2[(c >> 1) & 1] = f32x2_fma(f32x2_pack(e0, e1), one2, z2[(c >> 1) & 1]);
               w[c >> 1] = pack_bf16x2(e0, e1);
             }
-            tmem_st32(tS + 32u * h, w);
-            float s0, s1, s2, s3;
-            f32x2_unpack(f32x2_fma(z2[0], one2, z2[1]), s0, s1);
-            f32x2_unpack(f32x2_fma(z2[2], one2, z2[3]), s2, s3);
-            z += (s0 + s1) + (s2 + s3);
-            tmem_st_wait();
+            tmem_st32(tS + c0 / 2, w);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&pFull[2 * g + h]);
+          if (((c0 + 64) & 63) == 0) {  // 64 keys are done
+            if (any) tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pFull[2 * g + (c0 >> 6)]);
+          }
+        }
+        if (any) {
+          float s0, s1, s2, s3;
+          f32x2_unpack(z2[0], s0, s1);
+          f32x2_unpack(z2[1], s2, s3);
+          z += (s0 + s1) + (s2 + s3);
         }
       }
       if (stop) break;
@@ -802,10 +818,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  wait_for_launch_before();
   const int np = p.head->prefix_parts;
   if (row >= (long long)p.head->n_tokens * p.Hq) return;
   const int t = (int)(row / p.Hq), hq = (int)(row % p.Hq);
-  const int4 map = __ldg(p.tokens + t);
+  const int4 map = __ldcg(p.tokens + t);
   if (map.z < 0) return;
   const int n = np + map.z, n_tokens = p.head->n_tokens;
   auto slot = [&](int i) {
@@ -813,7 +830,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
   };
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) {
-    const float2 s = p.stat[slot(i)];
+    const float2 s = __ldcg(p.stat + slot(i));
     if (s.y != 0.f) M = fmaxf(M, s.x);
   }
   M = warp_max(M);
@@ -822,11 +839,17 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const size_t at = slot(i);
-      const float2 s = p.stat[at];
-      if (s.y == 0.f) continue;
-      const float f = ex2_approx(s.x - M);
+      const float2 s = __ldcg(p.stat + at);
+      float a[E];
+      if (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.acc + at * D) + lane);
+        a[0] = v.x; a[1] = v.y; a[2 % E] = v.z; a[3 % E] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.acc + at * D) + lane);
+        a[0] = v.x; a[1] = v.y;
+      }
+      const float f = s.y == 0.f ? 0.f : ex2_approx(s.x - M);  // (a part without keys has z = 0 and o = 0)
       Z = fmaf(s.y, f, Z);
-      const float* a = p.acc + at * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = fmaf(a[e], f, o[e]);
     }
@@ -844,9 +867,24 @@ static cudaError_t launch_attention(const AttnParams& p, const CUtensorMap& mq, 
   static std::atomic<unsigned long long> attr{0};
   cudaError_t e = set_smem_limit_once((const void*)attn_tiles_kernel<D>, (int)AttnSmem<D>::kTotal, attr);
   if (e != cudaSuccess) return e;
-  attn_plan_kernel<<<1, kAPlanThreads, 0, s>>>(p);
-  attn_tiles_kernel<D><<<p.sms, kAThreads, AttnSmem<D>::kTotal, s>>>(mq, mk, mv, p, q_rows, box_rows);
-  attn_join_kernel<D><<<ceil_div((long long)p.T * p.Hq, 8), 256, 0, s>>>(p);
+  attn_plan_kernel<<<1, std::min(kAPlanThreads, std::max(128, (p.R + 31) & ~31)), 0, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // the next two may be set up before the one before has ended
+  cudaLaunchAttribute early;
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(p.sms);
+  cfg.blockDim = dim3(kAThreads);
+  cfg.dynamicSmemBytes = AttnSmem<D>::kTotal;
+  if ((e = cudaLaunchKernelEx(&cfg, attn_tiles_kernel<D>, mq, mk, mv, p, q_rows, box_rows)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(ceil_div((long long)p.T * p.Hq, 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  if ((e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p)) != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
