@@ -70,24 +70,48 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
     tok += n;
     pg += missing(c, n);
   }
-  tok = block_sum_ll(tok, sh);
-  pg = block_sum_ll(pg, sh);
-  if (tid < nr) {
-    int c, n;
-    lengths(r0 + tid, c, n);
-    s_c[tid] = c;
-    s_have[tid] = (int)(((long long)c + p.page - 1) / p.page);
-    s_tok[tid + 1] = n;
-    s_pg[tid + 1] = missing(c, n);
-    const long long end = (long long)c + n;
-    bad |= end > 0x7fffffffll;
-    p.kv_len[r0 + tid] = (int)min(end, 0x7fffffffll);
+  if (r0 > 0) {
+    tok = block_sum_ll(tok, sh);
+    pg = block_sum_ll(pg, sh);
+  }
+  if (tid < kPlanReqs) {  // this CTA's requests: running sums over four warps
+    int c = 0, n = 0;
+    long long miss = 0;
+    if (tid < nr) {
+      lengths(r0 + tid, c, n);
+      miss = missing(c, n);
+      s_c[tid] = c;
+      s_have[tid] = (int)(((long long)c + p.page - 1) / p.page);
+      const long long end = (long long)c + n;
+      bad |= end > 0x7fffffffll;
+      p.kv_len[r0 + tid] = (int)min(end, 0x7fffffffll);
+    }
+    long long a = n, b = miss;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+      if ((tid & 31) >= o) { a += x; b += y; }
+    }
+    s_tok[tid + 1] = a;
+    s_pg[tid + 1] = b;
   }
   __syncthreads();
-  if (tid == 0) {
-    s_tok[0] = tok;
-    s_pg[0] = pg;
-    for (int i = 0; i < nr; ++i) { s_tok[i + 1] += s_tok[i]; s_pg[i + 1] += s_pg[i]; }
+  if (tid < kPlanReqs) {
+    long long a = tok + s_tok[tid + 1], b = pg + s_pg[tid + 1];
+    for (int w = 0; w < (tid >> 5); ++w) { a += s_tok[32 * w + 32]; b += s_pg[32 * w + 32]; }
+    tok = a;  // (held back until every thread has read the warps' sums)
+    pg = b;
+  }
+  __syncthreads();
+  if (tid < kPlanReqs) {
+    s_tok[tid + 1] = tok;
+    s_pg[tid + 1] = pg;
+    if (tid == 0) {
+      int c, n;
+      lengths(r0, c, n);
+      s_tok[0] = tok - n;
+      s_pg[0] = pg - missing(c, n);
+    }
   }
   __syncthreads();
   // new entries of the block table: -1 where the list has run out

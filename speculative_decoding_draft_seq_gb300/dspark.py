@@ -298,10 +298,31 @@ def copy_scheduled_rows(host_target, device_target, host_sched_len, stream=None)
            "dspark_copy_scheduled_rows")
 
 
-def _shape(t, *want, name):
-    """Refuses a tensor whose shape is not `want` (None: any size)."""
-    if len(t.shape) != len(want) or any(w is not None and w != n for n, w in zip(t.shape, want)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('any' if w is None else w for w in want)}")
+# Calls of a serving step are short: these helpers do what _ptr and _stream do with fewer Python steps.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current_raw_stream is not None:
+        return _current_raw_stream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _addr(t, dtype):
+    """Device address of a dense CUDA tensor of this type; refuses what _ptr refuses."""
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, dtype).value
+
+
+def _shapes(**named):
+    """Refuses tensors whose shape is not the one given: name=(tensor, shape), None for any size."""
+    for name, (t, want) in named.items():
+        if len(t.shape) != len(want) or any(w is not None and w != n for n, w in zip(t.shape, want)):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
+                             f"{tuple('any' if w is None else w for w in want)}")
 
 
 def page_plan(cached_len, new_len, free_pages, page_size, block_table, q_start, kv_len, positions, slots, used, ws,
@@ -310,30 +331,34 @@ def page_plan(cached_len, new_len, free_pages, page_size, block_table, q_start, 
     [R, max_pages] from free_pages, and q_start [R+1], kv_len [R], positions and slots [capacity]
     (int32, int64) and used [1]."""
     R, max_pages = block_table.shape
-    _shape(cached_len, R, name="cached_len")
-    _shape(new_len, R, name="new_len")
-    _shape(q_start, R + 1, name="q_start")
-    _shape(kv_len, R, name="kv_len")
-    _shape(slots, positions.numel(), name="slots")
-    _check(lib.dspark_page_plan(R, int(page_size), max_pages, free_pages.numel(), positions.numel(),
-                                _ptr(cached_len, _I32), _ptr(new_len, _I32), _ptr(free_pages, _I32),
-                                _ptr(block_table, _I32), _ptr(q_start, _I32), _ptr(kv_len, _I32),
-                                _ptr(positions, _I32), _ptr(slots, _I64), _ptr(used, _I32), _ptr(ws, _U8), ws.numel(),
-                                _stream(stream)), "dspark_page_plan")
+    capacity = positions.numel()
+    if (cached_len.shape != (R,) or new_len.shape != (R,) or q_start.shape != (R + 1,) or kv_len.shape != (R,) or
+            slots.shape != (capacity,) or used.numel() < 1):
+        _shapes(cached_len=(cached_len, (R,)), new_len=(new_len, (R,)), q_start=(q_start, (R + 1,)),
+                kv_len=(kv_len, (R,)), slots=(slots, (capacity,)), used=(used, (1,)))
+    status = lib.dspark_page_plan(R, page_size, max_pages, free_pages.numel(), capacity, _addr(cached_len, _I32),
+                                  _addr(new_len, _I32), _addr(free_pages, _I32), _addr(block_table, _I32),
+                                  _addr(q_start, _I32), _addr(kv_len, _I32), _addr(positions, _I32),
+                                  _addr(slots, _I64), _addr(used, _I32), _addr(ws, _U8), ws.numel(),
+                                  _raw_stream(stream))
+    if status:
+        _check(status, "dspark_page_plan")
 
 
 def kv_append(k, v, slots, k_cache, v_cache, ws, stream=None):
     """k_cache[slots[t]] = k[t] and the same for v: k, v [T, Hkv, D], caches
     [pages, page_size, Hkv, D] (any leading dimensions), slots [T] int64; negative slots are skipped."""
     T, Hkv, D = k.shape
-    _shape(v, T, Hkv, D, name="v")
-    _shape(slots, T, name="slots")
-    if k_cache.shape != v_cache.shape or k_cache.shape[-2:] != k.shape[-2:]:
+    if v.shape != (T, Hkv, D) or slots.shape != (T,):
+        _shapes(v=(v, (T, Hkv, D)), slots=(slots, (T,)))
+    if k_cache.shape != v_cache.shape or k_cache.shape[-2:] != (Hkv, D):
         raise ValueError("k_cache and v_cache must have one shape that ends in (Hkv, D)")
     dt = k.dtype
-    _check(lib.dspark_kv_append(T, Hkv, D, _dtype_code(k), _ptr(k), _ptr(v, dt), _ptr(slots, _I64),
-                                k_cache.numel() // (Hkv * D), _ptr(k_cache, dt), _ptr(v_cache, dt), _ptr(ws, _U8),
-                                ws.numel(), _stream(stream)), "dspark_kv_append")
+    status = lib.dspark_kv_append(T, Hkv, D, _dtype_code(k), _addr(k, dt), _addr(v, dt), _addr(slots, _I64),
+                                  k_cache.numel() // (Hkv * D), _addr(k_cache, dt), _addr(v_cache, dt),
+                                  _addr(ws, _U8), ws.numel(), _raw_stream(stream))
+    if status:
+        _check(status, "dspark_kv_append")
 
 
 def attention_workspace_bytes(R, T, Hq, Hkv, D):
@@ -355,49 +380,54 @@ def prefix_attention(q, k_cache, v_cache, prefix_pages, prefix_len, block_table,
     [n_pages, page_size, Hkv, D], block_table [R, max_pages]); writes out like q and, unless None,
     lse [T, Hq] float32."""
     T, Hq, D = q.shape
-    n_pages, page, Hkv = k_cache.shape[:3]
+    n_pages, page, Hkv, Dk = k_cache.shape
     R, max_pages = block_table.shape
-    _shape(k_cache, None, None, None, D, name="k_cache")
-    _shape(v_cache, *k_cache.shape, name="v_cache")
-    _shape(out, T, Hq, D, name="out")
-    _shape(q_start, R + 1, name="q_start")
-    _shape(kv_len, R, name="kv_len")
-    if lse is not None:
-        _shape(lse, T, Hq, name="lse")
+    if (Dk != D or v_cache.shape != k_cache.shape or out.shape != q.shape or q_start.shape != (R + 1,) or
+            kv_len.shape != (R,) or (lse is not None and lse.shape != (T, Hq))):
+        _shapes(k_cache=(k_cache, (None, None, None, D)), v_cache=(v_cache, tuple(k_cache.shape)),
+                out=(out, (T, Hq, D)), q_start=(q_start, (R + 1,)), kv_len=(kv_len, (R,)),
+                **({} if lse is None else {"lse": (lse, (T, Hq))}))
     if prefix_len > 0 and prefix_pages.numel() * page < prefix_len:
         raise ValueError("prefix_pages does not cover prefix_len")
-    _check(lib.dspark_prefix_attention(R, T, Hq, Hkv, D, page, n_pages, max_pages, int(prefix_len), _ptr(q, _BF16),
-                                       _ptr(k_cache, _BF16), _ptr(v_cache, _BF16),
-                                       _ptr(prefix_pages, _I32) if prefix_len > 0 else None, _ptr(block_table, _I32),
-                                       _ptr(q_start, _I32), _ptr(kv_len, _I32), float(scale), _ptr(out, _BF16),
-                                       _ptr(lse, _F32), _ptr(ws, _U8), ws.numel(), _stream(stream)),
-           "dspark_prefix_attention")
+    status = lib.dspark_prefix_attention(R, T, Hq, Hkv, D, page, n_pages, max_pages, prefix_len, _addr(q, _BF16),
+                                         _addr(k_cache, _BF16), _addr(v_cache, _BF16),
+                                         _addr(prefix_pages, _I32) if prefix_len > 0 else None,
+                                         _addr(block_table, _I32), _addr(q_start, _I32), _addr(kv_len, _I32), scale,
+                                         _addr(out, _BF16), None if lse is None else _addr(lse, _F32), _addr(ws, _U8),
+                                         ws.numel(), _raw_stream(stream))
+    if status:
+        _check(status, "dspark_prefix_attention")
 
 
 def _rule(logits, temperature, top_k, top_p, min_p):
     N, V = logits.shape
-    for t, name in ((temperature, "temperature"), (top_k, "top_k"), (top_p, "top_p"), (min_p, "min_p")):
-        _shape(t, N, name=name)
-    return (N, V, _dtype_code(logits), _ptr(logits), _ptr(temperature, _F32), _ptr(top_k, _I32), _ptr(top_p, _F32),
-            _ptr(min_p, _F32))
+    if temperature.shape != (N,) or top_k.shape != (N,) or top_p.shape != (N,) or min_p.shape != (N,):
+        _shapes(temperature=(temperature, (N,)), top_k=(top_k, (N,)), top_p=(top_p, (N,)), min_p=(min_p, (N,)))
+    return (N, V, _dtype_code(logits), _addr(logits, logits.dtype), _addr(temperature, _F32), _addr(top_k, _I32),
+            _addr(top_p, _F32), _addr(min_p, _F32))
 
 
 def sample(logits, temperature, top_k, top_p, min_p, u, tokens, ws, prob=None, stream=None):
     """One token a row of logits [N, V] by temperature, top-k, top-p and min-p (one of each a row)
     from the uniforms u [N] float64; tokens [N] int32, prob [N] float32 or None."""
-    _shape(u, logits.shape[0], name="u")
-    _shape(tokens, logits.shape[0], name="tokens")
-    if prob is not None:
-        _shape(prob, logits.shape[0], name="prob")
-    _check(lib.dspark_sample(*_rule(logits, temperature, top_k, top_p, min_p), _ptr(u, _F64), _ptr(tokens, _I32),
-                             _ptr(prob, _F32), _ptr(ws, _U8), ws.numel(), _stream(stream)), "dspark_sample")
+    rule = _rule(logits, temperature, top_k, top_p, min_p)
+    N = rule[0]
+    if u.shape != (N,) or tokens.shape != (N,) or (prob is not None and prob.shape != (N,)):
+        _shapes(u=(u, (N,)), tokens=(tokens, (N,)), **({} if prob is None else {"prob": (prob, (N,))}))
+    status = lib.dspark_sample(*rule, _addr(u, _F64), _addr(tokens, _I32), None if prob is None else _addr(prob, _F32),
+                               _addr(ws, _U8), ws.numel(), _raw_stream(stream))
+    if status:
+        _check(status, "dspark_sample")
 
 
 def truncate(logits, temperature, top_k, top_p, min_p, out, ws, stream=None):
     """out [N, V]: logits with every entry outside the rule's kept set at the type's lowest value."""
-    _shape(out, *logits.shape, name="out")
-    _check(lib.dspark_truncate(*_rule(logits, temperature, top_k, top_p, min_p), _ptr(out, logits.dtype), _ptr(ws, _U8),
-                               ws.numel(), _stream(stream)), "dspark_truncate")
+    rule = _rule(logits, temperature, top_k, top_p, min_p)
+    if out.shape != logits.shape:
+        _shapes(out=(out, tuple(logits.shape)))
+    status = lib.dspark_truncate(*rule, _addr(out, logits.dtype), _addr(ws, _U8), ws.numel(), _raw_stream(stream))
+    if status:
+        _check(status, "dspark_truncate")
 
 
 def wait_selftest(which, ws, stream=None):
