@@ -129,18 +129,21 @@ struct MassPair {  // the two halves of two masses, above the bits of 8
   }
 };
 struct MassSum {
-  static constexpr uint32_t kBits = 0x7fffffu;
-  uint32_t hi = 0, lo = 0;
+  uint32_t hi = 0, lo = 0, n = 0;  // n of the masses were added with the bits of 8
   __device__ __forceinline__ void add(const MassPair& m) {
-    hi += (m.hi[0] & kBits) + (m.hi[1] & kBits);
-    lo += (m.lo[0] & kBits) + (m.lo[1] & kBits);
+    hi += m.hi[0] + m.hi[1];
+    lo += m.lo[0] + m.lo[1];
+    n += 2;
   }
   __device__ __forceinline__ void add_if(const MassPair& m, bool p0, bool p1) {
-    const uint32_t k0 = p0 ? kBits : 0u, k1 = p1 ? kBits : 0u;
+    const uint32_t k0 = p0 ? 0x7fffffu : 0u, k1 = p1 ? 0x7fffffu : 0u;
     hi += (m.hi[0] & k0) + (m.hi[1] & k1);
     lo += (m.lo[0] & k0) + (m.lo[1] & k1);
   }
-  __device__ __forceinline__ unsigned long long total() const { return ((unsigned long long)hi << 20) + lo; }
+  __device__ __forceinline__ unsigned long long total() const {
+    const uint32_t eights = n * 0x41000000u;
+    return ((unsigned long long)(hi - eights) << 20) + (lo - eights);
+  }
 };
 
 __device__ __forceinline__ unsigned long long block_sum_u64(unsigned long long v, unsigned long long* sh) {
