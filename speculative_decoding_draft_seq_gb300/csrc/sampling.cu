@@ -653,12 +653,14 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
             head = move == 0 && cum_c[jb] <= kSList / 2;
           }
           float lo = logit_at((float)(jb + 1)), hi = head ? INFINITY : logit_at((float)ja);
-          if (move > 0) {  // no entry of the range before is in this one
+          // no entry of the range before is in this one, and it reaches a bin further (more at a later attempt)
+          const float reach = 1.5f * (float)attempt / bins.c;
+          if (move > 0) {
             hi = fminf(hi, key_logit(logit_key(r_lo) - 1));
-            lo = fminf(lo, hi);
+            lo = fminf(lo, r_lo - reach);
           } else if (move < 0) {
             lo = fmaxf(lo, key_logit(logit_key(r_hi) + 1));
-            hi = fmaxf(lo, hi);
+            hi = fmaxf(hi, r_hi + reach);
           }
           if (tid == 0) {
             shf[0] = lo;
