@@ -60,10 +60,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
     c = max(c, 0);
     n = max(n, 0);
   };
-  auto missing = [&](int c, int n) {
-    return ((long long)c + n + p.page - 1) / p.page - ((long long)c + p.page - 1) / p.page;
-  };
+  // lengths are below 2^31, their sums below 2^32: 32-bit divisions, the quotients formed once a request
+  const uint32_t page = (uint32_t)p.page;
+  auto pages_of = [&](uint32_t x) { return x / page + (x % page != 0 ? 1u : 0u); };
+  auto missing = [&](int c, int n) { return (long long)pages_of((uint32_t)c + (uint32_t)n) - (long long)pages_of((uint32_t)c); };
   long long tok = 0, pg = 0;
+#pragma unroll 4
   for (int r = tid; r < r0; r += kPlanThreads) {
     int c, n;
     lengths(r, c, n);
@@ -81,7 +83,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
       lengths(r0 + tid, c, n);
       miss = missing(c, n);
       s_c[tid] = c;
-      s_have[tid] = (int)(((long long)c + p.page - 1) / p.page);
+      s_have[tid] = (int)pages_of((uint32_t)c);
       const long long end = (long long)c + n;
       bad |= end > 0x7fffffffll;
       p.kv_len[r0 + tid] = (int)min(end, 0x7fffffffll);
@@ -138,19 +140,19 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
       if (s_tok[mid] <= t) lo = mid;
       else hi = mid - 1;
     }
-    const long long pos = s_c[lo] + (t - s_tok[lo]);
-    const long long col = pos / p.page;
-    int page = -1;
-    if (col < p.max_pages) {
-      if (col < s_have[lo]) {
-        page = __ldg(p.table + (size_t)(r0 + lo) * p.max_pages + col);
+    const uint32_t pos = (uint32_t)s_c[lo] + (uint32_t)(t - s_tok[lo]);
+    const uint32_t col = pos / page;
+    int id = -1;
+    if (col < (uint32_t)p.max_pages) {
+      if (col < (uint32_t)s_have[lo]) {
+        id = __ldg(p.table + (size_t)(r0 + lo) * p.max_pages + col);
       } else {
         const long long at = s_pg[lo] + col - s_have[lo];
-        if (at < p.n_free) page = __ldg(p.free_pages + at);
+        if (at < p.n_free) id = __ldg(p.free_pages + at);
       }
     }
     p.positions[t] = (int)pos;
-    p.slots[t] = page < 0 ? -1ll : (long long)page * p.page + pos % p.page;
+    p.slots[t] = id < 0 ? -1ll : (long long)id * p.page + pos % page;
   }
   if (r0 + nr == p.R) {
     if (tid == 0) {
@@ -172,19 +174,24 @@ __global__ void __launch_bounds__(256)
     kv_append_kernel(long long n_vec, int per_row, const Tv* __restrict__ k, const Tv* __restrict__ v,
                      const long long* __restrict__ slots, long long n_slots, Tv* __restrict__ k_cache,
                      Tv* __restrict__ v_cache, uint32_t* status) {
+  // piece i is piece `off` of token t; both advance by a fixed step, so the divisions are made once
   const long long step = (long long)gridDim.x * blockDim.x;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n_vec; i += step) {
-    const long long t = i / per_row;
+  long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long t_step = step / per_row, t0 = i / per_row;
+  const int off_step = (int)(step - t_step * per_row);
+  int off = (int)(i - t0 * per_row);
+  for (long long t = t0; i < n_vec; i += step) {
+    const Tv a = k[i], b = v[i];  // read whatever the slot says: in flight together with it
     const long long slot = __ldg(slots + t);
-    if (slot < 0) continue;
     if (slot >= n_slots) {
       set_status(status, DSPARK_ERR_RANGE);
-      continue;
+    } else if (slot >= 0) {
+      k_cache[slot * per_row + off] = a;
+      v_cache[slot * per_row + off] = b;
     }
-    const long long at = slot * per_row + (i - t * per_row);
-    const Tv a = k[i], b = v[i];
-    k_cache[at] = a;
-    v_cache[at] = b;
+    t += t_step;
+    off += off_step;
+    if (off >= per_row) { off -= per_row; ++t; }
   }
 }
 

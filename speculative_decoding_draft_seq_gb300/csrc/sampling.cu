@@ -1107,6 +1107,7 @@ extern "C" dspark_status dspark_sample(int32_t N, int32_t V, int32_t dtype, cons
                                        const int32_t* top_k, const float* top_p, const float* min_p, const double* u,
                                        int32_t* tokens, float* prob, void* workspace, size_t workspace_bytes,
                                        dspark_stream_t stream) {
+  note_launches(0);
   if (N > 0 && (!u || !tokens)) return DSPARK_ERR_INVALID_ARG;
   return sampling_entry(N, V, dtype, logits, temperature, top_k, top_p, min_p, u, tokens, prob, nullptr, workspace,
                         workspace_bytes, stream);
@@ -1116,6 +1117,7 @@ extern "C" dspark_status dspark_truncate(int32_t N, int32_t V, int32_t dtype, co
                                          const float* temperature, const int32_t* top_k, const float* top_p,
                                          const float* min_p, void* out, void* workspace, size_t workspace_bytes,
                                          dspark_stream_t stream) {
+  note_launches(0);
   if (N > 0 && !out) return DSPARK_ERR_INVALID_ARG;
   return sampling_entry(N, V, dtype, logits, temperature, top_k, top_p, min_p, nullptr, nullptr, nullptr, out, workspace,
                         workspace_bytes, stream);
