@@ -39,8 +39,10 @@ namespace dspark {
 constexpr int kSBits = 10;               // key bits that a selection round settles
 constexpr int kSBins = 1 << kSBits;
 constexpr int kWBins = 2048;    // weight bins, 16 an octave
-constexpr int kSList = 6144;    // collected entries (64 KB with the bins: two blocks an SM leave 96 KB to L1)
-constexpr uint32_t kSSmem = kWBins * 4 + kWBins * 4 + kSList * 8;
+constexpr int kSList = 6144;    // collected entries (72 KB with all else: two blocks an SM leave 80 KB to L1)
+constexpr int kRun = 128;       // neighbouring pieces whose mass above the collected range is kept for the draw
+constexpr int kRuns = kSBins;
+constexpr uint32_t kSSmem = kWBins * 4 + kWBins * 4 + kSList * 8 + kRuns * 8;
 static_assert(kSBins * 12 <= kWBins * 8, "the selection's arrays lie over the weight bins");
 
 struct SampleParams {
@@ -184,6 +186,7 @@ __device__ __forceinline__ unsigned long long block_scan_u64(unsigned long long 
 template <class Tin, int U>
 struct RowView {
   static constexpr int E = 16 / (int)sizeof(Tin), kInFlight = U;
+  static_assert(U % 4 == 0, "after() follows four rows of pieces");
   const Tin* row;
   int V, a0, nv;
   __device__ RowView(const Tin* r, int n) : row(r), V(n) {
@@ -219,27 +222,34 @@ struct RowView {
     const uint32_t w = E == 8 ? 0xff80ff80u : 0xff800000u;
     return make_uint4(w, w, w, w);
   }
-  // f(piece, first index, is it one) for the pieces g0 <= g < g1, the tid-th of every nt; the lanes of a warp stay together
-  template <class F>
-  __device__ __forceinline__ void pieces(int g0, int g1, int tid, int nt, F f) const {
+  // f(piece, first index, is it one) for the pieces g0 <= g < g1, the tid-th of every nt; the lanes of a warp stay
+  // together. after(g) follows every four pieces, g the first of them, `gap` apart: nt, or with kRuns 32, so that a
+  // warp's four rows of pieces are kRun neighbours (6% slower where the row comes from memory).
+  struct Nothing {
+    __device__ __forceinline__ void operator()(int) const {}
+  };
+  template <bool kRuns = false, class F, class After = Nothing>
+  __device__ __forceinline__ void pieces(int g0, int g1, int tid, int nt, F f, After after = After()) const {
     if (g0 >= g1) return;
+    const int gap = kRuns ? 32 : nt, at = kRuns ? (tid >> 5) * 32 * U + (tid & 31) : tid;
     uint4 q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int g = g0 + tid + u * nt;
+      const int g = g0 + at + u * gap;
       q[u] = g < g1 ? piece(g) : nothing();
     }
     for (int b = g0; b < g1; b += U * nt) {  // the next loads are on their way while these are looked at
       uint4 next[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int g = b + tid + (U + u) * nt;
+        const int g = b + at + U * nt + u * gap;
         next[u] = g < g1 ? piece(g) : nothing();
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int g = b + tid + u * nt;
+        const int g = b + at + u * gap;
         f(q[u], a0 + g * E, g < g1);
+        if (u % 4 == 3) after(g - 3 * gap);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) q[u] = next[u];
@@ -341,13 +351,19 @@ struct SelectScratch {
 
 // The key at which the running count or (kByMass) mass in descending order first reaches `target`, among
 // the keys lo..hi of the entries that `source` enumerates; `above`: that of the larger keys it leaves out.
-template <bool kByMass, class Source, class Mass>
+// The keys' lowest kUnit bits are the same for all keys of one sign (bf16 logits: 16): bins of 2^kUnit hold one key.
+template <bool kByMass, int kUnit, class Source, class Mass>
 __device__ Threshold select_key(Source source, Mass mass_of, unsigned long long target, unsigned long long above, uint32_t lo,
                                 uint32_t hi, const SelectScratch& s) {
   const int tid = threadIdx.x, nt = blockDim.x;
   for (int round = 0;; ++round) {
     const uint32_t span = hi - lo;
-    const int bits = 32 - __clz(span), shift = bits > kSBits ? bits - kSBits : 0;
+    const int bits = 32 - __clz(span), shift = max(bits - kSBits, kUnit);
+    // the key of a bin of one: of a logit below 0 its low bits are ones, also where hi's are not
+    auto key_of = [&](uint32_t b) {
+      const uint32_t k = hi - (b << shift);
+      return kUnit > 0 && k < 0x80000000u ? (k - 1u) | ((1u << kUnit) - 1u) : k;
+    };
     __syncthreads();
     for (int b = tid; b < kSBins; b += nt) {
       s.cnt[b] = 0;
@@ -358,21 +374,21 @@ __device__ Threshold select_key(Source source, Mass mass_of, unsigned long long 
       if (k < lo || k > hi) return;
       const uint32_t b = (hi - k) >> shift;
       atomicAdd(&s.cnt[b], 1u);
-      if (kByMass && shift > 0) add_mass(&s.mass[b], mass_of(k));
+      if (kByMass && shift > kUnit) add_mass(&s.mass[b], mass_of(k));
     });
     __syncthreads();
     auto value = [&](int b) -> unsigned long long {
       if (!kByMass) return s.cnt[b];
-      if (shift > 0) return s.mass[b].value();
+      if (shift > kUnit) return s.mass[b].value();
       const unsigned long long n = s.cnt[b];  // a bin of one key
-      return n ? n * mass_of(hi - (uint32_t)b) : 0ull;
+      return n ? n * mass_of(key_of((uint32_t)b)) : 0ull;
     };
     find_bin(value, target, above, s.sh, s.pick);
     const uint32_t b = (uint32_t)s.pick[0];
     above = s.pick[1];
-    if (shift == 0 || round == 32) {  // (a round settles kSBits of at most 32 bits)
+    if (shift == kUnit || round == 32) {  // (a round settles kSBits of at most 32 bits)
       Threshold t;
-      t.key = hi - b;
+      t.key = key_of(b);
       t.count = s.cnt[b];
       const unsigned long long w = kByMass ? mass_of(t.key) : 1ull;
       t.ties = (uint32_t)min((unsigned long long)t.count, (target - above + w - 1) / w);
@@ -436,7 +452,7 @@ struct WeightBins {
   static __device__ __forceinline__ float edge(int bin) { return 8388608.f + (float)bin; }
 };
 
-template <class Tin, int NT, int kBlocks>
+template <class Tin, int NT, int kBlocks, bool kDraw>
 __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams p) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   __shared__ unsigned long long sh[32], s_pick[4];
@@ -452,19 +468,21 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   unsigned long long* s_u64 = reinterpret_cast<unsigned long long*>(s_raw);
   const RankScratch few{s_u64, reinterpret_cast<MassBin*>(s_u64 + kRanked), reinterpret_cast<uint32_t*>(s_u64 + 2 * kRanked)};
   uint2* few_list = reinterpret_cast<uint2*>(s_u64 + 3 * kRanked);
+  MassBin* run_mass = reinterpret_cast<MassBin*>(list + kSList);  // [kRuns]
   const int tid = threadIdx.x, V = p.V;
-  constexpr int nt = NT;
+  constexpr int nt = NT, kUnit = sizeof(Tin) == 2 ? 16 : 0;
   const size_t r = blockIdx.x;
   const RowView<Tin, (kBlocks > 1 ? 4 : 8)> row(static_cast<const Tin*>(p.logits) + r * V, V);
   const float T = __ldg(p.temperature + r), tp = __ldg(p.top_p + r);
   const float min_w = fminf(fmaxf(__ldg(p.min_p + r), 0.f), 1.f);
   const int k = __ldg(p.top_k + r);
   const bool greedy = !(T > 0.f), by_k = !greedy && k > 0 && k < V, by_p = !greedy && tp < 1.f;
-  const float rate = fminf(__fdiv_rn(1.4426950408889634f, T), 1e30f);
+  const float rate = fminf(fmaxf(__fdiv_rn(1.4426950408889634f, T), 1e-37f), 1e30f);  // (T = inf: no product 0 inf)
 
   // ---- 1: maximum and weight bins ----
   using Row = RowView<Tin, (kBlocks > 1 ? 4 : 8)>;
-  WeightBins bins{16.f * rate, 0.f};
+  const float octave = by_k ? 16.f : 64.f, bin = 1.f / octave;  // bins an octave, and octaves a bin
+  WeightBins bins{octave * rate, 0.f};
   bool binned = by_k || by_p;
   float M = -INFINITY, mine = -INFINITY;  // the row's maximum; a greedy row: this thread's, and the piece it is in
   int first_at = V;
@@ -483,7 +501,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
     if (!(fabsf(m0) < INFINITY)) m0 = 0.f;
     const float o = rintf(m0 * bins.c);
     binned = fabsf(o) <= 524288.f && rate > 0.f;  // else too far for bins of 1/16 octave in float32
-    bins.off = 8388608.f + (kWBins / 2) - o;
+    bins.off = 8388608.f + (by_k ? kWBins / 2 : kWBins - 6 * 64) - o;
     auto count = [&](float x, uint32_t n) { atomicAdd(&cum_c[kWBins - 1 - WeightBins::index(bins.pos(x))], n); };
     auto visit = [&](const uint4& q, int, bool ok) {
       const float g = Row::largest(q);
@@ -523,16 +541,22 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   if (!(M < INFINITY) || M == -INFINITY) {  // a NaN or +inf, or nothing finite: no distribution
     if (tid == 0) {
       set_status(p.status, DSPARK_ERR_NONFINITE);
-      if (p.tokens) p.tokens[r] = -1;
-      if (p.prob) p.prob[r] = 0.f;
+      if (kDraw) p.tokens[r] = -1;
+      if (kDraw && p.prob) p.prob[r] = 0.f;
     }
-    if (p.out) {
+    if (!kDraw) {
       Tin* out = static_cast<Tin*>(p.out) + r * V;
       for (int v = tid; v < V; v += nt) out[v] = row.row[v];
     }
     return;
   }
   M = __fadd_rn(M, 0.f);
+  const unsigned long long neg_m = f32x2_pack(-M, -M), rate2 = f32x2_pack(rate, rate);
+  auto weights = [&](float x0, float x1) {  // rule_weight of two entries, as masses
+    float y0, y1;
+    f32x2_unpack(f32x2_mul(f32x2_add(f32x2_pack(x0, x1), neg_m), rate2), y0, y1);
+    return MassPair(ex2_approx(y0), ex2_approx(y1));
+  };
   auto mass_of = [&](uint32_t key) { return fx40(rule_weight(key_logit(key), M, rate)); };
   auto from_row = [&](auto f) { row.all([&](float x, int) { f(logit_key(x)); }); };
 
@@ -544,6 +568,12 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   constexpr int kPart = kSList / (NT / 32);
   uint2* part = list + (tid >> 5) * kPart;
   int n_part = 0, n_list = 0;  // entries of the warp's part, and of all
+  // run_mass: each run's mass above run_hi, where the list holds every kept entry up to it; loose entries go with
+  // the first and the last run
+  const int n_runs = max(1, (row.nv + kRun - 1) / kRun);
+  const bool by_run = kDraw && row.nv > 0 && n_runs <= kRuns;
+  auto run_of = [&](int v) { return min(max(v - row.a0, 0) / (kRun * Row::E), n_runs - 1); };
+  float run_hi = -INFINITY;
   if (greedy) {
     int at = block_min_i(mine == M ? first_at : V, shi);
     while (at < V - 1 && row.at(at) != M) ++at;  // within the piece
@@ -552,7 +582,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   } else if (by_k || by_p) {
     const uint32_t hi = logit_key(M), lowest = logit_key(-INFINITY);
     const float tm = __fmaf_rn(M, bins.c, bins.off - 8388608.f);  // the maximum's place on the bins' axis
-    binned = binned && tm > 0.f && tm < kWBins - 1;
+    binned = binned && tm > 0.f;
     Threshold th{0, 0, 0};
     bool found = false;
     unsigned long long S = 0, want = 0, above = 0;  // top-p's whole, its limit, and what lies above the list
@@ -569,7 +599,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       // running sums from the top bin down, a stretch of neighbouring bins a warp
       constexpr int per = kWBins / (NT / 32);
       const int lane = tid & 31, w0 = (tid >> 5) * per;
-      auto weight = [&](int j) { return ex2_approx(((float)(kWBins - 1 - j) - tm) * 0.0625f); };
+      auto weight = [&](int j) { return j == 0 && tm >= kWBins - 1 ? 1.f : ex2_approx(((float)(kWBins - 1 - j) - tm) * bin); };
       uint32_t c = 0;
       float m = 0.f;
 #pragma unroll 4
@@ -635,7 +665,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       float slack = est * 0.0156f;
       float r_lo = 0.f, r_hi = 0.f;  // the range before
       int move = 0;                  // 1: further down than it, -1: further up
-      int half = kSList / 6;         // entries either side of the goal
+      int half = kSList / 4;         // entries either side of the goal
       for (int attempt = 0; attempt < 6; ++attempt) {
         if (tid < 32) {
           int ja = 0, jb;
@@ -677,17 +707,12 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
         const uint4 none = make_uint4(nan_w, nan_w, nan_w, nan_w);
         n_part = 0;
         const uint32_t below = (1u << (tid & 31)) - 1u;
-        auto collect = [&](float x, int v) {  // by whole warps
-          const bool in = x >= x_lo && x <= x_hi;
-          const uint32_t all = __ballot_sync(0xffffffffu, in);
-          if (all == 0) return;
-          const int at = n_part + __popc(all & below);
-          if (in && at < kPart) part[at] = make_uint2(logit_key(x), (uint32_t)v);
-          n_part += __popc(all);
-        };
-        auto collect_piece = [&](const uint4& q, int v) {
+        // the indices of the entries in range, by whole warps: an entry a step of the lane that has most among four
+        // pieces (bits 0..15: their float32 entries or low halves, four a piece; above: the high halves)
+        uint32_t in4 = 0;
+        auto collect_piece = [&](const uint4& q) {
           const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-          uint32_t in = 0;  // bit i: entry i (float32), or the low half of word i; bit 16 + i: the high half
+          uint32_t in = 0;
           if (Row::E == 8) {  // two compares at a time, against the ends rounded inwards to bf16
             const __nv_bfloat16 a = __float2bfloat16_ru(x_lo), b = __float2bfloat16_rd(x_hi);
             const __nv_bfloat162 a2 = __halves2bfloat162(a, a), b2 = __halves2bfloat162(b, b);
@@ -700,65 +725,88 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
 #pragma unroll
             for (int i = 0; i < 4; ++i) in |= __uint_as_float(w[i]) >= x_lo && __uint_as_float(w[i]) <= x_hi ? 1u << i : 0u;
           }
-          for (uint32_t any = __reduce_or_sync(0xffffffffu, in); any; any &= any - 1) {
-            const int bit = __ffs(any) - 1, i = bit & 3;
-            const bool mine = (in >> bit) & 1u;
-            const uint32_t all = __ballot_sync(0xffffffffu, mine);
-            const int at = n_part + __popc(all & below);
-            if (mine && at < kPart) {
-              const uint32_t x = i & 2 ? i & 1 ? w[3] : w[2] : i & 1 ? w[1] : w[0];
-              const float f = __uint_as_float(Row::E == 4 ? x : bit & 16 ? x & 0xffff0000u : x << 16);
-              part[at] = make_uint2(logit_key(f), (uint32_t)(v + (Row::E == 4 ? i : 2 * i + (bit >> 4))));
-            }
+          in4 = (in4 >> 4) & 0x0fff0fffu | in << 12;  // (each piece moves the ones before it down)
+        };
+        auto skip_piece = [&]() { in4 = (in4 >> 4) & 0x0fff0fffu; };
+        auto collect = [&](int g, int gap) {
+          const int v = row.a0 + g * Row::E;
+          for (uint32_t all; (all = __ballot_sync(0xffffffffu, in4 != 0)) != 0; in4 &= in4 - 1) {
+            const int bit = __ffs(in4) - 1, i = bit & 3, at = n_part + __popc(all & below);
+            if (in4 != 0 && at < kPart)
+              part[at].y = (uint32_t)(v + ((bit >> 2) & 3) * gap * Row::E + (Row::E == 4 ? i : 2 * i + (bit >> 4)));
             n_part += __popc(all);
           }
         };
         auto collect_loose = [&]() {  // at most 2 E entries: the first warp takes them
           if (tid >= 32) return;
           const int n = V - row.nv * Row::E, v = tid < row.a0 ? tid : tid + row.nv * Row::E;
-          collect(tid < n ? row.at(v) : nan, v);
-        };
-        const unsigned long long neg_m = f32x2_pack(-M, -M), rate2 = f32x2_pack(rate, rate);
-        auto pair = [&](float x0, float x1) {
-          float y0, y1;
-          f32x2_unpack(f32x2_mul(f32x2_add(f32x2_pack(x0, x1), neg_m), rate2), y0, y1);
-          return MassPair(ex2_approx(y0), ex2_approx(y1));
+          const float x = tid < n ? row.at(v) : nan;
+          const bool in = x >= x_lo && x <= x_hi;
+          const uint32_t all = __ballot_sync(0xffffffffu, in);
+          const int at = n_part + __popc(all & below);
+          if (in && at < kPart) part[at].y = (uint32_t)v;
+          n_part += __popc(all);
         };
         unsigned long long gap_mass = 0;
         if (by_k) {
           row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
-            if (__any_sync(0xffffffffu, ok && Row::largest(q) >= x_lo)) collect_piece(ok ? q : none, v);
-          });
+            if (__any_sync(0xffffffffu, ok && Row::largest(q) >= x_lo)) collect_piece(ok ? q : none);
+            else skip_piece();
+          }, [&](int g) { collect(g, nt); });
           collect_loose();
         } else if (move == 0) {  // the row's mass, and what lies above the range
           MassSum sum, over;
-          row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
+          bool ups = false;
+          row.template pieces<kDraw>(0, row.nv, tid, nt, [&](const uint4& q, int, bool ok) {
             float x[Row::E];
             Row::split(q, x);
             const float g = Row::largest(q);
             const bool some = __any_sync(0xffffffffu, g > x_hi);
+            ups |= some;
 #pragma unroll
             for (int e = 0; e < Row::E; e += 2) {
-              const MassPair m = pair(x[e], x[e + 1]);
+              const MassPair m = weights(x[e], x[e + 1]);
               sum.add(m);
               if (some) over.add_if(m, x[e] > x_hi, x[e + 1] > x_hi);
             }
-            if (__any_sync(0xffffffffu, ok && g >= x_lo)) collect_piece(ok ? q : none, v);
+            if (__any_sync(0xffffffffu, ok && g >= x_lo)) collect_piece(ok ? q : none);
+            else skip_piece();
+          }, [&](int g) {
+            collect(g, kDraw ? 32 : nt);
+            if (!by_run) return;
+            unsigned long long m = 0;
+            if (ups) {  // (32 lanes' 4 E masses: the halves' sums fit 32 bits)
+              const uint32_t hi = __reduce_add_sync(0xffffffffu, over.hi), lo = __reduce_add_sync(0xffffffffu, over.lo);
+              m = ((unsigned long long)hi << 20) + lo;
+            }
+            if ((tid & 31) == 0 && g < row.nv) run_mass[g / kRun] = MassBin{(uint32_t)m, (uint32_t)(m >> 32)};
+            over = MassSum();
+            ups = false;
           });
-          row.loose(tid, nt, [&](float x, int) {
-            const MassPair m = pair(x, x);
+          __syncthreads();
+          row.loose(tid, nt, [&](float x, int v) {
+            const MassPair m = weights(x, x);
             sum.add_if(m, true, false);
-            over.add_if(m, x > x_hi, false);
+            if (!by_run) over.add_if(m, x > x_hi, false);
+            else if (x > x_hi) add_mass(run_mass + run_of(v), mass_of(logit_key(x)));
           });
           collect_loose();
           S = block_sum_u64(sum.total(), sh);
-          above = headed ? 0ull : block_sum_u64(over.total(), sh);
+          unsigned long long up = over.total();
+          if (by_run)
+            for (int i = tid; i < n_runs; i += nt) up += run_mass[i].value();
+          above = headed ? 0ull : block_sum_u64(up, sh);
+          run_hi = by_run && !headed ? x_hi : -INFINITY;
           want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
         } else {  // another range: only what lies between the two counts
+          run_hi = -INFINITY;
           MassSum gap;
           const float g_lo = move > 0 ? x_hi : r_hi, g_hi = move > 0 ? r_lo : x_lo, least = move > 0 ? x_lo : r_hi;
           row.pieces(0, row.nv, tid, nt, [&](const uint4& q, int v, bool ok) {
-            if (!__any_sync(0xffffffffu, ok && Row::largest(q) >= least)) return;
+            if (!__any_sync(0xffffffffu, ok && Row::largest(q) >= least)) {
+              skip_piece();
+              return;
+            }
             const uint4 p = ok ? q : none;
             float x[Row::E];
             Row::split(p, x);
@@ -768,11 +816,11 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
             if (__any_sync(0xffffffffu, some)) {
 #pragma unroll
               for (int e = 0; e < Row::E; e += 2)
-                gap.add_if(pair(x[e], x[e + 1]), x[e] > g_lo && x[e] < g_hi, x[e + 1] > g_lo && x[e + 1] < g_hi);
+                gap.add_if(weights(x[e], x[e + 1]), x[e] > g_lo && x[e] < g_hi, x[e + 1] > g_lo && x[e + 1] < g_hi);
             }
-            collect_piece(p, v);
-          });
-          row.loose(tid, nt, [&](float x, int) { gap.add_if(pair(x, x), x > g_lo && x < g_hi, false); });
+            collect_piece(p);
+          }, [&](int g) { collect(g, nt); });
+          row.loose(tid, nt, [&](float x, int) { gap.add_if(weights(x, x), x > g_lo && x < g_hi, false); });
           collect_loose();
           gap_mass = block_sum_u64(gap.total(), sh);
         }
@@ -783,6 +831,11 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
         for (int i = 0; i < NT / 32; ++i) {
           const int n = (int)s_range[i].x;
           n_list = n > kPart || n_list > kSList ? kSList + 1 : n_list + n;
+        }
+        if (n_list <= kSList) {
+#pragma unroll 4
+          for (int i = tid & 31; i < n_part; i += 32) part[i].x = logit_key(row.at((int)part[i].y));
+          __syncwarp();
         }
         // does the rule end among the list's entries?
         if (n_list > kSList) {  // a smaller range, from the upper end of this one on
@@ -862,23 +915,35 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
             k_hi = max(k_hi, s_range[i].y);
           }
           if (by_k) {
-            th = select_key<false>(from_list, no_mass, (unsigned long long)k, 0ull, k_lo, k_hi, scratch);
+            th = select_key<false, kUnit>(from_list, no_mass, (unsigned long long)k, 0ull, k_lo, k_hi, scratch);
             if (by_p) {
               S = top_mass(from_list);
               want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
-              th = select_key<true>(from_list, mass_of, want, 0ull, th.key, k_hi, scratch);
+              th = select_key<true, kUnit>(from_list, mass_of, want, 0ull, th.key, k_hi, scratch);
             }
           } else {
-            th = select_key<true>(from_list, mass_of, want, above, k_lo, k_hi, scratch);
+            th = select_key<true, kUnit>(from_list, mass_of, want, above, k_lo, k_hi, scratch);
           }
         }
         if (th.ties < th.count) {  // the index of the last tie that is kept: the ties-th smallest
-          auto tie_index = [&](auto f) {
+          if (th.count <= (uint32_t)kRanked) {
+            __syncthreads();
+            if (tid == 0) shi[0] = 0;
+            __syncthreads();
             for (int i = tid & 31; i < n_part; i += 32)
-              if (part[i].x == th.key) f(~part[i].y);
-          };
-          const Threshold at = select_key<false>(tie_index, no_mass, th.ties, 0ull, ~(uint32_t)(V - 1), 0xffffffffu, scratch);
-          cut = (int)~at.key + 1;
+              if (part[i].x == th.key) few_list[atomicAdd(&shi[0], 1)] = part[i];  // in any order: a rank does not depend on it
+            const Ranked e = rank_entries(few_list, (int)th.count, no_mass, [](const uint2& a, const uint2& b) { return a.y < b.y; }, few);
+            if (tid < (int)th.count && e.rank == (int)th.ties - 1) s_pick[0] = few_list[tid].y;
+            __syncthreads();
+            cut = (int)s_pick[0] + 1;
+          } else {
+            auto tie_index = [&](auto f) {
+              for (int i = tid & 31; i < n_part; i += 32)
+                if (part[i].x == th.key) f(~part[i].y);
+            };
+            const Threshold at = select_key<false, 0>(tie_index, no_mass, th.ties, 0ull, ~(uint32_t)(V - 1), 0xffffffffu, scratch);
+            cut = (int)~at.key + 1;
+          }
         }
       }
     }
@@ -887,7 +952,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       cut = V;
       uint32_t lo = lowest;
       if (by_k) {
-        th = select_key<false>(from_row, no_mass, (unsigned long long)k, 0ull, lo, hi, scratch);
+        th = select_key<false, kUnit>(from_row, no_mass, (unsigned long long)k, 0ull, lo, hi, scratch);
         lo = th.key;
         if (by_p) S = top_mass(from_row);
       } else {
@@ -897,7 +962,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       }
       if (by_p) {
         want = max(1ull, scale_mass((double)fminf(tp, 1.f - 0x1p-24f), S));
-        th = select_key<true>(from_row, mass_of, want, 0ull, lo, hi, scratch);
+        th = select_key<true, kUnit>(from_row, mass_of, want, 0ull, lo, hi, scratch);
       }
       if (th.ties < th.count) {
         const float xs = key_logit(th.key);
@@ -906,7 +971,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
             if (x == xs) f(~(uint32_t)v);
           });
         };
-        const Threshold at = select_key<false>(tie_index, no_mass, th.ties, 0ull, ~(uint32_t)(V - 1), 0xffffffffu, scratch);
+        const Threshold at = select_key<false, 0>(tie_index, no_mass, th.ties, 0ull, ~(uint32_t)(V - 1), 0xffffffffu, scratch);
         cut = (int)~at.key + 1;
       }
     }
@@ -929,7 +994,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   const float xs = key_logit(key);
   auto kept = [&](float x, int v) { return x > xs || (x == xs && v < cut); };
 
-  if (p.out) {
+  if (!kDraw) {
     Tin* out = static_cast<Tin*>(p.out) + r * V;
     const bool aligned = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.row)) & 15) == 0;
     const uint32_t low = sizeof(Tin) == 2 ? 0xff7fu : 0xff7fffffu;  // the lowest finite value
@@ -965,7 +1030,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       else *reinterpret_cast<uint32_t*>(out + v) = low;
     }
   }
-  if (!p.tokens) return;
+  if (!kDraw) return;
   if (greedy) {
     if (tid == 0) {
       p.tokens[r] = cut - 1;
@@ -1015,42 +1080,72 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
     }
     return;
   }
-  // the draw on the row: masses of one stretch of pieces a warp (the loose entries before the first piece go
-  // with the first stretch, those after the last with the last), then the entries of the stretch
-  const int warp = tid >> 5, nw = nt >> 5, stretch = (row.nv + nw - 1) / nw;
-  const int g0 = min(warp * stretch, row.nv), g1 = min(g0 + stretch, row.nv);
-  auto first_of = [&](int w) { return w == 0 ? 0 : row.a0 + min(w * stretch, row.nv) * Row::E; };
-  auto end_of = [&](int w) { return w == nw - 1 ? V : first_of(w + 1); };
+  // the draw on the row: where the token's piece is, then the masses of a few pieces a thread
   MassSum sum;
-  auto weigh = [&](float x, int v) { sum.add(MassPair(kept(x, v) ? rule_weight(x, M, rate) : 0.f, 0.f)); };
-  row.pieces(g0, g1, tid & 31, 32, [&](const uint4& q, int v, bool ok) {
-    if (!ok || Row::largest(q) < xs) return;
+  auto weigh = [&](int v) {
+    const float x = row.at(v);
+    sum.add(MassPair(kept(x, v) ? rule_weight(x, M, rate) : 0.f, 0.f));
+  };
+  auto weigh_piece = [&](const uint4& q, int v) {
     float x[Row::E];
     Row::split(q, x);
+    const bool plain = v + Row::E <= cut;  // ties of the whole piece are kept
 #pragma unroll
     for (int e = 0; e < Row::E; e += 2)
-      sum.add(MassPair(kept(x[e], v + e) ? rule_weight(x[e], M, rate) : 0.f,
-                        kept(x[e + 1], v + e + 1) ? rule_weight(x[e + 1], M, rate) : 0.f));
-  });
-  if (warp == 0)
-    for (int v = tid; v < row.a0; v += 32) weigh(row.at(v), v);
-  if (warp == nw - 1)
-    for (int v = row.a0 + row.nv * Row::E + (tid & 31); v < V; v += 32) weigh(row.at(v), v);
-  unsigned long long m = sum.total();
-  const unsigned long long end = block_scan_u64(m, sh), Z = block_sum_u64(m, sh);
-  const unsigned long long t = scale_mass(p.u[r], Z);
-  unsigned long long start = __shfl_sync(0xffffffffu, end - m, 0);
-  const unsigned long long stop = __shfl_sync(0xffffffffu, end, 31);
-  if (start <= t && stop > t && (tid & 31) == 0) { s_pick[0] = warp; s_pick[1] = start; }
-  __syncthreads();
-  const int s0 = first_of((int)s_pick[0]), s1 = end_of((int)s_pick[0]);
-  start = s_pick[1];
-  const int each = (s1 - s0 + nt - 1) / nt, a = min(s0 + tid * each, s1), e = min(a + each, s1);
-  m = 0;
-  for (int v = a; v < e; ++v) {
-    const float x = row.at(v);
-    if (kept(x, v)) m += fx40(rule_weight(x, M, rate));
+      sum.add_if(weights(x[e], x[e + 1]), plain ? x[e] >= xs : kept(x[e], v + e), plain ? x[e + 1] >= xs : kept(x[e + 1], v + e + 1));
+  };
+  unsigned long long Z, t, start;
+  int g0, g1;
+  bool at_first, at_last;
+  if (run_hi >= xs) {  // the runs' masses are known but for the list's entries
+    __syncthreads();
+    for (int i = tid & 31; i < n_part; i += 32)
+      if (kept(key_logit(part[i].x), (int)part[i].y)) add_mass(run_mass + run_of((int)part[i].y), mass_of(part[i].x));
+    __syncthreads();
+    Z = 0;
+    for (int i = tid; i < n_runs; i += nt) Z += run_mass[i].value();
+    Z = block_sum_u64(Z, sh);
+    t = scale_mass(p.u[r], Z);
+    __syncthreads();
+    find_bin([&](int b) { return b < n_runs ? run_mass[b].value() : 0ull; }, t + 1, 0ull, sh, s_pick);
+    const int c = (int)s_pick[0];
+    g0 = c * kRun;
+    g1 = min(g0 + kRun, row.nv);
+    at_first = c == 0;
+    at_last = c == n_runs - 1;
+  } else {  // a stretch of pieces a warp; the loose entries go with the first and the last
+    const int warp = tid >> 5, nw = nt >> 5, stretch = (row.nv + nw - 1) / nw;
+    row.pieces(min(warp * stretch, row.nv), min((warp + 1) * stretch, row.nv), tid & 31, 32, [&](const uint4& q, int v, bool ok) {
+      if (ok && Row::largest(q) >= xs) weigh_piece(q, v);
+    });
+    if (warp == 0)
+      for (int v = tid; v < row.a0; v += 32) weigh(v);
+    if (warp == nw - 1)
+      for (int v = row.a0 + row.nv * Row::E + (tid & 31); v < V; v += 32) weigh(v);
+    const unsigned long long m = sum.total();
+    const unsigned long long end = block_scan_u64(m, sh);
+    Z = block_sum_u64(m, sh);
+    t = scale_mass(p.u[r], Z);
+    start = __shfl_sync(0xffffffffu, end - m, 0);
+    const unsigned long long stop = __shfl_sync(0xffffffffu, end, 31);
+    if (start <= t && stop > t && (tid & 31) == 0) { s_pick[0] = warp; s_pick[1] = start; }
+    __syncthreads();
+    g0 = min((int)s_pick[0] * stretch, row.nv);
+    g1 = min(g0 + stretch, row.nv);
+    at_first = s_pick[0] == 0;
+    at_last = (int)s_pick[0] == nw - 1;
   }
+  start = s_pick[1];
+  const int each = (g1 - g0 + nt - 1) / nt;
+  const int ga = min(g0 + tid * each, g1), ge = min(ga + each, g1);
+  const int p0 = row.a0 + ga * Row::E, p1 = row.a0 + ge * Row::E;
+  const int a = at_first && tid == 0 ? 0 : p0, e = at_last && tid == nt - 1 ? V : p1;
+  sum = MassSum();
+  for (int v = a; v < p0; ++v) weigh(v);
+#pragma unroll 2
+  for (int g = ga; g < ge; ++g) weigh_piece(row.piece(g), row.a0 + g * Row::E);
+  for (int v = p1; v < e; ++v) weigh(v);
+  const unsigned long long m = sum.total();
   unsigned long long c = block_scan_u64(m, sh) - m + start;
   if (c <= t && c + m > t) {
     for (int v = a; v < e; ++v) {
@@ -1067,15 +1162,21 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   }
 }
 
-template <class Tin, int NT, int kBlocks>
+template <class Tin, int NT, int kBlocks, bool kDraw>
 static cudaError_t launch_rule(const SampleParams& p, int N, cudaStream_t s) {
   static std::atomic<unsigned long long> attr{0};
-  const cudaError_t e = set_smem_limit_once((const void*)sampling_rule_kernel<Tin, NT, kBlocks>, (int)kSSmem, attr);
+  const cudaError_t e = set_smem_limit_once((const void*)sampling_rule_kernel<Tin, NT, kBlocks, kDraw>, (int)kSSmem, attr);
   if (e != cudaSuccess) return e;
-  sampling_rule_kernel<Tin, NT, kBlocks><<<N, NT, kSSmem, s>>>(p);
+  sampling_rule_kernel<Tin, NT, kBlocks, kDraw><<<N, NT, kSSmem, s>>>(p);
   return cudaGetLastError();
 }
 
+template <class Tin, bool kDraw>
+static cudaError_t launch_rule(const SampleParams& p, int N, bool alone, cudaStream_t s) {
+  return alone ? launch_rule<Tin, 512, 1, kDraw>(p, N, s) : launch_rule<Tin, 512, 2, kDraw>(p, N, s);
+}
+
+template <bool kDraw>
 static dspark_status sampling_entry(int32_t N, int32_t V, int32_t dtype, const void* logits, const float* temperature,
                                     const int32_t* top_k, const float* top_p, const float* min_p, const double* u,
                                     int32_t* tokens, float* prob, void* out, void* workspace, size_t workspace_bytes,
@@ -1090,11 +1191,8 @@ static dspark_status sampling_entry(int32_t N, int32_t V, int32_t dtype, const v
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSPARK_ERR_CUDA;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const bool wide = N <= sms;
-  const cudaError_t e = dtype == DSPARK_BF16 ? wide ? launch_rule<__nv_bfloat16, 512, 1>(p, N, (cudaStream_t)stream)
-                                                    : launch_rule<__nv_bfloat16, 512, 2>(p, N, (cudaStream_t)stream)
-                                             : wide ? launch_rule<float, 512, 1>(p, N, (cudaStream_t)stream)
-                                                    : launch_rule<float, 512, 2>(p, N, (cudaStream_t)stream);
+  const cudaError_t e = dtype == DSPARK_BF16 ? launch_rule<__nv_bfloat16, kDraw>(p, N, N <= sms, (cudaStream_t)stream)
+                                             : launch_rule<float, kDraw>(p, N, N <= sms, (cudaStream_t)stream);
   note_launches(1);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
@@ -1109,7 +1207,7 @@ extern "C" dspark_status dspark_sample(int32_t N, int32_t V, int32_t dtype, cons
                                        dspark_stream_t stream) {
   note_launches(0);
   if (N > 0 && (!u || !tokens)) return DSPARK_ERR_INVALID_ARG;
-  return sampling_entry(N, V, dtype, logits, temperature, top_k, top_p, min_p, u, tokens, prob, nullptr, workspace,
+  return sampling_entry<true>(N, V, dtype, logits, temperature, top_k, top_p, min_p, u, tokens, prob, nullptr, workspace,
                         workspace_bytes, stream);
 }
 
@@ -1119,6 +1217,6 @@ extern "C" dspark_status dspark_truncate(int32_t N, int32_t V, int32_t dtype, co
                                          dspark_stream_t stream) {
   note_launches(0);
   if (N > 0 && !out) return DSPARK_ERR_INVALID_ARG;
-  return sampling_entry(N, V, dtype, logits, temperature, top_k, top_p, min_p, nullptr, nullptr, nullptr, out, workspace,
+  return sampling_entry<false>(N, V, dtype, logits, temperature, top_k, top_p, min_p, nullptr, nullptr, nullptr, out, workspace,
                         workspace_bytes, stream);
 }

@@ -154,3 +154,81 @@ def test_page_plan_sum_past_31_bits():
     assert status in (dspark.ERR_RANGE, dspark.ERR_CAPACITY)
     assert q_start.tolist() == [0, 9, 11] and kv_len.tolist() == [2 ** 31 - 1, 6]
     assert pos.tolist()[9:] == [4, 5] and slots.tolist()[9:] == [4, 5]
+
+
+def plain_rule(x, T, k, p, m, u):
+    """The rule's definition with torch's operations on the device, row by row: kept mask and token. The same float32
+    weights (CUDA's exp2f on the same argument), masses and sums in integers."""
+    V = x.numel()
+    x = x.float()
+    M = x.max()
+    rate = min(np.float32(np.float32(1.4426950408889634) / np.float32(T)), np.float32(1e30))
+    mass = (torch.exp2((x - M) * float(rate)).double() * 2.0 ** 40).floor().long()
+    order = torch.sort(x, descending=True, stable=True).indices
+    sorted_mass = mass[order]
+    n = V if k <= 0 or k >= V else k
+    before = sorted_mass.cumsum(0) - sorted_mass
+    if p < 1:
+        S = int(sorted_mass[:n].sum())
+        num, den = float(p).as_integer_ratio()
+        n = min(n, int((before[:n] < max(1, S * num // den)).sum()))
+    kept = torch.zeros(V, dtype=torch.bool, device=x.device)
+    kept[order[:n]] = True
+    kept &= mass >= 0 if m <= 0 else torch.exp2((x - M) * float(rate)) >= float(np.float32(m))
+    kept &= x > -float("inf")
+    mass = torch.where(kept, mass, 0)
+    c = mass.cumsum(0)
+    num, den = float(u).as_integer_ratio()
+    return kept, int((c > int(c[-1]) * num // den).nonzero()[0])
+
+
+def shaped_row(kind, V, rng):
+    x = rng.normal(size=V) * 2
+    if kind == "descending":
+        x = -np.sort(-x)
+    elif kind == "ascending":
+        x = np.sort(x)
+    elif kind == "one_above":      # one entry far above all others, late in the row
+        x[V - 3] = 60.0
+    elif kind == "some_above":     # a few hundred, of differing weights, above what the row's start shows
+        x[-V // 5:][::37] += 20 + rng.random(len(x[-V // 5:][::37])) * 12
+    elif kind == "two_levels":     # half the row far below the other half
+        x[rng.permutation(V)[:V // 2]] -= 45
+    elif kind == "ramp":           # hundreds of octaves from end to end
+        x = np.linspace(-300, 20, V)[rng.permutation(V)]
+    elif kind == "wide":
+        x *= 40
+    return x.astype(np.float32)
+
+
+KINDS = ["normal", "descending", "ascending", "one_above", "some_above", "two_levels", "ramp", "wide"]
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 6001), ("bf16", 65537), ("fp32", 30011), ("bf16", 129280), ("fp32", 600000)])
+def test_rule_on_shaped_rows(dtype, V):
+    """Rows whose distribution over values and over indices differs from what a row's start or a sample of it
+    shows: exactly the definition's kept set and token, in both kernels."""
+    rng = np.random.default_rng(V)
+    rows = [(kind, T, k, p, m) for kind in KINDS
+            for T, k, p, m in [(1.0, 0, 0.95, 0.0), (1.7, 0, 0.9, 0.0), (1.3, 0, 0.999, 1e-5), (0.2, 0, 0.99, 0.0), (1.0, 1000, 1.0, 0.0),
+                               (1.5, 3000, 0.9, 0.0), (0.6, 7, 0.8, 0.1), (2.0, 0, 1.0, 0.02)]]
+    x = torch.from_numpy(np.stack([shaped_row(kind, V, rng) for kind, *_ in rows])).to(DEV).to(G.TORCH[dtype])
+    T, k, p, m = (np.array(a) for a in list(zip(*rows))[1:])
+    u = rng.random(len(rows))
+    for n in (len(rows), 200):  # alone on its SM, and with other rows
+        g = np.arange(n) % len(rows)
+        tokens, prob, out, st, st2 = G.run_rule(x[torch.from_numpy(g).to(DEV)].contiguous(), T[g], k[g], p[g], m[g], u[g])
+        assert st == dspark.OK and st2 == dspark.OK
+        for i in range(len(rows)):
+            kept, token = plain_rule(x[i], np.float32(T[i]), int(k[i]), np.float32(p[i]), m[i], u[i])
+            G.check_kept(x, out[i:i + 1].repeat(i + 1, axis=0), i, kept.cpu().numpy())
+            assert tokens[i] == token, rows[i]
+        if n == 200 and V > 200000:
+            break
+
+
+def test_rule_at_infinite_temperature():
+    """Temperature inf: every finite entry weighs 1, whatever its size."""
+    x = torch.tensor([[-3e38, 3e38, 0.0, -float("inf"), 1.0, 2.0]], device=DEV).repeat(3, 1)
+    tokens, prob, out, st, _ = G.run_rule(x, np.float32(np.inf), 0, 1.0, 0.0, [0.05, 0.5, 0.99])
+    assert st == dspark.OK and set(tokens.tolist()) <= {0, 1, 2, 4, 5}
