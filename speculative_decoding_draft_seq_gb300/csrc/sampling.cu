@@ -39,7 +39,7 @@ namespace dspark {
 constexpr int kSBits = 10;               // key bits that a selection round settles
 constexpr int kSBins = 1 << kSBits;
 constexpr int kWBins = 2048;    // weight bins, 16 an octave
-constexpr int kSList = 6144;    // collected entries (72 KB with all else: two blocks an SM leave 80 KB to L1)
+constexpr int kSList = 7168;    // collected entries (80 KB with all else: two blocks an SM leave 64 KB to L1)
 constexpr int kRun = 128;       // neighbouring pieces whose mass above the collected range is kept for the draw
 constexpr int kRuns = kSBins;
 constexpr uint32_t kSSmem = kWBins * 4 + kWBins * 4 + kSList * 8 + kRuns * 8;
@@ -665,42 +665,44 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
       float slack = est * 0.0156f;
       float r_lo = 0.f, r_hi = 0.f;  // the range before
       int move = 0;                  // 1: further down than it, -1: further up
-      int half = kSList / 4;         // entries either side of the goal
+      int half = kSList / 5;         // entries either side of the goal
       for (int attempt = 0; attempt < 6; ++attempt) {
-        if (tid < 32) {
-          int ja = 0, jb;
-          bool head = true;
-          if (by_k) {
-            jb = first(cum_c, (uint32_t)k);
-            head = cum_c[jb] >= (uint32_t)k && k <= kSList;
-          } else {
-            const int jg = first(cum_m, goal);
-            ja = first(cum_m, fmaxf(goal - slack, 0.f));
-            jb = first(cum_m, goal + slack);
-            const int at = (int)cum_c[jg];  // well within what the list holds
-            ja = max(ja, min(first(cum_c, (uint32_t)max(at - half, 1)), jg));
-            jb = min(jb, max(first(cum_c, (uint32_t)(at + half)) - 1, jg));
-            head = move == 0 && cum_c[jb] <= kSList / 2;
-          }
-          float lo = logit_at((float)(jb + 1)), hi = head ? INFINITY : logit_at((float)ja);
-          // no entry of the range before is in this one, and it reaches a bin further (more at a later attempt)
-          const float reach = 1.5f * (float)attempt / bins.c;
-          if (move > 0) {
-            hi = fminf(hi, key_logit(logit_key(r_lo) - 1));
-            lo = fminf(lo, r_lo - reach);
-          } else if (move < 0) {
-            lo = fmaxf(lo, key_logit(logit_key(r_hi) + 1));
-            hi = fmaxf(hi, r_hi + reach);
-          }
-          if (tid == 0) {
-            shf[0] = lo;
-            shf[1] = hi;
-            shf[2] = head ? 1.f : 0.f;
-          }
+        // the ends' bins: a search a warp
+        const int warp = tid >> 5;
+        if (by_k) {
+          if (warp == 0) shi[0] = first(cum_c, (uint32_t)k);
+        } else if (warp < 3) {
+          shi[warp] = first(cum_m, warp == 0 ? goal : warp == 1 ? fmaxf(goal - slack, 0.f) : goal + slack);
         }
         __syncthreads();
-        const float x_lo = shf[0], x_hi = shf[1];
-        headed = shf[2] != 0.f;
+        int ja = 0, jb = shi[0];
+        if (by_k) {
+          headed = cum_c[jb] >= (uint32_t)k && k <= kSList;
+        } else {
+          const int jg = shi[0], at = (int)cum_c[jg];
+          if (warp < 4)  // so many entries up and down; the bins next to the goal's that hold any
+            shi[4 + warp] = first(cum_c, warp == 0 ? (uint32_t)max(at - half, 1) : warp == 1 ? (uint32_t)(at + half)
+                                         : warp == 2 ? (uint32_t)(at + 1) : jg > 0 ? cum_c[jg - 1] : 0u);
+          __syncthreads();
+          auto entries = [&](int a, int b) { return (int)cum_c[b] - (a > 0 ? (int)cum_c[a - 1] : 0); };
+          // within the slack, and well within what the list holds; but a bin on either side if it can (one bf16 value
+          // may stand for thousands of entries)
+          ja = max(shi[1], min(shi[4], jg));
+          jb = min(shi[2], max(shi[5] - 1, jg));
+          if (entries(min(ja, shi[7]), jb) <= kSList * 6 / 7) ja = min(ja, shi[7]);
+          if (entries(ja, max(jb, shi[6])) <= kSList * 6 / 7) jb = max(jb, shi[6]);
+          headed = move == 0 && cum_c[jb] <= kSList / 2;
+        }
+        float x_lo = logit_at((float)(jb + 1)), x_hi = headed ? INFINITY : logit_at((float)ja);
+        // no entry of the range before is in this one, and it reaches a bin further (more at a later attempt)
+        const float reach = 1.5f * (float)attempt / bins.c;
+        if (move > 0) {
+          x_hi = fminf(x_hi, key_logit(logit_key(r_lo) - 1));
+          x_lo = fminf(x_lo, r_lo - reach);
+        } else if (move < 0) {
+          x_lo = fmaxf(x_lo, key_logit(logit_key(r_hi) + 1));
+          x_hi = fmaxf(x_hi, r_hi + reach);
+        }
         if (by_k && !headed) break;
         const float nan = __uint_as_float(0x7fc00000u);  // in no range
         const uint32_t nan_w = Row::E == 8 ? 0x7fc07fc0u : __float_as_uint(nan);
