@@ -22,25 +22,42 @@
 //   attn_join_kernel   adds a row's parts up.
 //
 // attn_tiles_kernel: rows are (token, query head of the key head), packed
-// floor(128 / group) tokens a 128-row half. Per 128-key tile: S = Q K^T into TMEM
-// (128 columns), four warps turn S into bf16 weights in place (one thread a row),
-// O += P V with P read from TMEM, the first 64 keys while the others' weights are
-// formed. Two such groups of warps, each with an S / P and an O of its own, keep two
-// tiles in flight, so that one's softmax runs under the other's MMAs: an item with more
-// tokens than a half holds gives each one a half of the rows (K and V tiles are
-// read once for both); an item with fewer gives them the even and the odd key
-// tiles of the same rows (two parts). The weights use a reference maximum that is
-// moved, and O rescaled, only when the row's maximum has risen by more than 8 (2^8
-// fits every type on the way), so O is rarely rescaled.
+// floor(128 / group) tokens a 128-row half. Per step of 64 keys: S = Q K^T into
+// one of two 64-column buffers of TMEM, four warps turn S into bf16 weights in
+// place (one thread a row; S is in registers for the maximum and the weights),
+// O += P V with P read from TMEM. S of the next step is formed meanwhile. Two such
+// groups of warps, each with its buffers and an O, work side by side: an item with
+// more tokens than a half holds gives each one a half of the rows (K and V tiles are
+// read once for both); an item with fewer gives them the even and the odd 128-key
+// tiles of the same rows (two parts).
+//   Roundings: the weights that multiply v, and out, to bf16, which the tensor cores
+// take; scores, maxima, sums and O are float32 (the sum is of the unrounded weights).
+//   The weights use a reference maximum that is moved, and O rescaled, only when
+// the row's maximum has risen by more than 8 (2^8 fits every type on the way), so O is
+// rarely rescaled.
 //   warps 0..3, 4..7  softmax and epilogue of group 0, 1
 //   warp 8            takes the items; TMA loads: Q once an item, a ring of K and V
 //                     tiles, one box a page (or 128 rows of a longer one), 64
 //                     columns wide
-//   warps 9, 10       MMA issue of group 0, 1 (and TMEM allocation). The waits and
-//                     commits of a tile take one warp longer than its MMAs (64
-//                     cycles each): one warp for both groups was the bound. The V
-//                     rows of the last 16-key group that lie past the keys are
-//                     zeroed here (a weight of 0 times a NaN is a NaN).
+//   warps 9, 10       MMA issue of group 0, 1 (and TMEM allocation): the waits and
+//                     commits for both groups would take one warp longer than the
+//                     MMAs. The V rows of the last 16-key group that lie past the
+//                     keys are zeroed here (a weight of 0 times a NaN is a NaN).
+//
+// What bounds it. A step of both groups (256 rows, 64 keys) at D = 128 is 1,040
+// cycles of MMAs issued back to back and 1,000 of softmax, which overlap; it takes
+// about 1,750, in which each issuing warp is held for 740 cycles by an S's eight MMAs (33
+// cycles each alone) and 410 by a product's four (64 each): the tensor pipe is 42% busy, the
+// warps issue in 32% of the cycles, L2 and DRAM under 20%. Steps of 128 keys, one buffer, wait
+// for the softmax instead: 294 us for a prefix of 65,553 (316 tokens, 28 heads on
+// 4, D = 64; 149 GFLOP) instead of 271 (0.29 of the measured tensor rate), 304 instead of
+// 299 for 128 requests, 1,144 tokens, with a prefix of 8,192 and up to 2,048 own keys
+// (32 heads on 8, D = 128; 173 GFLOP, 0.59 GB; 0.31). TMEM's 512 columns are all taken at
+// D = 128 (two O, four S), so that wider steps with two buffers have no room.
+// 128 requests of one token, up to 4,096 own keys: 234 us, 4.7 TB/s (0.69 of the
+// measured copy bandwidth; the ring's five tiles are what the SM has in flight).
+// One token over 1,333 keys: 22.5 us, three dependent launches.
+//
 // Every wait is bounded: one that runs out records DSPARK_ERR_TIMEOUT, the
 // roles wind down, issued copies and MMAs land, and the TMEM is freed.
 #include <algorithm>
@@ -52,7 +69,8 @@
 
 namespace dspark {
 
-constexpr int kATile = 128;        // keys a tile
+constexpr int kATile = 128;        // keys a tile of the ring
+constexpr int kAChunk = 64;        // keys a step
 constexpr int kASoftmaxWarps = 8;    // four a group: one thread a row
 constexpr int kAThreads = 32 * (kASoftmaxWarps + 3);
 constexpr int kPlanShare = 6;      // items are at most about 1/6 of an SM's share of the work
@@ -344,10 +362,10 @@ __global__ void __launch_bounds__(kAThreads, 1)
   uint64_t* empty = full + kSlots;
   uint64_t* qFull = empty + kSlots;  // [2] Q of a half
   uint64_t* qEmpty = qFull + 2;      // [2]
-  uint64_t* sFull = qEmpty + 2;   // [2] S of a half is in TMEM
-  uint64_t* pFull = sFull + 2;    // [2][2] P of a group is in TMEM: its first 64 keys, the others
-  uint64_t* oFull = pFull + 4;    // [2] O of a half is complete
-  uint64_t* oEmpty = oFull + 2;   // [2] the epilogue has read O
+  uint64_t* sFull = qEmpty + 2;   // [2][2] S of a group and buffer is in TMEM
+  uint64_t* pFull = sFull + 4;    // [2][2] P is, in its place
+  uint64_t* oDone = pFull + 4;    // [2][2] P V has been added to O
+  uint64_t* oEmpty = oDone + 4;   // [2] the epilogue has read O
   uint64_t* drain = oEmpty + 2;
   uint64_t* iFull = drain + 1;    // [2] an item is there
   uint64_t* iEmpty = iFull + 2;   // [2] every role has read it
@@ -363,10 +381,11 @@ __global__ void __launch_bounds__(kAThreads, 1)
     for (int g = 0; g < 2; ++g) {
       mbar_init(&qFull[g], 1);
       mbar_init(&qEmpty[g], 2);
-      mbar_init(&sFull[g], 1);
-      mbar_init(&pFull[2 * g], kASoftmaxWarps / 2);
-      mbar_init(&pFull[2 * g + 1], kASoftmaxWarps / 2);
-      mbar_init(&oFull[g], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sFull[2 * g + b], 1);
+        mbar_init(&pFull[2 * g + b], kASoftmaxWarps / 2);
+        mbar_init(&oDone[2 * g + b], 1);
+      }
       mbar_init(&oEmpty[g], kASoftmaxWarps / 2);
       mbar_init(&iFull[g], 1);
       mbar_init(&iEmpty[g], kASoftmaxWarps + 2);
@@ -499,8 +518,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
   } else if (warp > kASoftmaxWarps) {
     // ---- MMA issue, a warp for each group: the whole warp goes through the waits, one elected lane issues ----
     const uint32_t g = warp - (kASoftmaxWarps + 1);
-    const uint32_t idesc_qk = idesc_bf16_f32(128, 128, 0), idesc_pv = idesc_bf16_f32(128, D, 1);
-    uint32_t pPhase = 0, oPhase = 1, qPhase[2] = {0, 0}, q_turn = 0;
+    const uint32_t idesc_qk = idesc_bf16_f32(128, kAChunk, 0), idesc_pv = idesc_bf16_f32(128, D, 1);
+    uint32_t pPhase = 0, oPhase = 1, qPhase = 0, q_turn = 0;  // (pPhase, qPhase: a bit a buffer)
     uint32_t ring = 0, passed = 0;  // ring tiles of the items before; tiles whose arrival this warp has seen
     bool stop = false;
     // descriptor words: start addresses in 16-byte units, the rest constant
@@ -524,56 +543,52 @@ __global__ void __launch_bounds__(kAThreads, 1)
       tc_fence_after();
       return slot;
     };
-    // S of the group from Q buffer qb and the K tile in slot s0, which is signed off
-    auto qk = [&](uint32_t qb, uint32_t s0) {
-      const uint32_t q = q_lo + qb * kTileUnits, kk = kv_lo + s0 * kTileUnits;
+    constexpr uint32_t kChunkUnits = kAChunk * 128 / 16;
+    // S of the group, in buffer h, from Q buffer qb and chunk h of the K tile in slot s0; signed off: the tile if `done`,
+    // Q if `end`
+    auto qk = [&](uint32_t qb, uint32_t s0, uint32_t h, bool done, bool end) {
+      const uint32_t q = q_lo + qb * kTileUnits, kk = kv_lo + s0 * kTileUnits + h * kChunkUnits;
       if (elect_one()) {
 #pragma unroll 1
-        for (int s = 0; s < D / 16; ++s) {
-          const uint32_t off = (s >> 2) * kBoxUnits + (s & 3) * 2;
-          tc_mma_bf16_lo(128u * g, q + off, kHi, kk + off, kHi, idesc_qk, s > 0);
-        }
-        tc_commit(&sFull[g]);
-        tc_commit(&empty[s0]);
+        for (uint32_t c = 0; c < kHalves; ++c)  // (four a turn: 75 cycles an issued step fell to those of the products)
+#pragma unroll
+          for (uint32_t s = 0; s < 4; ++s)
+            tc_mma_bf16_lo(128u * g + kAChunk * h, q + c * kBoxUnits + 2 * s, kHi, kk + c * kBoxUnits + 2 * s, kHi, idesc_qk,
+                           s > 0 ? 1u : c);
+        tc_commit(&sFull[2 * g + h]);
+        if (done) tc_commit(&empty[s0]);
+        if (end) tc_commit(&qEmpty[qb]);
       }
     };
-    // `steps` 16-key steps of O += P V from the `from`-th on
-    auto pv_steps = [&](uint32_t s0, uint32_t from, uint32_t steps, bool first) {
-      const uint32_t v = (kv_lo + s0 * kTileUnits + 128u * from) | (kBoxUnits << 16);  // MN-major: the leading offset is a box
-      const uint32_t d = 256u + 128u * g, a = 128u * g + 8u * from;
-      if (elect_one()) {
-#pragma unroll 1
-        for (uint32_t s = 0; s < steps; ++s) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
-      }
-    };
-    // O += P V with the V tile in slot s0 of `keys` keys, as P arrives (at the group's first tile of an item, once the
-    // epilogue before has read O); the tile is signed off, and O is complete with the last tile
-    auto pv = [&](uint32_t s0, uint32_t keys, bool first_tile, bool last_tile) {
+    // O += P V with chunk h of `keys` keys of the V tile in slot s0, once P is there (at the group's first chunk of an item,
+    // once the epilogue before has read O); the tile is signed off if `done`
+    auto pv = [&](uint32_t s0, uint32_t h, uint32_t keys, bool first, bool done) {
       const uint32_t steps = (keys + 15) >> 4;
       if (keys & 15) {  // V rows past the keys: their weights are 0, but the rows may hold anything
-        unsigned char* v = sKV + s0 * S::kTileBytes;
+        unsigned char* v = sKV + s0 * S::kTileBytes + (kAChunk * h + keys) * 128;
         const uint32_t rows = 16 - (keys & 15);
         for (uint32_t i = lane; i < rows * 8 * kHalves; i += 32) {
           const uint32_t c = i / (rows * 8), rest = i - c * rows * 8;
-          *reinterpret_cast<uint4*>(v + c * S::kBox + (keys + rest / 8) * 128 + (rest % 8) * 16) = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(v + c * S::kBox + rest * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (!warp_wait(&pFull[2 * g], pPhase)) return false;
-      if (first_tile) {
+      if (!warp_wait(&pFull[2 * g + h], (pPhase >> h) & 1u)) return false;
+      pPhase ^= 1u << h;
+      if (first) {
         if (!warp_wait(&oEmpty[g], oPhase)) return false;
         oPhase ^= 1;
       }
       tc_fence_after();
-      pv_steps(s0, 0, min(steps, 4u), first_tile);
-      if (!warp_wait(&pFull[2 * g + 1], pPhase)) return false;
-      pPhase ^= 1;
-      tc_fence_after();
-      if (steps > 4) pv_steps(s0, 4, steps - 4, false);
+      const uint32_t v = (kv_lo + s0 * kTileUnits + h * kChunkUnits) | (kBoxUnits << 16);  // MN-major: the leading offset is a box
+      const uint32_t d = 256u + 128u * g, a = 128u * g + kAChunk * h;
       if (elect_one()) {
-        tc_commit(&empty[s0]);
-        if (last_tile) tc_commit(&oFull[g]);
+#pragma unroll
+        for (uint32_t s = 0; s < kAChunk / 16; ++s)
+          if (s < steps) tc_mma_bf16_ts_lo(d, a + 8u * s, v + 128u * s, kHi, idesc_pv, s > 0 || !first);
+        tc_commit(&oDone[2 * g + h]);
+        if (done) tc_commit(&empty[s0]);
       }
       return true;
     };
@@ -583,45 +598,40 @@ __global__ void __launch_bounds__(kAThreads, 1)
       const uint32_t n_keys = __reduce_max_sync(0xffffffffu, (uint32_t)it.n_keys);
       const uint32_t halves = __reduce_max_sync(0xffffffffu, it.head & kAlternate ? 0u : 1u);
       if (n_keys == 0) break;
-      const uint32_t nt = (n_keys + kATile - 1) / kATile, last_keys = n_keys - (nt - 1) * kATile;
-      if (halves) {  // half g of the rows over every tile: K0 V0 K1 V1 ... in the ring
-        for (uint32_t b = 0; b < 2 && !stop; ++b) {
-          if (!warp_wait(&qFull[b], qPhase[b])) stop = true;
-          qPhase[b] ^= 1;
-        }
-        if (stop) break;
+      const uint32_t nt = (n_keys + kATile - 1) / kATile;
+      // half g of the rows over every tile (K0 V0 K1 V1 ... in the ring), or tiles g, g + 2, ... of all rows
+      // (K0 K1 V0 K2 V1 K3 ...)
+      const uint32_t first = halves ? 0u : g, step = halves ? 1u : 2u, qb = halves ? g : q_turn;
+      for (uint32_t b = 0; b < 2 && !stop; ++b) {
+        if (!halves && b != q_turn) continue;
+        if (!warp_wait(&qFull[b], (qPhase >> b) & 1u)) stop = true;
+        qPhase ^= 1u << b;
+      }
+      if (stop) break;
+      if (halves) {
         if (elect_one()) mbar_arrive(&qEmpty[g ^ 1]);
-        uint32_t s0 = tile(ring);
-        if (stop) break;
-        qk(g, s0);
-        for (uint32_t j = 0; j < nt; ++j) {
-          const bool more = j + 1 < nt;
-          if (!more && elect_one()) tc_commit(&qEmpty[g]);  // no S is left to form
-          s0 = tile(ring + 2 * j + 1);
-          const uint32_t s1 = more ? tile(ring + 2 * j + 2) : 0;  // (seen before P is, not between its MMAs)
-          if (stop || !pv(s0, more ? kATile : last_keys, j == 0, !more)) { stop = true; break; }
-          if (more) qk(g, s1);
-        }
-      } else {  // tiles g, g + 2, ... of all rows: K0 K1 V0 K2 V1 K3 ... in the ring
-        const uint32_t qb = q_turn;
+      } else {
         q_turn ^= 1;
-        if (!warp_wait(&qFull[qb], qPhase[qb])) break;
-        qPhase[qb] ^= 1;
-        if (g < nt) {
-          uint32_t s0 = tile(ring + g);
-          if (stop) break;
-          qk(qb, s0);
-          for (uint32_t j = g; j < nt; j += 2) {
-            const bool more = j + 2 < nt;
-            if (!more && elect_one()) tc_commit(&qEmpty[qb]);
-            s0 = tile(j + 1 < nt ? ring + 2 + 2 * j : ring + 2 * nt - 1);
-            const uint32_t s1 = more ? tile(ring + 2 * j + 3) : 0;
-            if (stop || !pv(s0, j + 1 < nt ? kATile : last_keys, j == g, !more)) { stop = true; break; }
-            if (more) qk(qb, s1);
-          }
-        } else if (elect_one()) {
-          mbar_arrive(&qEmpty[qb]);
+      }
+      auto chunks = [&](uint32_t j) { return n_keys - j * kATile > kAChunk ? 2u : 1u; };
+      if (first < nt) {
+        // two chunks ahead: S of a chunk is formed while the softmax of the one before runs
+        const uint32_t s0 = tile(ring + first), n0 = chunks(first);
+        if (stop) break;
+        qk(qb, s0, 0, n0 == 1, n0 == 1);
+        if (n0 > 1) qk(qb, s0, 1, true, first + step >= nt);
+        for (uint32_t j = first; j < nt; j += step) {
+          const uint32_t next = j + step, n = chunks(j), n1 = next < nt ? chunks(next) : 0u;
+          const uint32_t sv = tile(halves ? ring + 2 * j + 1 : j + 1 < nt ? ring + 2 + 2 * j : ring + 2 * nt - 1);
+          const uint32_t sk = n1 ? tile(ring + 2 * j + 1 + step) : 0;  // (seen before P is, not between its MMAs)
+          const bool end = next + step >= nt;
+          if (stop || !pv(sv, 0, min(n_keys - j * kATile, (uint32_t)kAChunk), j == first, n == 1)) { stop = true; break; }
+          if (n1) qk(qb, sk, 0, n1 == 1, end && n1 == 1);
+          if (n > 1 && !pv(sv, 1, min(n_keys - j * kATile - kAChunk, (uint32_t)kAChunk), false, true)) { stop = true; break; }
+          if (n1 > 1) qk(qb, sk, 1, true, end);
         }
+      } else if (elect_one()) {
+        mbar_arrive(&qEmpty[qb]);
       }
       ring += 2 * nt;
       pass(ring);
@@ -635,7 +645,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + 128u * g, tO = tmem + lane_base + 256u + 128u * g;
     const unsigned long long rate2 = f32x2_pack(p.rate, p.rate), one2 = f32x2_pack(1.f, 1.f);
-    uint32_t nS = 0, nI = 0;
+    uint32_t sPhase = 0, pCount = 0;  // of each buffer: S's phase, the parity of its P's (a bit a buffer)
     bool stop = false;
     for (int k = 0; !stop; ++k) {
       const AttnItem it = take(k);
@@ -650,38 +660,37 @@ __global__ void __launch_bounds__(kAThreads, 1)
       clear = warp_min_i(clear);
       const bool any = clear != 0x7fffffff;
       float m = -INFINITY, z = 0.f;
-      for (int j = halves ? 0 : g; j < nt; j += halves ? 1 : 2, ++nS) {
-        if (!warp_wait(&sFull[g], nS & 1)) { stop = true; break; }
+      bool first = true;
+      uint32_t last = 0;  // the last chunk's buffer
+      for (int key = halves ? 0 : g * kATile; key < it.n_keys;) {
+        const uint32_t h = (key / kAChunk) & 1;
+        if (!warp_wait(&sFull[2 * g + h], (sPhase >> h) & 1u)) { stop = true; break; }
+        sPhase ^= 1u << h;
         tc_fence_after();
-        // Short loops over pieces of S, read from TMEM twice: what is unrolled further overflows the instruction
-        // caches, for which the softmax, MMA and load warps compete.
-        if (any && (j + 1) * kATile > clear) {  // scores of keys that the row does not see: -inf, in TMEM
-          const int left = limit - j * kATile;
-#pragma unroll 1
-          for (int c = 0; c < kATile; c += 8) {
-            uint32_t u[8];
-            tmem_ld8(tS + c, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = c + i < left ? u[i] : 0xff800000u;
-            tmem_st8(tS + c, u);
-          }
-          tmem_st_wait();
-        }
-        float neg = 0.f;
+        const uint32_t tC = tS + kAChunk * h;
         if (any) {
+          if (key + kAChunk > clear) {  // scores of keys that the row does not see: -inf, in TMEM
+            const int left = limit - key;
+#pragma unroll 1
+            for (int c = 0; c < kAChunk; c += 8) {
+              uint32_t u[8];
+              tmem_ld8(tC + c, u);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) u[i] = c + i < left ? u[i] : 0xff800000u;
+              tmem_st8(tC + c, u);
+            }
+            tmem_st_wait();
+          }
+          uint32_t s[kAChunk], w[kAChunk / 2];
+          tmem_ld64_nowait(tC, s);
+          tmem_ld_wait64(s);
           float x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < kATile; c += 64) {
-            uint32_t s[64];
-            tmem_ld64_nowait(tS + c, s);
-            tmem_ld_wait64(s);
+          for (int e = 0; e < 4; ++e) x[e] = fmaxf(__uint_as_float(s[e]), __uint_as_float(s[4 + e]));
 #pragma unroll
-            for (int i = 0; i < 64; i += 8)
+          for (int i = 8; i < kAChunk; i += 8)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) x[e] = max3(x[e], __uint_as_float(s[i + e]), __uint_as_float(s[i + 4 + e]));
-          }
+            for (int e = 0; e < 4; ++e) x[e] = max3(x[e], __uint_as_float(s[i + e]), __uint_as_float(s[i + 4 + e]));
           const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.rate;
           const bool rise = top > m + 8.f || (m == -INFINITY && top > m);
           if (__any_sync(0xffffffffu, rise)) {
@@ -689,7 +698,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
             const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);  // mn >= m; 1 where m stays
             m = mn;
             z *= f;
-            if (j > (halves ? 0 : 1))
+            if (!first) {  // (the chunk before may still be being added; this S says that those before it are)
+              if (!warp_wait(&oDone[2 * g + (h ^ 1)], ((pCount >> (h ^ 1)) & 1u) ^ 1u)) { stop = true; break; }
+              tc_fence_after();
 #pragma unroll 1
               for (int c = 0; c < D; c += 8) {
                 uint32_t u[8];
@@ -698,45 +709,38 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
                 tmem_st8(tO + c, u);
               }
-          }
-          neg = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet: 2^(-inf) = 0
-        }
-        const unsigned long long neg2 = f32x2_pack(neg, neg);
-        unsigned long long z2[2] = {0ull, 0ull};
-#pragma unroll 1
-        for (int c0 = 0; c0 < kATile; c0 += 64) {  // the weights of 64 keys, over columns of S that have been read
-          if (any) {
-            uint32_t s[64], w[64 / 2];
-            tmem_ld64_nowait(tS + c0, s);
-            tmem_ld_wait64(s);
-#pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              float e0, e1;
-              f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), rate2, neg2), e0, e1);
-              e0 = ex2_approx(e0);
-              e1 = ex2_approx(e1);
-              z2[(c >> 1) & 1] = f32x2_fma(f32x2_pack(e0, e1), one2, z2[(c >> 1) & 1]);
-              w[c >> 1] = pack_bf16x2(e0, e1);
             }
-            tmem_st32(tS + c0 / 2, w);
           }
-          if (((c0 + 64) & 63) == 0) {  // 64 keys are done
-            if (any) tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pFull[2 * g + (c0 >> 6)]);
+          const float neg = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet: 2^(-inf) = 0
+          const unsigned long long neg2 = f32x2_pack(neg, neg);
+          unsigned long long z2[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < kAChunk; c += 2) {
+            float e0, e1;
+            f32x2_unpack(f32x2_fma(f32x2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), rate2, neg2), e0, e1);
+            e0 = ex2_approx(e0);
+            e1 = ex2_approx(e1);
+            z2[(c >> 1) & 1] = f32x2_fma(f32x2_pack(e0, e1), one2, z2[(c >> 1) & 1]);
+            w[c >> 1] = pack_bf16x2(e0, e1);
           }
-        }
-        if (any) {
+          tmem_st32(tC, w);
           float s0, s1, s2, s3;
           f32x2_unpack(z2[0], s0, s1);
           f32x2_unpack(z2[1], s2, s3);
           z += (s0 + s1) + (s2 + s3);
+          tmem_st_wait();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pFull[2 * g + h]);
+        pCount ^= 1u << h;
+        last = h;
+        first = false;
+        key += kAChunk;
+        if (!halves && h) key += kATile;  // the other group's tile
       }
       if (stop) break;
-      if (!warp_wait(&oFull[g], nI & 1)) break;
-      ++nI;
+      if (!warp_wait(&oDone[2 * g + last], ((pCount >> last) & 1u) ^ 1u)) break;
       tc_fence_after();
       if (any) {
         const int hq = (it.head & ~kAlternate) * p.G + row % p.G;

@@ -8,9 +8,12 @@
 //   first entry is the sum of the missing pages before it, and its first token's
 //   index the sum of n before it. Each CTA plans kPlanReqs requests and forms
 //   both sums over all earlier requests itself: at 8,192 requests that reads at
-//   most 64 KB from L2 in a CTA, and no CTA waits for another.
-// kv_append_kernel  one 16-byte piece of one token's key or value row a thread
-//   step; bound by bytes (each read once and written once).
+//   most 64 KB from L2 in a CTA, and no CTA waits for another. Bound by latency:
+//   128 requests, 1,144 tokens 8 us a call (the launch's host side), 8,192 requests,
+//   73,720 tokens 12 us (1.05 MB, 0.16 us of bandwidth).
+// kv_append_kernel  one 16-byte piece of one token's key and value row a thread
+//   step; bound by bytes (each read once and written once): 15,904 tokens of 8 heads
+//   of 128 bf16 (130 MB) 23 us, 5.6 TB/s, 0.83 of the measured copy bandwidth.
 #include <algorithm>
 
 #include "common.cuh"

@@ -11,11 +11,12 @@
 // of the top-k set; min-p keeps the entries with w >= min_p. All three are
 // prefixes of that order, so the kept set is "logit above x*, or equal to it
 // and index below cut": one threshold, found in three steps.
-//   1  the row streams in once from memory: its maximum, and an estimate of its
-//      distribution in 2048 bins of 1/16 octave of weight. The largest entry of
-//      each 16-byte piece is counted once; for top-p the piece's first entry, if
-//      it is another one, stands for the rest of all pieces. (A shared-memory add
-//      for every entry bounds the pass: 15 us a row of 129,280 instead of 6.)
+//   1  the row streams in once from memory: its maximum, and for top-k and top-p an
+//      estimate of its distribution in 2048 bins, 16 an octave of weight for top-k (a
+//      rank may lie far down), 64 for top-p. The largest entry of each 16-byte piece
+//      is counted once; for top-p the piece's first entry, if it is another one,
+//      stands for the rest of all pieces. (A shared-memory add for every entry bounds
+//      the pass: 15 us a row of 129,280 instead of 6.)
 //   2  the estimate says down to which logit top-k reaches (at least k pieces have
 //      a larger one), or between which two logits top-p ends, with a margin; a
 //      second pass (from L2) collects the entries of that range, or all from its
@@ -25,9 +26,21 @@
 //   3  exact selection among the collected entries: by comparing all pairs of a
 //      short list, else by radix selection on order-preserving integer keys
 //      (1024-bin histograms of counts or masses over a shrinking key range).
+// A draw needs the kept masses in index order: those above the collected range are kept
+// by runs of 128 pieces in the second pass, the list's are added to them, and only the run
+// that holds the token is read again. Without such a pass (top-p off) the row is.
 // Where no range fits the list (thousands of equal entries, logits hundreds of
 // octaves apart), the radix selection runs on the row itself. One block a row: a
 // row of 129,280 bf16 is 258 KB, and the rows in flight stay in L2 between passes.
+//
+// What bounds it: issue slots. A pass that only compares takes 6,500 cycles a row of
+// 129,280 bf16 entries on an SM of its own, one that weighs every entry 19,000, and one that also
+// adds up what lies above the range and collects 38,000; the serial steps between
+// (bins, selection, ties) are 25,000. 128 such rows drawn, one an SM: greedy 9 us, top-k
+// 50 19, top-k 1000 27, top-p 0.95 48, top-p 0.99 52, all entries 21 (floor 4.9, the bytes);
+// 128 rows of mixed parameters 51. 2,176 rows truncated, two blocks an SM: greedy 236 us (4.8 TB/s),
+// top-k 50 329, top-p 0.95 555, mixed 350 (3.2 TB/s, 0.48 of the measured copy
+// bandwidth). 288 rows of 32,003 float32 truncated, mixed: 50 us.
 #include <algorithm>
 
 #include "common.cuh"
@@ -43,6 +56,7 @@ constexpr int kSList = 7168;    // collected entries (80 KB with all else: two b
 constexpr int kRun = 128;       // neighbouring pieces whose mass above the collected range is kept for the draw
 constexpr int kRuns = kSBins;
 constexpr uint32_t kSSmem = kWBins * 4 + kWBins * 4 + kSList * 8 + kRuns * 8;
+static_assert(kRuns == kSBins, "find_bin looks the token's run up");
 static_assert(kSBins * 12 <= kWBins * 8, "the selection's arrays lie over the weight bins");
 
 struct SampleParams {
@@ -223,15 +237,15 @@ struct RowView {
     return make_uint4(w, w, w, w);
   }
   // f(piece, first index, is it one) for the pieces g0 <= g < g1, the tid-th of every nt; the lanes of a warp stay
-  // together. after(g) follows every four pieces, g the first of them, `gap` apart: nt, or with kRuns 32, so that a
+  // together. after(g) follows every four pieces, g the first of them, `gap` apart: nt, or with kByRun 32, so that a
   // warp's four rows of pieces are kRun neighbours (6% slower where the row comes from memory).
   struct Nothing {
     __device__ __forceinline__ void operator()(int) const {}
   };
-  template <bool kRuns = false, class F, class After = Nothing>
+  template <bool kByRun = false, class F, class After = Nothing>
   __device__ __forceinline__ void pieces(int g0, int g1, int tid, int nt, F f, After after = After()) const {
     if (g0 >= g1) return;
-    const int gap = kRuns ? 32 : nt, at = kRuns ? (tid >> 5) * 32 * U + (tid & 31) : tid;
+    const int gap = kByRun ? 32 : nt, at = kByRun ? (tid >> 5) * 32 * U + (tid & 31) : tid;
     uint4 q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
