@@ -372,12 +372,15 @@ dspark_status dspark_sts_apply(int32_t R, int32_t gamma, const float* conf, cons
  *   block_table [R, max_pages] int32 in/out  the new pages' entries are written (-1 where the
  *                                   list has run out), all others left as they are
  *   q_start     [R+1] int32 out     first new token of each request, and their number T
- *   kv_len      [R] int32 out       cached_len + new_len
+ *   kv_len      [R] int32 out       cached_len + new_len (of the tokens within the capacity)
  *   positions   [capacity] int32 out  position of each new token in its request; -1 past T
  *   slots       [capacity] int64 out  page * page_size + offset; -1 where there is no page, and past T
  *   used        [1] int32 out       free pages taken
- * A list, a table row or a capacity that is too short sets DSPARK_ERR_CAPACITY
- * (tokens past the capacity are not written, q_start stays within it).
+ * A list, a table row or a capacity that is too short sets DSPARK_ERR_CAPACITY.
+ * Where new_len sums to more than the capacity, the outputs are the plan of the
+ * tokens that fit: the request that the capacity cuts gets what is left of it,
+ * the later ones nothing, in kv_len and pages too, so that the calls below
+ * place and attend the tokens that fit as they stand in their requests.
  */
 dspark_status dspark_page_plan(int32_t R, int32_t page_size, int32_t max_pages, int32_t n_free,
                                int32_t capacity, const int32_t* cached_len, const int32_t* new_len,

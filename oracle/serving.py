@@ -7,14 +7,15 @@ import numpy as np
 
 
 def page_plan(cached, new, free, page, table, capacity):
-    """Block table, starts, lengths, positions, slots and pages used; short lists leave -1."""
+    """Block table, starts, lengths, positions, slots and pages used; short lists leave -1. Of the new tokens those that
+    fit the capacity are planned, in request order."""
     table = np.array(table, dtype=np.int64)
     R, width = table.shape
-    taken, tok, short = 0, 0, False
+    taken, tok, short = 0, 0, sum(max(0, int(n)) for n in new) > capacity
     q_start, kv_len, positions, slots = [], [], [], []
     for r in range(R):
-        q_start.append(min(tok, capacity))
-        c, n = int(cached[r]), int(new[r])
+        q_start.append(tok)
+        c, n = int(cached[r]), min(int(new[r]), capacity - tok)
         for col in range(-(-c // page), -(-(c + n) // page)):
             page_id = int(free[taken]) if taken < len(free) else -1
             short |= page_id < 0 or col >= width
@@ -28,11 +29,9 @@ def page_plan(cached, new, free, page, table, capacity):
             slots.append(-1 if page_id < 0 else page_id * page + pos % page)
             tok += 1
         kv_len.append(c + n)
-    short |= tok > capacity
-    q_start.append(min(tok, capacity))
-    pad = max(0, capacity - tok)
-    return {"table": table, "q_start": q_start, "kv_len": kv_len, "positions": (positions + [-1] * pad)[:capacity],
-            "slots": (slots + [-1] * pad)[:capacity], "used": min(taken, len(free)), "short": short}
+    q_start.append(tok)
+    pad = [-1] * (capacity - tok)
+    return {"table": table, "q_start": q_start, "kv_len": kv_len, "positions": positions + pad, "slots": slots + pad, "used": min(taken, len(free)), "short": short}
 
 
 def attention(q, k_cache, v_cache, prefix_pages, prefix_len, table, q_start, kv_len, scale):

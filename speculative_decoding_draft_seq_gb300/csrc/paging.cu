@@ -6,7 +6,8 @@
 //   tokens and needs ceil((c + n) / p) for n more (page size p). The missing
 //   ones are taken from the list of free pages in request order, so a request's
 //   first entry is the sum of the missing pages before it, and its first token's
-//   index the sum of n before it. Each CTA plans kPlanReqs requests and forms
+//   index the sum of n before it. A request that the token capacity cuts asks for
+//   what is left of it, the later ones for nothing. Each CTA plans kPlanReqs requests and forms
 //   both sums over all earlier requests itself: at 8,192 requests that reads at
 //   most 64 KB from L2 in a CTA, and no CTA waits for another. Bound by latency:
 //   128 requests, 1,144 tokens 8 us a call (the launch's host side), 8,192 requests,
@@ -53,6 +54,7 @@ __device__ __forceinline__ long long block_sum_ll(long long v, long long* sh) {
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
   __shared__ long long sh[32];
   __shared__ long long s_tok[kPlanReqs + 1], s_pg[kPlanReqs + 1];  // token / free-list starts of this CTA's requests
+  __shared__ long long s_warp[kPlanReqs / 32];
   __shared__ int s_c[kPlanReqs], s_have[kPlanReqs];
   const int tid = threadIdx.x, r0 = blockIdx.x * kPlanReqs, nr = min(kPlanReqs, p.R - r0);
   bool bad = false;
@@ -79,46 +81,38 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
     tok = block_sum_ll(tok, sh);
     pg = block_sum_ll(pg, sh);
   }
-  if (tid < kPlanReqs) {  // this CTA's requests: running sums over four warps
-    int c = 0, n = 0;
-    long long miss = 0;
-    if (tid < nr) {
-      lengths(r0 + tid, c, n);
-      miss = missing(c, n);
-      s_c[tid] = c;
-      s_have[tid] = (int)pages_of((uint32_t)c);
-      const long long end = (long long)c + n;
-      bad |= end > 0x7fffffffll;
-      p.kv_len[r0 + tid] = (int)min(end, 0x7fffffffll);
-    }
-    long long a = n, b = miss;
+  // This CTA's requests: running sums over four warps. Tokens first: the capacity may cut a request's.
+  auto running = [&](long long a, long long first, long long* to) {  // to[i] = first + the sum of a over requests 0..i-1
+    if (tid < kPlanReqs) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-      if ((tid & 31) >= o) { a += x; b += y; }
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, a, o);
+        if ((tid & 31) >= o) a += x;
+      }
+      if ((tid & 31) == 31) s_warp[tid >> 5] = a;
     }
-    s_tok[tid + 1] = a;
-    s_pg[tid + 1] = b;
-  }
-  __syncthreads();
-  if (tid < kPlanReqs) {
-    long long a = tok + s_tok[tid + 1], b = pg + s_pg[tid + 1];
-    for (int w = 0; w < (tid >> 5); ++w) { a += s_tok[32 * w + 32]; b += s_pg[32 * w + 32]; }
-    tok = a;  // (held back until every thread has read the warps' sums)
-    pg = b;
-  }
-  __syncthreads();
-  if (tid < kPlanReqs) {
-    s_tok[tid + 1] = tok;
-    s_pg[tid + 1] = pg;
-    if (tid == 0) {
-      int c, n;
-      lengths(r0, c, n);
-      s_tok[0] = tok - n;
-      s_pg[0] = pg - missing(c, n);
+    __syncthreads();
+    if (tid < kPlanReqs) {
+      for (int w = 0; w < (tid >> 5); ++w) a += s_warp[w];
+      to[tid + 1] = first + a;
+      if (tid == 0) to[0] = first;
     }
+    __syncthreads();
+  };
+  int c = 0, n = 0;
+  if (tid < nr) lengths(r0 + tid, c, n);
+  running(n, tok, s_tok);
+  long long miss = 0;
+  if (tid < nr) {
+    const int fit = (int)max(0ll, min((long long)n, p.capacity - s_tok[tid]));
+    miss = missing(c, fit);
+    s_c[tid] = c;
+    s_have[tid] = (int)pages_of((uint32_t)c);
+    const long long end = (long long)c + fit;
+    bad |= end > 0x7fffffffll;
+    p.kv_len[r0 + tid] = (int)min(end, 0x7fffffffll);
   }
-  __syncthreads();
+  running(miss, pg, s_pg);
   // new entries of the block table: -1 where the list has run out
   bool full = false;
   const int warp = tid >> 5, lane = tid & 31;
@@ -157,11 +151,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
     p.positions[t] = (int)pos;
     p.slots[t] = id < 0 ? -1ll : (long long)id * p.page + pos % page;
   }
+  // pages are taken up to the CTA in which the capacity is reached (pg of the later ones is not their start: a request
+  // that the capacity cuts counts in full there)
+  if (tid == 0 && (r0 == 0 || s_tok[0] < p.capacity) && (t_end >= p.capacity || r0 + nr == p.R))
+    p.used[0] = (int)min(s_pg[nr], (long long)p.n_free);
   if (r0 + nr == p.R) {
-    if (tid == 0) {
-      p.q_start[p.R] = (int)min(t_end, (long long)p.capacity);
-      p.used[0] = (int)min(s_pg[nr], (long long)p.n_free);
-    }
+    if (tid == 0) p.q_start[p.R] = (int)min(t_end, (long long)p.capacity);
     for (long long t = t_end + tid; t < p.capacity; t += kPlanThreads) {
       p.positions[t] = -1;
       p.slots[t] = -1ll;

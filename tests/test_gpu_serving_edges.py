@@ -1,0 +1,82 @@
+"""Serving operators where one call's result meets another's assumptions: short token capacities, calls without
+tokens, scores that are no number, temperatures and logits at the ends of float32."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_serving as G
+import test_gpu_serving_use as U
+from oracle import serving as S
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from speculative_decoding_draft_seq_gb300 import dspark
+
+DEV = "cuda"
+
+
+# ---------------------------------------------------------------------------------------------
+# a plan whose token capacity runs out
+
+@pytest.mark.parametrize("capacity", [0, 1, 4, 7, 8, 11, 300, 301, 1000, "128 requests", "256 requests"])
+@pytest.mark.parametrize("page", [1, 16])
+def test_page_plan_past_its_capacity(capacity, page):
+    """A short plan is the plan of the tokens that fit, with the status word set: lengths, table entries and pages taken
+    as if the request that is cut had asked for what is left of it, and the later ones for nothing."""
+    rng = np.random.default_rng(5)
+    R = 400
+    c, n = rng.integers(0, 50, R), rng.integers(0, 6, R)
+    n[:3] = [4, 3, 4]
+    if isinstance(capacity, str):  # exactly what the first of them ask for
+        capacity = int(n[:int(capacity.split()[0])].sum())
+    width = int((-(-(c + n) // page)).max())
+    table = np.arange(R * width).reshape(R, width)
+    free = 100000 + rng.permutation(3000)
+    fit = np.clip(capacity - (np.cumsum(n) - n), 0, n)
+    want = S.page_plan(c, fit, free, page, table, capacity)
+    t, q_start, kv_len, pos, slots, used, status = G.run_plan(c, n, free, page, table, capacity)
+    assert status == (dspark.ERR_CAPACITY if n.sum() > capacity else dspark.OK)
+    assert q_start.tolist() == want["q_start"] and kv_len.tolist() == want["kv_len"]
+    assert np.array_equal(t.cpu().numpy(), want["table"]) and used.item() == want["used"]
+    assert pos.tolist() == want["positions"] and slots.tolist() == want["slots"]
+
+
+def test_attention_after_a_short_plan():
+    """plan -> append -> attention with room for 6 of 9 new tokens: the tokens that fit are attended at their own
+    positions, over keys that were appended (the others' slots hold NaN)."""
+    page, Hq, Hkv, D = 16, 4, 2, 64
+    cached, new, capacity = [20, 15, 40], [3, 4, 2], 6
+    whole = G.attention_case([3, 3], [23, 18], 0, Hq, Hkv, D, page, seed=11)  # request 1 cut to 3 tokens, request 2 without
+    n_pages = whole["k"].shape[0] + 4
+    k, v = (torch.full((n_pages, page, Hkv, D), math.nan, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    kn, vn = (torch.full((sum(new), Hkv, D), math.nan, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    table = torch.full((3, 4), n_pages - 1, dtype=torch.int32, device=DEV)
+    free, at = [], 0
+    for r in range(2):
+        for j in range(-(-int(whole["kv_len"][r]) // page)):
+            src, first = int(whole["table"][r, j]), j * page
+            if first < cached[r]:
+                table[r, j] = src
+                m = min(page, cached[r] - first)
+                k[src, :m], v[src, :m] = whole["k"][src, :m], whole["v"][src, :m]
+            else:
+                free.append(src)
+        for i in range(3):
+            pos = cached[r] + i
+            pg, off = int(whole["table"][r, pos // page]), pos % page
+            kn[at], vn[at] = whole["k"][pg, off], whole["v"][pg, off]
+            at += 1
+    free += list(range(whole["k"].shape[0], n_pages - 1))
+    i32 = dict(dtype=torch.int32, device=DEV)
+    q_start, kv_len, pos = torch.empty(4, **i32), torch.empty(3, **i32), torch.empty(capacity, **i32)
+    slots, used = torch.empty(capacity, dtype=torch.int64, device=DEV), torch.empty(1, **i32)
+    ws = G._ws()
+    dspark.page_plan(G._i32(cached), G._i32(new), G._i32(free), page, table, q_start, kv_len, pos, slots, used, ws)
+    assert dspark.device_status(ws) == dspark.ERR_CAPACITY
+    dspark.kv_append(kn[:capacity], vn[:capacity], slots, k, v, G._ws())
+    want, want_lse = G.run_attention(whole)
+    got, got_lse = G.run_attention(dict(whole, k=k, v=v, table=table, q_start=q_start, kv_len=kv_len))
+    assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
