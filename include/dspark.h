@@ -426,7 +426,7 @@ dspark_status dspark_kv_append(int32_t T, int32_t n_kv_heads, int32_t head_dim, 
  * id outside [0, n_pages) (its keys and values read as zeros), by a kv_len
  * outside [0, max_pages * page_size] (clamped), and by a q_start that does not
  * begin at 0, falls or passes T (nothing is written then). Nothing outside the
- * tensors is read. Three launches.
+ * tensors is read. Three launches; none for T = 0, whatever the pointers.
  */
 size_t dspark_attention_workspace_bytes(int32_t R, int32_t T, int32_t n_heads, int32_t n_kv_heads,
                                         int32_t head_dim);

@@ -920,7 +920,7 @@ extern "C" dspark_status dspark_prefix_attention(int32_t R, int32_t T, int32_t n
       (page_size & (page_size - 1)) != 0 || n_pages < 1 || max_pages < 1 || prefix_len < 0 || prefix_len > 0x7fffff00 ||
       (long long)T * n_heads > (1ll << 30) || !(scale > 0.f) || !isfinite(scale))
     return DSPARK_ERR_INVALID_ARG;
-  if (!q || !k_cache || !v_cache || (prefix_len > 0 && !prefix_pages) || !block_table || !q_start || !kv_len || !out)
+  if (T > 0 && (!q || !k_cache || !v_cache || (prefix_len > 0 && !prefix_pages) || !block_table || !q_start || !kv_len || !out))
     return DSPARK_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
        reinterpret_cast<uintptr_t>(out)) & 15)

@@ -80,3 +80,15 @@ def test_attention_after_a_short_plan():
     want, want_lse = G.run_attention(whole)
     got, got_lse = G.run_attention(dict(whole, k=k, v=v, table=table, q_start=q_start, kv_len=kv_len))
     assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
+
+
+# ---------------------------------------------------------------------------------------------
+# a call without tokens
+
+def test_attention_without_tokens():
+    c = G.attention_case([0, 0], [40, 8], 64, 8, 2, 64, 16)
+    assert c["q"].shape[0] == 0
+    out, lse = G.run_attention(c)
+    assert out.shape == (0, 8, 64) and lse.shape == (0, 8)
+    out, _ = G.run_attention(G.attention_case([0, 0], [40, 8], 64, 8, 2, 64, 16, capacity=3))
+    assert torch.all(out == 77.0)
