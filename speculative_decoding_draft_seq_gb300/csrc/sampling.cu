@@ -80,6 +80,11 @@ __device__ __forceinline__ uint32_t logit_key(float x) {  // larger logit, large
 __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
+// The next smaller logit. The key below 0's would be -0's, which no entry has: -0 is equal to 0 in every comparison.
+__device__ __forceinline__ float logit_below(float x) {
+  const uint32_t k = logit_key(x) - 1u;
+  return key_logit(k == 0x7fffffffu ? k - 1u : k);
+}
 __device__ __forceinline__ float rule_weight(float x, float M, float rate) {
   return x == -INFINITY ? 0.f : exp2f(__fmul_rn(__fsub_rn(x, M), rate));
 }
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
         // no entry of the range before is in this one, and it reaches a bin further (more at a later attempt)
         const float reach = 1.5f * (float)attempt / bins.c;
         if (move > 0) {
-          x_hi = fminf(x_hi, key_logit(logit_key(r_lo) - 1));
+          x_hi = fminf(x_hi, logit_below(r_lo));
           x_lo = fminf(x_lo, r_lo - reach);
         } else if (move < 0) {
           x_lo = fmaxf(x_lo, key_logit(logit_key(r_hi) + 1));

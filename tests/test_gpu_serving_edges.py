@@ -92,3 +92,38 @@ def test_attention_without_tokens():
     assert out.shape == (0, 8, 64) and lse.shape == (0, 8)
     out, _ = G.run_attention(G.attention_case([0, 0], [40, 8], 64, 8, 2, 64, 16, capacity=3))
     assert torch.all(out == 77.0)
+
+
+# ---------------------------------------------------------------------------------------------
+# sampling: a search for top-p's end that moves its range across zero
+
+@pytest.mark.parametrize("rows", [1, 200])
+def test_top_p_ranges_that_meet_at_zero(rows):
+    """A row whose sampled distribution (the largest and the first entry of four) misleads the search for top-p's end
+    twice, each time further down, with the second range ending at a logit of 0 that hundreds of entries have. At the
+    temperature whose rate is 1, with bins of 1/64:
+      first   of the estimate's mass the limit lies at logit 1 and the next bin with entries is that of 2/64
+      second  from 1.5/64 down; 1/64 is estimated at four times its number, so that the range goes no further than 0
+      third   from 0 down, exclusive: the limit is met among the entries of -1/64
+    Weights 2^(x - 1), the masses in floor(. 2^40): kept set and token in exact integers."""
+    T = np.float32(1.4426950408889634)
+    rng = np.random.default_rng(4)
+    r = -0.05
+    pieces = ([[1 / 64, 1.0, r, r]] * 1525 + [[1.0, r, r, r]] * 2000 + [[2 / 64, r, r, r]] * 20 + [[-1 / 64, r, r, r]] * 100)
+    x = np.array(pieces, dtype=np.float32)[rng.permutation(len(pieces))]
+    hidden = np.flatnonzero(x[:, 0] > 0)  # where the third of four is neither the first nor the largest
+    x[rng.permutation(hidden)[:400], 2] = 0.0
+    x = x.reshape(-1)
+    w = np.floor(np.exp2(x.astype(np.float64) - 1) * 2.0 ** 40)
+    ten = 10 * 2.0 ** 40  # of the 49.5 that the entries of -1/64 weigh
+    p = np.float32((w[x >= 0].sum() + ten) / w.sum())
+    xt = torch.from_numpy(np.tile(x, (rows, 1))).to(DEV)
+    tokens, prob, out, st, _ = G.run_rule(xt, T, 0, p, 0.0, np.linspace(0.0, 0.999, rows))
+    assert st == dspark.OK
+    kept, _ = (a.cpu().numpy() if torch.is_tensor(a) else a for a in U.plain_rule(xt[0], T, 0, p, 0.0, 0.5))
+    assert kept[x >= 0].all() and 15 <= kept[x < 0].sum() <= 25 and np.all(x[kept] >= np.float32(-1 / 64))
+    for i in range(rows):
+        G.check_kept(xt, out, i, kept)
+    c = np.cumsum(np.where(kept, w, 0.0))
+    for i, u in enumerate(np.linspace(0.0, 0.999, rows)):
+        assert tokens[i] == np.searchsorted(c, u * c[-1], side="right") or np.abs(c - u * c[-1]).min() < 2.0 ** -17 * c[-1]
