@@ -443,7 +443,8 @@ dspark_status dspark_prefix_attention(int32_t R, int32_t T, int32_t n_heads, int
  * The target's sampling rule on N rows of logits [N, V] dtype (V <= 2^20), its
  * parameters one a row: temperature (0 = greedy: the first maximum alone),
  * top_k (<= 0 or >= V: off), top_p (>= 1: off), min_p (<= 0: off, at most 1).
- *   weights w = 2^((l - M) r) in float32, M the row's maximum, r = min(log2(e) / T, 1e30); masses
+ *   weights w = 2^((l - M) r) in float32, M the row's maximum, r = min(log2(e) / T, 1e30) (0 at
+ *   T = inf, where every finite entry weighs 1; an l - M past float32's range counts in full); masses
  *   floor(w 2^40). With the row sorted by (logit descending, index ascending), top-k keeps the
  *   first top_k entries; of these top-p keeps the ones whose mass before them is below
  *   max(1, floor(top_p S)), S the mass of the top-k set; of these min-p keeps the ones with

@@ -85,8 +85,13 @@ __device__ __forceinline__ float logit_below(float x) {
   const uint32_t k = logit_key(x) - 1u;
   return key_logit(k == 0x7fffffffu ? k - 1u : k);
 }
+// (A distance that overflows is multiplied at half its size. That matters to rates below kTinyRate alone: at larger ones
+// 2^(-inf) = 0 and 2^(-3.4e38 rate) = 0 are the same weight.)
+constexpr float kTinyRate = 1e-36f;
 __device__ __forceinline__ float rule_weight(float x, float M, float rate) {
-  return x == -INFINITY ? 0.f : exp2f(__fmul_rn(__fsub_rn(x, M), rate));
+  const float d = __fsub_rn(x, M);
+  const float y = d == -INFINITY ? 2.f * __fmul_rn(__fsub_rn(0.5f * x, 0.5f * M), rate) : __fmul_rn(d, rate);
+  return x == -INFINITY ? 0.f : exp2f(y);
 }
 // floor(x S) for x in [0, 1), x to 53 bits, from the bits of x (FP64 instructions are slow here)
 __device__ __forceinline__ unsigned long long scale_mass(double x, unsigned long long S) {
@@ -496,7 +501,8 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
   const float min_w = fminf(fmaxf(__ldg(p.min_p + r), 0.f), 1.f);
   const int k = __ldg(p.top_k + r);
   const bool greedy = !(T > 0.f), by_k = !greedy && k > 0 && k < V, by_p = !greedy && tp < 1.f;
-  const float rate = fminf(fmaxf(__fdiv_rn(1.4426950408889634f, T), 1e-37f), 1e30f);  // (T = inf: no product 0 inf)
+  const float rate = fminf(__fdiv_rn(1.4426950408889634f, T), 1e30f);  // (0 at T = inf)
+  const bool tiny = rate < kTinyRate;  // weights by rule_weight alone: the packed ones know no distance past float32's range
 
   // ---- 1: maximum and weight bins ----
   using Row = RowView<Tin, (kBlocks > 1 ? 4 : 8)>;
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
     m0 = block_max(m0, shf);
     if (!(fabsf(m0) < INFINITY)) m0 = 0.f;
     const float o = rintf(m0 * bins.c);
-    binned = fabsf(o) <= 524288.f && rate > 0.f;  // else too far for bins of 1/16 octave in float32
+    binned = fabsf(o) <= 524288.f && !tiny;  // else too far for bins of 1/16 octave in float32
     bins.off = 8388608.f + (by_k ? kWBins / 2 : kWBins - 6 * 64) - o;
     auto count = [&](float x, uint32_t n) { atomicAdd(&cum_c[kWBins - 1 - WeightBins::index(bins.pos(x))], n); };
     auto visit = [&](const uint4& q, int, bool ok) {
@@ -1108,6 +1114,11 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
     sum.add(MassPair(kept(x, v) ? rule_weight(x, M, rate) : 0.f, 0.f));
   };
   auto weigh_piece = [&](const uint4& q, int v) {
+    if (tiny) {
+#pragma unroll 1
+      for (int e = 0; e < Row::E; ++e) weigh(v + e);
+      return;
+    }
     float x[Row::E];
     Row::split(q, x);
     const bool plain = v + Row::E <= cut;  // ties of the whole piece are kept

@@ -95,6 +95,56 @@ def test_attention_without_tokens():
 
 
 # ---------------------------------------------------------------------------------------------
+# sampling: temperatures and logits at the ends of float32
+
+def test_rule_at_infinite_temperature_is_uniform():
+    """Every finite entry weighs 1, whatever its size and whatever the distance to the maximum overflows to."""
+    inf = math.inf
+    x = torch.tensor([[-3e38, 3e38, 0.0, -inf, 1.0, 2.0]], device=DEV).repeat(6, 1)
+    tokens, prob, out, st, _ = G.run_rule(x, np.float32(np.inf), [0, 0, 0, 0, 4, 0], [1.0, 1.0, 1.0, 0.5, 1.0, 1.0],
+                                          [0.0, 0.0, 0.0, 0.0, 0.0, 1.0], [0.05, 0.5, 0.99, 0.99, 0.99, 0.99])
+    assert st == dspark.OK
+    # kept: all five; by logit 3e38, 2, 1 reach a mass of 2.5 of 5; the four largest; all five reach min_p = 1
+    assert tokens.tolist() == [0, 2, 5, 5, 5, 5]
+    assert np.allclose(prob, [0.2, 0.2, 0.2, 1 / 3, 0.25, 0.2], rtol=2.0 ** -22)
+    low = float(torch.finfo(torch.float32).min)
+    assert np.array_equal(out[0] == low, [False, False, False, True, False, False])
+    assert np.array_equal(out[3] == low, [True, False, True, True, False, False])
+    assert np.array_equal(out[4] == low, [True, False, False, True, False, False])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T", [3e35, 2e36, 3e37, 1e38, 3.4e38, np.inf])
+@pytest.mark.parametrize("V,at", [(3, 0), (90, 0), (90, 1), (5000, 3)])
+def test_rule_at_huge_temperatures(dtype, T, V, at):
+    """Logits of up to float32's range at temperatures of the same size, against the oracle in 64 bits. (The rate is
+    rounded to float32 or below its normal range, 2^-149 of up to 2^-126.8 at 3.4e38: 2^-22, times an exponent of at most 6.)"""
+    rng = np.random.default_rng([V, at])
+    x = (rng.random((24, V)) * 6.7e38 - 3.35e38).astype(np.float32)
+    x[::4, ::3] = -math.inf
+    x[:, V // 2] = 3.3e38
+    flat = torch.zeros(24 * V + at, dtype=G.TORCH[dtype], device=DEV)
+    xt = flat[at:].view(24, V)
+    xt.copy_(torch.from_numpy(x))
+    k, p = rng.choice([0, 0, 2, V // 2], 24), rng.choice([1.0, 1.0, 0.4, 0.9], 24).astype(np.float32)
+    m, u = rng.choice([0.0, 0.0, 0.2], 24).astype(np.float32), rng.random(24)
+    tokens, prob, out, st, st2 = G.run_rule(xt, np.float32(T), k, p, m, u)
+    assert st == dspark.OK and st2 == dspark.OK
+    eps, sure = 2.0 ** -17 + V * 2.0 ** -40, 0
+    for r in range(24):
+        kept, w, margin = S.rule(xt[r].float().cpu().numpy(), float(np.float32(T)), int(k[r]), float(p[r]), float(m[r]))
+        if margin <= 4 * eps:
+            continue
+        G.check_kept(xt, out, r, kept)
+        v, pr, gap = S.draw(kept, w, u[r])
+        if gap <= 4 * eps:
+            continue
+        sure += 1
+        assert tokens[r] == v and abs(prob[r] - pr) <= 4 * eps * pr + 2.0 ** -40
+    assert sure >= 8
+
+
+# ---------------------------------------------------------------------------------------------
 # sampling: a search for top-p's end that moves its range across zero
 
 @pytest.mark.parametrize("rows", [1, 200])
