@@ -417,7 +417,8 @@ dspark_status dspark_kv_append(int32_t T, int32_t n_kv_heads, int32_t head_dim, 
  *   lse          [T, n_heads] float out or NULL, the natural log of the sum of e^score
  * A query that sees no key gets out = 0 and lse = -inf. Cache entries that no
  * query of the call sees are never part of a result, whatever bits they hold;
- * those that one sees must be finite. Rows of q past q_start[R] are left out.
+ * those that one sees must be finite. A query with a NaN score gets out and lse
+ * NaN. Rows of q past q_start[R] are left out.
  * Scores, softmax statistics and accumulators are float32; the weights that
  * multiply v are rounded to bf16 (their sum is not).
  * Requirements: bf16; head_dim 64 or 128; n_heads a multiple of n_kv_heads, at

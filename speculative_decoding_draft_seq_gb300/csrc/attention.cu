@@ -836,7 +836,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnParams p) {
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) {
     const float2 s = __ldcg(p.stat + slot(i));
-    if (s.y != 0.f) M = fmaxf(M, s.x);
+    if (s.y != 0.f) M = fmaxf(M, s.y == s.y ? s.x : 0.f);  // (a sum that is NaN: the row's, whatever the maximum)
   }
   M = warp_max(M);
   float o[E] = {}, Z = 0.f;

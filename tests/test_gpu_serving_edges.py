@@ -95,6 +95,21 @@ def test_attention_without_tokens():
 
 
 # ---------------------------------------------------------------------------------------------
+# scores that are no number
+
+@pytest.mark.parametrize("private,prefix", [(9, 0), (700, 0), (9, 3000), (300, 40)])
+def test_attention_of_a_nan_query(private, prefix):
+    """A query that holds a NaN has no softmax: NaN, however many parts its keys are split into, and in its row alone."""
+    c = G.attention_case([3, 1], [private, 50], prefix, 8, 2, 64, 16, seed=12)
+    want, want_lse = G.run_attention(c)
+    c["q"][1, 5, 3] = math.nan
+    out, lse = G.run_attention(c)
+    assert torch.all(torch.isnan(out[1, 5])) and torch.isnan(lse[1, 5])
+    out[1, 5], lse[1, 5] = want[1, 5], want_lse[1, 5]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+# ---------------------------------------------------------------------------------------------
 # sampling: temperatures and logits at the ends of float32
 
 def test_rule_at_infinite_temperature_is_uniform():
