@@ -3,9 +3,9 @@
 // outside the kept set masked.
 //
 // Weights of a row with maximum M at temperature T: w = 2^((l - M) log2(e)/T)
-// in float32, each operation rounded once, and their masses the integers
-// floor(w 2^40). Sums of masses are integer sums, so they do not depend on an
-// order, and every comparison below is exact. With the row sorted by (logit
+// in float32 (difference and product rounded once, the power by ex2.approx, within
+// 2^-22 of it), and their masses the integers floor(w 2^40). Sums of masses are
+// integer sums, so they do not depend on an order, and every comparison below is exact. With the row sorted by (logit
 // descending, index ascending), top-k keeps the first k entries; top-p keeps,
 // of these, the entries whose mass before them is below floor(p S), S the mass
 // of the top-k set; min-p keeps the entries with w >= min_p. All three are
@@ -88,11 +88,14 @@ __device__ __forceinline__ float logit_below(float x) {
 // (A distance that overflows is multiplied at half its size. That matters to rates below kTinyRate alone: at larger ones
 // 2^(-inf) = 0 and 2^(-3.4e38 rate) = 0 are the same weight.)
 constexpr float kTinyRate = 1e-36f;
-__device__ __forceinline__ float rule_weight(float x, float M, float rate) {
+__device__ __forceinline__ float rule_exponent(float x, float M, float rate) {
   const float d = __fsub_rn(x, M);
   const float y = d == -INFINITY ? 2.f * __fmul_rn(__fsub_rn(0.5f * x, 0.5f * M), rate) : __fmul_rn(d, rate);
-  return x == -INFINITY ? 0.f : exp2f(y);
+  return x == -INFINITY ? -INFINITY : y;
 }
+// Every mass, wherever it is added, subtracted or walked over, is that of this weight or of the packed pair of it (the
+// same three instructions on two entries), so that they agree to the last bit.
+__device__ __forceinline__ float rule_weight(float x, float M, float rate) { return ex2_approx(rule_exponent(x, M, rate)); }
 // floor(x S) for x in [0, 1), x to 53 bits, from the bits of x (FP64 instructions are slow here)
 __device__ __forceinline__ unsigned long long scale_mass(double x, unsigned long long S) {
   const unsigned long long b = (unsigned long long)__double_as_longlong(x), one = 1ull << 53;
@@ -1005,12 +1008,14 @@ __global__ void __launch_bounds__(NT, kBlocks) sampling_rule_kernel(SampleParams
     if (th.key >= key) key = th.key;
     else cut = V;  // the threshold fell on entries of -inf: all others are kept
   }
-  if (!greedy && min_w > 0.f) {  // the smallest key whose weight reaches min_p, by 32-way search
+  // the smallest key whose weight reaches min_p, by 32-way search (exp2f has weights below 2^-126 too; above, it and
+  // ex2.approx have given the same bits for every float32 argument)
+  if (!greedy && min_w > 0.f) {
     uint32_t lo = key, hi = logit_key(M);  // the weight of hi is 1
     for (int round = 0; lo < hi && round < 32; ++round) {
       const uint32_t step = (hi - lo) / 32 + 1;
       const uint32_t at = (uint32_t)min((unsigned long long)hi, lo + (unsigned long long)step * (tid & 31));
-      const uint32_t ok = __ballot_sync(0xffffffffu, rule_weight(key_logit(at), M, rate) >= min_w);
+      const uint32_t ok = __ballot_sync(0xffffffffu, exp2f(rule_exponent(key_logit(at), M, rate)) >= min_w);
       const int first = ok ? __ffs(ok) - 1 : 32;  // lanes before it lie below
       hi = (uint32_t)min((unsigned long long)hi, lo + (unsigned long long)step * first);
       if (first > 0) lo = (uint32_t)min((unsigned long long)hi, lo + (unsigned long long)step * (first - 1) + 1);

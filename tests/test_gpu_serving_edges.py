@@ -192,3 +192,34 @@ def test_top_p_ranges_that_meet_at_zero(rows):
     c = np.cumsum(np.where(kept, w, 0.0))
     for i, u in enumerate(np.linspace(0.0, 0.999, rows)):
         assert tokens[i] == np.searchsorted(c, u * c[-1], side="right") or np.abs(c - u * c[-1]).min() < 2.0 ** -17 * c[-1]
+
+
+# ---------------------------------------------------------------------------------------------
+# sampling: one weight for an entry, whichever part of a call forms it
+
+@pytest.mark.parametrize("dtype,V", [("fp32", 8), ("fp32", 4100), ("bf16", 16)])
+def test_every_token_has_the_mass_it_is_drawn_by(dtype, V):
+    """Rows over many exponents at the temperature whose rate is 1 (maximum 0: the exponent is the logit), drawn at a
+    uniform in the middle of one entry's mass: that token, with its mass over the row's, masses floor(2^x 2^40) by
+    torch's float32 exp2. Entries next to the drawn one are as large, so that a unit's difference between the sum and the
+    walk would show."""
+    N = (1 << 21) // V
+    g = torch.Generator(device=DEV).manual_seed(V)
+    x = -40 * torch.rand((N, V), generator=g, device=DEV) ** 2
+    x[:, 0] = 0.0
+    x = x.to(G.TORCH[dtype])
+    mass = (torch.exp2(x.float()).double() * 2.0 ** 40).floor().long()
+    c = mass.cumsum(1)
+    at = torch.randint(0, V, (N,), generator=g, device=DEV)
+    here, Z = mass.gather(1, at[:, None])[:, 0], c[:, -1]
+    first = c.gather(1, at[:, None])[:, 0] - here
+    u = (first.double() + 0.5 * here.double()) / Z.double()
+    sure = here > (Z >> 51) + 8  # (u is rounded to 2^-53 of 1)
+    par = (torch.full((N,), 1.4426950408889634, device=DEV), torch.zeros(N, dtype=torch.int32, device=DEV),
+           torch.ones(N, device=DEV), torch.zeros(N, device=DEV))
+    tokens, prob, ws = torch.full((N,), -7, dtype=torch.int32, device=DEV), torch.full((N,), -7.0, device=DEV), G._ws()
+    dspark.sample(x, *par, u, tokens, ws, prob=prob)
+    assert dspark.device_status(ws) == dspark.OK
+    assert torch.equal(tokens[sure].long(), at[sure]) and int(sure.sum()) > N // 2
+    want = (here.double() / Z.double()).float()
+    assert torch.equal(prob[sure], want[sure])
