@@ -223,3 +223,19 @@ def test_every_token_has_the_mass_it_is_drawn_by(dtype, V):
     assert torch.equal(tokens[sure].long(), at[sure]) and int(sure.sum()) > N // 2
     want = (here.double() / Z.double()).float()
     assert torch.equal(prob[sure], want[sure])
+
+
+# ---------------------------------------------------------------------------------------------
+# plans of more requests than a block has threads, long pages, long prompts
+
+@pytest.mark.parametrize("new,private,prefix,Hq,Hkv,D,page", [
+    ([i % 3 for i in range(1500)], [2 + (i * 37) % 90 for i in range(1500)], 70, 2, 1, 64, 16),   # two turns of the plan
+    ([1] * 2049, [1 + i % 40 for i in range(2049)], 0, 2, 2, 64, 32),                             # three, the last one request
+    ([2, 1] * 5 + [0] * 1100 + [3], [300 + i for i in range(10)] + [5] * 1100 + [200], 150, 4, 1, 128, 16),
+    ([3, 1], [1500, 700], 1000, 4, 2, 128, 512),                                                  # a page of several tiles
+    ([2], [5000], 4097, 4, 1, 64, 4096),                                                          # the longest page
+    ([1100, 1], [1300, 40], 200, 2, 1, 64, 16),                                                   # a prompt chunk of many blocks
+])
+def test_attention_of_many_requests_and_long_ones(new, private, prefix, Hq, Hkv, D, page):
+    c = G.attention_case(new, private, prefix, Hq, Hkv, D, page)
+    G.check_attention(c, *G.run_attention(c))
