@@ -359,7 +359,8 @@ dspark_status dspark_sts_apply(int32_t R, int32_t gamma, const float* conf, cons
  * the round's tokens, their keys and values into the paged cache, attention
  * over a shared prefix and each request's own pages, and the target's sampling
  * rule. (After the LM head, the logits of dspark_truncate are the
- * target_logits of dspark_verify.) These calls take any workspace of at least
+ * target_logits of dspark_verify, of rows that share its one temperature: see
+ * dspark_truncate.) These calls take any workspace of at least
  * 256 bytes for the device status word; dspark_prefix_attention needs the size
  * that dspark_attention_workspace_bytes gives.
  *
@@ -417,8 +418,10 @@ dspark_status dspark_kv_append(int32_t T, int32_t n_kv_heads, int32_t head_dim, 
  *   lse          [T, n_heads] float out or NULL, the natural log of the sum of e^score
  * A query that sees no key gets out = 0 and lse = -inf. Cache entries that no
  * query of the call sees are never part of a result, whatever bits they hold;
- * those that one sees must be finite. A query with a NaN score gets out and lse
- * NaN. Rows of q past q_start[R] are left out.
+ * those that one sees must be finite (an infinity or NaN among a request's own
+ * values reaches its earlier queries of the call too: their weight of 0 times
+ * it is NaN). A query with a NaN score gets out and lse NaN. Rows of q past
+ * q_start[R] are left out.
  * Scores, softmax statistics and accumulators are float32; the weights that
  * multiply v are rounded to bf16 (their sum is not).
  * Requirements: bf16; head_dim 64 or 128; n_heads a multiple of n_kv_heads, at
@@ -428,6 +431,8 @@ dspark_status dspark_kv_append(int32_t T, int32_t n_kv_heads, int32_t head_dim, 
  * outside [0, max_pages * page_size] (clamped), and by a q_start that does not
  * begin at 0, falls or passes T (nothing is written then). Nothing outside the
  * tensors is read. Three launches; none for T = 0, whatever the pointers.
+ * The workspace holds parts of the result for 3 T + 8192 tokens in float32:
+ * with 32 heads of 128, 136 MB for one token, 546 MB for 8,192.
  */
 size_t dspark_attention_workspace_bytes(int32_t R, int32_t T, int32_t n_heads, int32_t n_kv_heads,
                                         int32_t head_dim);
@@ -455,7 +460,11 @@ dspark_status dspark_prefix_attention(int32_t R, int32_t T, int32_t n_heads, int
  *   tokens [N] int32 out, prob [N] float out or NULL: the token's mass / Z (1 if greedy)
  * dspark_truncate writes out [N, V] dtype: the kept entries as they are, all
  * others the lowest finite value of the type (weight 0 for every consumer;
- * out may be logits itself).
+ * out may be logits itself). The kept logits are not divided by the
+ * temperature, and dspark_verify applies one temperature T to all rows: a
+ * batch whose requests differ in it is verified in a call for each
+ * temperature, or with the rows of temperature T_r multiplied by T / T_r
+ * beforehand and truncated at T.
  * A row with a NaN or +inf, or with nothing above -inf, sets
  * DSPARK_ERR_NONFINITE: its token is -1 with prob 0, dspark_truncate copies it.
  */

@@ -329,7 +329,7 @@ def page_plan(cached_len, new_len, free_pages, page_size, block_table, q_start, 
               stream=None):
     """Cache pages and slots of new_len[r] tokens a request: fills the new entries of block_table
     [R, max_pages] from free_pages, and q_start [R+1], kv_len [R], positions and slots [capacity]
-    (int32, int64) and used [1]."""
+    (int32, int64) and used [1]. Tokens past the capacity are left out of all of them (ERR_CAPACITY)."""
     R, max_pages = block_table.shape
     capacity = positions.numel()
     if (cached_len.shape != (R,) or new_len.shape != (R,) or q_start.shape != (R + 1,) or kv_len.shape != (R,) or
@@ -421,7 +421,8 @@ def sample(logits, temperature, top_k, top_p, min_p, u, tokens, ws, prob=None, s
 
 
 def truncate(logits, temperature, top_k, top_p, min_p, out, ws, stream=None):
-    """out [N, V]: logits with every entry outside the rule's kept set at the type's lowest value."""
+    """out [N, V]: logits with every entry outside the rule's kept set at the type's lowest value. The kept ones are not
+    divided by the temperature: verify applies its own, one for all rows."""
     rule = _rule(logits, temperature, top_k, top_p, min_p)
     if out.shape != logits.shape:
         _shapes(out=(out, tuple(logits.shape)))

@@ -226,6 +226,26 @@ def test_every_token_has_the_mass_it_is_drawn_by(dtype, V):
 
 
 # ---------------------------------------------------------------------------------------------
+# rows of several temperatures for a verification at one
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_of_other_temperatures_scale_to_one(dtype):
+    """Rows of temperature T_r, multiplied by T / T_r and truncated at T, keep what they keep at T_r; at ratios of two
+    every step of the weights is the same float32 number."""
+    rng = np.random.default_rng(21)
+    T, ratio = 0.8, np.tile([0.5, 1.0, 2.0, 4.0], 10).astype(np.float32)
+    x = torch.from_numpy((rng.normal(size=(40, 5000)) * 2).astype(np.float32)).to(DEV).to(G.TORCH[dtype])
+    f = lambda a: torch.from_numpy(np.asarray(a, dtype=np.float32)).to(DEV)  # noqa: E731
+    k, p, m = G._i32(rng.choice([0, 20, 400], 40)), f(rng.choice([0.9, 0.99, 1.0], 40)), f(rng.choice([0.0, 0.01], 40))
+    scaled = (x.float() * f(ratio)[:, None]).to(x.dtype)
+    a, b, ws = torch.empty_like(x), torch.empty_like(x), G._ws()
+    dspark.truncate(x, f(np.float32(T) / ratio), k, p, m, a, ws)
+    dspark.truncate(scaled, f(np.full(40, T)), k, p, m, b, ws)
+    low = torch.finfo(x.dtype).min
+    assert dspark.device_status(ws) == dspark.OK and torch.equal(a > low, b > low) and not torch.all(a > low)
+
+
+# ---------------------------------------------------------------------------------------------
 # plans of more requests than a block has threads, long pages, long prompts
 
 @pytest.mark.parametrize("new,private,prefix,Hq,Hkv,D,page", [
