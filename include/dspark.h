@@ -477,6 +477,173 @@ dspark_status dspark_truncate(int32_t N, int32_t V, int32_t dtype, const void* l
                               const float* min_p, void* out, void* workspace, size_t workspace_bytes,
                               dspark_stream_t stream);
 
+/*
+ * After the target's pass: its rows of logits become probabilities, these decide
+ * which drafted tokens stand (any drafter's, by the caller's own uniforms), the
+ * cache's pages follow that decision, and the rows' largest entries teach the
+ * drafter. These calls take any workspace of at least 256 bytes for the device
+ * status word; dspark_page_collect, _fork and _compact need the size that
+ * dspark_page_workspace_bytes gives.
+ *
+ * dspark_probabilities: probs[r] = softmax(logits[r] / T_r), N rows [N, V]
+ * (V <= 2^20), with the weights of dspark_sample: w = 2^((l - M) r), r =
+ * min(log2(e) / T, 1e30), p = w / sum w, in float32 and rounded once. T <= 0 (or NaN): 1 at
+ * the row's first maximum; T = inf: the same value for every finite entry. An entry
+ * of -inf has probability 0, and so have entries that dspark_truncate masked
+ * (the type's lowest value) at any T below 1e36.
+ *   logits      [N, V] dtype
+ *   temperature [N] float
+ *   probs       [N, V] probs_dtype out (not the logits' memory unless of the same type)
+ * A row with a NaN or +inf, or with nothing above -inf, sets
+ * DSPARK_ERR_NONFINITE and gets zeros.
+ */
+dspark_status dspark_probabilities(int32_t N, int32_t V, int32_t dtype, const void* logits,
+                                   const float* temperature, int32_t probs_dtype, void* probs,
+                                   void* workspace, size_t workspace_bytes, dspark_stream_t stream);
+
+/*
+ * dspark_verify_probs: dspark_verify for any drafter, from rows of
+ * probabilities and given uniforms, the target's rows packed as
+ * dspark_page_plan lays out a round's tokens.
+ *   target_probs [T, V] dtype      row q_start[r] + k: the target's distribution after request r's
+ *                                  anchor and k drafts
+ *   q_start      [R+1] int32       request r has n = q_start[r+1] - q_start[r] rows and n - 1 drafts (at
+ *                                  most gamma); n = 0: it takes no part (accepted_len 0, out_tokens -1)
+ *   draft_probs  [R, gamma, V] dtype or NULL   the distribution each draft was drawn from; NULL: drafts
+ *                                  without one (a table lookup), taken as certain
+ *   draft_tokens [R, gamma] int32
+ *   u            [R, gamma+1] double in [0, 1)  u[r, k] for draft k, u[r, gamma] for the draw
+ *   out_tokens   [R, gamma+1] int32 out  the accepted drafts, then the corrected or bonus token; -1 after
+ *   accepted_len [R] int32 out
+ *   p_tok        [R, gamma] float out  the target's probability of each draft, 0 past the last
+ * Draft x stands iff u q < p, strictly, the product in double. At the first that
+ * does not, the token is drawn from w = max(0, p - q) (the difference rounded to
+ * float32), from p if that has no mass; after the last, from the next row. Masses are
+ * floor(min(w, 1) 2^40) (a NaN or negative entry: 0), Z their sum, the token the
+ * smallest v whose mass up to and including v exceeds floor(u Z). Rows need not sum to 1.
+ * DSPARK_ERR_RANGE: a draft outside [0, V) (rejected, and drawn from p), q_start
+ * that falls or leaves [0, T] (as n = 0), more than gamma drafts (the first gamma
+ * count). DSPARK_ERR_NONFINITE: a NaN or infinity among the entries read, or a row
+ * drawn from that has no mass (token -1).
+ */
+dspark_status dspark_verify_probs(int32_t R, int32_t gamma, int32_t V, int32_t T, int32_t dtype,
+                                  const void* target_probs, const int32_t* q_start,
+                                  const void* draft_probs, const int32_t* draft_tokens,
+                                  const double* u, int32_t* out_tokens, int32_t* accepted_len,
+                                  float* p_tok, void* workspace, size_t workspace_bytes,
+                                  dspark_stream_t stream);
+
+/*
+ * Pages of the cache. The block table is the one record of who holds a page:
+ * row r holds the pages of its first ceil(kv_len[r] / page_size) entries, several
+ * rows may hold one page, and `pinned` [n_pinned] names pages held by something
+ * else (a shared prefix; NULL if n_pinned = 0). The calls form everything from that, so
+ * a page is freed by shortening or dropping the rows that hold it. An entry
+ * outside [0, n_pages) within a row's length, or a length outside
+ * [0, max_pages * page_size] (clamped), sets DSPARK_ERR_RANGE; such an entry is
+ * nobody's page and is carried along as it is.
+ *
+ * dspark_page_collect: the holders of each page, and the free pages.
+ *   block_table [R, max_pages] int32, kv_len [R] int32
+ *   refs        [n_pages] int32 out   entries that hold the page
+ *   free_pages  [n_pages] int32 out   pages with none, ascending, then -1: the list for
+ *                                     dspark_page_plan and dspark_page_fork
+ *   n_free      [1] int32 out
+ */
+size_t dspark_page_workspace_bytes(int32_t n_pages);
+dspark_status dspark_page_collect(int32_t R, int32_t page_size, int32_t max_pages, int32_t n_pages,
+                                  int32_t n_pinned, const int32_t* block_table, const int32_t* kv_len,
+                                  const int32_t* pinned, int32_t* refs, int32_t* free_pages,
+                                  int32_t* n_free, void* workspace, size_t workspace_bytes,
+                                  dspark_stream_t stream);
+
+/*
+ * dspark_page_fork: R new rows, new row i the first fork_len[i] tokens of row
+ * parent[i] of R_from (samples of a prompt, beams that are dropped, doubled,
+ * reordered or cut). Pages are shared, except one that a new row ends inside and
+ * will write to next: it stays the row's own if no new row holds it in full, no
+ * earlier new row ends inside it and it is not pinned; else the row gets a free
+ * page and a copy to make with dspark_page_copy.
+ *   parent     [R] int32           in [0, R_from), or -1: an empty row
+ *   fork_len   [R] int32 or NULL   at most the parent's kv_len (NULL: all of it)
+ *   free_pages [n_free] int32      taken in order (a negative id ends the list)
+ *   new_table  [R, max_pages] int32 out, -1 past a row's pages; not block_table
+ *   new_len    [R] int32 out
+ *   src, dst, tokens [R] int32 out the copy of row i, its tokens; -1, -1, 0 where none is needed
+ *   used       [1] int32 out       free pages taken
+ * A list that is too short sets DSPARK_ERR_CAPACITY: the row's last entry is then
+ * -1. A parent or fork_len out of range sets DSPARK_ERR_RANGE (an empty row;
+ * clamped). Every row that is to live on has to be among the new ones.
+ */
+dspark_status dspark_page_fork(int32_t R_from, int32_t R, int32_t page_size, int32_t max_pages,
+                               int32_t n_pages, int32_t n_free, int32_t n_pinned,
+                               const int32_t* block_table, const int32_t* kv_len,
+                               const int32_t* parent, const int32_t* fork_len,
+                               const int32_t* free_pages, const int32_t* pinned, int32_t* new_table,
+                               int32_t* new_len, int32_t* src, int32_t* dst, int32_t* tokens,
+                               int32_t* used, void* workspace, size_t workspace_bytes,
+                               dspark_stream_t stream);
+
+/*
+ * dspark_page_compact: with m pages held, the held pages m and above move to the
+ * free ones below m, in ascending order both, so that the front m pages of the
+ * cache hold everything.
+ *   new_table  [R, max_pages] int32 out  the rows with their new page ids, -1 past their pages (may be
+ *                                        block_table itself)
+ *   new_pinned [n_pinned] int32 out      (may be pinned itself)
+ *   src, dst   [n_pages / 2] int32 out   the moves, then -1: for dspark_page_copy with tokens = NULL
+ *   n_live     [1] int32 out             m
+ */
+dspark_status dspark_page_compact(int32_t R, int32_t page_size, int32_t max_pages, int32_t n_pages,
+                                  int32_t n_pinned, const int32_t* block_table, const int32_t* kv_len,
+                                  const int32_t* pinned, int32_t* new_table, int32_t* new_pinned,
+                                  int32_t* src, int32_t* dst, int32_t* n_live, void* workspace,
+                                  size_t workspace_bytes, dspark_stream_t stream);
+
+/*
+ * dspark_page_copy: page dst[i] of every layer gets the first tokens[i] tokens
+ * of page src[i], keys and values, i < n. Pairs with a negative id are skipped; one
+ * with an id >= n_pages too (DSPARK_ERR_RANGE). No dst may be another pair's src or dst.
+ *   src, dst [n] int32, tokens [n] int32 (clamped to [0, page_size]) or NULL: whole pages
+ *   k_cache, v_cache [n_layers, n_pages, page_size, n_kv_heads, head_dim] dtype in/out
+ */
+dspark_status dspark_page_copy(int32_t n, int32_t n_layers, int32_t n_pages, int32_t page_size,
+                               int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const int32_t* src,
+                               const int32_t* dst, const int32_t* tokens, void* k_cache, void* v_cache,
+                               void* workspace, size_t workspace_bytes, dspark_stream_t stream);
+
+/*
+ * dspark_distill: the divergence of N rows of a drafter's logits from a
+ * teacher's top K logits, and its gradient, in one pass. With tau = temperature,
+ * s = softmax(x / tau) over the vocabulary and p_j the teacher's probability of
+ * listed entry j:
+ *   teacher_lse NULL:  p = softmax(t / tau) over the row's listed entries,
+ *                      loss = sum_j p_j (ln p_j - ln s_{id_j})
+ *   teacher_lse given: the natural log of sum e^(t / tau) over the teacher's whole
+ *                      vocabulary; p_j = e^(t_j / tau - lse), p_R = 1 - sum_j p_j (at least 0), s_R =
+ *                      the sum of s over all entries that are not listed, and the loss has the term
+ *                      p_R (ln p_R - ln s_R) too (0 if either is 0)
+ *   grad[r, v] = weight[r] d loss_r / d x_v
+ *   logits      [N, V] dtype (V <= 2^20)
+ *   ids         [N, K] int32   1 <= K <= 1024; a negative id pads a shorter list; of an id that comes
+ *                              twice both entries count
+ *   teacher     [N, K] float   the teacher's logits of these entries
+ *   teacher_lse [N] float or NULL
+ *   weight      [N] float or NULL (1): the gradient coming from above (1 / N for a mean; 0 leaves a row out)
+ *   temperature in [1e-6, 1e6]
+ *   loss        [N] float out, not weighted
+ *   grad        [N, V] dtype out or NULL (loss alone); may be logits itself
+ * A list without entries has loss 0 and gradient 0. A listed entry that the
+ * drafter gives probability 0 makes the loss infinite. DSPARK_ERR_RANGE: an id >= V
+ * (left out). DSPARK_ERR_NONFINITE: a row with a NaN or +inf, or with nothing above -inf, or whose listed teacher
+ * logits or lse hold a NaN or infinity (other than a logit of -inf: probability 0): loss NaN, gradient 0.
+ * Statistics and the listed entries' terms are summed in float32 or float64.
+ */
+dspark_status dspark_distill(int32_t N, int32_t V, int32_t K, int32_t dtype, const void* logits,
+                             const int32_t* ids, const float* teacher, const float* teacher_lse,
+                             const float* weight, float temperature, float* loss, void* grad,
+                             void* workspace, size_t workspace_bytes, dspark_stream_t stream);
+
 /* Synchronises `stream`, then returns the workspace's sticky device status
  * (DSPARK_OK if no device-side error was recorded). */
 dspark_status dspark_device_status(const void* workspace, dspark_stream_t stream);

@@ -90,6 +90,17 @@ def _load():
     lib.dspark_status_string.argtypes = [i32]
     lib.dspark_last_launch_count.restype = i32
     lib.dspark_last_launch_count.argtypes = []
+    lib.dspark_probabilities.argtypes = [i32] * 3 + [vp, vp, i32, vp, vp, sz, vp]
+    lib.dspark_verify_probs.argtypes = [i32] * 5 + [vp] * 9 + [sz, vp]
+    lib.dspark_page_workspace_bytes.restype = sz
+    lib.dspark_page_workspace_bytes.argtypes = [i32]
+    lib.dspark_page_collect.argtypes = [i32] * 5 + [vp] * 7 + [sz, vp]
+    lib.dspark_page_fork.argtypes = [i32] * 7 + [vp] * 13 + [sz, vp]
+    lib.dspark_page_compact.argtypes = [i32] * 5 + [vp] * 9 + [sz, vp]
+    lib.dspark_page_copy.argtypes = [i32] * 7 + [vp] * 6 + [sz, vp]
+    lib.dspark_distill.argtypes = [i32] * 4 + [vp] * 5 + [f32] + [vp] * 3 + [sz, vp]
+    for name in ("probabilities", "verify_probs", "page_collect", "page_fork", "page_compact", "page_copy", "distill"):
+        getattr(lib, "dspark_" + name).restype = i32
     return lib
 
 
@@ -429,6 +440,188 @@ def truncate(logits, temperature, top_k, top_p, min_p, out, ws, stream=None):
     status = lib.dspark_truncate(*rule, _addr(out, logits.dtype), _addr(ws, _U8), ws.numel(), _raw_stream(stream))
     if status:
         _check(status, "dspark_truncate")
+
+
+# The calls after the target's pass. Their tensors have to be on the device whose stream the call runs on.
+_current_device = torch._C._cuda_getDevice
+
+
+def _here(stream):
+    """(device index, stream handle) of a call."""
+    return (_current_device(), _raw_stream(None)) if stream is None else (stream.device_index, stream.cuda_stream)
+
+
+def _addr_on(t, dtype, device):
+    """Device address of a dense tensor of this type on this device; refuses what _ptr refuses, and another device."""
+    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    _ptr(t, dtype)
+    raise ValueError(f"tensor is on cuda:{t.get_device()}, the call runs on cuda:{device}")
+
+
+def probabilities(logits, temperature, probs, ws, stream=None):
+    """probs [N, V] (float32 or bfloat16) = softmax of the rows of logits [N, V], temperature [N] float32 (<= 0: one at
+    the first maximum)."""
+    N, V = logits.shape
+    if temperature.shape != (N,) or probs.shape != (N, V):
+        _shapes(temperature=(temperature, (N,)), probs=(probs, (N, V)))
+    dev, s = _here(stream)
+    status = lib.dspark_probabilities(N, V, _dtype_code(logits), _addr_on(logits, logits.dtype, dev),
+                                      _addr_on(temperature, _F32, dev), _dtype_code(probs),
+                                      _addr_on(probs, probs.dtype, dev), _addr_on(ws, _U8, dev), ws.numel(), s)
+    if status:
+        _check(status, "dspark_probabilities")
+
+
+def verify_probs(target_probs, q_start, draft_probs, draft_tokens, u, out_tokens, accepted_len, p_tok, ws, stream=None):
+    """Verifies draft_tokens [R, gamma] against packed rows target_probs [T, V] (rows q_start[r] .. q_start[r+1] - 1 of
+    request r, one more than its drafts); draft_probs [R, gamma, V] like them, or None for drafts without
+    probabilities; u [R, gamma + 1] float64. Fills out_tokens [R, gamma + 1], accepted_len [R], p_tok [R, gamma]."""
+    T, V = target_probs.shape
+    R, gamma = draft_tokens.shape
+    if (q_start.shape != (R + 1,) or (draft_probs is not None and draft_probs.shape != (R, gamma, V)) or
+            u.shape != (R, gamma + 1) or out_tokens.shape != (R, gamma + 1) or accepted_len.shape != (R,) or
+            p_tok.shape != (R, gamma)):
+        _shapes(q_start=(q_start, (R + 1,)), u=(u, (R, gamma + 1)), out_tokens=(out_tokens, (R, gamma + 1)),
+                accepted_len=(accepted_len, (R,)), p_tok=(p_tok, (R, gamma)),
+                **({} if draft_probs is None else {"draft_probs": (draft_probs, (R, gamma, V))}))
+    dev, s = _here(stream)
+    dt = target_probs.dtype
+    status = lib.dspark_verify_probs(R, gamma, V, T, _dtype_code(target_probs), _addr_on(target_probs, dt, dev),
+                                     _addr_on(q_start, _I32, dev),
+                                     None if draft_probs is None else _addr_on(draft_probs, dt, dev),
+                                     _addr_on(draft_tokens, _I32, dev), _addr_on(u, _F64, dev),
+                                     _addr_on(out_tokens, _I32, dev), _addr_on(accepted_len, _I32, dev),
+                                     _addr_on(p_tok, _F32, dev), _addr_on(ws, _U8, dev), ws.numel(), s)
+    if status:
+        _check(status, "dspark_verify_probs")
+
+
+def page_workspace_bytes(n_pages):
+    return int(lib.dspark_page_workspace_bytes(n_pages))
+
+
+def new_page_workspace(n_pages, device="cuda", stream=None):
+    """Allocates (with PyTorch) and clears a workspace for the page calls on a cache of n_pages."""
+    n = page_workspace_bytes(n_pages)
+    if n == 0:
+        raise DSparkError(ERR_INVALID_ARG, "dspark_page_workspace_bytes")
+    return _aligned_workspace(n, device, stream)
+
+
+def page_collect(block_table, kv_len, page_size, refs, free_pages, n_free, ws, pinned=None, stream=None):
+    """refs [n_pages]: holders of each page (rows of block_table [R, max_pages] within kv_len [R], and pinned);
+    free_pages [n_pages]: the pages without, ascending, then -1; n_free [1]. All int32."""
+    R, max_pages = block_table.shape
+    n_pages = refs.numel()
+    if kv_len.shape != (R,) or free_pages.shape != (n_pages,) or n_free.numel() < 1:
+        _shapes(kv_len=(kv_len, (R,)), free_pages=(free_pages, (n_pages,)), n_free=(n_free, (1,)))
+    dev, s = _here(stream)
+    n_pinned = 0 if pinned is None else pinned.numel()
+    status = lib.dspark_page_collect(R, page_size, max_pages, n_pages, n_pinned, _addr_on(block_table, _I32, dev),
+                                     _addr_on(kv_len, _I32, dev), _addr_on(pinned, _I32, dev) if n_pinned else None,
+                                     _addr_on(refs, _I32, dev), _addr_on(free_pages, _I32, dev),
+                                     _addr_on(n_free, _I32, dev), _addr_on(ws, _U8, dev), ws.numel(), s)
+    if status:
+        _check(status, "dspark_page_collect")
+
+
+def page_fork(block_table, kv_len, parent, fork_len, page_size, n_pages, free_pages, new_table, new_len, src, dst, tokens,
+              used, ws, pinned=None, stream=None):
+    """new_table [R, max_pages]: row i the first fork_len[i] tokens (None: all) of row parent[i] (-1: empty) of
+    block_table [R_from, max_pages]; pages shared, those that a row writes next its own, from free_pages. Fills
+    new_len, and the copies to make: src, dst, tokens [R] (-1, -1, 0: none), used [1]. All int32."""
+    R_from, max_pages = block_table.shape
+    R = new_table.shape[0]
+    rows = (R,)
+    if (new_table.shape != (R, max_pages) or kv_len.shape != (R_from,) or parent.shape != rows or new_len.shape != rows or
+            src.shape != rows or dst.shape != rows or tokens.shape != rows or used.numel() < 1 or
+            (fork_len is not None and fork_len.shape != rows)):
+        _shapes(new_table=(new_table, (R, max_pages)), kv_len=(kv_len, (R_from,)), parent=(parent, rows),
+                new_len=(new_len, rows), src=(src, rows), dst=(dst, rows), tokens=(tokens, rows), used=(used, (1,)),
+                **({} if fork_len is None else {"fork_len": (fork_len, rows)}))
+    dev, s = _here(stream)
+    n_free, n_pinned = free_pages.numel(), 0 if pinned is None else pinned.numel()
+    status = lib.dspark_page_fork(R_from, R, page_size, max_pages, n_pages, n_free, n_pinned,
+                                  _addr_on(block_table, _I32, dev), _addr_on(kv_len, _I32, dev),
+                                  _addr_on(parent, _I32, dev),
+                                  None if fork_len is None else _addr_on(fork_len, _I32, dev),
+                                  _addr_on(free_pages, _I32, dev) if n_free else None,
+                                  _addr_on(pinned, _I32, dev) if n_pinned else None, _addr_on(new_table, _I32, dev),
+                                  _addr_on(new_len, _I32, dev), _addr_on(src, _I32, dev), _addr_on(dst, _I32, dev),
+                                  _addr_on(tokens, _I32, dev), _addr_on(used, _I32, dev), _addr_on(ws, _U8, dev),
+                                  ws.numel(), s)
+    if status:
+        _check(status, "dspark_page_fork")
+
+
+def page_compact(block_table, kv_len, page_size, n_pages, new_table, src, dst, n_live, ws, pinned=None, new_pinned=None,
+                 stream=None):
+    """The held pages moved to the front n_live [1] of the cache: new_table like block_table (may be it), new_pinned like
+    pinned (may be it), and the moves src, dst [n_pages // 2] for page_copy. All int32."""
+    R, max_pages = block_table.shape
+    n_pinned = 0 if pinned is None else pinned.numel()
+    half = (n_pages // 2,)
+    if (new_table.shape != (R, max_pages) or kv_len.shape != (R,) or src.shape != half or dst.shape != half or
+            n_live.numel() < 1 or (n_pinned and (new_pinned is None or new_pinned.numel() != n_pinned))):
+        if n_pinned and (new_pinned is None or new_pinned.numel() != n_pinned):
+            raise ValueError("new_pinned must be as long as pinned")
+        _shapes(new_table=(new_table, (R, max_pages)), kv_len=(kv_len, (R,)), src=(src, half), dst=(dst, half),
+                n_live=(n_live, (1,)))
+    dev, s = _here(stream)
+    status = lib.dspark_page_compact(R, page_size, max_pages, n_pages, n_pinned, _addr_on(block_table, _I32, dev),
+                                     _addr_on(kv_len, _I32, dev), _addr_on(pinned, _I32, dev) if n_pinned else None,
+                                     _addr_on(new_table, _I32, dev),
+                                     _addr_on(new_pinned, _I32, dev) if n_pinned else None,
+                                     _addr_on(src, _I32, dev), _addr_on(dst, _I32, dev), _addr_on(n_live, _I32, dev),
+                                     _addr_on(ws, _U8, dev), ws.numel(), s)
+    if status:
+        _check(status, "dspark_page_compact")
+
+
+def page_copy(src, dst, k_cache, v_cache, ws, tokens=None, stream=None):
+    """Page dst[i] of k_cache and v_cache [.., n_pages, page_size, Hkv, D] (any leading dimensions: layers) gets the first
+    tokens[i] tokens (None: all) of page src[i]; negative ids are skipped."""
+    n_pages, page, Hkv, D = k_cache.shape[-4:]
+    n = src.numel()
+    if k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    if dst.shape != (n,) or src.shape != (n,) or (tokens is not None and tokens.shape != (n,)):
+        _shapes(src=(src, (n,)), dst=(dst, (n,)), **({} if tokens is None else {"tokens": (tokens, (n,))}))
+    dev, s = _here(stream)
+    dt = k_cache.dtype
+    status = lib.dspark_page_copy(n, k_cache.numel() // (n_pages * page * Hkv * D), n_pages, page, Hkv, D,
+                                  _dtype_code(k_cache), _addr_on(src, _I32, dev), _addr_on(dst, _I32, dev),
+                                  None if tokens is None else _addr_on(tokens, _I32, dev), _addr_on(k_cache, dt, dev),
+                                  _addr_on(v_cache, dt, dev), _addr_on(ws, _U8, dev), ws.numel(), s)
+    if status:
+        _check(status, "dspark_page_copy")
+
+
+def distill(logits, ids, teacher, temperature, loss, ws, grad=None, weight=None, teacher_lse=None, stream=None):
+    """loss [N] float32: divergence of the rows of logits [N, V] from a teacher's logits `teacher` [N, K] float32 of the
+    entries ids [N, K] int32 (-1: none), both at `temperature`; with teacher_lse [N] float32 (the log of the sum of
+    e^(teacher logit / temperature) over the whole vocabulary) the entries that are not listed count as one more. grad
+    [N, V] like logits (may be logits): weight[r] (None: 1) times the loss's gradient."""
+    N, V = logits.shape
+    K = ids.shape[-1]
+    if (ids.shape != (N, K) or teacher.shape != (N, K) or loss.shape != (N,) or
+            (grad is not None and grad.shape != (N, V)) or (weight is not None and weight.shape != (N,)) or
+            (teacher_lse is not None and teacher_lse.shape != (N,))):
+        _shapes(ids=(ids, (N, K)), teacher=(teacher, (N, K)), loss=(loss, (N,)),
+                **({} if grad is None else {"grad": (grad, (N, V))}),
+                **({} if weight is None else {"weight": (weight, (N,))}),
+                **({} if teacher_lse is None else {"teacher_lse": (teacher_lse, (N,))}))
+    dev, s = _here(stream)
+    dt = logits.dtype
+    status = lib.dspark_distill(N, V, K, _dtype_code(logits), _addr_on(logits, dt, dev), _addr_on(ids, _I32, dev),
+                                _addr_on(teacher, _F32, dev),
+                                None if teacher_lse is None else _addr_on(teacher_lse, _F32, dev),
+                                None if weight is None else _addr_on(weight, _F32, dev), temperature,
+                                _addr_on(loss, _F32, dev), None if grad is None else _addr_on(grad, dt, dev),
+                                _addr_on(ws, _U8, dev), ws.numel(), s)
+    if status:
+        _check(status, "dspark_distill")
 
 
 def wait_selftest(which, ws, stream=None):
