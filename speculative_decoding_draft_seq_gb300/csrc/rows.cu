@@ -3,11 +3,13 @@
 //
 // Both need a row's maximum M and Z = sum 2^((x - M) r) before they can write
 // anything of the row's size, and are bound by bytes (a row in, a row out) if the row is read
-// once. So a cluster of CTAs holds a row in registers, kPieces 16-byte pieces a
-// thread: every warp forms the maximum and the sum of its own pieces, the warps of all
-// CTAs exchange these pairs through distributed shared memory, and after one cluster
-// barrier each thread combines them in the same order and writes its pieces. A row too long
-// for the registers of a cluster is read again instead (kHold false).
+// once. So a cluster of CTAs holds a row in shared memory: every thread copies its own 16-byte
+// pieces there (asynchronously; nobody else reads them, so it waits for itself only), every warp forms
+// the maximum and the sum of its pieces, the warps of all CTAs exchange these pairs through
+// distributed shared memory, and after one cluster barrier each thread combines them in the
+// same order and writes its pieces. At kPieces pieces a thread three CTAs of an SM load, wait and write
+// independently of each other. A row longer than a cluster holds is taken in windows, which are read again for
+// the results.
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -28,6 +30,36 @@ __device__ __forceinline__ float nan_max(float a, float b) {  // NaN if either i
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
+__device__ __forceinline__ float warp_nan_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = nan_max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ unsigned long long pair_mul(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long pair_add(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ void copy_async(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <class T>
+__device__ __forceinline__ float row_elem(const T* p) {
+  if constexpr (sizeof(T) == 4) return *p;
+  else return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16);
+}
+template <class T>
+__device__ __forceinline__ void store_elem(T* p, float v) {
+  if constexpr (sizeof(T) == 4) *p = v;
+  else *p = __float2bfloat16_rn(v);
+}
 
 // One row of V elements as this thread sees it: 16-byte pieces, of which it owns number
 // (i C + rank) NT + tid, i = 0, 1, .., and the loose elements before the first and after the last
@@ -43,17 +75,18 @@ struct RowPart {
     n = (V - a0) / E;
   }
   __device__ __forceinline__ int loose() const { return V - n * E; }
-  __device__ __forceinline__ int loose_index(int i) const { return i < a0 ? i : i + n * E; }
   __device__ __forceinline__ int piece(int i) const { return (i * C + rank) * kRowThreads + (int)threadIdx.x; }
-  __device__ __forceinline__ int steps() const { return ceil_div(n, C * kRowThreads); }
-  __device__ __forceinline__ uint4 load(int g) const {
-    uint4 q;
-    const void* p = row + a0 + (size_t)g * E;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "l"(p) : "memory");
-    return q;
+  // pieces that this thread owns
+  __device__ __forceinline__ int own() const {
+    const int step = C * kRowThreads, first = rank * kRowThreads + (int)threadIdx.x;
+    return first < n ? (n - first + step - 1) / step : 0;
   }
-  // whether this thread owns a loose element, and which
-  __device__ __forceinline__ int own_loose() const { return rank == 0 && (int)threadIdx.x < loose() ? loose_index(threadIdx.x) : -1; }
+  __device__ __forceinline__ int steps() const { return ceil_div(n, C * kRowThreads); }
+  // the loose element that this thread owns, or -1
+  __device__ __forceinline__ int own_loose() const {
+    const int i = threadIdx.x;
+    return rank == 0 && i < loose() ? (i < a0 ? i : i + n * E) : -1;
+  }
   // owner of element v: CTA, and the local number of its piece (step * NT + thread); loose ones: -1 - number
   __device__ __forceinline__ int owner(int v, int& local, int& at) const {
     if (v < a0 || v >= a0 + n * E) {
@@ -67,57 +100,47 @@ struct RowPart {
     local = step * kRowThreads + t % kRowThreads;
     return t / kRowThreads;
   }
+  // starts the copies of this thread's pieces i0 .. min(i0 + kPieces, own) - 1
+  __device__ __forceinline__ void fetch(uint4* held, int i0) const {
+    const int m = min(own() - i0, kPieces);
+    for (int i = 0; i < m; ++i) copy_async(held + i * kRowThreads + threadIdx.x, row + a0 + (size_t)piece(i0 + i) * E);
+  }
 };
+
+// The two logits of each 32-bit word of a piece (of each two words, float32).
 template <class T>
-__device__ __forceinline__ float row_elem(const T* p) {
-  if constexpr (sizeof(T) == 4) return *p;
-  else return __uint_as_float((uint32_t)*reinterpret_cast<const unsigned short*>(p) << 16);
-}
-template <class T>
-__device__ __forceinline__ void split_piece(const uint4& q, float (&x)[16 / sizeof(T)]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void split_piece(const uint4& q, unsigned long long (&x)[8 / sizeof(T)]) {
+  if constexpr (sizeof(T) == 4) {
+    x[0] = (unsigned long long)q.y << 32 | q.x;
+    x[1] = (unsigned long long)q.w << 32 | q.z;
+  } else {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (sizeof(T) == 4) {
-      x[i] = __uint_as_float(w[i]);
-    } else {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) x[i] = (unsigned long long)(w[i] & 0xffff0000u) << 32 | w[i] << 16;
   }
 }
 template <class T>
-__device__ __forceinline__ uint4 empty_piece() {  // -inf throughout
-  const uint32_t e = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-  return make_uint4(e, e, e, e);
-}
-template <class T>
 __device__ __forceinline__ float piece_max(const uint4& q) {
-  float x[16 / sizeof(T)];
-  split_piece<T>(q, x);
-  float m = x[0];
-#pragma unroll
-  for (int e = 1; e < (int)(16 / sizeof(T)); ++e) m = nan_max(m, x[e]);
-  return m;
+  if constexpr (sizeof(T) == 4) {
+    return nan_max(nan_max(__uint_as_float(q.x), __uint_as_float(q.y)), nan_max(__uint_as_float(q.z), __uint_as_float(q.w)));
+  } else {
+    uint32_t a, b;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(q.x), "r"(q.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(q.z), "r"(q.w));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+    return nan_max(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+  }
 }
-__device__ __forceinline__ float warp_nan_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = nan_max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-template <class T>
-__device__ __forceinline__ void store_elem(T* p, float v) {
-  if constexpr (sizeof(T) == 4) *p = v;
-  else *p = __float2bfloat16_rn(v);
-}
-// E neighbouring results to out[0..E-1]; `wide`: out + any piece's first element is 16-byte aligned
+// E neighbouring results to out[0..E-1]; `wide`: aligned to their size
 template <class To, int E>
 __device__ __forceinline__ void store_piece(To* out, const float (&y)[E], bool wide) {
   if (wide) {
-    if constexpr (sizeof(To) == 4) {
-#pragma unroll
-      for (int i = 0; i < E; i += 4)
-        __stcs(reinterpret_cast<float4*>(out + i), make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]));
+    if constexpr (sizeof(To) == 4 && E == 8) {
+      asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]),
+                   "f"(y[5]), "f"(y[6]), "f"(y[7])
+                   : "memory");
+    } else if constexpr (sizeof(To) == 4) {
+      __stcs(reinterpret_cast<float4*>(out), make_float4(y[0], y[1], y[2], y[3]));
     } else {
       uint32_t w[E / 2];
 #pragma unroll
@@ -135,74 +158,85 @@ __device__ __forceinline__ void store_piece(To* out, const float (&y)[E], bool w
 }
 
 // The exponent of an entry's weight: (x - M) r, as fma(x, h, -M h) (r / h) with h = 1, or 1/2 for rates so small
-// that differences past float32's range count.
+// that differences past float32's range count. One entry, or two at a time with the same bits.
 struct Weigher {
   float h, Mh, rate;
   __device__ __forceinline__ Weigher(float M, float h_, float rate_) : h(h_), Mh(M * h_), rate(rate_) {}
-  __device__ __forceinline__ float exponent(float x) const { return __fmul_rn(__fmaf_rn(x, h, -Mh), rate); }
-  __device__ __forceinline__ float operator()(float x) const { return ex2_approx(exponent(x)); }
+  __device__ __forceinline__ float operator()(float x) const { return ex2_approx(__fmul_rn(__fmaf_rn(x, h, -Mh), rate)); }
+  __device__ __forceinline__ unsigned long long both(unsigned long long x) const {
+    const unsigned long long y = pair_mul(f32x2_fma(x, f32x2_pack(h, h), f32x2_pack(-Mh, -Mh)), f32x2_pack(rate, rate));
+    float a, b;
+    f32x2_unpack(y, a, b);
+    return f32x2_pack(ex2_approx(a), ex2_approx(b));
+  }
 };
 
-// (maximum, sum) of a warp's pieces, continued over chunks of pieces; `listed` the part of the sum that is marked.
+// (maximum, sum) of a warp's pieces, continued over windows; `listed` the part of the sum that is marked.
 struct WarpSum {
   float m = -INFINITY, z = 0.f, listed = 0.f;
 };
-template <class T, int P, class Marks>
-__device__ __forceinline__ void add_pieces(WarpSum& s, const uint4 (&q)[P], float loose, float h, float rate, Marks marks) {
-  constexpr int E = 16 / sizeof(T);
-  float m = loose;
-#pragma unroll
-  for (int i = 0; i < P; ++i) m = nan_max(m, piece_max<T>(q[i]));
-  m = nan_max(s.m, warp_nan_max(m));
-  if (m == -INFINITY) return;  // (the whole warp)
-  const Weigher w(m, h, rate);
+// Adds the window's m pieces of this thread and its loose element (-inf: none). marks(i): the listed entries of piece i as
+// bits, marks(-1): whether the loose one is.
+template <class T, bool kMarks, class Marks>
+__device__ __forceinline__ void add_pieces(WarpSum& s, const uint4* held, int m, float loose, float h, float rate, Marks marks) {
+  constexpr int W = 8 / sizeof(T);
+  const uint4* mine = held + threadIdx.x;
+  float top = loose;
+#pragma unroll 4
+  for (int i = 0; i < m; ++i) top = nan_max(top, piece_max<T>(mine[i * kRowThreads]));
+  top = nan_max(s.m, warp_nan_max(top));
+  if (top == -INFINITY) return;  // (the whole warp)
+  const Weigher w(top, h, rate);
   if (s.m != -INFINITY) {
     const float f = w(s.m);
     s.z *= f;
     s.listed *= f;
   }
-  s.m = m;
-  float a = 0.f, b = 0.f, l = 0.f;
+  s.m = top;
+  unsigned long long a = 0, b = 0;
+  float l = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < m; ++i) {
+    unsigned long long x[W];
+    split_piece<T>(mine[i * kRowThreads], x);
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    float x[E];
-    split_piece<T>(q[i], x);
-    const uint32_t bits = marks(i);
-    if (bits == 0) {
+    for (int e = 0; e < W; ++e) x[e] = w.both(x[e]);
+    if (kMarks) {
+      const uint32_t bits = marks(i);
+      if (bits) {
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        a += w(x[e]);
-        b += w(x[e + 1]);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float y = w(x[e]);
-        if (bits >> e & 1) l += y;
-        else a += y;
+        for (int e = 0; e < W; ++e) {
+          float y0, y1;
+          f32x2_unpack(x[e], y0, y1);
+          if (bits >> (2 * e) & 1) l += y0, y0 = 0.f;
+          if (bits >> (2 * e + 1) & 1) l += y1, y1 = 0.f;
+          x[e] = f32x2_pack(y0, y1);
+        }
       }
     }
+#pragma unroll
+    for (int e = 0; e < W; e += 2) {
+      a = pair_add(a, x[e]);
+      b = pair_add(b, x[e + 1]);
+    }
   }
+  float a0, a1, b0, b1;
+  f32x2_unpack(a, a0, a1);
+  f32x2_unpack(b, b0, b1);
   if (loose != -INFINITY) {
     const float y = w(loose);
-    if (marks(-1)) l += y;
-    else a += y;
+    if (kMarks && marks(-1)) l += y;
+    else a0 += y;
   }
-  s.z += a + b;
+  s.z += (a0 + a1) + (b0 + b1);
   s.listed += l;
 }
 
-// The row's maximum and sums from those of all warps of the cluster, the same in every thread: combined in float64
-// (a warp's lanes each take every 32nd entry, then a fixed tree).
+// The row's maximum and sums from those of all warps of the cluster, the same in every thread (a warp's lanes each
+// take every 32nd entry, then a fixed tree).
 struct RowSum {
-  float M;
-  double z, listed;
+  float M, z, listed;
 };
-__device__ __forceinline__ double warp_add_d(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 __device__ __forceinline__ RowSum exchange(WarpSum s, float4* all, int C, int rank, float h, float rate) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   s.z = warp_sum(s.z);
@@ -211,7 +245,7 @@ __device__ __forceinline__ RowSum exchange(WarpSum s, float4* all, int C, int ra
   __syncwarp();
   cluster_arrive();
   cluster_wait();
-  RowSum r{-INFINITY, 0.0, 0.0};
+  RowSum r{-INFINITY, 0.f, 0.f};
   for (int i = lane; i < C * kRowWarps; i += 32) r.M = nan_max(r.M, all[i].x);
   r.M = warp_nan_max(r.M);
   if (r.M == -INFINITY) return r;
@@ -220,11 +254,11 @@ __device__ __forceinline__ RowSum exchange(WarpSum s, float4* all, int C, int ra
     const float4 t = all[i];
     if (t.x == -INFINITY) continue;
     const float f = w(t.x);
-    r.z += (double)t.y * f;
-    r.listed += (double)t.z * f;
+    r.z += t.y * f;
+    r.listed += t.z * f;
   }
-  r.z = warp_add_d(r.z);
-  r.listed = warp_add_d(r.listed);
+  r.z = warp_sum(r.z);
+  r.listed = warp_sum(r.listed);
   return r;
 }
 
@@ -237,93 +271,101 @@ struct ProbsParams {
   uint32_t* status;
 };
 
-template <class T, class To, bool kHold>
-__global__ void __launch_bounds__(kRowThreads) probabilities_kernel(ProbsParams p) {
-  constexpr int E = 16 / sizeof(T);
+template <class T, class To>
+__global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsParams p) {
+  constexpr int E = 16 / sizeof(T), W = E / 2;
+  extern __shared__ __align__(16) uint4 held[];
   __shared__ float4 all[kMaxCluster * kRowWarps];
   __shared__ uint32_t first[kMaxCluster * kRowWarps];
   const int rank = (int)cluster_rank(), C = p.C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   cluster_arrive();  // the others' shared memory is theirs once they run: waited for before the exchange
   const size_t r = blockIdx.x / C;
   const RowPart<T> part(static_cast<const T*>(p.logits) + r * p.V, p.V, C, rank);
+  part.fetch(held, 0);
   To* out = static_cast<To*>(p.probs) + r * p.V;
-  const bool wide = (reinterpret_cast<uintptr_t>(out + part.a0) & (E * sizeof(To) < 16 ? E * sizeof(To) - 1 : 15)) == 0;
+  const bool wide = (reinterpret_cast<uintptr_t>(out + part.a0) & (E * sizeof(To) - 1)) == 0;
   const float T_ = __ldg(p.temperature + r);
   const bool greedy = !(T_ > 0.f);
   // the smallest rate (T = inf) still takes an entry of -inf to weight 0
   const float rate0 = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269504088896340736f, T_), 1e30f), 1e-45f);
   const float h = rate0 < 1e-36f ? 0.5f : 1.f, rate = rate0 < 1e-36f ? 2.f * rate0 : rate0;
-  const int loose_at = part.own_loose();
+  const int loose_at = part.own_loose(), own = part.own();
   const float loose = loose_at >= 0 ? row_elem(part.row + loose_at) : -INFINITY;
-  const auto unmarked = [](int) { return 0u; };
+  const int windows = max(1, ceil_div(part.steps(), kPieces));
 
-  uint4 q[kPieces];
   WarpSum s;
-  const int chunks = kHold ? 1 : ceil_div(part.steps(), kPieces);
-  const auto fetch = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int g = part.piece(c * kPieces + i);
-      q[i] = g < part.n ? part.load(g) : empty_piece<T>();
-    }
-  };
-  for (int c = 0; c < max(chunks, 1); ++c) {
-    fetch(c);
-    add_pieces<T>(s, q, c == 0 ? loose : -INFINITY, h, rate, unmarked);
+  for (int c = 0; c < windows; ++c) {
+    if (c > 0) part.fetch(held, c * kPieces);
+    copies_done();
+    add_pieces<T, false>(s, held, min(own - c * kPieces, kPieces), c == 0 ? loose : -INFINITY, h, rate, [](int) { return 0u; });
   }
   cluster_wait();
   const RowSum sum = exchange(s, all, C, rank, h, rate);
   const bool bad = !(fabsf(sum.M) < INFINITY);
   if (bad && rank == 0 && threadIdx.x == 0) set_status(p.status, DSPARK_ERR_NONFINITE);
-
-  int top = INT_MAX;  // greedy: the first maximum
-  if (greedy && !bad) {
-    for (int c = 0; c < max(chunks, 1); ++c) {
-      if (!kHold) fetch(c);
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) {
-        float x[E];
-        split_piece<T>(q[i], x);
-        const int g = part.piece(c * kPieces + i);
-#pragma unroll
-        for (int e = E - 1; e >= 0; --e)
-          if (g < part.n && x[e] == sum.M) top = min(top, part.a0 + g * E + e);
+  // f(piece's number in the window's memory, first element) for this thread's pieces
+  const auto each = [&](auto f) {
+    for (int c = 0; c < windows; ++c) {
+      if (windows > 1) {
+        part.fetch(held, c * kPieces);
+        copies_done();
       }
+      const int m = min(own - c * kPieces, kPieces);
+#pragma unroll 2
+      for (int i = 0; i < m; ++i) f(held[i * kRowThreads + threadIdx.x], part.a0 + part.piece(c * kPieces + i) * E);
     }
-    if (loose_at >= 0 && loose == sum.M) top = min(top, loose_at);
-    top = warp_min_i(top);
-    if (lane < C) store_peer(peer_address(first + rank * kRowWarps + warp, lane), (uint32_t)top);
-    __syncwarp();
-    cluster_arrive();
-    cluster_wait();
-    top = INT_MAX;
-    for (int i = lane; i < C * kRowWarps; i += 32) top = min(top, (int)first[i]);
-    top = warp_min_i(top);
-  }
+  };
 
-  const Weigher w(sum.M, h, rate);
-  const float inv = bad ? 0.f : (float)(1.0 / sum.z);
-  const auto result = [&](float x, int v) { return bad ? 0.f : greedy ? (v == top ? 1.f : 0.f) : w(x) * inv; };
-  for (int c = 0; c < max(chunks, 1); ++c) {
-    if (!kHold) fetch(c);
+  if (bad || greedy) {
+    int top = INT_MAX;  // the first maximum
+    if (!bad) {
+      each([&](const uint4& q, int v) {
+        unsigned long long x[W];
+        split_piece<T>(q, x);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int g = part.piece(c * kPieces + i);
-      if (g >= part.n) continue;
-      float x[E];
-      split_piece<T>(q[i], x);
-      const int v = part.a0 + g * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = result(x[e], v + e);
-      store_piece<To, E>(out + v, x, wide);
+        for (int e = 0; e < W; ++e) {
+          float x0, x1;
+          f32x2_unpack(x[e], x0, x1);
+          if (x0 == sum.M) top = min(top, v + 2 * e);
+          if (x1 == sum.M) top = min(top, v + 2 * e + 1);
+        }
+      });
+      if (loose_at >= 0 && loose == sum.M) top = min(top, loose_at);
+      top = warp_min_i(top);
+      if (lane < C) store_peer(peer_address(first + rank * kRowWarps + warp, lane), (uint32_t)top);
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+      top = INT_MAX;
+      for (int i = lane; i < C * kRowWarps; i += 32) top = min(top, (int)first[i]);
+      top = warp_min_i(top);
     }
+    for (int i = 0; i < own; ++i) {
+      const int v = part.a0 + part.piece(i) * E;
+      float y[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = v + e == top ? 1.f : 0.f;
+      store_piece<To, E>(out + v, y, wide);
+    }
+    if (loose_at >= 0) store_elem(out + loose_at, loose_at == top ? 1.f : 0.f);
+    return;
   }
-  if (loose_at >= 0) store_elem(out + loose_at, result(loose, loose_at));
+  const Weigher w(sum.M, h, rate);
+  const float inv = __fdiv_rn(1.f, sum.z);
+  each([&](const uint4& q, int v) {
+    unsigned long long x[W];
+    split_piece<T>(q, x);
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < W; ++e) f32x2_unpack(pair_mul(w.both(x[e]), f32x2_pack(inv, inv)), y[2 * e], y[2 * e + 1]);
+    store_piece<To, E>(out + v, y, wide);
+  });
+  if (loose_at >= 0) store_elem(out + loose_at, w(loose) * inv);
 }
 
 // ---------------------------------------------------------------------------
 struct DistillParams {
-  int V, K, C, marks;  // marks: bytes of the marked-entry map
+  int V, K, C, held, marks;  // bytes of the held pieces and of the map of marked entries
   const void* logits;
   const int32_t* ids;
   const float* teacher;
@@ -335,51 +377,43 @@ struct DistillParams {
   uint32_t* status;
 };
 
-__device__ __forceinline__ double block_sum_dd(double v, double* sh) {
-  v = warp_add_d(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.0;
+__device__ __forceinline__ double warp_add_d(double v) {
 #pragma unroll
-  for (int i = 0; i < kRowWarps; ++i) v += sh[i];
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// e^y to float32's precision: the power of the fraction, |f| <= 1/2, so that y's size costs none
+__device__ __forceinline__ float exp_of(double y) {
+  const double o = fmax(y * 1.44269504088896340736, -160.0), n = rint(o);
+  return ldexpf(exp2f((float)(o - n)), (int)n);
+}
 
-template <class T, bool kHold>
-__global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillParams p) {
-  constexpr int E = 16 / sizeof(T);
-  extern __shared__ __align__(16) unsigned char dyn[];
+template <class T, bool kRest>
+__global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p) {
+  constexpr int E = 16 / sizeof(T), W = E / 2;
+  extern __shared__ __align__(16) uint4 held[];
   __shared__ float4 all[kMaxCluster * kRowWarps];
   __shared__ double sums[kRowWarps];
+  __shared__ double s_share;  // written by CTA 0 of the cluster
   __shared__ float maxima[kRowWarps];
   __shared__ uint32_t loose_marks;
   __shared__ int twice;
-  // of the listed entries: id (-1: none), teacher's logit, the student's, the teacher's probability
-  int* s_id = reinterpret_cast<int*>(dyn);
-  float* s_t = reinterpret_cast<float*>(s_id + p.K);
+  // of the listed entries: the teacher's probability (CTA 0), its logit, the student's, the id (-1: none); then the map
+  double* s_p = reinterpret_cast<double*>(reinterpret_cast<char*>(held) + p.held);
+  float* s_t = reinterpret_cast<float*>(s_p + p.K);
   float* s_x = s_t + p.K;
-  double* s_p = reinterpret_cast<double*>(dyn + (((size_t)p.K * 12 + 15) & ~(size_t)15));
-  uint32_t* s_marks = reinterpret_cast<uint32_t*>(s_p + p.K);
+  int* s_id = reinterpret_cast<int*>(s_x + p.K);
+  uint32_t* s_marks = reinterpret_cast<uint32_t*>(s_id + p.K);
   const int rank = (int)cluster_rank(), C = p.C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   cluster_arrive();
   const size_t r = blockIdx.x / C;
   const T* row = static_cast<const T*>(p.logits) + r * p.V;
   const RowPart<T> part(row, p.V, C, rank);
-  const bool with_rest = p.teacher_lse != nullptr;
+  part.fetch(held, 0);
   const float rate = __fdiv_rn(1.44269504088896340736f, p.tau);
-  const int loose_at = part.own_loose();
+  const int loose_at = part.own_loose(), own = part.own();
   const float loose = loose_at >= 0 ? row_elem(row + loose_at) : -INFINITY;
 
-  uint4 q[kPieces];
-  const auto fetch = [&](int c) {
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int g = part.piece(c * kPieces + i);
-      q[i] = g < part.n ? part.load(g) : empty_piece<T>();
-    }
-  };
-  fetch(0);
   // the listed entries, in every CTA; those of this CTA's pieces are marked
   for (int i = tid; i < p.marks / 4; i += kRowThreads) s_marks[i] = 0;
   if (tid == 0) {
@@ -387,14 +421,12 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillParams p) {
     twice = 0;
   }
   __syncthreads();
-  bool out_of_range = false;
   float t_max = -INFINITY;
   for (int j = tid; j < p.K; j += kRowThreads) {
     int id = __ldg(p.ids + r * p.K + j);
-    out_of_range |= id >= p.V;
-    if (id >= p.V) id = -1;
     float t = __ldg(p.teacher + r * p.K + j);
-    if (id < 0) {
+    if (id >= p.V) set_status(p.status, DSPARK_ERR_RANGE);
+    if (id < 0 || id >= p.V) {
       id = -1;
       t = -INFINITY;
     }
@@ -402,124 +434,134 @@ __global__ void __launch_bounds__(kRowThreads) distill_kernel(DistillParams p) {
     s_t[j] = t;
     s_x[j] = id >= 0 ? row_elem(row + id) : -INFINITY;
     t_max = nan_max(t_max, t);
-    if (id >= 0) {
-      int local, at;
-      if (part.owner(id, local, at) == rank) {
-        bool again;
-        if (local < 0) {
-          const uint32_t bit = 1u << (-1 - local);
-          again = atomicOr(&loose_marks, bit) & bit;
-        } else {
-          const uint32_t bit = 1u << ((local & 3) * 8 + at);
-          again = atomicOr(s_marks + (local >> 2), bit) & bit;
-        }
-        if (again) twice = 1;
-      }
+    int local, at;
+    if (id >= 0 && part.owner(id, local, at) == rank) {
+      uint32_t* word = local < 0 ? &loose_marks : s_marks + (local >> 2);
+      const uint32_t bit = local < 0 ? 1u << (-1 - local) : 1u << ((local & 3) * 8 + at);
+      if (atomicOr(word, bit) & bit) twice = 1;
     }
   }
-  if (out_of_range) set_status(p.status, DSPARK_ERR_RANGE);
   t_max = warp_nan_max(t_max);
   if (lane == 0) maxima[warp] = t_max;
   __syncthreads();
-  t_max = maxima[0];
-#pragma unroll
-  for (int i = 1; i < kRowWarps; ++i) t_max = nan_max(t_max, maxima[i]);
-  const double lse = with_rest ? (double)__ldg(p.teacher_lse + r) : 0.0;
+  t_max = lane < kRowWarps ? maxima[lane] : -INFINITY;
+  t_max = warp_nan_max(t_max);
+  const float lse = kRest ? __ldg(p.teacher_lse + r) : t_max;
   const bool none = t_max == -INFINITY;
-  const bool bad_teacher = !(t_max < INFINITY) || (with_rest && !(fabs(lse) < (double)INFINITY));
-  // the teacher's probabilities: float64, since what they leave of 1 and the logarithms' differences may be small
+  const bool bad_teacher = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < INFINITY));
+  const bool listless = none || bad_teacher;
   const double per_tau = 1.0 / (double)p.tau;
-  double share = 0.0;
-  for (int j = tid; j < p.K; j += kRowThreads) {
-    const double y = with_rest ? (double)s_t[j] * per_tau - lse : ((double)s_t[j] - (double)t_max) * per_tau;
-    const double e = none || bad_teacher || s_id[j] < 0 ? 0.0 : exp(y);
-    s_p[j] = e;
-    share += e;
+  // ln of an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum
+  const auto ln_p = [&](float t) { return kRest ? (double)t * per_tau - (double)lse : ((double)t - (double)lse) * per_tau; };
+  // their sum in float64: what it leaves of 1, and the logarithms' differences, may be small
+  if (rank == 0) {
+    double share = 0.0;
+    if (warp * 32 < p.K) {
+      for (int j = tid; j < p.K; j += kRowThreads) {
+        const double e = listless || s_id[j] < 0 ? 0.0 : exp(ln_p(s_t[j]));
+        s_p[j] = e;
+        share += e;
+      }
+      share = warp_add_d(share);
+    }
+    if (lane == 0) sums[warp] = share;
+    __syncthreads();
+    if (warp == 0) {
+      share = lane < min(ceil_div(p.K, 32), kRowWarps) ? sums[lane] : 0.0;
+      share = warp_add_d(share);
+    }
+    if (warp == 0) sums[0] = share;  // (read after the cluster's barrier)
   }
-  share = block_sum_dd(share, sums);
-  const double norm = with_rest || share == 0.0 ? 1.0 : 1.0 / share;
-  const double p_rest = with_rest ? fmax(0.0, 1.0 - share) : 0.0;
 
   WarpSum s;
-  const int chunks = kHold ? 1 : max(ceil_div(part.steps(), kPieces), 1);
-  for (int c = 0; c < chunks; ++c) {
-    if (c > 0) fetch(c);
+  const int windows = max(1, ceil_div(part.steps(), kPieces));
+  for (int c = 0; c < windows; ++c) {
+    if (c > 0) part.fetch(held, c * kPieces);
+    copies_done();
     const auto marks = [&](int i) -> uint32_t {
-      if (!with_rest) return 0u;
       if (i < 0) return loose_marks >> tid & 1u;
       const int local = (c * kPieces + i) * kRowThreads + tid;
-      return local < p.marks ? s_marks[local >> 2] >> ((local & 3) * 8) & 255u : 0u;
+      return s_marks[local >> 2] >> ((local & 3) * 8) & 255u;
     };
-    add_pieces<T>(s, q, c == 0 ? loose : -INFINITY, 1.f, rate, marks);
+    add_pieces<T, kRest>(s, held, min(own - c * kPieces, kPieces), c == 0 ? loose : -INFINITY, 1.f, rate, marks);
   }
   cluster_wait();
+  if (rank == 0 && warp == 0 && lane < C)
+    store_peer(peer_address(&s_share, lane), (unsigned long long)__double_as_longlong(sums[0]));
   const RowSum sum = exchange(s, all, C, rank, 1.f, rate);
-  const double z = sum.z + sum.listed, z_rest = sum.z;
   const bool bad = !(fabsf(sum.M) < INFINITY) || bad_teacher;
-  const bool some = p_rest > 0.0 && z_rest > 0.0;  // a rest without mass on either side counts for nothing
   const Weigher w(sum.M, 1.f, rate);
+  const float z = sum.z + sum.listed, z_rest = sum.z;
+  const double share = s_share;
+  const float p_rest = kRest ? (float)fmax(0.0, 1.0 - share) : 0.f;
+  const bool some = kRest && p_rest > 0.f && z_rest > 0.f;  // a rest without mass on either side counts for nothing
 
-  if (rank == 0) {
-    const double step = (double)rate * 0.69314718055994530942;  // 1 / tau as the weights have it
-    double a = 0.0;
-    for (int j = tid; j < p.K; j += kRowThreads) {
-      const double e = s_p[j];
-      if (e > 0.0) {
-        const double y = with_rest ? (double)s_t[j] * per_tau - lse : ((double)s_t[j] - (double)t_max) * per_tau;
-        a += e * (y - ((double)s_x[j] - (double)sum.M) * step);
+  if (p.grad) {
+    // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v)
+    T* grad = static_cast<T*>(p.grad) + r * p.V;
+    const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
+    const float scale = (float)((p.weight ? (double)__ldg(p.weight + r) : 1.0) * per_tau);
+    const float norm = kRest ? 1.f : share > 0.0 ? (float)(1.0 / share) : 0.f;
+    const float total = kRest ? (float)(share + (some ? (double)p_rest : 0.0)) : share > 0.0 ? 1.f : 0.f;
+    const float per_z = total / z;
+    const float listed_f = bad ? 0.f : scale * per_z;
+    const float rest_f = bad ? 0.f : scale * (per_z - (some ? p_rest / z_rest : 0.f));
+    for (int c = 0; c < windows; ++c) {
+      if (windows > 1) {
+        part.fetch(held, c * kPieces);
+        copies_done();
+      }
+      const int m = min(own - c * kPieces, kPieces);
+#pragma unroll 2
+      for (int i = 0; i < m; ++i) {
+        unsigned long long x[W];
+        split_piece<T>(held[i * kRowThreads + tid], x);
+        float y[E];
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          f32x2_unpack(pair_mul(w.both(x[e]), f32x2_pack(rest_f, rest_f)), y[2 * e], y[2 * e + 1]);
+          if (bad) y[2 * e] = y[2 * e + 1] = 0.f;
+        }
+        store_piece<T, E>(grad + part.a0 + (size_t)part.piece(c * kPieces + i) * E, y, wide);
       }
     }
-    a = block_sum_dd(a, sums);
-    if (tid == 0) {
+    if (loose_at >= 0) store_elem(grad + loose_at, bad ? 0.f : w(loose) * rest_f);
+    // the listed entries of this CTA over what was just written
+    __syncthreads();
+    for (int j = tid; j < p.K && !bad; j += kRowThreads) {
+      const int id = s_id[j];
+      int local, at;
+      if (id < 0 || part.owner(id, local, at) != rank) continue;
+      float e = listless ? 0.f : exp_of(ln_p(s_t[j]));
+      if (twice) {  // an id that comes more than once: every occurrence writes the sum of all
+        e = 0.f;
+        for (int i = 0; i < p.K; ++i)
+          if (s_id[i] == id && !listless) e += exp_of(ln_p(s_t[i]));
+      }
+      store_elem(grad + id, __fmaf_rn(-scale * norm, e, w(s_x[j]) * listed_f));
+    }
+  }
+
+  if (rank == 0 && warp == 0) {
+    const double step = (double)rate * 0.69314718055994530942;  // 1 / tau as the weights have it
+    double a = 0.0;
+    for (int j = lane; j < p.K; j += 32) {
+      const double e = s_p[j];
+      if (e > 0.0) a += e * (ln_p(s_t[j]) - ((double)s_x[j] - (double)sum.M) * step);
+    }
+    a = warp_add_d(a);
+    if (lane == 0) {
       double loss = 0.0;
-      const double ln_z = log(z);
-      if (with_rest) {
-        loss = a + share * ln_z;
-        if (some) loss += p_rest * (log(p_rest) - log(z_rest) + ln_z);
+      if (kRest) {
+        const double left = fmax(0.0, 1.0 - share);
+        loss = a + share * log((double)z);
+        if (some) loss += left * log(left * ((double)z / (double)z_rest));
       } else if (share > 0.0) {
-        loss = a * norm + ln_z - log(share);
+        loss = a / share + log((double)z / share);
       }
       p.loss[r] = bad ? NAN : (float)loss;
       if (bad) set_status(p.status, DSPARK_ERR_NONFINITE);
     }
-  }
-  if (!p.grad) return;
-
-  // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v)
-  T* grad = static_cast<T*>(p.grad) + r * p.V;
-  const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
-  const double scale = (p.weight ? (double)__ldg(p.weight + r) : 1.0) * per_tau;
-  const double total = with_rest ? share + (some ? p_rest : 0.0) : (share > 0.0 ? 1.0 : 0.0);
-  const float listed_f = bad ? 0.f : (float)(scale * total / z);
-  const float rest_f = bad ? 0.f : (float)(scale * (total / z - (some ? p_rest / z_rest : 0.0)));
-  for (int c = 0; c < chunks; ++c) {
-    if (!kHold) fetch(c);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const int g = part.piece(c * kPieces + i);
-      if (g >= part.n) continue;
-      float x[E];
-      split_piece<T>(q[i], x);
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = bad ? 0.f : w(x[e]) * rest_f;
-      store_piece<T, E>(grad + part.a0 + (size_t)g * E, x, wide);
-    }
-  }
-  if (loose_at >= 0) store_elem(grad + loose_at, bad ? 0.f : w(loose) * rest_f);
-  if (bad) return;
-  // the listed entries of this CTA over what was just written
-  __syncthreads();
-  for (int j = tid; j < p.K; j += kRowThreads) {
-    const int id = s_id[j];
-    int local, at;
-    if (id < 0 || part.owner(id, local, at) != rank) continue;
-    double e = s_p[j];
-    if (twice) {  // an id that comes more than once: every occurrence writes the sum of all
-      e = 0.0;
-      for (int i = 0; i < p.K; ++i)
-        if (s_id[i] == id) e += s_p[i];
-    }
-    store_elem(grad + id, (float)((double)(w(s_x[j]) * listed_f) - scale * norm * e));
   }
 }
 
@@ -531,31 +573,33 @@ static int sm_count() {
   return sms;
 }
 
-// CTAs a row: as few as hold it, more while the rows leave SMs idle.
-static int row_cluster(int N, int V, int elem, int sms, bool& hold) {
+// CTAs a row: as few as hold it, more while the rows leave SMs idle. `held`: the bytes that a CTA keeps of it.
+static int row_cluster(int N, int V, int elem, int sms, int& held) {
   const long long pieces = (long long)V * elem / 16;
   int C = 1;
   while (C < kMaxCluster && (pieces > (long long)C * kRowThreads * kPieces || ((long long)N * C * 2 <= sms && pieces > (long long)C * kRowThreads)))
     C *= 2;
-  hold = pieces <= (long long)C * kRowThreads * kPieces;
+  held = std::min(kPieces, ceil_div(pieces, (long long)C * kRowThreads)) * kRowThreads * 16;
   return C;
 }
 
 template <class T, class To>
-static cudaError_t launch_probs(const ProbsParams& p, int N, bool hold, cudaStream_t s) {
-  return launch_clusters(hold ? probabilities_kernel<T, To, true> : probabilities_kernel<T, To, false>, p, (unsigned)N * p.C, p.C,
-                         kRowThreads, 0, s);
+static cudaError_t launch_probs(const ProbsParams& p, int N, int held, cudaStream_t s) {
+  static std::atomic<unsigned long long> attr{0};
+  const cudaError_t e = set_smem_limit_once((const void*)probabilities_kernel<T, To>, kPieces * kRowThreads * 16, attr);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(probabilities_kernel<T, To>, p, (unsigned)N * p.C, p.C, kRowThreads, held, s);
 }
 
-constexpr size_t kDistillSmem = (size_t)kMaxTop * 20 + 16 + ((1 << 20) / 4 / kMaxCluster + kRowThreads);  // float32 rows of 2^20
+// the pieces, 20 bytes a listed entry, and a byte for each piece of a row of 2^20 float32
+constexpr int kDistillSmem = kPieces * kRowThreads * 16 + kMaxTop * 20 + (1 << 20) / 4 / kMaxCluster + kRowThreads;
 
-template <class T, bool kHold>
+template <class T, bool kRest>
 static cudaError_t launch_distill(const DistillParams& p, int N, cudaStream_t s) {
   static std::atomic<unsigned long long> attr{0};
-  const size_t smem = (((size_t)p.K * 12 + 15) & ~(size_t)15) + (size_t)p.K * 8 + p.marks;
-  const cudaError_t e = set_smem_limit_once((const void*)distill_kernel<T, kHold>, (int)kDistillSmem, attr);
+  const cudaError_t e = set_smem_limit_once((const void*)distill_kernel<T, kRest>, kDistillSmem, attr);
   if (e != cudaSuccess) return e;
-  return launch_clusters(distill_kernel<T, kHold>, p, (unsigned)N * p.C, p.C, kRowThreads, smem, s);
+  return launch_clusters(distill_kernel<T, kRest>, p, (unsigned)N * p.C, p.C, kRowThreads, (size_t)p.held + (size_t)p.K * 20 + p.marks, s);
 }
 
 static bool row_args(int32_t N, int32_t V, int32_t dtype) {
@@ -579,16 +623,16 @@ extern "C" dspark_status dspark_probabilities(int32_t N, int32_t V, int32_t dtyp
   if (N == 0) return DSPARK_OK;
   const int sms = sm_count();
   if (sms == 0) return DSPARK_ERR_CUDA;
-  bool hold;
-  const int C = row_cluster(N, V, dtype == DSPARK_BF16 ? 2 : 4, sms, hold);
+  int held;
+  const int C = row_cluster(N, V, dtype == DSPARK_BF16 ? 2 : 4, sms, held);
   const ProbsParams p{V, C, logits, temperature, probs, static_cast<uint32_t*>(workspace)};
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
   if (dtype == DSPARK_BF16)
-    e = probs_dtype == DSPARK_BF16 ? launch_probs<__nv_bfloat16, __nv_bfloat16>(p, N, hold, s)
-                                   : launch_probs<__nv_bfloat16, float>(p, N, hold, s);
+    e = probs_dtype == DSPARK_BF16 ? launch_probs<__nv_bfloat16, __nv_bfloat16>(p, N, held, s)
+                                   : launch_probs<__nv_bfloat16, float>(p, N, held, s);
   else
-    e = probs_dtype == DSPARK_BF16 ? launch_probs<float, __nv_bfloat16>(p, N, hold, s) : launch_probs<float, float>(p, N, hold, s);
+    e = probs_dtype == DSPARK_BF16 ? launch_probs<float, __nv_bfloat16>(p, N, held, s) : launch_probs<float, float>(p, N, held, s);
   note_launches(1);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
@@ -605,17 +649,17 @@ extern "C" dspark_status dspark_distill(int32_t N, int32_t V, int32_t K, int32_t
   if (N == 0) return DSPARK_OK;
   const int sms = sm_count();
   if (sms == 0) return DSPARK_ERR_CUDA;
-  bool hold;
+  int held;
   const int elem = dtype == DSPARK_BF16 ? 2 : 4;
-  const int C = row_cluster(N, V, elem, sms, hold);
+  const int C = row_cluster(N, V, elem, sms, held);
   // one byte a piece of this CTA, whole steps of the block
   const int marks = ceil_div((long long)V * elem / 16, (long long)C * kRowThreads) * kRowThreads;
-  const DistillParams p{V, K, C, marks, logits, ids, teacher, teacher_lse, weight, temperature, loss, grad,
+  const DistillParams p{V, K, C, held, marks, logits, ids, teacher, teacher_lse, weight, temperature, loss, grad,
                         static_cast<uint32_t*>(workspace)};
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  if (dtype == DSPARK_BF16) e = hold ? launch_distill<__nv_bfloat16, true>(p, N, s) : launch_distill<__nv_bfloat16, false>(p, N, s);
-  else e = hold ? launch_distill<float, true>(p, N, s) : launch_distill<float, false>(p, N, s);
+  if (dtype == DSPARK_BF16) e = teacher_lse ? launch_distill<__nv_bfloat16, true>(p, N, s) : launch_distill<__nv_bfloat16, false>(p, N, s);
+  else e = teacher_lse ? launch_distill<float, true>(p, N, s) : launch_distill<float, false>(p, N, s);
   note_launches(1);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
