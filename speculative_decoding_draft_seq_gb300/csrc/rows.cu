@@ -23,6 +23,7 @@ constexpr int kRowThreads = 512;
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kPieces = 8;       // 16-byte pieces of a row that a thread holds
 constexpr int kMaxCluster = 8;   // the portable limit
+static_assert(kRowThreads == 512 && kMaxCluster == 8, "RowPart takes logarithms of both");
 constexpr int kMaxTop = 1024;    // listed teacher entries of a row
 
 __device__ __forceinline__ float nan_max(float a, float b) {  // NaN if either is
@@ -68,24 +69,22 @@ template <class T>
 struct RowPart {
   static constexpr int E = 16 / sizeof(T);
   const T* row;
-  int V, a0, n, C, rank;
-  __device__ RowPart(const T* r, int V_, int C_, int rank_) : row(r), V(V_), C(C_), rank(rank_) {
+  int a0, n, shift, rank;  // C NT = 2^shift, C a power of two up to kMaxCluster
+  __device__ RowPart(const T* r, int V, int C, int rank_) : row(r), shift(9 + (C >= 2) + (C >= 4) + (C >= 8)), rank(rank_) {
     const int off = (int)((reinterpret_cast<uintptr_t>(r) & 15) / sizeof(T));
     a0 = min(off ? E - off : 0, V);
     n = (V - a0) / E;
   }
-  __device__ __forceinline__ int loose() const { return V - n * E; }
-  __device__ __forceinline__ int piece(int i) const { return (i * C + rank) * kRowThreads + (int)threadIdx.x; }
+  __device__ __forceinline__ int piece(int i) const { return (i << shift) + rank * kRowThreads + (int)threadIdx.x; }
   // pieces that this thread owns
   __device__ __forceinline__ int own() const {
-    const int step = C * kRowThreads, first = rank * kRowThreads + (int)threadIdx.x;
-    return first < n ? (n - first + step - 1) / step : 0;
+    return (n - 1 - piece(0) + (1 << shift)) >> shift;
   }
-  __device__ __forceinline__ int steps() const { return ceil_div(n, C * kRowThreads); }
+  __device__ __forceinline__ int steps() const { return (n + (1 << shift) - 1) >> shift; }
   // the loose element that this thread owns, or -1
-  __device__ __forceinline__ int own_loose() const {
+  __device__ __forceinline__ int own_loose(int V) const {
     const int i = threadIdx.x;
-    return rank == 0 && i < loose() ? (i < a0 ? i : i + n * E) : -1;
+    return rank == 0 && i < V - n * E ? (i < a0 ? i : i + n * E) : -1;
   }
   // owner of element v: CTA, and the local number of its piece (step * NT + thread); loose ones: -1 - number
   __device__ __forceinline__ int owner(int v, int& local, int& at) const {
@@ -94,10 +93,9 @@ struct RowPart {
       at = 0;
       return 0;
     }
-    const int g = (v - a0) / E;
+    const int g = (v - a0) / E, t = g & ((1 << shift) - 1);
     at = (v - a0) % E;
-    const int step = g / (C * kRowThreads), t = g - step * C * kRowThreads;
-    local = step * kRowThreads + t % kRowThreads;
+    local = (g >> shift) * kRowThreads + t % kRowThreads;
     return t / kRowThreads;
   }
   // starts the copies of this thread's pieces i0 .. min(i0 + kPieces, own) - 1
@@ -171,6 +169,19 @@ struct Weigher {
   }
 };
 
+// f(i) for i < m <= kPieces, U at a time.
+template <int U, class F>
+__device__ __forceinline__ void for_pieces(int m, F f) {
+  int i = 0;
+#pragma unroll 1
+  for (; i + U <= m; i += U) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) f(i + j);
+  }
+#pragma unroll 1
+  for (; i < m; ++i) f(i);
+}
+
 // (maximum, sum) of a warp's pieces, continued over windows; `listed` the part of the sum that is marked.
 struct WarpSum {
   float m = -INFINITY, z = 0.f, listed = 0.f;
@@ -182,8 +193,7 @@ __device__ __forceinline__ void add_pieces(WarpSum& s, const uint4* held, int m,
   constexpr int W = 8 / sizeof(T);
   const uint4* mine = held + threadIdx.x;
   float top = loose;
-#pragma unroll 4
-  for (int i = 0; i < m; ++i) top = nan_max(top, piece_max<T>(mine[i * kRowThreads]));
+  for_pieces<4>(m, [&](int i) { top = nan_max(top, piece_max<T>(mine[i * kRowThreads])); });
   top = nan_max(s.m, warp_nan_max(top));
   if (top == -INFINITY) return;  // (the whole warp)
   const Weigher w(top, h, rate);
@@ -195,8 +205,7 @@ __device__ __forceinline__ void add_pieces(WarpSum& s, const uint4* held, int m,
   s.m = top;
   unsigned long long a = 0, b = 0;
   float l = 0.f;
-#pragma unroll 2
-  for (int i = 0; i < m; ++i) {
+  for_pieces<2>(m, [&](int i) {
     unsigned long long x[W];
     split_piece<T>(mine[i * kRowThreads], x);
 #pragma unroll
@@ -219,7 +228,7 @@ __device__ __forceinline__ void add_pieces(WarpSum& s, const uint4* held, int m,
       a = pair_add(a, x[e]);
       b = pair_add(b, x[e + 1]);
     }
-  }
+  });
   float a0, a1, b0, b1;
   f32x2_unpack(a, a0, a1);
   f32x2_unpack(b, b0, b1);
@@ -289,9 +298,9 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
   // the smallest rate (T = inf) still takes an entry of -inf to weight 0
   const float rate0 = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269504088896340736f, T_), 1e30f), 1e-45f);
   const float h = rate0 < 1e-36f ? 0.5f : 1.f, rate = rate0 < 1e-36f ? 2.f * rate0 : rate0;
-  const int loose_at = part.own_loose(), own = part.own();
+  const int loose_at = part.own_loose(p.V), own = part.own();
   const float loose = loose_at >= 0 ? row_elem(part.row + loose_at) : -INFINITY;
-  const int windows = max(1, ceil_div(part.steps(), kPieces));
+  const int windows = max(1, (part.steps() + kPieces - 1) / kPieces);
 
   WarpSum s;
   for (int c = 0; c < windows; ++c) {
@@ -311,8 +320,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
         copies_done();
       }
       const int m = min(own - c * kPieces, kPieces);
-#pragma unroll 2
-      for (int i = 0; i < m; ++i) f(held[i * kRowThreads + threadIdx.x], part.a0 + part.piece(c * kPieces + i) * E);
+      for_pieces<2>(m, [&](int i) { f(held[i * kRowThreads + threadIdx.x], part.a0 + part.piece(c * kPieces + i) * E); });
     }
   };
 
@@ -371,7 +379,8 @@ struct DistillParams {
   const float* teacher;
   const float* teacher_lse;
   const float* weight;
-  float tau;
+  double per_tau;      // 1 / temperature
+  float k_hi, k_lo;    // log2(e) / temperature
   float* loss;
   void* grad;
   uint32_t* status;
@@ -382,10 +391,21 @@ __device__ __forceinline__ double warp_add_d(double v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// e^y to float32's precision: the power of the fraction, |f| <= 1/2, so that y's size costs none
-__device__ __forceinline__ float exp_of(double y) {
-  const double o = fmax(y * 1.44269504088896340736, -160.0), n = rint(o);
-  return ldexpf(exp2f((float)(o - n)), (int)n);
+// a b as a float and what its rounding left
+struct Split {
+  float hi, lo;
+};
+__device__ __forceinline__ Split product(float a, float b_hi, float b_lo) {
+  const float p = __fmul_rn(a, b_hi);
+  return {p, __fmaf_rn(a, b_lo, __fmaf_rn(a, b_hi, -p))};
+}
+// 2^(a - b) to float32's precision whatever the size of a and b: the difference with what rounding cut off, the power
+// of its fraction
+__device__ __forceinline__ float exp2_difference(Split a, Split b) {
+  const float d = __fsub_rn(a.hi, b.hi), v = __fsub_rn(d, a.hi);
+  const float cut = __fsub_rn(__fsub_rn(a.hi, __fsub_rn(d, v)), __fadd_rn(b.hi, v));
+  const float n = fmaxf(rintf(d), -160.f);
+  return ldexpf(exp2f(__fadd_rn(__fsub_rn(d, n), __fadd_rn(cut, __fsub_rn(a.lo, b.lo)))), (int)n);
 }
 
 template <class T, bool kRest>
@@ -394,7 +414,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
   extern __shared__ __align__(16) uint4 held[];
   __shared__ float4 all[kMaxCluster * kRowWarps];
   __shared__ double sums[kRowWarps];
-  __shared__ double s_share;  // written by CTA 0 of the cluster
+  __shared__ float4 s_teacher;  // from CTA 0 of the cluster: 1 / share (or 1), share, what it leaves of 1, their sum
   __shared__ float maxima[kRowWarps];
   __shared__ uint32_t loose_marks;
   __shared__ int twice;
@@ -410,8 +430,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
   const T* row = static_cast<const T*>(p.logits) + r * p.V;
   const RowPart<T> part(row, p.V, C, rank);
   part.fetch(held, 0);
-  const float rate = __fdiv_rn(1.44269504088896340736f, p.tau);
-  const int loose_at = part.own_loose(), own = part.own();
+  const float rate = p.k_hi;
+  const int loose_at = part.own_loose(p.V), own = part.own();
   const float loose = loose_at >= 0 ? row_elem(row + loose_at) : -INFINITY;
 
   // the listed entries, in every CTA; those of this CTA's pieces are marked
@@ -450,31 +470,30 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
   const bool none = t_max == -INFINITY;
   const bool bad_teacher = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < INFINITY));
   const bool listless = none || bad_teacher;
-  const double per_tau = 1.0 / (double)p.tau;
-  // ln of an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum
-  const auto ln_p = [&](float t) { return kRest ? (double)t * per_tau - (double)lse : ((double)t - (double)lse) * per_tau; };
-  // their sum in float64: what it leaves of 1, and the logarithms' differences, may be small
+  const Split ref = kRest ? product(lse, 1.44269502e+00f, 1.92596303e-08f) : product(lse, p.k_hi, p.k_lo);
+  // an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum
+  const auto share_of = [&](int j) {
+    const float t = s_t[j];
+    return t == -INFINITY || listless ? 0.f : exp2_difference(product(t, p.k_hi, p.k_lo), ref);
+  };
+  const auto ln_p = [&](float t) { return kRest ? (double)t * p.per_tau - (double)lse : ((double)t - (double)lse) * p.per_tau; };
+  // CTA 0: in float64, since what they leave of 1, and the logarithms' differences, may be small
   if (rank == 0) {
-    double share = 0.0;
     if (warp * 32 < p.K) {
+      double share = 0.0;
       for (int j = tid; j < p.K; j += kRowThreads) {
         const double e = listless || s_id[j] < 0 ? 0.0 : exp(ln_p(s_t[j]));
         s_p[j] = e;
         share += e;
       }
       share = warp_add_d(share);
+      if (lane == 0) sums[warp] = share;
     }
-    if (lane == 0) sums[warp] = share;
     __syncthreads();
-    if (warp == 0) {
-      share = lane < min(ceil_div(p.K, 32), kRowWarps) ? sums[lane] : 0.0;
-      share = warp_add_d(share);
-    }
-    if (warp == 0) sums[0] = share;  // (read after the cluster's barrier)
   }
 
   WarpSum s;
-  const int windows = max(1, ceil_div(part.steps(), kPieces));
+  const int windows = max(1, (part.steps() + kPieces - 1) / kPieces);
   for (int c = 0; c < windows; ++c) {
     if (c > 0) part.fetch(held, c * kPieces);
     copies_done();
@@ -486,23 +505,27 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
     add_pieces<T, kRest>(s, held, min(own - c * kPieces, kPieces), c == 0 ? loose : -INFINITY, 1.f, rate, marks);
   }
   cluster_wait();
-  if (rank == 0 && warp == 0 && lane < C)
-    store_peer(peer_address(&s_share, lane), (unsigned long long)__double_as_longlong(sums[0]));
+  double share = 0.0;
+  if (rank == 0 && warp == 0) {
+    for (int i = 0; i < min((p.K + 31) / 32, kRowWarps); ++i) share += sums[i];
+    const double left = kRest ? fmax(0.0, 1.0 - share) : 0.0;
+    if (lane < C)
+      store_peer(peer_address(&s_teacher, lane),
+                 make_float4(kRest ? 1.f : share > 0.0 ? __fdiv_rn(1.f, (float)share) : 0.f, (float)share, (float)left, (float)(share + left)));
+  }
   const RowSum sum = exchange(s, all, C, rank, 1.f, rate);
   const bool bad = !(fabsf(sum.M) < INFINITY) || bad_teacher;
   const Weigher w(sum.M, 1.f, rate);
   const float z = sum.z + sum.listed, z_rest = sum.z;
-  const double share = s_share;
-  const float p_rest = kRest ? (float)fmax(0.0, 1.0 - share) : 0.f;
+  const float norm = s_teacher.x, p_rest = s_teacher.z;
   const bool some = kRest && p_rest > 0.f && z_rest > 0.f;  // a rest without mass on either side counts for nothing
 
   if (p.grad) {
     // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v)
     T* grad = static_cast<T*>(p.grad) + r * p.V;
     const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
-    const float scale = (float)((p.weight ? (double)__ldg(p.weight + r) : 1.0) * per_tau);
-    const float norm = kRest ? 1.f : share > 0.0 ? (float)(1.0 / share) : 0.f;
-    const float total = kRest ? (float)(share + (some ? (double)p_rest : 0.0)) : share > 0.0 ? 1.f : 0.f;
+    const float scale = __fmul_rn(p.weight ? __ldg(p.weight + r) : 1.f, (float)p.per_tau);
+    const float total = kRest ? (some ? s_teacher.w : s_teacher.y) : norm > 0.f ? 1.f : 0.f;
     const float per_z = total / z;
     const float listed_f = bad ? 0.f : scale * per_z;
     const float rest_f = bad ? 0.f : scale * (per_z - (some ? p_rest / z_rest : 0.f));
@@ -512,8 +535,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
         copies_done();
       }
       const int m = min(own - c * kPieces, kPieces);
-#pragma unroll 2
-      for (int i = 0; i < m; ++i) {
+      for_pieces<2>(m, [&](int i) {
         unsigned long long x[W];
         split_piece<T>(held[i * kRowThreads + tid], x);
         float y[E];
@@ -523,7 +545,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
           if (bad) y[2 * e] = y[2 * e + 1] = 0.f;
         }
         store_piece<T, E>(grad + part.a0 + (size_t)part.piece(c * kPieces + i) * E, y, wide);
-      }
+      });
     }
     if (loose_at >= 0) store_elem(grad + loose_at, bad ? 0.f : w(loose) * rest_f);
     // the listed entries of this CTA over what was just written
@@ -532,11 +554,11 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
       const int id = s_id[j];
       int local, at;
       if (id < 0 || part.owner(id, local, at) != rank) continue;
-      float e = listless ? 0.f : exp_of(ln_p(s_t[j]));
+      float e = share_of(j);
       if (twice) {  // an id that comes more than once: every occurrence writes the sum of all
         e = 0.f;
         for (int i = 0; i < p.K; ++i)
-          if (s_id[i] == id && !listless) e += exp_of(ln_p(s_t[i]));
+          if (s_id[i] == id) e += share_of(i);
       }
       store_elem(grad + id, __fmaf_rn(-scale * norm, e, w(s_x[j]) * listed_f));
     }
@@ -654,7 +676,9 @@ extern "C" dspark_status dspark_distill(int32_t N, int32_t V, int32_t K, int32_t
   const int C = row_cluster(N, V, elem, sms, held);
   // one byte a piece of this CTA, whole steps of the block
   const int marks = ceil_div((long long)V * elem / 16, (long long)C * kRowThreads) * kRowThreads;
-  const DistillParams p{V, K, C, held, marks, logits, ids, teacher, teacher_lse, weight, temperature, loss, grad,
+  const double k = 1.44269504088896340736 / (double)temperature;
+  const DistillParams p{V, K, C, held, marks, logits, ids, teacher, teacher_lse, weight, 1.0 / (double)temperature, (float)k,
+                        (float)(k - (double)(float)k), loss, grad,
                         static_cast<uint32_t*>(workspace)};
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
