@@ -19,11 +19,13 @@
 
 namespace dspark {
 
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 256;
 constexpr int kRowWarps = kRowThreads / 32;
-constexpr int kPieces = 8;       // 16-byte pieces of a row that a thread holds
+constexpr int kPieces = 16;      // 16-byte pieces of a row that a thread holds
+constexpr int kGroup = 4;        // pieces that are waited for and added together
+constexpr int kGroups = kPieces / kGroup;
 constexpr int kMaxCluster = 8;   // the portable limit
-static_assert(kRowThreads == 512 && kMaxCluster == 8, "RowPart takes logarithms of both");
+static_assert(kRowThreads == 256 && kMaxCluster == 8, "RowPart takes logarithms of both");
 constexpr int kMaxTop = 1024;    // listed teacher entries of a row
 
 __device__ __forceinline__ float nan_max(float a, float b) {  // NaN if either is
@@ -32,9 +34,9 @@ __device__ __forceinline__ float nan_max(float a, float b) {  // NaN if either i
   return d;
 }
 __device__ __forceinline__ float warp_nan_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = nan_max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  float d;
+  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+  return d;
 }
 __device__ __forceinline__ unsigned long long pair_mul(unsigned long long a, unsigned long long b) {
   unsigned long long d;
@@ -49,7 +51,11 @@ __device__ __forceinline__ unsigned long long pair_add(unsigned long long a, uns
 __device__ __forceinline__ void copy_async(uint4* to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
-__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void copies_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_done() {  // all groups but the last kLeft
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
 
 template <class T>
 __device__ __forceinline__ float row_elem(const T* p) {
@@ -70,7 +76,7 @@ struct RowPart {
   static constexpr int E = 16 / sizeof(T);
   const T* row;
   int a0, n, shift, rank;  // C NT = 2^shift, C a power of two up to kMaxCluster
-  __device__ RowPart(const T* r, int V, int C, int rank_) : row(r), shift(9 + (C >= 2) + (C >= 4) + (C >= 8)), rank(rank_) {
+  __device__ RowPart(const T* r, int V, int C, int rank_) : row(r), shift(8 + (C >= 2) + (C >= 4) + (C >= 8)), rank(rank_) {
     const int off = (int)((reinterpret_cast<uintptr_t>(r) & 15) / sizeof(T));
     a0 = min(off ? E - off : 0, V);
     n = (V - a0) / E;
@@ -98,10 +104,15 @@ struct RowPart {
     local = (g >> shift) * kRowThreads + t % kRowThreads;
     return t / kRowThreads;
   }
-  // starts the copies of this thread's pieces i0 .. min(i0 + kPieces, own) - 1
-  __device__ __forceinline__ void fetch(uint4* held, int i0) const {
-    const int m = min(own() - i0, kPieces);
-    for (int i = 0; i < m; ++i) copy_async(held + i * kRowThreads + threadIdx.x, row + a0 + (size_t)piece(i0 + i) * E);
+  // starts the copies of this thread's pieces i0 .. i0 + m - 1, m <= kPieces, in kGroups groups
+  __device__ __forceinline__ void fetch(uint4* held, int i0, int m) const {
+    const T* from = row + a0 + (size_t)piece(i0) * E;
+    const size_t step = (size_t)E << shift;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if (i < m) copy_async(held + i * kRowThreads + threadIdx.x, from + i * step);
+      if (i % kGroup == kGroup - 1) copies_group();
+    }
   }
 };
 
@@ -118,16 +129,23 @@ __device__ __forceinline__ void split_piece(const uint4& q, unsigned long long (
   }
 }
 template <class T>
-__device__ __forceinline__ float piece_max(const uint4& q) {
-  if constexpr (sizeof(T) == 4) {
-    return nan_max(nan_max(__uint_as_float(q.x), __uint_as_float(q.y)), nan_max(__uint_as_float(q.z), __uint_as_float(q.w)));
-  } else {
-    uint32_t a, b;
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(q.x), "r"(q.y));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(q.z), "r"(q.w));
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
-    return nan_max(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
-  }
+__device__ __forceinline__ uint4 empty_piece() {  // -inf throughout
+  const uint32_t e = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+  return make_uint4(e, e, e, e);
+}
+template <class T>
+__device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b) {  // of one float32 or two bf16
+  uint32_t d;
+  if constexpr (sizeof(T) == 4) d = __float_as_uint(nan_max(__uint_as_float(a), __uint_as_float(b)));
+  else asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+template <class T, int N>
+__device__ __forceinline__ float pieces_max(const uint4 (&q)[N]) {
+  uint32_t m = word_max<T>(word_max<T>(q[0].x, q[0].y), word_max<T>(q[0].z, q[0].w));
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = word_max<T>(m, word_max<T>(word_max<T>(q[i].x, q[i].y), word_max<T>(q[i].z, q[i].w)));
+  return sizeof(T) == 4 ? __uint_as_float(m) : nan_max(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 // E neighbouring results to out[0..E-1]; `wide`: aligned to their size
 template <class To, int E>
@@ -155,70 +173,70 @@ __device__ __forceinline__ void store_piece(To* out, const float (&y)[E], bool w
   }
 }
 
-// The exponent of an entry's weight: (x - M) r, as fma(x, h, -M h) (r / h) with h = 1, or 1/2 for rates so small
-// that differences past float32's range count. One entry, or two at a time with the same bits.
+// Weights 2^((x - M) rate) of a row's entries. Where c = fl(M rate) is of an ordinary size the exponent is one fma,
+// x rate - c, rounded once at its own size; the weights are then 2^lost too large, lost what c's rounding cut off, and
+// `scale` takes that off a sum or a result. Else it is (x - M) rate as fma(x, h, -M h) (rate / h), with h = 1/2 for rates
+// so small that differences past float32's range count (scale 1).
+struct Rate {
+  float h, rate;  // rate / h
+};
+__device__ __forceinline__ bool plain_exponent(const Rate& r, float M) { return r.h == 1.f && fabsf(M * r.rate) < 0x1p20f; }
+template <bool kPlain>
 struct Weigher {
-  float h, Mh, rate;
-  __device__ __forceinline__ Weigher(float M, float h_, float rate_) : h(h_), Mh(M * h_), rate(rate_) {}
-  __device__ __forceinline__ float operator()(float x) const { return ex2_approx(__fmul_rn(__fmaf_rn(x, h, -Mh), rate)); }
-  __device__ __forceinline__ unsigned long long both(unsigned long long x) const {
-    const unsigned long long y = pair_mul(f32x2_fma(x, f32x2_pack(h, h), f32x2_pack(-Mh, -Mh)), f32x2_pack(rate, rate));
-    float a, b;
-    f32x2_unpack(y, a, b);
-    return f32x2_pack(ex2_approx(a), ex2_approx(b));
+  float a, b, rate, scale;
+  __device__ __forceinline__ Weigher(const Rate& r, float M) : rate(r.rate) {
+    if constexpr (kPlain) {
+      a = r.rate;
+      b = -__fmul_rn(M, r.rate);
+      scale = ex2_approx(-__fmaf_rn(M, r.rate, b));
+    } else {
+      a = r.h;
+      b = -M * r.h;
+      scale = 1.f;
+    }
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    const float y = __fmaf_rn(x, a, b);
+    return ex2_approx(kPlain ? y : __fmul_rn(y, rate));
+  }
+  __device__ __forceinline__ unsigned long long both(unsigned long long x) const {  // two entries, the same bits
+    unsigned long long y = f32x2_fma(x, f32x2_pack(a, a), f32x2_pack(b, b));
+    if (!kPlain) y = pair_mul(y, f32x2_pack(rate, rate));
+    float y0, y1;
+    f32x2_unpack(y, y0, y1);
+    return f32x2_pack(ex2_approx(y0), ex2_approx(y1));
   }
 };
+// 2^((x - M) rate), what a sum relative to x is multiplied by to be one relative to M
+__device__ __forceinline__ float rescale(const Rate& r, float x, float M) { return Weigher<false>(r, M)(x); }
 
-// f(i) for i < m <= kPieces, U at a time.
-template <int U, class F>
-__device__ __forceinline__ void for_pieces(int m, F f) {
-  int i = 0;
-#pragma unroll 1
-  for (; i + U <= m; i += U) {
-#pragma unroll
-    for (int j = 0; j < U; ++j) f(i + j);
-  }
-#pragma unroll 1
-  for (; i < m; ++i) f(i);
-}
-
-// (maximum, sum) of a warp's pieces, continued over windows; `listed` the part of the sum that is marked.
-struct WarpSum {
+// (maximum, sum) of a thread's entries so far; `listed` the part of the sum that is marked.
+struct ThreadSum {
   float m = -INFINITY, z = 0.f, listed = 0.f;
 };
-// Adds the window's m pieces of this thread and its loose element (-inf: none). marks(i): the listed entries of piece i as
-// bits, marks(-1): whether the loose one is.
-template <class T, bool kMarks, class Marks>
-__device__ __forceinline__ void add_pieces(WarpSum& s, const uint4* held, int m, float loose, float h, float rate, Marks marks) {
+// Adds kGroup pieces and a loose element (-inf: none). bits(i): the marked entries of piece i, bits(-1): whether the
+// loose one is.
+template <class T, bool kMarks, bool kPlain, class Bits>
+__device__ __forceinline__ void add_weights(ThreadSum& s, const uint4 (&q)[kGroup], float loose, const Rate& r, Bits bits) {
   constexpr int W = 8 / sizeof(T);
-  const uint4* mine = held + threadIdx.x;
-  float top = loose;
-  for_pieces<4>(m, [&](int i) { top = nan_max(top, piece_max<T>(mine[i * kRowThreads])); });
-  top = nan_max(s.m, warp_nan_max(top));
-  if (top == -INFINITY) return;  // (the whole warp)
-  const Weigher w(top, h, rate);
-  if (s.m != -INFINITY) {
-    const float f = w(s.m);
-    s.z *= f;
-    s.listed *= f;
-  }
-  s.m = top;
+  const Weigher<kPlain> w(r, s.m);
   unsigned long long a = 0, b = 0;
   float l = 0.f;
-  for_pieces<2>(m, [&](int i) {
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i) {
     unsigned long long x[W];
-    split_piece<T>(mine[i * kRowThreads], x);
+    split_piece<T>(q[i], x);
 #pragma unroll
     for (int e = 0; e < W; ++e) x[e] = w.both(x[e]);
     if (kMarks) {
-      const uint32_t bits = marks(i);
-      if (bits) {
+      const uint32_t marked = bits(i);
+      if (marked) {
 #pragma unroll
         for (int e = 0; e < W; ++e) {
           float y0, y1;
           f32x2_unpack(x[e], y0, y1);
-          if (bits >> (2 * e) & 1) l += y0, y0 = 0.f;
-          if (bits >> (2 * e + 1) & 1) l += y1, y1 = 0.f;
+          if (marked >> (2 * e) & 1) l += y0, y0 = 0.f;
+          if (marked >> (2 * e + 1) & 1) l += y1, y1 = 0.f;
           x[e] = f32x2_pack(y0, y1);
         }
       }
@@ -228,17 +246,44 @@ __device__ __forceinline__ void add_pieces(WarpSum& s, const uint4* held, int m,
       a = pair_add(a, x[e]);
       b = pair_add(b, x[e + 1]);
     }
-  });
+  }
   float a0, a1, b0, b1;
   f32x2_unpack(a, a0, a1);
   f32x2_unpack(b, b0, b1);
   if (loose != -INFINITY) {
     const float y = w(loose);
-    if (kMarks && marks(-1)) l += y;
+    if (kMarks && bits(-1)) l += y;
     else a0 += y;
   }
-  s.z += (a0 + a1) + (b0 + b1);
-  s.listed += l;
+  s.z = __fmaf_rn((a0 + a1) + (b0 + b1), w.scale, s.z);
+  if (kMarks) s.listed = __fmaf_rn(l, w.scale, s.listed);
+}
+template <class T, bool kMarks, class Bits>
+__device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, Bits bits) {
+  uint4 q[kGroup];
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i) q[i] = i < m ? mine[i * kRowThreads] : empty_piece<T>();
+  const float top = nan_max(nan_max(s.m, loose), pieces_max<T>(q));
+  if (top == -INFINITY) return;
+  if (top != s.m) {
+    if (s.m != -INFINITY) {
+      const float f = rescale(r, s.m, top);
+      s.z *= f;
+      if (kMarks) s.listed *= f;
+    }
+    s.m = top;
+  }
+  if (plain_exponent(r, top)) add_weights<T, kMarks, true>(s, q, loose, r, bits);
+  else add_weights<T, kMarks, false>(s, q, loose, r, bits);
+}
+// A window's pieces, a group as soon as it has arrived; its first group is number g0 of the row.
+template <class T, bool kMarks, int g, class Bits>
+__device__ __forceinline__ void add_groups(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, Bits bits) {
+  copies_done<kGroups - 1 - g>();
+  if (g == 0 || m > g * kGroup)
+    add_group<T, kMarks>(s, mine + g * kGroup * kRowThreads, m - g * kGroup, g == 0 ? loose : -INFINITY, r,
+                         [&](int i) { return bits(i < 0 ? i : i + g * kGroup); });
+  if constexpr (g + 1 < kGroups) add_groups<T, kMarks, g + 1>(s, mine, m, loose, r, bits);
 }
 
 // The row's maximum and sums from those of all warps of the cluster, the same in every thread (a warp's lanes each
@@ -246,28 +291,26 @@ __device__ __forceinline__ void add_pieces(WarpSum& s, const uint4* held, int m,
 struct RowSum {
   float M, z, listed;
 };
-__device__ __forceinline__ RowSum exchange(WarpSum s, float4* all, int C, int rank, float h, float rate) {
+template <bool kMarks>
+__device__ __forceinline__ RowSum exchange(ThreadSum s, float4* all, int C, int rank, const Rate& rate) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  s.z = warp_sum(s.z);
-  s.listed = warp_sum(s.listed);
-  if (lane < C) store_peer(peer_address(all + rank * kRowWarps + warp, lane), make_float4(s.m, s.z, s.listed, 0.f));
+  const float m = warp_nan_max(s.m);
+  const float f = s.m == -INFINITY ? 0.f : rescale(rate, s.m, m);
+  const float zw = warp_sum(s.z * f), lw = kMarks ? warp_sum(s.listed * f) : 0.f;
+  if (lane < C) store_peer(peer_address(all + rank * kRowWarps + warp, lane), make_float4(m, zw, lw, 0.f));
   __syncwarp();
   cluster_arrive();
   cluster_wait();
   RowSum r{-INFINITY, 0.f, 0.f};
-  for (int i = lane; i < C * kRowWarps; i += 32) r.M = nan_max(r.M, all[i].x);
-  r.M = warp_nan_max(r.M);
+  const int n = C * kRowWarps;
+  static_assert(kMaxCluster * kRowWarps <= 64, "two entries a lane");
+  const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  const float4 t0 = lane < n ? all[lane] : none, t1 = lane + 32 < n ? all[lane + 32] : none;
+  r.M = warp_nan_max(nan_max(t0.x, t1.x));
   if (r.M == -INFINITY) return r;
-  const Weigher w(r.M, h, rate);
-  for (int i = lane; i < C * kRowWarps; i += 32) {
-    const float4 t = all[i];
-    if (t.x == -INFINITY) continue;
-    const float f = w(t.x);
-    r.z += t.y * f;
-    r.listed += t.z * f;
-  }
-  r.z = warp_sum(r.z);
-  r.listed = warp_sum(r.listed);
+  const float f0 = t0.x == -INFINITY ? 0.f : rescale(rate, t0.x, r.M), f1 = t1.x == -INFINITY ? 0.f : rescale(rate, t1.x, r.M);
+  r.z = warp_sum(__fmaf_rn(t0.y, f0, t1.y * f1));
+  if (kMarks) r.listed = warp_sum(__fmaf_rn(t0.z, f0, t1.z * f1));
   return r;
 }
 
@@ -280,6 +323,56 @@ struct ProbsParams {
   uint32_t* status;
 };
 
+template <class T, class To, bool kPlain>
+__device__ __forceinline__ void scaled_piece(const uint4& q, const Weigher<kPlain>& w, float by, To* out, bool wide) {
+  constexpr int E = 16 / sizeof(T), W = E / 2;
+  unsigned long long x[W];
+  split_piece<T>(q, x);
+  float y[E];
+#pragma unroll
+  for (int e = 0; e < W; ++e) f32x2_unpack(pair_mul(w.both(x[e]), f32x2_pack(by, by)), y[2 * e], y[2 * e + 1]);
+  store_piece<To, E>(out, y, wide);
+}
+// out[v] = weight of entry v times `by`, for this thread's pieces and its loose element.
+template <class T, class To, bool kPlain>
+__device__ __forceinline__ void write_weights(const RowPart<T>& part, uint4* held, int own, int windows, const Weigher<kPlain>& w, float by,
+                                              To* out, bool wide, int loose_at, float loose) {
+  constexpr int E = 16 / sizeof(T);
+  const uint4* mine = held + threadIdx.x;
+  const size_t step = (size_t)E << part.shift;
+  for (int c = 0; c < windows; ++c) {
+    const int m = min(own - c * kPieces, kPieces);
+    if (windows > 1) {
+      part.fetch(held, c * kPieces, m);
+      copies_done<0>();
+    }
+    To* to = out + part.a0 + (size_t)part.piece(c * kPieces) * E;
+    int i = 0;
+#pragma unroll 1
+    for (; i + 2 <= m; i += 2) {
+      const uint4 q0 = mine[i * kRowThreads], q1 = mine[(i + 1) * kRowThreads];
+      scaled_piece<T>(q0, w, by, to + i * step, wide);
+      scaled_piece<T>(q1, w, by, to + (i + 1) * step, wide);
+    }
+    if (i < m) scaled_piece<T>(mine[i * kRowThreads], w, by, to + i * step, wide);
+  }
+  if (loose_at >= 0) store_elem(out + loose_at, w(loose) * by);
+}
+// out[v] = 1 at v = top, else 0
+template <class T, class To>
+__device__ __forceinline__ void write_one(const RowPart<T>& part, int own, int top, To* out, bool wide, int loose_at) {
+  constexpr int E = 16 / sizeof(T);
+#pragma unroll 1
+  for (int i = 0; i < own; ++i) {
+    const int v = part.a0 + part.piece(i) * E;
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[e] = v + e == top ? 1.f : 0.f;
+    store_piece<To, E>(out + v, y, wide);
+  }
+  if (loose_at >= 0) store_elem(out + loose_at, loose_at == top ? 1.f : 0.f);
+}
+
 template <class T, class To>
 __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsParams p) {
   constexpr int E = 16 / sizeof(T), W = E / 2;
@@ -290,46 +383,45 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
   cluster_arrive();  // the others' shared memory is theirs once they run: waited for before the exchange
   const size_t r = blockIdx.x / C;
   const RowPart<T> part(static_cast<const T*>(p.logits) + r * p.V, p.V, C, rank);
-  part.fetch(held, 0);
+  const int own = part.own();
+  part.fetch(held, 0, min(own, kPieces));
   To* out = static_cast<To*>(p.probs) + r * p.V;
   const bool wide = (reinterpret_cast<uintptr_t>(out + part.a0) & (E * sizeof(To) - 1)) == 0;
   const float T_ = __ldg(p.temperature + r);
   const bool greedy = !(T_ > 0.f);
   // the smallest rate (T = inf) still takes an entry of -inf to weight 0
   const float rate0 = greedy ? 1.f : fmaxf(fminf(__fdiv_rn(1.44269504088896340736f, T_), 1e30f), 1e-45f);
-  const float h = rate0 < 1e-36f ? 0.5f : 1.f, rate = rate0 < 1e-36f ? 2.f * rate0 : rate0;
-  const int loose_at = part.own_loose(p.V), own = part.own();
+  const Rate rate{rate0 < 1e-36f ? 0.5f : 1.f, rate0 < 1e-36f ? 2.f * rate0 : rate0};
+  const int loose_at = part.own_loose(p.V);
   const float loose = loose_at >= 0 ? row_elem(part.row + loose_at) : -INFINITY;
   const int windows = max(1, (part.steps() + kPieces - 1) / kPieces);
+  const auto unmarked = [](int) { return 0u; };
 
-  WarpSum s;
+  ThreadSum s;
   for (int c = 0; c < windows; ++c) {
-    if (c > 0) part.fetch(held, c * kPieces);
-    copies_done();
-    add_pieces<T, false>(s, held, min(own - c * kPieces, kPieces), c == 0 ? loose : -INFINITY, h, rate, [](int) { return 0u; });
+    const int m = min(own - c * kPieces, kPieces);
+    if (c > 0) part.fetch(held, c * kPieces, m);
+    add_groups<T, false, 0>(s, held + threadIdx.x, m, c == 0 ? loose : -INFINITY, rate, unmarked);
   }
   cluster_wait();
-  const RowSum sum = exchange(s, all, C, rank, h, rate);
+  const RowSum sum = exchange<false>(s, all, C, rank, rate);
   const bool bad = !(fabsf(sum.M) < INFINITY);
   if (bad && rank == 0 && threadIdx.x == 0) set_status(p.status, DSPARK_ERR_NONFINITE);
-  // f(piece's number in the window's memory, first element) for this thread's pieces
-  const auto each = [&](auto f) {
-    for (int c = 0; c < windows; ++c) {
-      if (windows > 1) {
-        part.fetch(held, c * kPieces);
-        copies_done();
-      }
-      const int m = min(own - c * kPieces, kPieces);
-      for_pieces<2>(m, [&](int i) { f(held[i * kRowThreads + threadIdx.x], part.a0 + part.piece(c * kPieces + i) * E); });
-    }
-  };
-
-  if (bad || greedy) {
+  if (bad) {
+    write_one(part, own, -1, out, wide, loose_at);
+  } else if (greedy) {
     int top = INT_MAX;  // the first maximum
-    if (!bad) {
-      each([&](const uint4& q, int v) {
+    for (int c = 0; c < windows; ++c) {
+      const int m = min(own - c * kPieces, kPieces);
+      if (windows > 1) {
+        part.fetch(held, c * kPieces, m);
+        copies_done<0>();
+      }
+#pragma unroll 1
+      for (int i = 0; i < m; ++i) {
+        const int v = part.a0 + part.piece(c * kPieces + i) * E;
         unsigned long long x[W];
-        split_piece<T>(q, x);
+        split_piece<T>(held[i * kRowThreads + threadIdx.x], x);
 #pragma unroll
         for (int e = 0; e < W; ++e) {
           float x0, x1;
@@ -337,38 +429,23 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
           if (x0 == sum.M) top = min(top, v + 2 * e);
           if (x1 == sum.M) top = min(top, v + 2 * e + 1);
         }
-      });
-      if (loose_at >= 0 && loose == sum.M) top = min(top, loose_at);
-      top = warp_min_i(top);
-      if (lane < C) store_peer(peer_address(first + rank * kRowWarps + warp, lane), (uint32_t)top);
-      __syncwarp();
-      cluster_arrive();
-      cluster_wait();
-      top = INT_MAX;
-      for (int i = lane; i < C * kRowWarps; i += 32) top = min(top, (int)first[i]);
-      top = warp_min_i(top);
+      }
     }
-    for (int i = 0; i < own; ++i) {
-      const int v = part.a0 + part.piece(i) * E;
-      float y[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = v + e == top ? 1.f : 0.f;
-      store_piece<To, E>(out + v, y, wide);
-    }
-    if (loose_at >= 0) store_elem(out + loose_at, loose_at == top ? 1.f : 0.f);
-    return;
+    if (loose_at >= 0 && loose == sum.M) top = min(top, loose_at);
+    top = warp_min_i(top);
+    if (lane < C) store_peer(peer_address(first + rank * kRowWarps + warp, lane), (uint32_t)top);
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    top = INT_MAX;
+    for (int i = lane; i < C * kRowWarps; i += 32) top = min(top, (int)first[i]);
+    write_one(part, own, warp_min_i(top), out, wide, loose_at);
+  } else if (plain_exponent(rate, sum.M)) {
+    const Weigher<true> w(rate, sum.M);
+    write_weights(part, held, own, windows, w, __fdiv_rn(w.scale, sum.z), out, wide, loose_at, loose);
+  } else {
+    write_weights(part, held, own, windows, Weigher<false>(rate, sum.M), __fdiv_rn(1.f, sum.z), out, wide, loose_at, loose);
   }
-  const Weigher w(sum.M, h, rate);
-  const float inv = __fdiv_rn(1.f, sum.z);
-  each([&](const uint4& q, int v) {
-    unsigned long long x[W];
-    split_piece<T>(q, x);
-    float y[E];
-#pragma unroll
-    for (int e = 0; e < W; ++e) f32x2_unpack(pair_mul(w.both(x[e]), f32x2_pack(inv, inv)), y[2 * e], y[2 * e + 1]);
-    store_piece<To, E>(out + v, y, wide);
-  });
-  if (loose_at >= 0) store_elem(out + loose_at, w(loose) * inv);
 }
 
 // ---------------------------------------------------------------------------
@@ -408,19 +485,27 @@ __device__ __forceinline__ float exp2_difference(Split a, Split b) {
   return ldexpf(exp2f(__fadd_rn(__fsub_rn(d, n), __fadd_rn(cut, __fsub_rn(a.lo, b.lo)))), (int)n);
 }
 
+// ln v, its exponent's part in float64: within 2^-24 whatever the size
+__device__ __forceinline__ double ln_of(double v) {
+  const float f = (float)v;
+  int e;
+  float m = frexpf(f, &e);  // [1/2, 1)
+  if (m < 0.70710678f) m *= 2.f, --e;
+  return (double)e * 0.69314718055994530942 + (double)__fadd_rn(logf(m), (float)(v - (double)f) * __fdiv_rn(1.f, f));
+}
+
 template <class T, bool kRest>
 __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p) {
-  constexpr int E = 16 / sizeof(T), W = E / 2;
   extern __shared__ __align__(16) uint4 held[];
   __shared__ float4 all[kMaxCluster * kRowWarps];
-  __shared__ double sums[kRowWarps];
-  __shared__ float4 s_teacher;  // from CTA 0 of the cluster: 1 / share (or 1), share, what it leaves of 1, their sum
+  __shared__ double sums[kRowWarps][3];
+  __shared__ float4 s_teacher;  // from CTA 0 of the cluster: share, what it leaves of 1, their sum
   __shared__ float maxima[kRowWarps];
   __shared__ uint32_t loose_marks;
   __shared__ int twice;
-  // of the listed entries: the teacher's probability (CTA 0), its logit, the student's, the id (-1: none); then the map
-  double* s_p = reinterpret_cast<double*>(reinterpret_cast<char*>(held) + p.held);
-  float* s_t = reinterpret_cast<float*>(s_p + p.K);
+  // of the listed entries: the teacher's share, its logit, the student's, the id (-1: none); then the map
+  float* s_e = reinterpret_cast<float*>(reinterpret_cast<char*>(held) + p.held);
+  float* s_t = s_e + p.K;
   float* s_x = s_t + p.K;
   int* s_id = reinterpret_cast<int*>(s_x + p.K);
   uint32_t* s_marks = reinterpret_cast<uint32_t*>(s_id + p.K);
@@ -429,9 +514,10 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
   const size_t r = blockIdx.x / C;
   const T* row = static_cast<const T*>(p.logits) + r * p.V;
   const RowPart<T> part(row, p.V, C, rank);
-  part.fetch(held, 0);
-  const float rate = p.k_hi;
-  const int loose_at = part.own_loose(p.V), own = part.own();
+  const int own = part.own();
+  part.fetch(held, 0, min(own, kPieces));
+  const Rate rate{1.f, p.k_hi};
+  const int loose_at = part.own_loose(p.V);
   const float loose = loose_at >= 0 ? row_elem(row + loose_at) : -INFINITY;
 
   // the listed entries, in every CTA; those of this CTA's pieces are marked
@@ -464,126 +550,127 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
   t_max = warp_nan_max(t_max);
   if (lane == 0) maxima[warp] = t_max;
   __syncthreads();
-  t_max = lane < kRowWarps ? maxima[lane] : -INFINITY;
-  t_max = warp_nan_max(t_max);
+  t_max = warp_nan_max(maxima[lane % kRowWarps]);
   const float lse = kRest ? __ldg(p.teacher_lse + r) : t_max;
-  const bool none = t_max == -INFINITY;
   const bool bad_teacher = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < INFINITY));
-  const bool listless = none || bad_teacher;
-  const Split ref = kRest ? product(lse, 1.44269502e+00f, 1.92596303e-08f) : product(lse, p.k_hi, p.k_lo);
+  const bool listless = t_max == -INFINITY || bad_teacher;
   // an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum
-  const auto share_of = [&](int j) {
+  const Split ref = kRest ? product(lse, 1.44269502e+00f, 1.92596299e-08f) : product(lse, p.k_hi, p.k_lo);
+  for (int j = tid; j < p.K; j += kRowThreads) {
     const float t = s_t[j];
-    return t == -INFINITY || listless ? 0.f : exp2_difference(product(t, p.k_hi, p.k_lo), ref);
-  };
-  const auto ln_p = [&](float t) { return kRest ? (double)t * p.per_tau - (double)lse : ((double)t - (double)lse) * p.per_tau; };
-  // CTA 0: in float64, since what they leave of 1, and the logarithms' differences, may be small
-  if (rank == 0) {
-    if (warp * 32 < p.K) {
-      double share = 0.0;
-      for (int j = tid; j < p.K; j += kRowThreads) {
-        const double e = listless || s_id[j] < 0 ? 0.0 : exp(ln_p(s_t[j]));
-        s_p[j] = e;
-        share += e;
-      }
-      share = warp_add_d(share);
-      if (lane == 0) sums[warp] = share;
-    }
-    __syncthreads();
+    s_e[j] = t == -INFINITY || listless ? 0.f : exp2_difference(product(t, p.k_hi, p.k_lo), ref);
   }
+  // CTA 0, for the loss: sums over the listed entries of e, e ln e and e x, in float64, since what they leave of 1, and
+  // differences of logarithms, may be small
+  if (rank == 0 && warp * 32 < p.K) {
+    double a = 0.0, b = 0.0, c = 0.0;
+    for (int j = tid; j < p.K; j += kRowThreads) {
+      const float t = s_t[j];
+      if (t == -INFINITY || listless) continue;
+      const double y = kRest ? (double)t * p.per_tau - (double)lse : ((double)t - (double)lse) * p.per_tau, e = exp(y);
+      if (e > 0.0) {
+        a += e;
+        b += e * y;
+        c += e * (double)s_x[j];
+      }
+    }
+    a = warp_add_d(a);
+    b = warp_add_d(b);
+    c = warp_add_d(c);
+    if (lane == 0) sums[warp][0] = a, sums[warp][1] = b, sums[warp][2] = c;
+  }
+  if (kRest && rank == 0) __syncthreads();
 
-  WarpSum s;
+  ThreadSum s;
   const int windows = max(1, (part.steps() + kPieces - 1) / kPieces);
   for (int c = 0; c < windows; ++c) {
-    if (c > 0) part.fetch(held, c * kPieces);
-    copies_done();
-    const auto marks = [&](int i) -> uint32_t {
+    const int m = min(own - c * kPieces, kPieces);
+    if (c > 0) part.fetch(held, c * kPieces, m);
+    add_groups<T, kRest, 0>(s, held + tid, m, c == 0 ? loose : -INFINITY, rate, [&](int i) -> uint32_t {
       if (i < 0) return loose_marks >> tid & 1u;
       const int local = (c * kPieces + i) * kRowThreads + tid;
-      return s_marks[local >> 2] >> ((local & 3) * 8) & 255u;
-    };
-    add_pieces<T, kRest>(s, held, min(own - c * kPieces, kPieces), c == 0 ? loose : -INFINITY, 1.f, rate, marks);
+      return local < p.marks ? s_marks[local >> 2] >> ((local & 3) * 8) & 255u : 0u;
+    });
   }
   cluster_wait();
-  double share = 0.0;
-  if (rank == 0 && warp == 0) {
-    for (int i = 0; i < min((p.K + 31) / 32, kRowWarps); ++i) share += sums[i];
-    const double left = kRest ? fmax(0.0, 1.0 - share) : 0.0;
-    if (lane < C)
-      store_peer(peer_address(&s_teacher, lane),
-                 make_float4(kRest ? 1.f : share > 0.0 ? __fdiv_rn(1.f, (float)share) : 0.f, (float)share, (float)left, (float)(share + left)));
+  const auto sum_of = [&](int i) {
+    double v = 0.0;
+    for (int w = 0; w < min((p.K + 31) / 32, kRowWarps); ++w) v += sums[w][i];
+    return v;
+  };
+  if (kRest && rank == 0 && warp == 0) {
+    const double share = sum_of(0), left = fmax(0.0, 1.0 - share);
+    if (lane < C) store_peer(peer_address(&s_teacher, lane), make_float4((float)share, (float)left, (float)(share + left), 0.f));
   }
-  const RowSum sum = exchange(s, all, C, rank, 1.f, rate);
+  const RowSum sum = exchange<kRest>(s, all, C, rank, rate);
   const bool bad = !(fabsf(sum.M) < INFINITY) || bad_teacher;
-  const Weigher w(sum.M, 1.f, rate);
-  const float z = sum.z + sum.listed, z_rest = sum.z;
-  const float norm = s_teacher.x, p_rest = s_teacher.z;
-  const bool some = kRest && p_rest > 0.f && z_rest > 0.f;  // a rest without mass on either side counts for nothing
+  const float z = sum.z + sum.listed;
+  const bool some = kRest && s_teacher.y > 0.f && sum.z > 0.f;  // a rest without mass on either side counts for nothing
 
   if (p.grad) {
     // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v)
     T* grad = static_cast<T*>(p.grad) + r * p.V;
     const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
     const float scale = __fmul_rn(p.weight ? __ldg(p.weight + r) : 1.f, (float)p.per_tau);
-    const float total = kRest ? (some ? s_teacher.w : s_teacher.y) : norm > 0.f ? 1.f : 0.f;
-    const float per_z = total / z;
-    const float listed_f = bad ? 0.f : scale * per_z;
-    const float rest_f = bad ? 0.f : scale * (per_z - (some ? p_rest / z_rest : 0.f));
-    for (int c = 0; c < windows; ++c) {
-      if (windows > 1) {
-        part.fetch(held, c * kPieces);
-        copies_done();
-      }
-      const int m = min(own - c * kPieces, kPieces);
-      for_pieces<2>(m, [&](int i) {
-        unsigned long long x[W];
-        split_piece<T>(held[i * kRowThreads + tid], x);
-        float y[E];
-#pragma unroll
-        for (int e = 0; e < W; ++e) {
-          f32x2_unpack(pair_mul(w.both(x[e]), f32x2_pack(rest_f, rest_f)), y[2 * e], y[2 * e + 1]);
-          if (bad) y[2 * e] = y[2 * e + 1] = 0.f;
-        }
-        store_piece<T, E>(grad + part.a0 + (size_t)part.piece(c * kPieces + i) * E, y, wide);
-      });
+    const float per_z = __fdiv_rn(kRest ? (some ? s_teacher.z : s_teacher.x) : listless ? 0.f : 1.f, z);
+    const float rest_f = scale * (per_z - (some ? __fdiv_rn(s_teacher.y, sum.z) : 0.f));
+    const bool plain = plain_exponent(rate, sum.M);
+    if (bad) {
+      write_one(part, own, -1, grad, wide, loose_at);
+    } else if (plain) {
+      const Weigher<true> w(rate, sum.M);
+      write_weights(part, held, own, windows, w, rest_f * w.scale, grad, wide, loose_at, loose);
+    } else {
+      write_weights(part, held, own, windows, Weigher<false>(rate, sum.M), rest_f, grad, wide, loose_at, loose);
     }
-    if (loose_at >= 0) store_elem(grad + loose_at, bad ? 0.f : w(loose) * rest_f);
     // the listed entries of this CTA over what was just written
     __syncthreads();
+    float norm = 1.f;
+    if (!kRest) {
+      norm = 0.f;
+      for (int j = lane; j < p.K; j += 32) norm += s_e[j];
+      norm = warp_sum(norm);
+      norm = norm > 0.f ? __fdiv_rn(1.f, norm) : 0.f;
+    }
     for (int j = tid; j < p.K && !bad; j += kRowThreads) {
       const int id = s_id[j];
       int local, at;
       if (id < 0 || part.owner(id, local, at) != rank) continue;
-      float e = share_of(j);
+      float e = s_e[j];
       if (twice) {  // an id that comes more than once: every occurrence writes the sum of all
         e = 0.f;
         for (int i = 0; i < p.K; ++i)
-          if (s_id[i] == id) e += share_of(i);
+          if (s_id[i] == id) e += s_e[i];
       }
-      store_elem(grad + id, __fmaf_rn(-scale * norm, e, w(s_x[j]) * listed_f));
+      const float x = s_x[j];
+      float y;
+      if (plain) {
+        const Weigher<true> w(rate, sum.M);
+        y = w(x) * w.scale;
+      } else {
+        y = Weigher<false>(rate, sum.M)(x);
+      }
+      store_elem(grad + id, __fmaf_rn(-scale * norm, e, y * (scale * per_z)));
     }
+  } else {
+    __syncthreads();
   }
 
-  if (rank == 0 && warp == 0) {
-    const double step = (double)rate * 0.69314718055994530942;  // 1 / tau as the weights have it
-    double a = 0.0;
-    for (int j = lane; j < p.K; j += 32) {
-      const double e = s_p[j];
-      if (e > 0.0) a += e * (ln_p(s_t[j]) - ((double)s_x[j] - (double)sum.M) * step);
+  if (rank == 0 && tid == 0) {
+    const double share = sum_of(0), step = (double)p.k_hi * 0.69314718055994530942;  // 1 / tau as the weights have it
+    const double a = sum_of(1) - step * (sum_of(2) - (double)sum.M * share), ln_z = ln_of((double)z);
+    double loss = 0.0;
+    if (kRest) {
+      const double left = fmax(0.0, 1.0 - share);
+      loss = a + share * ln_z;
+      if (some) loss += left * (ln_of(left) - ln_of((double)sum.z) + ln_z);
+    } else if (share > 0.0) {
+      double inv = (double)__fdiv_rn(1.f, (float)share);
+      inv *= 2.0 - share * inv;
+      loss = a * inv + ln_z - ln_of(share);
     }
-    a = warp_add_d(a);
-    if (lane == 0) {
-      double loss = 0.0;
-      if (kRest) {
-        const double left = fmax(0.0, 1.0 - share);
-        loss = a + share * log((double)z);
-        if (some) loss += left * log(left * ((double)z / (double)z_rest));
-      } else if (share > 0.0) {
-        loss = a / share + log((double)z / share);
-      }
-      p.loss[r] = bad ? NAN : (float)loss;
-      if (bad) set_status(p.status, DSPARK_ERR_NONFINITE);
-    }
+    p.loss[r] = bad ? NAN : (float)loss;
+    if (bad) set_status(p.status, DSPARK_ERR_NONFINITE);
   }
 }
 
@@ -613,15 +700,15 @@ static cudaError_t launch_probs(const ProbsParams& p, int N, int held, cudaStrea
   return launch_clusters(probabilities_kernel<T, To>, p, (unsigned)N * p.C, p.C, kRowThreads, held, s);
 }
 
-// the pieces, 20 bytes a listed entry, and a byte for each piece of a row of 2^20 float32
-constexpr int kDistillSmem = kPieces * kRowThreads * 16 + kMaxTop * 20 + (1 << 20) / 4 / kMaxCluster + kRowThreads;
+// the pieces, 16 bytes a listed entry, and a byte for each piece of a row of 2^20 float32
+constexpr int kDistillSmem = kPieces * kRowThreads * 16 + kMaxTop * 16 + (1 << 20) / 4 / kMaxCluster + kRowThreads;
 
 template <class T, bool kRest>
 static cudaError_t launch_distill(const DistillParams& p, int N, cudaStream_t s) {
   static std::atomic<unsigned long long> attr{0};
   const cudaError_t e = set_smem_limit_once((const void*)distill_kernel<T, kRest>, kDistillSmem, attr);
   if (e != cudaSuccess) return e;
-  return launch_clusters(distill_kernel<T, kRest>, p, (unsigned)N * p.C, p.C, kRowThreads, (size_t)p.held + (size_t)p.K * 20 + p.marks, s);
+  return launch_clusters(distill_kernel<T, kRest>, p, (unsigned)N * p.C, p.C, kRowThreads, (size_t)p.held + (size_t)p.K * 16 + p.marks, s);
 }
 
 static bool row_args(int32_t N, int32_t V, int32_t dtype) {
