@@ -12,6 +12,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// (Without memory ordering: for a barrier that only says that every CTA runs.)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Address of this CTA's shared-memory variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
@@ -27,6 +29,37 @@ __device__ __forceinline__ void store_peer(uint32_t a, uint32_t v) {
 }
 __device__ __forceinline__ void store_peer(uint32_t a, unsigned long long v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+
+// Clusters of C CTAs that the current device holds at once. The answer is a property of the kernel, the device and
+// these numbers; each thread keeps its last one.
+inline cudaError_t resident_clusters(const void* kernel, int C, int threads, size_t smem, int& n) {
+  static thread_local struct {
+    const void* kernel;
+    int device, C, n;
+    size_t smem;
+  } last{};
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (last.n == 0 || last.kernel != kernel || last.device != device || last.C != C || last.smem != smem) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(C);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = C;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int found = 0;
+    e = cudaOccupancyMaxActiveClusters(&found, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    last = {kernel, device, C, found > 0 ? found : 1, smem};
+  }
+  n = last.n;
+  return cudaSuccess;
 }
 
 // Launches `ctas` CTAs in clusters of C.

@@ -15,6 +15,7 @@
 #include "cluster.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "mass.cuh"
 #include "verify_common.cuh"
 
 namespace dspark {
@@ -25,7 +26,7 @@ constexpr int kPieces = 16;      // 16-byte pieces of a row that a thread holds
 constexpr int kGroup = 4;        // pieces that are waited for and added together
 constexpr int kGroups = kPieces / kGroup;
 constexpr int kMaxCluster = 8;   // the portable limit
-static_assert(kRowThreads == 256 && kMaxCluster == 8, "RowPart takes logarithms of both");
+static_assert(kMaxCluster == 8, "RowPart takes its logarithm");
 constexpr int kMaxTop = 1024;    // listed teacher entries of a row
 
 __device__ __forceinline__ float nan_max(float a, float b) {  // NaN if either is
@@ -36,16 +37,6 @@ __device__ __forceinline__ float nan_max(float a, float b) {  // NaN if either i
 __device__ __forceinline__ float warp_nan_max(float v) {
   float d;
   asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
-  return d;
-}
-__device__ __forceinline__ unsigned long long pair_mul(unsigned long long a, unsigned long long b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ unsigned long long pair_add(unsigned long long a, unsigned long long b) {
-  unsigned long long d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ void copy_async(uint4* to, const void* from) {
@@ -75,18 +66,18 @@ template <class T>
 struct RowPart {
   static constexpr int E = 16 / sizeof(T);
   const T* row;
-  int a0, n, shift, rank;  // C NT = 2^shift, C a power of two up to kMaxCluster
-  __device__ RowPart(const T* r, int V, int C, int rank_) : row(r), shift(8 + (C >= 2) + (C >= 4) + (C >= 8)), rank(rank_) {
+  int a0, n, shift, rank;  // C = 2^shift, up to kMaxCluster
+  __device__ RowPart(const T* r, int V, int C, int rank_) : row(r), shift((C >= 2) + (C >= 4) + (C >= 8)), rank(rank_) {
     const int off = (int)((reinterpret_cast<uintptr_t>(r) & 15) / sizeof(T));
     a0 = min(off ? E - off : 0, V);
     n = (V - a0) / E;
   }
-  __device__ __forceinline__ int piece(int i) const { return (i << shift) + rank * kRowThreads + (int)threadIdx.x; }
+  __device__ __forceinline__ int piece(int i) const { return ((i << shift) + rank) * kRowThreads + (int)threadIdx.x; }
   // pieces that this thread owns
   __device__ __forceinline__ int own() const {
-    return (n - 1 - piece(0) + (1 << shift)) >> shift;
+    return (n - 1 - (int)threadIdx.x + kRowThreads) / kRowThreads + (1 << shift) - 1 - rank >> shift;
   }
-  __device__ __forceinline__ int steps() const { return (n + (1 << shift) - 1) >> shift; }
+  __device__ __forceinline__ int steps() const { return ((n + kRowThreads - 1) / kRowThreads + (1 << shift) - 1) >> shift; }
   // the loose element that this thread owns, or -1
   __device__ __forceinline__ int own_loose(int V) const {
     const int i = threadIdx.x;
@@ -99,20 +90,25 @@ struct RowPart {
       at = 0;
       return 0;
     }
-    const int g = (v - a0) / E, t = g & ((1 << shift) - 1);
+    const int g = (v - a0) / E, block = g / kRowThreads;
     at = (v - a0) % E;
-    local = (g >> shift) * kRowThreads + t % kRowThreads;
-    return t / kRowThreads;
+    local = (block >> shift) * kRowThreads + g % kRowThreads;
+    return block & ((1 << shift) - 1);
   }
-  // starts the copies of this thread's pieces i0 .. i0 + m - 1, m <= kPieces, in kGroups groups
-  __device__ __forceinline__ void fetch(uint4* held, int i0, int m) const {
+  // starts the copies of group g of this thread's pieces i0 .. i0 + m - 1
+  __device__ __forceinline__ void fetch_group(uint4* held, int i0, int m, int g) const {
     const T* from = row + a0 + (size_t)piece(i0) * E;
-    const size_t step = (size_t)E << shift;
+    const size_t step = (size_t)(E * kRowThreads) << shift;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      if (i < m) copy_async(held + i * kRowThreads + threadIdx.x, from + i * step);
-      if (i % kGroup == kGroup - 1) copies_group();
+    for (int i = 0; i < kGroup; ++i) {
+      const int k = g * kGroup + i;
+      if (k < m) copy_async(held + k * kRowThreads + threadIdx.x, from + k * step);
     }
+    copies_group();
+  }
+  __device__ __forceinline__ void fetch(uint4* held, int i0, int m) const {
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) fetch_group(held, i0, m, g);
   }
 };
 
@@ -201,7 +197,7 @@ struct Weigher {
   }
   __device__ __forceinline__ unsigned long long both(unsigned long long x) const {  // two entries, the same bits
     unsigned long long y = f32x2_fma(x, f32x2_pack(a, a), f32x2_pack(b, b));
-    if (!kPlain) y = pair_mul(y, f32x2_pack(rate, rate));
+    if (!kPlain) y = f32x2_mul(y, f32x2_pack(rate, rate));
     float y0, y1;
     f32x2_unpack(y, y0, y1);
     return f32x2_pack(ex2_approx(y0), ex2_approx(y1));
@@ -243,8 +239,8 @@ __device__ __forceinline__ void add_weights(ThreadSum& s, const uint4 (&q)[kGrou
     }
 #pragma unroll
     for (int e = 0; e < W; e += 2) {
-      a = pair_add(a, x[e]);
-      b = pair_add(b, x[e + 1]);
+      a = f32x2_add(a, x[e]);
+      b = f32x2_add(b, x[e + 1]);
     }
   }
   float a0, a1, b0, b1;
@@ -276,14 +272,16 @@ __device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m
   if (plain_exponent(r, top)) add_weights<T, kMarks, true>(s, q, loose, r, bits);
   else add_weights<T, kMarks, false>(s, q, loose, r, bits);
 }
-// A window's pieces, a group as soon as it has arrived; its first group is number g0 of the row.
-template <class T, bool kMarks, int g, class Bits>
-__device__ __forceinline__ void add_groups(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, Bits bits) {
-  copies_done<kGroups - 1 - g>();
+// A window's pieces, a group as soon as it has arrived; after(g) may start another group's copies over group g's
+// (kRefill).
+template <class T, bool kMarks, bool kRefill, int g, class Bits, class After>
+__device__ __forceinline__ void add_groups(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, Bits bits, After after) {
+  copies_done<kRefill ? kGroups - 1 : kGroups - 1 - g>();
   if (g == 0 || m > g * kGroup)
     add_group<T, kMarks>(s, mine + g * kGroup * kRowThreads, m - g * kGroup, g == 0 ? loose : -INFINITY, r,
                          [&](int i) { return bits(i < 0 ? i : i + g * kGroup); });
-  if constexpr (g + 1 < kGroups) add_groups<T, kMarks, g + 1>(s, mine, m, loose, r, bits);
+  after(g);
+  if constexpr (g + 1 < kGroups) add_groups<T, kMarks, kRefill, g + 1>(s, mine, m, loose, r, bits, after);
 }
 
 // The row's maximum and sums from those of all warps of the cluster, the same in every thread (a warp's lanes each
@@ -303,14 +301,23 @@ __device__ __forceinline__ RowSum exchange(ThreadSum s, float4* all, int C, int 
   cluster_wait();
   RowSum r{-INFINITY, 0.f, 0.f};
   const int n = C * kRowWarps;
-  static_assert(kMaxCluster * kRowWarps <= 64, "two entries a lane");
-  const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-  const float4 t0 = lane < n ? all[lane] : none, t1 = lane + 32 < n ? all[lane + 32] : none;
-  r.M = warp_nan_max(nan_max(t0.x, t1.x));
+  constexpr int L = kMaxCluster * kRowWarps / 32;  // entries a lane
+  float4 t[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    t[i] = lane + 32 * i < n ? all[lane + 32 * i] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    r.M = nan_max(r.M, t[i].x);
+  }
+  r.M = warp_nan_max(r.M);
   if (r.M == -INFINITY) return r;
-  const float f0 = t0.x == -INFINITY ? 0.f : rescale(rate, t0.x, r.M), f1 = t1.x == -INFINITY ? 0.f : rescale(rate, t1.x, r.M);
-  r.z = warp_sum(__fmaf_rn(t0.y, f0, t1.y * f1));
-  if (kMarks) r.listed = warp_sum(__fmaf_rn(t0.z, f0, t1.z * f1));
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const float g = t[i].x == -INFINITY ? 0.f : rescale(rate, t[i].x, r.M);
+    r.z = __fmaf_rn(t[i].y, g, r.z);
+    if (kMarks) r.listed = __fmaf_rn(t[i].z, g, r.listed);
+  }
+  r.z = warp_sum(r.z);
+  if (kMarks) r.listed = warp_sum(r.listed);
   return r;
 }
 
@@ -330,16 +337,16 @@ __device__ __forceinline__ void scaled_piece(const uint4& q, const Weigher<kPlai
   split_piece<T>(q, x);
   float y[E];
 #pragma unroll
-  for (int e = 0; e < W; ++e) f32x2_unpack(pair_mul(w.both(x[e]), f32x2_pack(by, by)), y[2 * e], y[2 * e + 1]);
+  for (int e = 0; e < W; ++e) f32x2_unpack(f32x2_mul(w.both(x[e]), f32x2_pack(by, by)), y[2 * e], y[2 * e + 1]);
   store_piece<To, E>(out, y, wide);
 }
-// out[v] = weight of entry v times `by`, for this thread's pieces and its loose element.
-template <class T, class To, bool kPlain>
+// out[v] = weight of entry v times `by`, for this thread's pieces and its loose element; after(g) as above.
+template <class T, class To, bool kPlain, class After>
 __device__ __forceinline__ void write_weights(const RowPart<T>& part, uint4* held, int own, int windows, const Weigher<kPlain>& w, float by,
-                                              To* out, bool wide, int loose_at, float loose) {
+                                              To* out, bool wide, int loose_at, float loose, After after) {
   constexpr int E = 16 / sizeof(T);
-  const uint4* mine = held + threadIdx.x;
-  const size_t step = (size_t)E << part.shift;
+  static_assert(kGroup % 2 == 0, "pieces two at a time");
+  const size_t step = (size_t)(E * kRowThreads) << part.shift;
   for (int c = 0; c < windows; ++c) {
     const int m = min(own - c * kPieces, kPieces);
     if (windows > 1) {
@@ -347,14 +354,23 @@ __device__ __forceinline__ void write_weights(const RowPart<T>& part, uint4* hel
       copies_done<0>();
     }
     To* to = out + part.a0 + (size_t)part.piece(c * kPieces) * E;
-    int i = 0;
+    const uint4* mine = held + threadIdx.x;
 #pragma unroll 1
-    for (; i + 2 <= m; i += 2) {
-      const uint4 q0 = mine[i * kRowThreads], q1 = mine[(i + 1) * kRowThreads];
-      scaled_piece<T>(q0, w, by, to + i * step, wide);
-      scaled_piece<T>(q1, w, by, to + (i + 1) * step, wide);
+    for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+      for (int i = 0; i < kGroup; i += 2) {
+        if (g * kGroup + i + 1 < m) {
+          const uint4 q0 = mine[i * kRowThreads], q1 = mine[(i + 1) * kRowThreads];
+          scaled_piece<T>(q0, w, by, to + i * step, wide);
+          scaled_piece<T>(q1, w, by, to + (i + 1) * step, wide);
+        } else if (g * kGroup + i < m) {
+          scaled_piece<T>(mine[i * kRowThreads], w, by, to + i * step, wide);
+        }
+      }
+      after(g);
+      to += kGroup * step;
+      mine += kGroup * kRowThreads;
     }
-    if (i < m) scaled_piece<T>(mine[i * kRowThreads], w, by, to + i * step, wide);
   }
   if (loose_at >= 0) store_elem(out + loose_at, w(loose) * by);
 }
@@ -380,7 +396,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
   __shared__ float4 all[kMaxCluster * kRowWarps];
   __shared__ uint32_t first[kMaxCluster * kRowWarps];
   const int rank = (int)cluster_rank(), C = p.C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  cluster_arrive();  // the others' shared memory is theirs once they run: waited for before the exchange
+  cluster_arrive_relaxed();  // the others' shared memory is theirs once they run: waited for before the exchange
   const size_t r = blockIdx.x / C;
   const RowPart<T> part(static_cast<const T*>(p.logits) + r * p.V, p.V, C, rank);
   const int own = part.own();
@@ -401,7 +417,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
   for (int c = 0; c < windows; ++c) {
     const int m = min(own - c * kPieces, kPieces);
     if (c > 0) part.fetch(held, c * kPieces, m);
-    add_groups<T, false, 0>(s, held + threadIdx.x, m, c == 0 ? loose : -INFINITY, rate, unmarked);
+    add_groups<T, false, false, 0>(s, held + threadIdx.x, m, c == 0 ? loose : -INFINITY, rate, unmarked, [](int) {});
   }
   cluster_wait();
   const RowSum sum = exchange<false>(s, all, C, rank, rate);
@@ -442,15 +458,15 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
     write_one(part, own, warp_min_i(top), out, wide, loose_at);
   } else if (plain_exponent(rate, sum.M)) {
     const Weigher<true> w(rate, sum.M);
-    write_weights(part, held, own, windows, w, __fdiv_rn(w.scale, sum.z), out, wide, loose_at, loose);
+    write_weights(part, held, own, windows, w, __fdiv_rn(w.scale, sum.z), out, wide, loose_at, loose, [](int) {});
   } else {
-    write_weights(part, held, own, windows, Weigher<false>(rate, sum.M), __fdiv_rn(1.f, sum.z), out, wide, loose_at, loose);
+    write_weights(part, held, own, windows, Weigher<false>(rate, sum.M), __fdiv_rn(1.f, sum.z), out, wide, loose_at, loose, [](int) {});
   }
 }
 
 // ---------------------------------------------------------------------------
 struct DistillParams {
-  int V, K, C, held, marks;  // bytes of the held pieces and of the map of marked entries
+  int N, V, K, C, windows, held, marks;  // held, marks: bytes of the held pieces and of the map of marked entries
   const void* logits;
   const int32_t* ids;
   const float* teacher;
@@ -468,23 +484,41 @@ __device__ __forceinline__ double warp_add_d(double v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-// a b as a float and what its rounding left
+// A value as a float and what its rounding left.
 struct Split {
   float hi, lo;
 };
+__device__ __forceinline__ Split two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
 __device__ __forceinline__ Split product(float a, float b_hi, float b_lo) {
   const float p = __fmul_rn(a, b_hi);
   return {p, __fmaf_rn(a, b_lo, __fmaf_rn(a, b_hi, -p))};
 }
-// 2^(a - b) to float32's precision whatever the size of a and b: the difference with what rounding cut off, the power
-// of its fraction
-__device__ __forceinline__ float exp2_difference(Split a, Split b) {
-  const float d = __fsub_rn(a.hi, b.hi), v = __fsub_rn(d, a.hi);
-  const float cut = __fsub_rn(__fsub_rn(a.hi, __fsub_rn(d, v)), __fadd_rn(b.hi, v));
-  const float n = fmaxf(rintf(d), -160.f);
-  return ldexpf(exp2f(__fadd_rn(__fsub_rn(d, n), __fadd_rn(cut, __fsub_rn(a.lo, b.lo)))), (int)n);
+// 2^(a - b) within 2^-27 of it, whatever the size of a and b: float64 would do it on 1/64 of the lanes. With
+// a - b = n + f and u = f ln 2, |u| < 0.35, the exponential series of u: its first three terms with what their roundings
+// leave, the rest (to u^9 / 9!, below 2^-37) in float32.
+__device__ __forceinline__ Split exp2_difference(Split a, Split b) {
+  const Split d = two_sum(a.hi, -b.hi);
+  if (d.hi < -150.f) return {0.f, 0.f};
+  const float n = rintf(d.hi);
+  const Split f = two_sum(__fsub_rn(d.hi, n), __fadd_rn(d.lo, __fsub_rn(a.lo, b.lo)));  // (the difference is exact)
+  const float ln2_hi = 0.693147182f, ln2_lo = -1.90465421e-9f;
+  const float u = __fmul_rn(f.hi, ln2_hi), u_lo = __fmaf_rn(f.lo, ln2_hi, __fmaf_rn(f.hi, ln2_lo, __fmaf_rn(f.hi, ln2_hi, -u)));
+  const float s = __fmul_rn(u, u), s_lo = __fmaf_rn(2.f * u, u_lo, __fmaf_rn(u, u, -s));
+  float q = 1.f / 362880.f;
+  q = __fmaf_rn(q, u, 1.f / 40320.f);
+  q = __fmaf_rn(q, u, 1.f / 5040.f);
+  q = __fmaf_rn(q, u, 1.f / 720.f);
+  q = __fmaf_rn(q, u, 1.f / 120.f);
+  q = __fmaf_rn(q, u, 1.f / 24.f);
+  q = __fmaf_rn(q, u, 1.f / 6.f);
+  const Split w = two_sum(0.5f * s, __fmul_rn(__fmul_rn(s, u), q));
+  const Split v = two_sum(1.f, u), t = two_sum(v.hi, w.hi);
+  const float lo = __fadd_rn(__fadd_rn(t.lo, v.lo), __fadd_rn(w.lo, __fadd_rn(u_lo, 0.5f * s_lo)));
+  return {ldexpf(__fadd_rn(t.hi, lo), (int)n), ldexpf(__fsub_rn(lo, __fsub_rn(__fadd_rn(t.hi, lo), t.hi)), (int)n)};
 }
-
 // ln v, its exponent's part in float64: within 2^-24 whatever the size
 __device__ __forceinline__ double ln_of(double v) {
   const float f = (float)v;
@@ -494,12 +528,22 @@ __device__ __forceinline__ double ln_of(double v) {
   return (double)e * 0.69314718055994530942 + (double)__fadd_rn(logf(m), (float)(v - (double)f) * __fdiv_rn(1.f, f));
 }
 
-template <class T, bool kRest>
+// What the cluster's CTA 0 knows of a row's listed entries, in every CTA.
+struct __align__(16) Teacher {
+  float share, left, total, unused;  // the sum of their shares, what it leaves of 1, the sum of both
+  double sums[4];                    // over the entries: e, e ln e, e x
+};
+
+// A cluster takes rows cluster, cluster + clusters, .. one after the other: a row's pieces are overwritten by the
+// next row's as soon as they have been used for the last time, so that the next row arrives while this one's
+// gradient leaves, and the next row's listed entries are loaded meanwhile too.
+template <class T, bool kRest, bool kGrad>
 __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p) {
   extern __shared__ __align__(16) uint4 held[];
-  __shared__ float4 all[kMaxCluster * kRowWarps];
+  // two sets each: a CTA may write the next row's while another still reads this one's
+  __shared__ float4 all[2][kMaxCluster * kRowWarps];
+  __shared__ Teacher teachers[2];
   __shared__ double sums[kRowWarps][3];
-  __shared__ float4 s_teacher;  // from CTA 0 of the cluster: share, what it leaves of 1, their sum
   __shared__ float maxima[kRowWarps];
   __shared__ uint32_t loose_marks;
   __shared__ int twice;
@@ -510,168 +554,231 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
   int* s_id = reinterpret_cast<int*>(s_x + p.K);
   uint32_t* s_marks = reinterpret_cast<uint32_t*>(s_id + p.K);
   const int rank = (int)cluster_rank(), C = p.C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  cluster_arrive();
-  const size_t r = blockIdx.x / C;
-  const T* row = static_cast<const T*>(p.logits) + r * p.V;
-  const RowPart<T> part(row, p.V, C, rank);
-  const int own = part.own();
-  part.fetch(held, 0, min(own, kPieces));
+  cluster_arrive_relaxed();
+  const int clusters = gridDim.x / C;
   const Rate rate{1.f, p.k_hi};
-  const int loose_at = part.own_loose(p.V);
-  const float loose = loose_at >= 0 ? row_elem(row + loose_at) : -INFINITY;
+  const T* logits = static_cast<const T*>(p.logits);
+  const auto part_of = [&](int r) { return RowPart<T>(logits + (size_t)r * p.V, p.V, C, rank); };
+  // this thread's first listed entry of row r
+  struct Entry {
+    int id;
+    float t;
+  };
+  const auto entry = [&](int r, int j) {
+    Entry e{-1, -INFINITY};
+    if (r < p.N && j < p.K) {
+      asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(e.id) : "l"(p.ids + (size_t)r * p.K + j));
+      asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(e.t) : "l"(p.teacher + (size_t)r * p.K + j));
+    }
+    return e;
+  };
+  const auto student = [&](int r, int id) {
+    float x = -INFINITY;
+    if (id >= 0 && id < p.V) x = row_elem(logits + (size_t)r * p.V + id);
+    return x;
+  };
 
-  // the listed entries, in every CTA; those of this CTA's pieces are marked
+  int r = blockIdx.x / C;
+  RowPart<T> part = part_of(r);
+  int own = part.own();
+  if (p.windows == 1) part.fetch(held, 0, own);
+  Entry next = entry(r, tid);
   for (int i = tid; i < p.marks / 4; i += kRowThreads) s_marks[i] = 0;
   if (tid == 0) {
     loose_marks = 0;
     twice = 0;
   }
+  float next_x = student(r, next.id);
+  cluster_wait();
   __syncthreads();
-  float t_max = -INFINITY;
-  for (int j = tid; j < p.K; j += kRowThreads) {
-    int id = __ldg(p.ids + r * p.K + j);
-    float t = __ldg(p.teacher + r * p.K + j);
-    if (id >= p.V) set_status(p.status, DSPARK_ERR_RANGE);
-    if (id < 0 || id >= p.V) {
-      id = -1;
-      t = -INFINITY;
-    }
-    s_id[j] = id;
-    s_t[j] = t;
-    s_x[j] = id >= 0 ? row_elem(row + id) : -INFINITY;
-    t_max = nan_max(t_max, t);
-    int local, at;
-    if (id >= 0 && part.owner(id, local, at) == rank) {
-      uint32_t* word = local < 0 ? &loose_marks : s_marks + (local >> 2);
-      const uint32_t bit = local < 0 ? 1u << (-1 - local) : 1u << ((local & 3) * 8 + at);
-      if (atomicOr(word, bit) & bit) twice = 1;
-    }
-  }
-  t_max = warp_nan_max(t_max);
-  if (lane == 0) maxima[warp] = t_max;
-  __syncthreads();
-  t_max = warp_nan_max(maxima[lane % kRowWarps]);
-  const float lse = kRest ? __ldg(p.teacher_lse + r) : t_max;
-  const bool bad_teacher = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < INFINITY));
-  const bool listless = t_max == -INFINITY || bad_teacher;
-  // an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum
-  const Split ref = kRest ? product(lse, 1.44269502e+00f, 1.92596299e-08f) : product(lse, p.k_hi, p.k_lo);
-  for (int j = tid; j < p.K; j += kRowThreads) {
-    const float t = s_t[j];
-    s_e[j] = t == -INFINITY || listless ? 0.f : exp2_difference(product(t, p.k_hi, p.k_lo), ref);
-  }
-  // CTA 0, for the loss: sums over the listed entries of e, e ln e and e x, in float64, since what they leave of 1, and
-  // differences of logarithms, may be small
-  if (rank == 0 && warp * 32 < p.K) {
-    double a = 0.0, b = 0.0, c = 0.0;
+
+  for (int turn = 0; r < p.N; turn ^= 1) {
+    const int loose_at = part.own_loose(p.V);
+    const float loose = loose_at >= 0 ? row_elem(part.row + loose_at) : -INFINITY;
+
+    // the listed entries, in every CTA; those of this CTA's pieces are marked
+    float t_max = -INFINITY;
     for (int j = tid; j < p.K; j += kRowThreads) {
-      const float t = s_t[j];
-      if (t == -INFINITY || listless) continue;
-      const double y = kRest ? (double)t * p.per_tau - (double)lse : ((double)t - (double)lse) * p.per_tau, e = exp(y);
-      if (e > 0.0) {
-        a += e;
-        b += e * y;
-        c += e * (double)s_x[j];
+      Entry e = next;
+      float x = next_x;
+      if (j != tid) {
+        e = entry(r, j);
+        x = student(r, e.id);
+      }
+      if (e.id >= p.V) set_status(p.status, DSPARK_ERR_RANGE);
+      if (e.id < 0 || e.id >= p.V) e = Entry{-1, -INFINITY};
+      s_id[j] = e.id;
+      s_t[j] = e.t;
+      s_x[j] = x;
+      t_max = nan_max(t_max, e.t);
+      int local, at;
+      if (e.id >= 0 && part.owner(e.id, local, at) == rank) {
+        uint32_t* word = local < 0 ? &loose_marks : s_marks + (local >> 2);
+        const uint32_t bit = local < 0 ? 1u << (-1 - local) : 1u << ((local & 3) * 8 + at);
+        if (atomicOr(word, bit) & bit) twice = 1;
       }
     }
-    a = warp_add_d(a);
-    b = warp_add_d(b);
-    c = warp_add_d(c);
-    if (lane == 0) sums[warp][0] = a, sums[warp][1] = b, sums[warp][2] = c;
-  }
-  if (kRest && rank == 0) __syncthreads();
-
-  ThreadSum s;
-  const int windows = max(1, (part.steps() + kPieces - 1) / kPieces);
-  for (int c = 0; c < windows; ++c) {
-    const int m = min(own - c * kPieces, kPieces);
-    if (c > 0) part.fetch(held, c * kPieces, m);
-    add_groups<T, kRest, 0>(s, held + tid, m, c == 0 ? loose : -INFINITY, rate, [&](int i) -> uint32_t {
-      if (i < 0) return loose_marks >> tid & 1u;
-      const int local = (c * kPieces + i) * kRowThreads + tid;
-      return local < p.marks ? s_marks[local >> 2] >> ((local & 3) * 8) & 255u : 0u;
-    });
-  }
-  cluster_wait();
-  const auto sum_of = [&](int i) {
-    double v = 0.0;
-    for (int w = 0; w < min((p.K + 31) / 32, kRowWarps); ++w) v += sums[w][i];
-    return v;
-  };
-  if (kRest && rank == 0 && warp == 0) {
-    const double share = sum_of(0), left = fmax(0.0, 1.0 - share);
-    if (lane < C) store_peer(peer_address(&s_teacher, lane), make_float4((float)share, (float)left, (float)(share + left), 0.f));
-  }
-  const RowSum sum = exchange<kRest>(s, all, C, rank, rate);
-  const bool bad = !(fabsf(sum.M) < INFINITY) || bad_teacher;
-  const float z = sum.z + sum.listed;
-  const bool some = kRest && s_teacher.y > 0.f && sum.z > 0.f;  // a rest without mass on either side counts for nothing
-
-  if (p.grad) {
-    // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v)
-    T* grad = static_cast<T*>(p.grad) + r * p.V;
-    const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
-    const float scale = __fmul_rn(p.weight ? __ldg(p.weight + r) : 1.f, (float)p.per_tau);
-    const float per_z = __fdiv_rn(kRest ? (some ? s_teacher.z : s_teacher.x) : listless ? 0.f : 1.f, z);
-    const float rest_f = scale * (per_z - (some ? __fdiv_rn(s_teacher.y, sum.z) : 0.f));
-    const bool plain = plain_exponent(rate, sum.M);
-    if (bad) {
-      write_one(part, own, -1, grad, wide, loose_at);
-    } else if (plain) {
-      const Weigher<true> w(rate, sum.M);
-      write_weights(part, held, own, windows, w, rest_f * w.scale, grad, wide, loose_at, loose);
-    } else {
-      write_weights(part, held, own, windows, Weigher<false>(rate, sum.M), rest_f, grad, wide, loose_at, loose);
-    }
-    // the listed entries of this CTA over what was just written
+    t_max = warp_nan_max(t_max);
+    if (lane == 0) maxima[warp] = t_max;
     __syncthreads();
-    float norm = 1.f;
-    if (!kRest) {
-      norm = 0.f;
-      for (int j = lane; j < p.K; j += 32) norm += s_e[j];
-      norm = warp_sum(norm);
-      norm = norm > 0.f ? __fdiv_rn(1.f, norm) : 0.f;
+    t_max = warp_nan_max(maxima[lane % kRowWarps]);
+    const float lse = kRest ? __ldg(p.teacher_lse + r) : t_max;
+    const bool bad_teacher = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < INFINITY));
+    const bool listless = t_max == -INFINITY || bad_teacher;
+    // an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum. CTA 0 sums what the
+    // loss needs in float64, since what the shares leave of 1, and differences of logarithms, may be small
+    const Split ref = kRest ? product(lse, 1.44269502e+00f, 1.92596299e-08f) : product(lse, p.k_hi, p.k_lo);
+    if (warp * 32 < p.K) {
+      double a = 0.0, b = 0.0, c = 0.0;
+      for (int j = tid; j < p.K; j += kRowThreads) {
+        const float t = s_t[j];
+        Split e{0.f, 0.f};
+        if (t != -INFINITY && !listless) e = exp2_difference(product(t, p.k_hi, p.k_lo), ref);
+        s_e[j] = e.hi;
+        if (rank == 0 && e.hi > 0.f) {
+          const double d = (double)e.hi + (double)e.lo;
+          a += d;
+          b += d * (kRest ? (double)t * p.per_tau - (double)lse : ((double)t - (double)lse) * p.per_tau);
+          c += d * (double)s_x[j];
+        }
+      }
+      if (rank == 0) {
+        a = warp_add_d(a);
+        b = warp_add_d(b);
+        c = warp_add_d(c);
+        if (lane == 0) sums[warp][0] = a, sums[warp][1] = b, sums[warp][2] = c;
+      }
     }
-    for (int j = tid; j < p.K && !bad; j += kRowThreads) {
+
+    const int r_next = r + clusters;
+    const RowPart<T> follow = part_of(min(r_next, p.N - 1));
+    const int own_next = r_next < p.N && p.windows == 1 ? follow.own() : 0;
+    const auto refill = [&](int g) { follow.fetch_group(held, 0, own_next, g); };
+    ThreadSum s;
+    const auto bits = [&](int i0, int i) -> uint32_t {
+      if (i < 0) return loose_marks >> tid & 1u;
+      const int local = (i0 + i) * kRowThreads + tid;
+      return local < p.marks ? s_marks[local >> 2] >> ((local & 3) * 8) & 255u : 0u;
+    };
+    if (p.windows == 1) {
+      const auto mark = [&](int i) { return bits(0, i); };
+      if constexpr (kGrad) add_groups<T, kRest, false, 0>(s, held + tid, own, loose, rate, mark, [](int) {});
+      else add_groups<T, kRest, true, 0>(s, held + tid, own, loose, rate, mark, refill);
+    } else {
+      for (int c = 0; c < p.windows; ++c) {
+        const int m = min(own - c * kPieces, kPieces);
+        part.fetch(held, c * kPieces, m);
+        add_groups<T, kRest, false, 0>(s, held + tid, m, c == 0 ? loose : -INFINITY, rate, [&](int i) { return bits(c * kPieces, i); }, [](int) {});
+      }
+    }
+    Teacher& teacher = teachers[turn];
+    if (rank == 0) {
+      __syncthreads();
+      if (warp == 0) {
+        double v = 0.0;  // lanes 0, 1, 2 take a sum each
+        for (int w = 0; w < min((p.K + 31) / 32, kRowWarps); ++w) v += sums[w][lane % 3];
+        const double share = __shfl_sync(0xffffffffu, v, 0), left = kRest ? fmax(0.0, 1.0 - share) : 0.0;
+        for (int c = 0; c < C; ++c) {
+          if (lane < 3) store_peer(peer_address(&teacher.sums[lane], c), (unsigned long long)__double_as_longlong(v));
+          if (lane == 3) store_peer(peer_address(&teacher, c), make_float4((float)share, (float)left, (float)(share + left), 0.f));
+        }
+      }
+    }
+    const RowSum sum = exchange<kRest>(s, all[turn], C, rank, rate);
+    next = entry(r_next, tid);
+    const bool bad = !(fabsf(sum.M) < INFINITY) || bad_teacher;
+    const float z = sum.z + sum.listed;
+    const bool some = kRest && teacher.left > 0.f && sum.z > 0.f;  // a rest without mass on either side counts for nothing
+
+    if constexpr (kGrad) {
+      // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v)
+      T* grad = static_cast<T*>(p.grad) + (size_t)r * p.V;
+      const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
+      const float scale = __fmul_rn(p.weight ? __ldg(p.weight + r) : 1.f, (float)p.per_tau);
+      const float per_z = __fdiv_rn(kRest ? (some ? teacher.total : teacher.share) : listless ? 0.f : 1.f, z);
+      const float rest_f = scale * (per_z - (some ? __fdiv_rn(teacher.left, sum.z) : 0.f));
+      const bool plain = plain_exponent(rate, sum.M);
+      const auto after = [&](int g) {
+        if (p.windows == 1) refill(g);
+      };
+      if (bad) {
+        write_one(part, own, -1, grad, wide, loose_at);
+        for (int g = 0; g < kGroups; ++g) after(g);
+      } else if (plain) {
+        const Weigher<true> w(rate, sum.M);
+        write_weights(part, held, own, p.windows, w, rest_f * w.scale, grad, wide, loose_at, loose, after);
+      } else {
+        write_weights(part, held, own, p.windows, Weigher<false>(rate, sum.M), rest_f, grad, wide, loose_at, loose, after);
+      }
+      next_x = student(r_next, next.id);
+      // the listed entries of this CTA over what was just written
+      __syncthreads();
+      float norm = 1.f;
+      if (!kRest && warp * 32 < p.K) {
+        norm = 0.f;
+        for (int j = lane; j < p.K; j += 32) norm += s_e[j];
+        norm = warp_sum(norm);
+        norm = norm > 0.f ? __fdiv_rn(1.f, norm) : 0.f;
+      }
+      for (int j = tid; j < p.K && !bad; j += kRowThreads) {
+        const int id = s_id[j];
+        int local, at;
+        if (id < 0 || part.owner(id, local, at) != rank) continue;
+        float e = s_e[j];
+        if (twice) {  // an id that comes more than once: every occurrence writes the sum of all
+          e = 0.f;
+          for (int i = 0; i < p.K; ++i)
+            if (s_id[i] == id) e += s_e[i];
+        }
+        const float x = s_x[j];
+        float y;
+        if (plain) {
+          const Weigher<true> w(rate, sum.M);
+          y = w(x) * w.scale;
+        } else {
+          y = Weigher<false>(rate, sum.M)(x);
+        }
+        store_elem(grad + id, __fmaf_rn(-scale * norm, e, y * (scale * per_z)));
+      }
+    } else {
+      next_x = student(r_next, next.id);
+    }
+
+    // the loss: the last CTA's (CTA 0 has had the sums to form)
+    if (rank == C - 1 && tid == kRowThreads - 32) {
+      const double share = teacher.sums[0], step = (double)p.k_hi * 0.69314718055994530942;  // 1 / tau as the weights have it
+      const double a = teacher.sums[1] - step * (teacher.sums[2] - (double)sum.M * share), ln_z = ln_of((double)z);
+      double loss = 0.0;
+      if (kRest) {
+        const double left = fmax(0.0, 1.0 - share);
+        loss = a + share * ln_z;
+        if (some) loss += left * (ln_of(left) - ln_of((double)sum.z) + ln_z);
+      } else if (share > 0.0) {
+        double inv = (double)__fdiv_rn(1.f, (float)share);
+        inv *= 2.0 - share * inv;
+        loss = a * inv + ln_z - ln_of(share);
+      }
+      p.loss[r] = bad ? NAN : (float)loss;
+      if (bad) set_status(p.status, DSPARK_ERR_NONFINITE);
+    }
+
+    // the marks are taken back, the next row begins
+    __syncthreads();
+    for (int j = tid; j < p.K; j += kRowThreads) {
       const int id = s_id[j];
       int local, at;
-      if (id < 0 || part.owner(id, local, at) != rank) continue;
-      float e = s_e[j];
-      if (twice) {  // an id that comes more than once: every occurrence writes the sum of all
-        e = 0.f;
-        for (int i = 0; i < p.K; ++i)
-          if (s_id[i] == id) e += s_e[i];
-      }
-      const float x = s_x[j];
-      float y;
-      if (plain) {
-        const Weigher<true> w(rate, sum.M);
-        y = w(x) * w.scale;
-      } else {
-        y = Weigher<false>(rate, sum.M)(x);
-      }
-      store_elem(grad + id, __fmaf_rn(-scale * norm, e, y * (scale * per_z)));
+      if (id >= 0 && part.owner(id, local, at) == rank && local >= 0) s_marks[local >> 2] = 0;
     }
-  } else {
+    if (tid == 0) {
+      loose_marks = 0;
+      twice = 0;
+    }
     __syncthreads();
+    r = r_next;
+    part = follow;
+    own = part.own();
   }
-
-  if (rank == 0 && tid == 0) {
-    const double share = sum_of(0), step = (double)p.k_hi * 0.69314718055994530942;  // 1 / tau as the weights have it
-    const double a = sum_of(1) - step * (sum_of(2) - (double)sum.M * share), ln_z = ln_of((double)z);
-    double loss = 0.0;
-    if (kRest) {
-      const double left = fmax(0.0, 1.0 - share);
-      loss = a + share * ln_z;
-      if (some) loss += left * (ln_of(left) - ln_of((double)sum.z) + ln_z);
-    } else if (share > 0.0) {
-      double inv = (double)__fdiv_rn(1.f, (float)share);
-      inv *= 2.0 - share * inv;
-      loss = a * inv + ln_z - ln_of(share);
-    }
-    p.loss[r] = bad ? NAN : (float)loss;
-    if (bad) set_status(p.status, DSPARK_ERR_NONFINITE);
-  }
+  copies_done<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -703,12 +810,23 @@ static cudaError_t launch_probs(const ProbsParams& p, int N, int held, cudaStrea
 // the pieces, 16 bytes a listed entry, and a byte for each piece of a row of 2^20 float32
 constexpr int kDistillSmem = kPieces * kRowThreads * 16 + kMaxTop * 16 + (1 << 20) / 4 / kMaxCluster + kRowThreads;
 
-template <class T, bool kRest>
-static cudaError_t launch_distill(const DistillParams& p, int N, cudaStream_t s) {
+// Rows are taken in equal turns by as many clusters as the GPU holds at once (more would begin when those end).
+template <class T, bool kRest, bool kGrad>
+static cudaError_t launch_distill(const DistillParams& p, cudaStream_t s) {
   static std::atomic<unsigned long long> attr{0};
-  const cudaError_t e = set_smem_limit_once((const void*)distill_kernel<T, kRest>, kDistillSmem, attr);
+  const cudaError_t e = set_smem_limit_once((const void*)distill_kernel<T, kRest, kGrad>, kDistillSmem, attr);
   if (e != cudaSuccess) return e;
-  return launch_clusters(distill_kernel<T, kRest>, p, (unsigned)N * p.C, p.C, kRowThreads, (size_t)p.held + (size_t)p.K * 16 + p.marks, s);
+  const size_t smem = (size_t)p.held + (size_t)p.K * 16 + p.marks;
+  int resident = 0;
+  const cudaError_t f = resident_clusters((const void*)distill_kernel<T, kRest, kGrad>, p.C, kRowThreads, smem, resident);
+  if (f != cudaSuccess) return f;
+  const int turns = ceil_div(p.N, resident);
+  return launch_clusters(distill_kernel<T, kRest, kGrad>, p, (unsigned)(ceil_div(p.N, turns) * p.C), p.C, kRowThreads, smem, s);
+}
+template <class T>
+static cudaError_t launch_distill(const DistillParams& p, cudaStream_t s) {
+  if (p.teacher_lse) return p.grad ? launch_distill<T, true, true>(p, s) : launch_distill<T, true, false>(p, s);
+  return p.grad ? launch_distill<T, false, true>(p, s) : launch_distill<T, false, false>(p, s);
 }
 
 static bool row_args(int32_t N, int32_t V, int32_t dtype) {
@@ -764,13 +882,11 @@ extern "C" dspark_status dspark_distill(int32_t N, int32_t V, int32_t K, int32_t
   // one byte a piece of this CTA, whole steps of the block
   const int marks = ceil_div((long long)V * elem / 16, (long long)C * kRowThreads) * kRowThreads;
   const double k = 1.44269504088896340736 / (double)temperature;
-  const DistillParams p{V, K, C, held, marks, logits, ids, teacher, teacher_lse, weight, 1.0 / (double)temperature, (float)k,
-                        (float)(k - (double)(float)k), loss, grad,
-                        static_cast<uint32_t*>(workspace)};
+  const int windows = std::max(1, ceil_div(ceil_div((long long)V * elem / 16, (long long)C * kRowThreads), kPieces));
+  const DistillParams p{N, V, K, C, windows, held, marks, logits, ids, teacher, teacher_lse, weight, 1.0 / (double)temperature,
+                        (float)k, (float)(k - (double)(float)k), loss, grad, static_cast<uint32_t*>(workspace)};
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e;
-  if (dtype == DSPARK_BF16) e = teacher_lse ? launch_distill<__nv_bfloat16, true>(p, N, s) : launch_distill<__nv_bfloat16, false>(p, N, s);
-  else e = teacher_lse ? launch_distill<float, true>(p, N, s) : launch_distill<float, false>(p, N, s);
+  const cudaError_t e = dtype == DSPARK_BF16 ? launch_distill<__nv_bfloat16>(p, s) : launch_distill<float>(p, s);
   note_launches(1);
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }
