@@ -369,7 +369,7 @@ dspark_status dspark_sts_apply(int32_t R, int32_t gamma, const float* conf, cons
  * cached_len[r] tokens in ceil(cached_len / page_size) pages.
  *   cached_len, new_len [R] int32   >= 0 (a negative one counts as 0, DSPARK_ERR_RANGE)
  *   free_pages  [n_free] int32      ids of free pages, taken in order: request by request, each
- *                                   request's missing pages by position
+ *                                   request's missing pages by position; a negative id ends the list
  *   block_table [R, max_pages] int32 in/out  the new pages' entries are written (-1 where the
  *                                   list has run out), all others left as they are
  *   q_start     [R+1] int32 out     first new token of each request, and their number T

@@ -423,34 +423,52 @@ struct CopyParams {
   void* v;
   uint32_t* status;
 };
+constexpr int kCopyAhead = 8;  // units of a page that a thread has in flight
+// A CTA takes a piece of one page of one layer's keys or values at a time, and has the page numbers of the next one
+// ready when it is done.
 template <class Tv>
 __global__ void __launch_bounds__(256) page_copy_kernel(CopyParams p) {
   const long long page_units = (long long)p.page * p.per_token;
-  const long long items = (long long)p.n * p.layers * 2 * p.chunks;
+  const int per_entry = 2 * p.layers * p.chunks;
+  const long long items = (long long)p.n * per_entry;
+  struct Item {
+    int from, to, tokens, side, piece;
+  };
+  const auto item = [&](long long it) {
+    Item x{-1, -1, p.page, 0, 0};
+    if (it < items) {
+      const int i = (int)(it / per_entry), rest = (int)(it - (long long)i * per_entry);
+      x.side = rest / p.chunks;
+      x.piece = rest - x.side * p.chunks;
+      x.from = __ldg(p.src + i);
+      x.to = __ldg(p.dst + i);
+      if (p.tokens) x.tokens = __ldg(p.tokens + i);
+    }
+    return x;
+  };
+  Item next = item(blockIdx.x);
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int piece = (int)(it % p.chunks);
-    const long long rest = it / p.chunks;
-    const int side = (int)(rest % (2 * p.layers)), i = (int)(rest / (2 * p.layers));
-    const int from = __ldg(p.src + i), to = __ldg(p.dst + i);
-    if (from < 0 || to < 0) continue;
-    if (from >= p.n_pages || to >= p.n_pages) {
+    const Item x = next;
+    next = item(it + gridDim.x);
+    if (x.from < 0 || x.to < 0) continue;
+    if (x.from >= p.n_pages || x.to >= p.n_pages) {
       if (threadIdx.x == 0) set_status(p.status, DSPARK_ERR_RANGE);
       continue;
     }
-    const int tokens = p.tokens ? min(max(__ldg(p.tokens + i), 0), p.page) : p.page;
-    const long long lo = (long long)piece * p.chunk, hi = min(lo + p.chunk, (long long)tokens * p.per_token);
-    Tv* cache = static_cast<Tv*>(side & 1 ? p.v : p.k) + (long long)(side >> 1) * p.n_pages * page_units;
-    const Tv* a = cache + from * page_units;
-    Tv* b = cache + to * page_units;
-    long long x = lo + threadIdx.x;
-    for (; x + 768 < hi; x += 1024) {
-      const Tv q0 = a[x], q1 = a[x + 256], q2 = a[x + 512], q3 = a[x + 768];
-      b[x] = q0;
-      b[x + 256] = q1;
-      b[x + 512] = q2;
-      b[x + 768] = q3;
+    const long long lo = (long long)x.piece * p.chunk;
+    const long long hi = min(lo + p.chunk, (long long)min(max(x.tokens, 0), p.page) * p.per_token);
+    Tv* cache = static_cast<Tv*>(x.side & 1 ? p.v : p.k) + (long long)(x.side >> 1) * p.n_pages * page_units;
+    const Tv* a = cache + x.from * page_units;
+    Tv* b = cache + x.to * page_units;
+    for (long long u = lo + threadIdx.x; u < hi; u += 256 * kCopyAhead) {
+      Tv q[kCopyAhead];
+#pragma unroll
+      for (int i = 0; i < kCopyAhead; ++i)
+        if (u + 256 * i < hi) q[i] = a[u + 256 * i];
+#pragma unroll
+      for (int i = 0; i < kCopyAhead; ++i)
+        if (u + 256 * i < hi) b[u + 256 * i] = q[i];
     }
-    for (; x < hi; x += 256) b[x] = a[x];
   }
 }
 
@@ -546,11 +564,12 @@ extern "C" dspark_status dspark_page_copy(int32_t n, int32_t n_layers, int32_t n
   const long long row = (long long)n_kv_heads * head_dim * elem;
   const uintptr_t at = reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache);
   const int unit = ((at | (uintptr_t)row) & 15) == 0 ? 16 : elem;  // bytes a thread copies at a time
-  CopyParams p{n, n_layers, n_pages, page_size, (int)(row / unit), 0, 16384 / unit, src, dst, tokens, k_cache, v_cache,
+  CopyParams p{n, n_layers, n_pages, page_size, (int)(row / unit), 0, 256 * kCopyAhead, src, dst, tokens, k_cache, v_cache,
                static_cast<uint32_t*>(workspace)};
   p.chunks = ceil_div((long long)page_size * p.per_token, p.chunk);
+  if (2ll * n_layers * p.chunks > 0x7fffffff) return DSPARK_ERR_INVALID_ARG;
   const long long items = (long long)n * n_layers * 2 * p.chunks;
-  const int grid = (int)std::min<long long>(items, 152 * 8);
+  const int grid = (int)std::min<long long>(items, 152 * 16);
   cudaStream_t s = (cudaStream_t)stream;
   if (unit == 16) page_copy_kernel<uint4><<<grid, 256, 0, s>>>(p);
   else if (unit == 4) page_copy_kernel<uint32_t><<<grid, 256, 0, s>>>(p);

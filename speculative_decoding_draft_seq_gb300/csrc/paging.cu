@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
     full |= have + n_new > p.max_pages;
     for (long long j = lane; j < n_new && have + j < p.max_pages; j += 32) {
       const long long at = s_pg[i] + j;
-      full |= at >= p.n_free;
-      p.table[(size_t)(r0 + i) * p.max_pages + have + j] = at < p.n_free ? __ldg(p.free_pages + at) : -1;
+      const int id = at < p.n_free ? __ldg(p.free_pages + at) : -1;  // (a list may end early: dspark_page_collect's do)
+      full |= id < 0;
+      p.table[(size_t)(r0 + i) * p.max_pages + have + j] = id;
     }
   }
   if (tid < nr) p.q_start[r0 + tid] = (int)min(s_tok[tid], (long long)p.capacity);

@@ -442,33 +442,44 @@ def truncate(logits, temperature, top_k, top_p, min_p, out, ws, stream=None):
         _check(status, "dspark_truncate")
 
 
-# The calls after the target's pass. Their tensors have to be on the device whose stream the call runs on.
+# The calls after the target's pass. Their tensors have to be on the device whose stream the call runs on. The checks are
+# kept short: such a call costs the host about as long as the GPU.
 _current_device = torch._C._cuda_getDevice
 
 
 def _here(stream):
     """(device index, stream handle) of a call."""
-    return (_current_device(), _raw_stream(None)) if stream is None else (stream.device_index, stream.cuda_stream)
+    if stream is not None:
+        return stream.device_index, stream.cuda_stream
+    device = _current_device()
+    return device, (_current_raw_stream(device) if _current_raw_stream is not None else _raw_stream(None))
 
 
-def _addr_on(t, dtype, device):
-    """Device address of a dense tensor of this type on this device; refuses what _ptr refuses, and another device."""
-    if t.dtype is dtype and t.get_device() == device and t.is_contiguous():
-        return t.data_ptr()
-    _ptr(t, dtype)
-    raise ValueError(f"tensor is on cuda:{t.get_device()}, the call runs on cuda:{device}")
+def _addrs(device, dtype, *tensors):
+    """Device addresses of dense tensors of this type on this device; refuses what _ptr refuses, and another device."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+            _ptr(t, dtype)
+            raise ValueError(f"tensor is on cuda:{t.get_device()}, the call runs on cuda:{device}")
+    return [t.data_ptr() for t in tensors]
+
+
+def _maybe(device, dtype, t):
+    return None if t is None else _addrs(device, dtype, t)[0]
 
 
 def probabilities(logits, temperature, probs, ws, stream=None):
     """probs [N, V] (float32 or bfloat16) = softmax of the rows of logits [N, V], temperature [N] float32 (<= 0: one at
     the first maximum)."""
     N, V = logits.shape
-    if temperature.shape != (N,) or probs.shape != (N, V):
+    if temperature.numel() != N or probs.shape != (N, V):
         _shapes(temperature=(temperature, (N,)), probs=(probs, (N, V)))
     dev, s = _here(stream)
-    status = lib.dspark_probabilities(N, V, _dtype_code(logits), _addr_on(logits, logits.dtype, dev),
-                                      _addr_on(temperature, _F32, dev), _dtype_code(probs),
-                                      _addr_on(probs, probs.dtype, dev), _addr_on(ws, _U8, dev), ws.numel(), s)
+    x, = _addrs(dev, logits.dtype, logits)
+    t, = _addrs(dev, _F32, temperature)
+    y, = _addrs(dev, probs.dtype, probs)
+    w, = _addrs(dev, _U8, ws)
+    status = lib.dspark_probabilities(N, V, _dtype_code(logits), x, t, _dtype_code(probs), y, w, ws.numel(), s)
     if status:
         _check(status, "dspark_probabilities")
 
@@ -479,20 +490,21 @@ def verify_probs(target_probs, q_start, draft_probs, draft_tokens, u, out_tokens
     probabilities; u [R, gamma + 1] float64. Fills out_tokens [R, gamma + 1], accepted_len [R], p_tok [R, gamma]."""
     T, V = target_probs.shape
     R, gamma = draft_tokens.shape
-    if (q_start.shape != (R + 1,) or (draft_probs is not None and draft_probs.shape != (R, gamma, V)) or
-            u.shape != (R, gamma + 1) or out_tokens.shape != (R, gamma + 1) or accepted_len.shape != (R,) or
+    if (q_start.numel() != R + 1 or (draft_probs is not None and draft_probs.shape != (R, gamma, V)) or
+            u.shape != (R, gamma + 1) or out_tokens.shape != (R, gamma + 1) or accepted_len.numel() != R or
             p_tok.shape != (R, gamma)):
         _shapes(q_start=(q_start, (R + 1,)), u=(u, (R, gamma + 1)), out_tokens=(out_tokens, (R, gamma + 1)),
                 accepted_len=(accepted_len, (R,)), p_tok=(p_tok, (R, gamma)),
                 **({} if draft_probs is None else {"draft_probs": (draft_probs, (R, gamma, V))}))
     dev, s = _here(stream)
     dt = target_probs.dtype
-    status = lib.dspark_verify_probs(R, gamma, V, T, _dtype_code(target_probs), _addr_on(target_probs, dt, dev),
-                                     _addr_on(q_start, _I32, dev),
-                                     None if draft_probs is None else _addr_on(draft_probs, dt, dev),
-                                     _addr_on(draft_tokens, _I32, dev), _addr_on(u, _F64, dev),
-                                     _addr_on(out_tokens, _I32, dev), _addr_on(accepted_len, _I32, dev),
-                                     _addr_on(p_tok, _F32, dev), _addr_on(ws, _U8, dev), ws.numel(), s)
+    p, = _addrs(dev, dt, target_probs)
+    q0, tok, out, acc = _addrs(dev, _I32, q_start, draft_tokens, out_tokens, accepted_len)
+    uu, = _addrs(dev, _F64, u)
+    pt, = _addrs(dev, _F32, p_tok)
+    w, = _addrs(dev, _U8, ws)
+    status = lib.dspark_verify_probs(R, gamma, V, T, _dtype_code(target_probs), p, q0, _maybe(dev, dt, draft_probs), tok, uu,
+                                     out, acc, pt, w, ws.numel(), s)
     if status:
         _check(status, "dspark_verify_probs")
 
@@ -514,14 +526,14 @@ def page_collect(block_table, kv_len, page_size, refs, free_pages, n_free, ws, p
     free_pages [n_pages]: the pages without, ascending, then -1; n_free [1]. All int32."""
     R, max_pages = block_table.shape
     n_pages = refs.numel()
-    if kv_len.shape != (R,) or free_pages.shape != (n_pages,) or n_free.numel() < 1:
+    if kv_len.numel() != R or free_pages.numel() != n_pages or n_free.numel() < 1:
         _shapes(kv_len=(kv_len, (R,)), free_pages=(free_pages, (n_pages,)), n_free=(n_free, (1,)))
     dev, s = _here(stream)
     n_pinned = 0 if pinned is None else pinned.numel()
-    status = lib.dspark_page_collect(R, page_size, max_pages, n_pages, n_pinned, _addr_on(block_table, _I32, dev),
-                                     _addr_on(kv_len, _I32, dev), _addr_on(pinned, _I32, dev) if n_pinned else None,
-                                     _addr_on(refs, _I32, dev), _addr_on(free_pages, _I32, dev),
-                                     _addr_on(n_free, _I32, dev), _addr_on(ws, _U8, dev), ws.numel(), s)
+    table, length, r, f, n = _addrs(dev, _I32, block_table, kv_len, refs, free_pages, n_free)
+    w, = _addrs(dev, _U8, ws)
+    status = lib.dspark_page_collect(R, page_size, max_pages, n_pages, n_pinned, table, length,
+                                     _maybe(dev, _I32, pinned), r, f, n, w, ws.numel(), s)
     if status:
         _check(status, "dspark_page_collect")
 
@@ -532,24 +544,20 @@ def page_fork(block_table, kv_len, parent, fork_len, page_size, n_pages, free_pa
     block_table [R_from, max_pages]; pages shared, those that a row writes next its own, from free_pages. Fills
     new_len, and the copies to make: src, dst, tokens [R] (-1, -1, 0: none), used [1]. All int32."""
     R_from, max_pages = block_table.shape
-    R = new_table.shape[0]
-    rows = (R,)
-    if (new_table.shape != (R, max_pages) or kv_len.shape != (R_from,) or parent.shape != rows or new_len.shape != rows or
-            src.shape != rows or dst.shape != rows or tokens.shape != rows or used.numel() < 1 or
-            (fork_len is not None and fork_len.shape != rows)):
-        _shapes(new_table=(new_table, (R, max_pages)), kv_len=(kv_len, (R_from,)), parent=(parent, rows),
-                new_len=(new_len, rows), src=(src, rows), dst=(dst, rows), tokens=(tokens, rows), used=(used, (1,)),
-                **({} if fork_len is None else {"fork_len": (fork_len, rows)}))
+    R = parent.numel()
+    if (new_table.shape != (R, max_pages) or kv_len.numel() != R_from or new_len.numel() != R or src.numel() != R or
+            dst.numel() != R or tokens.numel() != R or used.numel() < 1 or (fork_len is not None and fork_len.numel() != R)):
+        R = new_table.shape[0]
+        _shapes(parent=(parent, (R,)), new_table=(new_table, (R, max_pages)), kv_len=(kv_len, (R_from,)),
+                new_len=(new_len, (R,)), src=(src, (R,)), dst=(dst, (R,)), tokens=(tokens, (R,)), used=(used, (1,)),
+                **({} if fork_len is None else {"fork_len": (fork_len, (R,))}))
     dev, s = _here(stream)
-    n_free, n_pinned = free_pages.numel(), 0 if pinned is None else pinned.numel()
-    status = lib.dspark_page_fork(R_from, R, page_size, max_pages, n_pages, n_free, n_pinned,
-                                  _addr_on(block_table, _I32, dev), _addr_on(kv_len, _I32, dev),
-                                  _addr_on(parent, _I32, dev),
-                                  None if fork_len is None else _addr_on(fork_len, _I32, dev),
-                                  _addr_on(free_pages, _I32, dev) if n_free else None,
-                                  _addr_on(pinned, _I32, dev) if n_pinned else None, _addr_on(new_table, _I32, dev),
-                                  _addr_on(new_len, _I32, dev), _addr_on(src, _I32, dev), _addr_on(dst, _I32, dev),
-                                  _addr_on(tokens, _I32, dev), _addr_on(used, _I32, dev), _addr_on(ws, _U8, dev),
+    n_pinned = 0 if pinned is None else pinned.numel()
+    table, length, par, free, to, to_len, a, b, t, n = _addrs(dev, _I32, block_table, kv_len, parent, free_pages, new_table,
+                                                              new_len, src, dst, tokens, used)
+    w, = _addrs(dev, _U8, ws)
+    status = lib.dspark_page_fork(R_from, R, page_size, max_pages, n_pages, free_pages.numel(), n_pinned, table, length, par,
+                                  _maybe(dev, _I32, fork_len), free, _maybe(dev, _I32, pinned), to, to_len, a, b, t, n, w,
                                   ws.numel(), s)
     if status:
         _check(status, "dspark_page_fork")
@@ -561,20 +569,18 @@ def page_compact(block_table, kv_len, page_size, n_pages, new_table, src, dst, n
     pinned (may be it), and the moves src, dst [n_pages // 2] for page_copy. All int32."""
     R, max_pages = block_table.shape
     n_pinned = 0 if pinned is None else pinned.numel()
-    half = (n_pages // 2,)
-    if (new_table.shape != (R, max_pages) or kv_len.shape != (R,) or src.shape != half or dst.shape != half or
-            n_live.numel() < 1 or (n_pinned and (new_pinned is None or new_pinned.numel() != n_pinned))):
-        if n_pinned and (new_pinned is None or new_pinned.numel() != n_pinned):
-            raise ValueError("new_pinned must be as long as pinned")
-        _shapes(new_table=(new_table, (R, max_pages)), kv_len=(kv_len, (R,)), src=(src, half), dst=(dst, half),
+    half = n_pages // 2
+    if n_pinned and (new_pinned is None or new_pinned.numel() != n_pinned):
+        raise ValueError("new_pinned must be as long as pinned")
+    if (new_table.shape != (R, max_pages) or kv_len.numel() != R or src.numel() != half or dst.numel() != half or
+            n_live.numel() < 1):
+        _shapes(new_table=(new_table, (R, max_pages)), kv_len=(kv_len, (R,)), src=(src, (half,)), dst=(dst, (half,)),
                 n_live=(n_live, (1,)))
     dev, s = _here(stream)
-    status = lib.dspark_page_compact(R, page_size, max_pages, n_pages, n_pinned, _addr_on(block_table, _I32, dev),
-                                     _addr_on(kv_len, _I32, dev), _addr_on(pinned, _I32, dev) if n_pinned else None,
-                                     _addr_on(new_table, _I32, dev),
-                                     _addr_on(new_pinned, _I32, dev) if n_pinned else None,
-                                     _addr_on(src, _I32, dev), _addr_on(dst, _I32, dev), _addr_on(n_live, _I32, dev),
-                                     _addr_on(ws, _U8, dev), ws.numel(), s)
+    table, length, to, a, b, n = _addrs(dev, _I32, block_table, kv_len, new_table, src, dst, n_live)
+    w, = _addrs(dev, _U8, ws)
+    status = lib.dspark_page_compact(R, page_size, max_pages, n_pages, n_pinned, table, length, _maybe(dev, _I32, pinned), to,
+                                     _maybe(dev, _I32, new_pinned), a, b, n, w, ws.numel(), s)
     if status:
         _check(status, "dspark_page_compact")
 
@@ -582,18 +588,22 @@ def page_compact(block_table, kv_len, page_size, n_pages, new_table, src, dst, n
 def page_copy(src, dst, k_cache, v_cache, ws, tokens=None, stream=None):
     """Page dst[i] of k_cache and v_cache [.., n_pages, page_size, Hkv, D] (any leading dimensions: layers) gets the first
     tokens[i] tokens (None: all) of page src[i]; negative ids are skipped."""
-    n_pages, page, Hkv, D = k_cache.shape[-4:]
+    *_, n_pages, page, Hkv, D = shape = k_cache.shape
     n = src.numel()
-    if k_cache.shape != v_cache.shape:
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape")
-    if dst.shape != (n,) or src.shape != (n,) or (tokens is not None and tokens.shape != (n,)):
-        _shapes(src=(src, (n,)), dst=(dst, (n,)), **({} if tokens is None else {"tokens": (tokens, (n,))}))
+    if dst.numel() != n or (tokens is not None and tokens.numel() != n):
+        _shapes(dst=(dst, (n,)), **({} if tokens is None else {"tokens": (tokens, (n,))}))
     dev, s = _here(stream)
     dt = k_cache.dtype
-    status = lib.dspark_page_copy(n, k_cache.numel() // (n_pages * page * Hkv * D), n_pages, page, Hkv, D,
-                                  _dtype_code(k_cache), _addr_on(src, _I32, dev), _addr_on(dst, _I32, dev),
-                                  None if tokens is None else _addr_on(tokens, _I32, dev), _addr_on(k_cache, dt, dev),
-                                  _addr_on(v_cache, dt, dev), _addr_on(ws, _U8, dev), ws.numel(), s)
+    a, b = _addrs(dev, _I32, src, dst)
+    k, v = _addrs(dev, dt, k_cache, v_cache)
+    w, = _addrs(dev, _U8, ws)
+    layers = 1
+    for x in shape[:-4]:
+        layers *= x
+    status = lib.dspark_page_copy(n, layers, n_pages, page, Hkv, D, _dtype_code(k_cache), a, b, _maybe(dev, _I32, tokens), k,
+                                  v, w, ws.numel(), s)
     if status:
         _check(status, "dspark_page_copy")
 
@@ -603,23 +613,22 @@ def distill(logits, ids, teacher, temperature, loss, ws, grad=None, weight=None,
     entries ids [N, K] int32 (-1: none), both at `temperature`; with teacher_lse [N] float32 (the log of the sum of
     e^(teacher logit / temperature) over the whole vocabulary) the entries that are not listed count as one more. grad
     [N, V] like logits (may be logits): weight[r] (None: 1) times the loss's gradient."""
-    N, V = logits.shape
+    N, V = shape = logits.shape
     K = ids.shape[-1]
-    if (ids.shape != (N, K) or teacher.shape != (N, K) or loss.shape != (N,) or
-            (grad is not None and grad.shape != (N, V)) or (weight is not None and weight.shape != (N,)) or
-            (teacher_lse is not None and teacher_lse.shape != (N,))):
+    if (ids.shape != (N, K) or teacher.shape != (N, K) or loss.numel() != N or (grad is not None and grad.shape != shape) or
+            (weight is not None and weight.numel() != N) or (teacher_lse is not None and teacher_lse.numel() != N)):
         _shapes(ids=(ids, (N, K)), teacher=(teacher, (N, K)), loss=(loss, (N,)),
                 **({} if grad is None else {"grad": (grad, (N, V))}),
                 **({} if weight is None else {"weight": (weight, (N,))}),
                 **({} if teacher_lse is None else {"teacher_lse": (teacher_lse, (N,))}))
     dev, s = _here(stream)
     dt = logits.dtype
-    status = lib.dspark_distill(N, V, K, _dtype_code(logits), _addr_on(logits, dt, dev), _addr_on(ids, _I32, dev),
-                                _addr_on(teacher, _F32, dev),
-                                None if teacher_lse is None else _addr_on(teacher_lse, _F32, dev),
-                                None if weight is None else _addr_on(weight, _F32, dev), temperature,
-                                _addr_on(loss, _F32, dev), None if grad is None else _addr_on(grad, dt, dev),
-                                _addr_on(ws, _U8, dev), ws.numel(), s)
+    x, = _addrs(dev, dt, logits)
+    i, = _addrs(dev, _I32, ids)
+    t, out = _addrs(dev, _F32, teacher, loss)
+    w, = _addrs(dev, _U8, ws)
+    status = lib.dspark_distill(N, V, K, _dtype_code(logits), x, i, t, _maybe(dev, _F32, teacher_lse),
+                                _maybe(dev, _F32, weight), temperature, out, _maybe(dev, dt, grad), w, ws.numel(), s)
     if status:
         _check(status, "dspark_distill")
 
