@@ -290,15 +290,17 @@ struct RowSum {
   float M, z, listed;
 };
 template <bool kMarks>
-__device__ __forceinline__ RowSum exchange(ThreadSum s, float4* all, int C, int rank, const Rate& rate) {
+__device__ __forceinline__ void send(const ThreadSum& s, float4* all, int C, int rank, const Rate& rate) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float m = warp_nan_max(s.m);
   const float f = s.m == -INFINITY ? 0.f : rescale(rate, s.m, m);
   const float zw = warp_sum(s.z * f), lw = kMarks ? warp_sum(s.listed * f) : 0.f;
   if (lane < C) store_peer(peer_address(all + rank * kRowWarps + warp, lane), make_float4(m, zw, lw, 0.f));
   __syncwarp();
-  cluster_arrive();
-  cluster_wait();
+}
+template <bool kMarks>
+__device__ __forceinline__ RowSum combine(const float4* all, int C, const Rate& rate) {
+  const int lane = threadIdx.x & 31;
   RowSum r{-INFINITY, 0.f, 0.f};
   const int n = C * kRowWarps;
   constexpr int L = kMaxCluster * kRowWarps / 32;  // entries a lane
@@ -319,6 +321,13 @@ __device__ __forceinline__ RowSum exchange(ThreadSum s, float4* all, int C, int 
   r.z = warp_sum(r.z);
   if (kMarks) r.listed = warp_sum(r.listed);
   return r;
+}
+
+template <bool kMarks>
+__device__ __forceinline__ RowSum receive(const float4* all, int C, const Rate& rate) {
+  cluster_arrive();
+  cluster_wait();
+  return combine<kMarks>(all, C, rate);
 }
 
 // ---------------------------------------------------------------------------
@@ -420,7 +429,8 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
     add_groups<T, false, false, 0>(s, held + threadIdx.x, m, c == 0 ? loose : -INFINITY, rate, unmarked, [](int) {});
   }
   cluster_wait();
-  const RowSum sum = exchange<false>(s, all, C, rank, rate);
+  send<false>(s, all, C, rank, rate);
+  const RowSum sum = receive<false>(all, C, rate);
   const bool bad = !(fabsf(sum.M) < INFINITY);
   if (bad && rank == 0 && threadIdx.x == 0) set_status(p.status, DSPARK_ERR_NONFINITE);
   if (bad) {
@@ -472,18 +482,13 @@ struct DistillParams {
   const float* teacher;
   const float* teacher_lse;
   const float* weight;
-  double per_tau;      // 1 / temperature
+  float per_tau;       // 1 / temperature
   float k_hi, k_lo;    // log2(e) / temperature
   float* loss;
   void* grad;
   uint32_t* status;
 };
 
-__device__ __forceinline__ double warp_add_d(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 // A value as a float and what its rounding left.
 struct Split {
   float hi, lo;
@@ -496,16 +501,32 @@ __device__ __forceinline__ Split product(float a, float b_hi, float b_lo) {
   const float p = __fmul_rn(a, b_hi);
   return {p, __fmaf_rn(a, b_lo, __fmaf_rn(a, b_hi, -p))};
 }
+__device__ __forceinline__ Split add(Split a, Split b) {
+  const Split s = two_sum(a.hi, b.hi);
+  const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
+  return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+__device__ __forceinline__ Split times(Split a, Split b) {
+  const float p = __fmul_rn(a.hi, b.hi);
+  return {p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p)))};
+}
+__device__ __forceinline__ Split warp_add(Split v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = add(v, Split{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+constexpr float kLn2 = 0.693147182f, kLn2Lo = -1.90465421e-9f;
 // 2^(a - b) within 2^-27 of it, whatever the size of a and b: float64 would do it on 1/64 of the lanes. With
 // a - b = n + f and u = f ln 2, |u| < 0.35, the exponential series of u: its first three terms with what their roundings
 // leave, the rest (to u^9 / 9!, below 2^-37) in float32.
-__device__ __forceinline__ Split exp2_difference(Split a, Split b) {
+__device__ __forceinline__ Split exp2_difference(Split a, Split b, Split& difference) {
   const Split d = two_sum(a.hi, -b.hi);
+  difference = {d.hi, __fadd_rn(d.lo, __fsub_rn(a.lo, b.lo))};
   if (d.hi < -150.f) return {0.f, 0.f};
   const float n = rintf(d.hi);
-  const Split f = two_sum(__fsub_rn(d.hi, n), __fadd_rn(d.lo, __fsub_rn(a.lo, b.lo)));  // (the difference is exact)
-  const float ln2_hi = 0.693147182f, ln2_lo = -1.90465421e-9f;
-  const float u = __fmul_rn(f.hi, ln2_hi), u_lo = __fmaf_rn(f.lo, ln2_hi, __fmaf_rn(f.hi, ln2_lo, __fmaf_rn(f.hi, ln2_hi, -u)));
+  const Split f = two_sum(__fsub_rn(d.hi, n), difference.lo);  // (the subtraction is exact)
+  const float u = __fmul_rn(f.hi, kLn2), u_lo = __fmaf_rn(f.lo, kLn2, __fmaf_rn(f.hi, kLn2Lo, __fmaf_rn(f.hi, kLn2, -u)));
   const float s = __fmul_rn(u, u), s_lo = __fmaf_rn(2.f * u, u_lo, __fmaf_rn(u, u, -s));
   float q = 1.f / 362880.f;
   q = __fmaf_rn(q, u, 1.f / 40320.f);
@@ -519,218 +540,357 @@ __device__ __forceinline__ Split exp2_difference(Split a, Split b) {
   const float lo = __fadd_rn(__fadd_rn(t.lo, v.lo), __fadd_rn(w.lo, __fadd_rn(u_lo, 0.5f * s_lo)));
   return {ldexpf(__fadd_rn(t.hi, lo), (int)n), ldexpf(__fsub_rn(lo, __fsub_rn(__fadd_rn(t.hi, lo), t.hi)), (int)n)};
 }
-// ln v, its exponent's part in float64: within 2^-24 whatever the size
-__device__ __forceinline__ double ln_of(double v) {
-  const float f = (float)v;
+// ln v, v > 0: within 2^-24 whatever its size, since only the logarithm of v's fraction is rounded to float32
+__device__ __forceinline__ Split ln_of(Split v) {
   int e;
-  float m = frexpf(f, &e);  // [1/2, 1)
+  float m = frexpf(v.hi, &e);  // [1/2, 1)
   if (m < 0.70710678f) m *= 2.f, --e;
-  return (double)e * 0.69314718055994530942 + (double)__fadd_rn(logf(m), (float)(v - (double)f) * __fdiv_rn(1.f, f));
+  const Split whole = product((float)e, kLn2, kLn2Lo);
+  return add(whole, two_sum(logf(m), __fdiv_rn(v.lo, v.hi)));
+}
+__device__ __forceinline__ Split negative(Split v) { return {-v.hi, -v.lo}; }
+__device__ __forceinline__ Split quotient(Split a, Split b) {
+  const float inv = __fdiv_rn(1.f, b.hi), q = __fmul_rn(a.hi, inv);
+  return two_sum(q, __fmul_rn(add(a, negative(times(b, Split{q, 0.f}))).hi, inv));
 }
 
-// What the cluster's CTA 0 knows of a row's listed entries, in every CTA.
-struct __align__(16) Teacher {
-  float share, left, total, unused;  // the sum of their shares, what it leaves of 1, the sum of both
-  double sums[4];                    // over the entries: e, e ln e, e x
+// What a CTA knows of those of a row's listed entries that lie in its pieces: the sum of their shares e, and of e log2 e
+// and e x. As pairs of floats, since what the shares leave of 1, and differences of logarithms, may be small (a float64
+// instruction takes the SM 16 cycles a warp).
+enum { kNoList = 1, kBadList = 2 };  // (of the whole row) nothing listed has a share; a NaN or infinity among the teacher's numbers
+struct __align__(16) ListSums {
+  Split share, e_log_e;
+  Split e_x;
+  int flags, unused;
+};
+// A listed entry as the gradient needs it.
+struct Listed {
+  float e, x;  // the teacher's share (before that, its logit) and the drafter's logit
+  int id;      // -1: none
 };
 
-// A cluster takes rows cluster, cluster + clusters, .. one after the other: a row's pieces are overwritten by the
-// next row's as soon as they have been used for the last time, so that the next row arrives while this one's
-// gradient leaves, and the next row's listed entries are loaded meanwhile too.
+constexpr int kListThreads = 64;
+constexpr int kDistillThreads = kRowThreads + kListThreads;
+template <int kId, int kThreads>
+__device__ __forceinline__ void named_sync() { asm volatile("barrier.cta.sync %0, %1;" ::"n"(kId), "n"(kThreads) : "memory"); }
+template <int kId, int kThreads>
+__device__ __forceinline__ void named_arrive() { asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kId), "n"(kThreads) : "memory"); }
+enum { kMarksReady = 1, kRowWritten = 2, kListSync = 3 };  // named barriers
+
+// What the weights of a row are multiplied by in its gradient: entries of the rest, listed ones; and the teacher's shares.
+struct Factors {
+  float rest, listed, teacher;
+  bool bad, some;  // some: a rest without mass on either side counts for nothing
+};
+template <bool kRest>
+__device__ __forceinline__ Factors factors(const ListSums* of, int C, const RowSum& sum, float weight, float per_tau) {
+  Split share{0.f, 0.f};
+  for (int c = 0; c < C; ++c) share = add(share, of[c].share);
+  const Split rest = two_sum(1.f, -share.hi);
+  const float left = kRest ? fmaxf(0.f, __fadd_rn(rest.hi, __fsub_rn(rest.lo, share.lo))) : 0.f, all = __fadd_rn(share.hi, share.lo);
+  const int flags = of[0].flags;
+  Factors f;
+  f.bad = !(fabsf(sum.M) < INFINITY) || flags & kBadList;
+  f.some = kRest && left > 0.f && sum.z > 0.f;
+  const float scale = __fmul_rn(weight, per_tau);
+  const float per_z = __fdiv_rn(kRest ? (f.some ? fmaxf(1.f, all) : all) : flags & kNoList ? 0.f : 1.f, sum.z + sum.listed);
+  f.listed = scale * per_z;
+  f.rest = scale * (per_z - (f.some ? __fdiv_rn(left, sum.z) : 0.f));
+  f.teacher = kRest ? scale : flags & kNoList ? 0.f : scale * __fdiv_rn(1.f, all);
+  return f;
+}
+
+// A cluster takes rows cluster, cluster + clusters, .. one after the other. kRowThreads threads of a CTA stream: a row's
+// pieces are overwritten by the next row's as soon as they have been used for the last time, so that the next row
+// arrives while this one's gradient leaves. Two more warps look after the listed entries: they load and mark the next
+// row's and form its sums while this row is written, then put this row's listed entries over what was written. The two groups
+// meet once a row, at the cluster's exchange (with a rest also where the marks have to be ready).
 template <class T, bool kRest, bool kGrad>
-__global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p) {
+__global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillParams p) {
   extern __shared__ __align__(16) uint4 held[];
   // two sets each: a CTA may write the next row's while another still reads this one's
   __shared__ float4 all[2][kMaxCluster * kRowWarps];
-  __shared__ Teacher teachers[2];
-  __shared__ double sums[kRowWarps][3];
-  __shared__ float maxima[kRowWarps];
+  __shared__ ListSums teachers[2][kMaxCluster];
+  __shared__ Split sums[kListThreads / 32][3];
+  __shared__ int counts[2][kListThreads / 32];
+  __shared__ float maxima[kListThreads / 32];
   __shared__ uint32_t loose_marks;
-  __shared__ int twice;
-  // of the listed entries: the teacher's share, its logit, the student's, the id (-1: none); then the map
-  float* s_e = reinterpret_cast<float*>(reinterpret_cast<char*>(held) + p.held);
-  float* s_t = s_e + p.K;
-  float* s_x = s_t + p.K;
-  int* s_id = reinterpret_cast<int*>(s_x + p.K);
-  uint32_t* s_marks = reinterpret_cast<uint32_t*>(s_id + p.K);
-  const int rank = (int)cluster_rank(), C = p.C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ int twice[2];
+  const int half = (p.K + 1) / 2;  // a warp's part of a list
+  Listed* lists = reinterpret_cast<Listed*>(reinterpret_cast<char*>(held) + p.held);  // two rows' two parts
+  uint32_t* s_marks = reinterpret_cast<uint32_t*>(lists + 4 * half);
+  const int rank = (int)cluster_rank(), C = p.C, tid = threadIdx.x, lane = tid & 31;
   cluster_arrive_relaxed();
   const int clusters = gridDim.x / C;
   const Rate rate{1.f, p.k_hi};
   const T* logits = static_cast<const T*>(p.logits);
   const auto part_of = [&](int r) { return RowPart<T>(logits + (size_t)r * p.V, p.V, C, rank); };
-  // this thread's first listed entry of row r
-  struct Entry {
-    int id;
-    float t;
-  };
-  const auto entry = [&](int r, int j) {
-    Entry e{-1, -INFINITY};
-    if (r < p.N && j < p.K) {
-      asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(e.id) : "l"(p.ids + (size_t)r * p.K + j));
-      asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(e.t) : "l"(p.teacher + (size_t)r * p.K + j));
-    }
-    return e;
-  };
-  const auto student = [&](int r, int id) {
-    float x = -INFINITY;
-    if (id >= 0 && id < p.V) x = row_elem(logits + (size_t)r * p.V + id);
-    return x;
-  };
-
   int r = blockIdx.x / C;
-  RowPart<T> part = part_of(r);
-  int own = part.own();
-  if (p.windows == 1) part.fetch(held, 0, own);
-  Entry next = entry(r, tid);
-  for (int i = tid; i < p.marks / 4; i += kRowThreads) s_marks[i] = 0;
-  if (tid == 0) {
-    loose_marks = 0;
-    twice = 0;
-  }
-  float next_x = student(r, next.id);
-  cluster_wait();
-  __syncthreads();
 
-  for (int turn = 0; r < p.N; turn ^= 1) {
-    const int loose_at = part.own_loose(p.V);
-    const float loose = loose_at >= 0 ? row_elem(part.row + loose_at) : -INFINITY;
-
-    // the listed entries, in every CTA; those of this CTA's pieces are marked
-    float t_max = -INFINITY;
-    for (int j = tid; j < p.K; j += kRowThreads) {
-      Entry e = next;
-      float x = next_x;
-      if (j != tid) {
-        e = entry(r, j);
-        x = student(r, e.id);
+  if (tid < kRowThreads) {
+    RowPart<T> part = part_of(r);
+    int own = part.own();
+    if (p.windows == 1) part.fetch(held, 0, own);
+    cluster_wait();
+#pragma unroll 1
+    for (int turn = 0; r < p.N; turn ^= 1) {
+      const int loose_at = part.own_loose(p.V);
+      const float loose = loose_at >= 0 ? row_elem(part.row + loose_at) : -INFINITY;
+      const int r_next = r + clusters;
+      const RowPart<T> follow = part_of(min(r_next, p.N - 1));
+      const int own_next = r_next < p.N && p.windows == 1 ? follow.own() : 0;
+      const auto refill = [&](int g) { follow.fetch_group(held, 0, own_next, g); };
+      if (kRest) named_sync<kMarksReady, kDistillThreads>();
+      ThreadSum s;
+      const auto bits = [&](int i0, int i) -> uint32_t {
+        if (i < 0) return loose_marks >> tid & 1u;
+        const int local = (i0 + i) * kRowThreads + tid;
+        return local < p.marks ? s_marks[local >> 2] >> ((local & 3) * 8) & 255u : 0u;
+      };
+      if (p.windows == 1) {
+        const auto mark = [&](int i) { return bits(0, i); };
+        if constexpr (kGrad) add_groups<T, kRest, false, 0>(s, held + tid, own, loose, rate, mark, [](int) {});
+        else add_groups<T, kRest, true, 0>(s, held + tid, own, loose, rate, mark, refill);
+      } else {
+        for (int c = 0; c < p.windows; ++c) {
+          const int m = min(own - c * kPieces, kPieces);
+          part.fetch(held, c * kPieces, m);
+          add_groups<T, kRest, false, 0>(s, held + tid, m, c == 0 ? loose : -INFINITY, rate, [&](int i) { return bits(c * kPieces, i); },
+                                         [](int) {});
+        }
       }
-      if (e.id >= p.V) set_status(p.status, DSPARK_ERR_RANGE);
-      if (e.id < 0 || e.id >= p.V) e = Entry{-1, -INFINITY};
-      s_id[j] = e.id;
-      s_t[j] = e.t;
-      s_x[j] = x;
-      t_max = nan_max(t_max, e.t);
+      send<kRest>(s, all[turn], C, rank, rate);
+      const RowSum sum = receive<kRest>(all[turn], C, rate);
+      if constexpr (kGrad) {
+        // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v), here without the last term
+        const Factors f = factors<kRest>(teachers[turn], C, sum, p.weight ? __ldg(p.weight + r) : 1.f, p.per_tau);
+        T* grad = static_cast<T*>(p.grad) + (size_t)r * p.V;
+        const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
+        const auto after = [&](int g) {
+          if (p.windows == 1) refill(g);
+        };
+        if (f.bad) {
+          write_one(part, own, -1, grad, wide, loose_at);
+#pragma unroll 1
+          for (int g = 0; g < kGroups; ++g) after(g);
+        } else if (plain_exponent(rate, sum.M)) {
+          const Weigher<true> w(rate, sum.M);
+          write_weights(part, held, own, p.windows, w, f.rest * w.scale, grad, wide, loose_at, loose, after);
+        } else {
+          write_weights(part, held, own, p.windows, Weigher<false>(rate, sum.M), f.rest, grad, wide, loose_at, loose, after);
+        }
+        named_arrive<kRowWritten, kDistillThreads>();
+      }
+      r = r_next;
+      part = follow;
+      own = part.own();
+    }
+    copies_done<0>();
+    return;
+  }
+
+  // The listed entries: each warp goes through half of the list and keeps, in order, those in this CTA's pieces.
+  const int j0 = tid - kRowThreads, warp = j0 >> 5;
+  struct Row {
+    int n, flags;  // entries kept by this warp
+  };
+  const auto list_of = [&](int turn, int w) { return lists + (turn * 2 + w) * half; };
+  // The first kEarly entries of the warp's half, loaded ahead of their use: ids and logits, then the drafter's logits.
+  constexpr int kEarly = 64;
+  struct Early {
+    int id[kEarly / 32];
+    float t[kEarly / 32], x[kEarly / 32];
+  };
+  const int first = warp * half, last = min(first + half, p.K);
+  const auto load = [&](int r, Early& e) {
+#pragma unroll
+    for (int i = 0; i < kEarly / 32; ++i) {
+      const int j = first + 32 * i + lane;
+      e.id[i] = -1;
+      e.t[i] = -INFINITY;
+      if (r < p.N && j < last) {
+        asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(e.id[i]) : "l"(p.ids + (size_t)r * p.K + j));
+        asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(e.t[i]) : "l"(p.teacher + (size_t)r * p.K + j));
+      }
+    }
+  };
+  const auto gather = [&](int r, Early& e) {
+#pragma unroll
+    for (int i = 0; i < kEarly / 32; ++i)
+      e.x[i] = e.id[i] >= 0 && e.id[i] < p.V ? row_elem(logits + (size_t)r * p.V + e.id[i]) : -INFINITY;
+  };
+  const auto prepare = [&](int r, int turn, const Early& early) {
+    Listed* list = list_of(turn, warp);
+    const RowPart<T> part = part_of(r);
+    float t_max = -INFINITY;
+    int n = 0;
+    const auto keep = [&](int id, float t, float x) {
+      if (id >= p.V) set_status(p.status, DSPARK_ERR_RANGE);
       int local, at;
-      if (e.id >= 0 && part.owner(e.id, local, at) == rank) {
+      const bool valid = id >= 0 && id < p.V, mine = valid && part.owner(id, local, at) == rank;
+      if (valid) t_max = nan_max(t_max, t);
+      const uint32_t b = __ballot_sync(0xffffffffu, mine);
+      if (mine) list[n + __popc(b & ((1u << lane) - 1u))] = Listed{t, x, id};
+      n += __popc(b);
+    };
+#pragma unroll
+    for (int i = 0; i < kEarly / 32; ++i) keep(early.id[i], early.t[i], early.x[i]);
+    for (int base = first + kEarly; base < last; base += 128) {
+      int id[4];
+      float t[4], x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = base + 32 * i + lane;
+        id[i] = j < last ? __ldg(p.ids + (size_t)r * p.K + j) : -1;
+        t[i] = j < last ? __ldg(p.teacher + (size_t)r * p.K + j) : -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = id[i] >= 0 && id[i] < p.V ? row_elem(part.row + id[i]) : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) keep(id[i], t[i], x[i]);
+    }
+    if (j0 == 0) twice[turn] = 0;
+    t_max = warp_nan_max(t_max);
+    if (lane == 0) {
+      maxima[warp] = t_max;
+      counts[turn][warp] = n;
+    }
+    named_sync<kListSync, kListThreads>();
+    t_max = nan_max(maxima[0], maxima[1]);
+    static_assert(kListThreads == 64, "two warps");
+    for (int k = lane; k < n; k += 32) {
+      const int id = list[k].id;
+      if (kRest) {
+        int local, at;
+        part.owner(id, local, at);
         uint32_t* word = local < 0 ? &loose_marks : s_marks + (local >> 2);
         const uint32_t bit = local < 0 ? 1u << (-1 - local) : 1u << ((local & 3) * 8 + at);
-        if (atomicOr(word, bit) & bit) twice = 1;
+        if (atomicOr(word, bit) & bit) twice[turn] = 1;
+      } else {  // nobody else needs the map
+        int same = 0;
+        for (int w = 0; w < 2; ++w)
+          for (int i = 0; i < counts[turn][w]; ++i) same += list_of(turn, w)[i].id == id;
+        if (same > 1) twice[turn] = 1;
       }
     }
-    t_max = warp_nan_max(t_max);
-    if (lane == 0) maxima[warp] = t_max;
-    __syncthreads();
-    t_max = warp_nan_max(maxima[lane % kRowWarps]);
+    if (kRest) named_arrive<kMarksReady, kDistillThreads>();
     const float lse = kRest ? __ldg(p.teacher_lse + r) : t_max;
-    const bool bad_teacher = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < INFINITY));
-    const bool listless = t_max == -INFINITY || bad_teacher;
-    // an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum. CTA 0 sums what the
-    // loss needs in float64, since what the shares leave of 1, and differences of logarithms, may be small
+    const bool bad = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < INFINITY));
+    const bool none = t_max == -INFINITY || bad;
+    // an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum
     const Split ref = kRest ? product(lse, 1.44269502e+00f, 1.92596299e-08f) : product(lse, p.k_hi, p.k_lo);
-    if (warp * 32 < p.K) {
-      double a = 0.0, b = 0.0, c = 0.0;
-      for (int j = tid; j < p.K; j += kRowThreads) {
-        const float t = s_t[j];
-        Split e{0.f, 0.f};
-        if (t != -INFINITY && !listless) e = exp2_difference(product(t, p.k_hi, p.k_lo), ref);
-        s_e[j] = e.hi;
-        if (rank == 0 && e.hi > 0.f) {
-          const double d = (double)e.hi + (double)e.lo;
-          a += d;
-          b += d * (kRest ? (double)t * p.per_tau - (double)lse : ((double)t - (double)lse) * p.per_tau);
-          c += d * (double)s_x[j];
-        }
-      }
-      if (rank == 0) {
-        a = warp_add_d(a);
-        b = warp_add_d(b);
-        c = warp_add_d(c);
-        if (lane == 0) sums[warp][0] = a, sums[warp][1] = b, sums[warp][2] = c;
+    Split a{0.f, 0.f}, b = a, c = a;
+    for (int k = lane; k < n; k += 32) {
+      const float t = list[k].e;
+      Split e{0.f, 0.f}, y = e;
+      if (t != -INFINITY && !none) e = exp2_difference(product(t, p.k_hi, p.k_lo), ref, y);
+      list[k].e = e.hi;
+      if (e.hi > 0.f) {
+        a = add(a, e);
+        b = add(b, times(e, y));
+        const float x = list[k].x;
+        c = x == -INFINITY ? Split{-INFINITY, 0.f} : add(c, times(e, Split{x, 0.f}));
       }
     }
-
-    const int r_next = r + clusters;
-    const RowPart<T> follow = part_of(min(r_next, p.N - 1));
-    const int own_next = r_next < p.N && p.windows == 1 ? follow.own() : 0;
-    const auto refill = [&](int g) { follow.fetch_group(held, 0, own_next, g); };
-    ThreadSum s;
-    const auto bits = [&](int i0, int i) -> uint32_t {
-      if (i < 0) return loose_marks >> tid & 1u;
-      const int local = (i0 + i) * kRowThreads + tid;
-      return local < p.marks ? s_marks[local >> 2] >> ((local & 3) * 8) & 255u : 0u;
-    };
-    if (p.windows == 1) {
-      const auto mark = [&](int i) { return bits(0, i); };
-      if constexpr (kGrad) add_groups<T, kRest, false, 0>(s, held + tid, own, loose, rate, mark, [](int) {});
-      else add_groups<T, kRest, true, 0>(s, held + tid, own, loose, rate, mark, refill);
-    } else {
-      for (int c = 0; c < p.windows; ++c) {
-        const int m = min(own - c * kPieces, kPieces);
-        part.fetch(held, c * kPieces, m);
-        add_groups<T, kRest, false, 0>(s, held + tid, m, c == 0 ? loose : -INFINITY, rate, [&](int i) { return bits(c * kPieces, i); }, [](int) {});
-      }
+    if (n > 0) {
+      a = warp_add(a);
+      b = warp_add(b);
+      const bool infinite = __any_sync(0xffffffffu, c.hi == -INFINITY);  // a listed entry to which the drafter gives nothing
+      c = infinite ? Split{-INFINITY, 0.f} : warp_add(c);
     }
-    Teacher& teacher = teachers[turn];
-    if (rank == 0) {
-      __syncthreads();
-      if (warp == 0) {
-        double v = 0.0;  // lanes 0, 1, 2 take a sum each
-        for (int w = 0; w < min((p.K + 31) / 32, kRowWarps); ++w) v += sums[w][lane % 3];
-        const double share = __shfl_sync(0xffffffffu, v, 0), left = kRest ? fmax(0.0, 1.0 - share) : 0.0;
-        for (int c = 0; c < C; ++c) {
-          if (lane < 3) store_peer(peer_address(&teacher.sums[lane], c), (unsigned long long)__double_as_longlong(v));
-          if (lane == 3) store_peer(peer_address(&teacher, c), make_float4((float)share, (float)left, (float)(share + left), 0.f));
-        }
-      }
-    }
-    const RowSum sum = exchange<kRest>(s, all[turn], C, rank, rate);
-    next = entry(r_next, tid);
-    const bool bad = !(fabsf(sum.M) < INFINITY) || bad_teacher;
-    const float z = sum.z + sum.listed;
-    const bool some = kRest && teacher.left > 0.f && sum.z > 0.f;  // a rest without mass on either side counts for nothing
-
-    if constexpr (kGrad) {
-      // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v)
-      T* grad = static_cast<T*>(p.grad) + (size_t)r * p.V;
-      const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
-      const float scale = __fmul_rn(p.weight ? __ldg(p.weight + r) : 1.f, (float)p.per_tau);
-      const float per_z = __fdiv_rn(kRest ? (some ? teacher.total : teacher.share) : listless ? 0.f : 1.f, z);
-      const float rest_f = scale * (per_z - (some ? __fdiv_rn(teacher.left, sum.z) : 0.f));
-      const bool plain = plain_exponent(rate, sum.M);
-      const auto after = [&](int g) {
-        if (p.windows == 1) refill(g);
+    if (lane == 0) sums[warp][0] = a, sums[warp][1] = b, sums[warp][2] = c;
+    named_sync<kListSync, kListThreads>();
+    return Row{n, (none ? kNoList : 0) | (bad ? kBadList : 0)};
+  };
+  if (kRest) {
+    for (int i = j0; i < p.marks / 4; i += kListThreads) s_marks[i] = 0;
+    if (j0 == 0) loose_marks = 0;
+    named_sync<kListSync, kListThreads>();
+  }
+  Early early;
+  load(r, early);
+  gather(r, early);
+  Row now = prepare(r, 0, early);
+  cluster_wait();
+#pragma unroll 1
+  for (int turn = 0; r < p.N; turn ^= 1) {
+    if (warp == 0) {
+      const auto both = [&](int i) {
+        const Split u = sums[0][i], v = sums[1][i];
+        return u.hi == -INFINITY || v.hi == -INFINITY ? Split{-INFINITY, 0.f} : add(u, v);
       };
-      if (bad) {
-        write_one(part, own, -1, grad, wide, loose_at);
-        for (int g = 0; g < kGroups; ++g) after(g);
-      } else if (plain) {
-        const Weigher<true> w(rate, sum.M);
-        write_weights(part, held, own, p.windows, w, rest_f * w.scale, grad, wide, loose_at, loose, after);
-      } else {
-        write_weights(part, held, own, p.windows, Weigher<false>(rate, sum.M), rest_f, grad, wide, loose_at, loose, after);
+      const Split a = both(0), b = both(1), c = both(2);
+      if (lane < C) {
+        ListSums* to = &teachers[turn][rank];
+        store_peer(peer_address(to, lane), make_float4(a.hi, a.lo, b.hi, b.lo));
+        store_peer(peer_address(&to->e_x, lane), make_float4(c.hi, c.lo, __int_as_float(now.flags), 0.f));
       }
-      next_x = student(r_next, next.id);
-      // the listed entries of this CTA over what was just written
-      __syncthreads();
-      float norm = 1.f;
-      if (!kRest && warp * 32 < p.K) {
-        norm = 0.f;
-        for (int j = lane; j < p.K; j += 32) norm += s_e[j];
-        norm = warp_sum(norm);
-        norm = norm > 0.f ? __fdiv_rn(1.f, norm) : 0.f;
-      }
-      for (int j = tid; j < p.K && !bad; j += kRowThreads) {
-        const int id = s_id[j];
+    }
+    __syncwarp();
+    const int r_next = r + clusters;
+    load(r_next, early);
+    cluster_arrive();
+    gather(min(r_next, p.N - 1), early);  // (past the last row: no ids)
+    cluster_wait();
+    const RowSum sum = combine<kRest>(all[turn], C, rate);
+    const Factors f = factors<kRest>(teachers[turn], C, sum, p.weight ? __ldg(p.weight + r) : 1.f, p.per_tau);
+    const RowPart<T> part = part_of(r);
+    const Listed* list = list_of(turn, warp);
+
+    // the marks are taken back and the next row's set
+    if (kRest) {
+      for (int k = lane; k < now.n; k += 32) {
         int local, at;
-        if (id < 0 || part.owner(id, local, at) != rank) continue;
-        float e = s_e[j];
-        if (twice) {  // an id that comes more than once: every occurrence writes the sum of all
+        part.owner(list[k].id, local, at);
+        if (local >= 0) s_marks[local >> 2] = 0;
+      }
+      if (j0 == 0) loose_marks = 0;
+      named_sync<kListSync, kListThreads>();
+    }
+    Row next{0, 0};
+    if (r_next < p.N) next = prepare(r_next, turn ^ 1, early);
+
+    // the loss: the last CTA's
+    if (rank == C - 1 && j0 == 32) {
+      Split share{0.f, 0.f}, a = share, x = share;
+      bool infinite = false;  // a listed entry to which the drafter gives nothing
+      for (int c = 0; c < C; ++c) {
+        const ListSums& of = teachers[turn][c];
+        share = add(share, of.share);
+        a = add(a, of.e_log_e);
+        infinite |= of.e_x.hi == -INFINITY;
+        x = add(x, of.e_x);
+      }
+      // sum of e (log2 e - log2 of the drafter's weight), then ln 2 of it; the rate as the weights have it
+      a = add(a, negative(times(add(x, negative(times(share, Split{sum.M, 0.f}))), Split{rate.rate, 0.f})));
+      a = times(a, Split{kLn2, kLn2Lo});
+      const Split z = two_sum(sum.z, sum.listed), ln_z = ln_of(z);
+      Split loss{0.f, 0.f};
+      if (kRest) {
+        const Split left = add(Split{1.f, 0.f}, negative(share));
+        loss = add(a, times(share, ln_z));
+        if (f.some) loss = add(loss, times(left, add(add(ln_of(left), negative(ln_of(Split{sum.z, 0.f}))), ln_z)));
+      } else if (share.hi > 0.f) {
+        loss = add(add(quotient(a, share), ln_z), negative(ln_of(share)));
+      }
+      if (infinite) loss.hi = INFINITY;
+      p.loss[r] = f.bad ? NAN : loss.hi;
+      if (f.bad) set_status(p.status, DSPARK_ERR_NONFINITE);
+    }
+
+    if constexpr (kGrad) {  // the listed entries of this CTA over what was written
+      named_sync<kRowWritten, kDistillThreads>();
+      T* grad = static_cast<T*>(p.grad) + (size_t)r * p.V;
+      const bool plain = plain_exponent(rate, sum.M);
+      for (int k = lane; k < now.n && !f.bad; k += 32) {
+        float e = list[k].e;
+        if (twice[turn]) {  // an id that comes more than once: every occurrence writes the sum of all
           e = 0.f;
-          for (int i = 0; i < p.K; ++i)
-            if (s_id[i] == id) e += s_e[i];
+          for (int w = 0; w < 2; ++w)
+            for (int i = 0; i < counts[turn][w]; ++i)
+              if (list_of(turn, w)[i].id == list[k].id) e += list_of(turn, w)[i].e;
         }
-        const float x = s_x[j];
+        const float x = list[k].x;
         float y;
         if (plain) {
           const Weigher<true> w(rate, sum.M);
@@ -738,47 +898,13 @@ __global__ void __launch_bounds__(kRowThreads, 3) distill_kernel(DistillParams p
         } else {
           y = Weigher<false>(rate, sum.M)(x);
         }
-        store_elem(grad + id, __fmaf_rn(-scale * norm, e, y * (scale * per_z)));
+        store_elem(grad + list[k].id, __fmaf_rn(-f.teacher, e, y * f.listed));
       }
-    } else {
-      next_x = student(r_next, next.id);
+      named_sync<kListSync, kListThreads>();
     }
-
-    // the loss: the last CTA's (CTA 0 has had the sums to form)
-    if (rank == C - 1 && tid == kRowThreads - 32) {
-      const double share = teacher.sums[0], step = (double)p.k_hi * 0.69314718055994530942;  // 1 / tau as the weights have it
-      const double a = teacher.sums[1] - step * (teacher.sums[2] - (double)sum.M * share), ln_z = ln_of((double)z);
-      double loss = 0.0;
-      if (kRest) {
-        const double left = fmax(0.0, 1.0 - share);
-        loss = a + share * ln_z;
-        if (some) loss += left * (ln_of(left) - ln_of((double)sum.z) + ln_z);
-      } else if (share > 0.0) {
-        double inv = (double)__fdiv_rn(1.f, (float)share);
-        inv *= 2.0 - share * inv;
-        loss = a * inv + ln_z - ln_of(share);
-      }
-      p.loss[r] = bad ? NAN : (float)loss;
-      if (bad) set_status(p.status, DSPARK_ERR_NONFINITE);
-    }
-
-    // the marks are taken back, the next row begins
-    __syncthreads();
-    for (int j = tid; j < p.K; j += kRowThreads) {
-      const int id = s_id[j];
-      int local, at;
-      if (id >= 0 && part.owner(id, local, at) == rank && local >= 0) s_marks[local >> 2] = 0;
-    }
-    if (tid == 0) {
-      loose_marks = 0;
-      twice = 0;
-    }
-    __syncthreads();
     r = r_next;
-    part = follow;
-    own = part.own();
+    now = next;
   }
-  copies_done<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -807,8 +933,8 @@ static cudaError_t launch_probs(const ProbsParams& p, int N, int held, cudaStrea
   return launch_clusters(probabilities_kernel<T, To>, p, (unsigned)N * p.C, p.C, kRowThreads, held, s);
 }
 
-// the pieces, 16 bytes a listed entry, and a byte for each piece of a row of 2^20 float32
-constexpr int kDistillSmem = kPieces * kRowThreads * 16 + kMaxTop * 16 + (1 << 20) / 4 / kMaxCluster + kRowThreads;
+// the pieces, two rows' listed entries, and a byte for each piece of a row of 2^20 float32
+constexpr int kDistillSmem = kPieces * kRowThreads * 16 + kMaxTop * 2 * (int)sizeof(Listed) + (1 << 20) / 4 / kMaxCluster + kRowThreads;
 
 // Rows are taken in equal turns by as many clusters as the GPU holds at once (more would begin when those end).
 template <class T, bool kRest, bool kGrad>
@@ -816,12 +942,12 @@ static cudaError_t launch_distill(const DistillParams& p, cudaStream_t s) {
   static std::atomic<unsigned long long> attr{0};
   const cudaError_t e = set_smem_limit_once((const void*)distill_kernel<T, kRest, kGrad>, kDistillSmem, attr);
   if (e != cudaSuccess) return e;
-  const size_t smem = (size_t)p.held + (size_t)p.K * 16 + p.marks;
+  const size_t smem = (size_t)p.held + (size_t)((p.K + 1) / 2) * 4 * sizeof(Listed) + p.marks;
   int resident = 0;
-  const cudaError_t f = resident_clusters((const void*)distill_kernel<T, kRest, kGrad>, p.C, kRowThreads, smem, resident);
+  const cudaError_t f = resident_clusters((const void*)distill_kernel<T, kRest, kGrad>, p.C, kDistillThreads, smem, resident);
   if (f != cudaSuccess) return f;
   const int turns = ceil_div(p.N, resident);
-  return launch_clusters(distill_kernel<T, kRest, kGrad>, p, (unsigned)(ceil_div(p.N, turns) * p.C), p.C, kRowThreads, smem, s);
+  return launch_clusters(distill_kernel<T, kRest, kGrad>, p, (unsigned)(ceil_div(p.N, turns) * p.C), p.C, kDistillThreads, smem, s);
 }
 template <class T>
 static cudaError_t launch_distill(const DistillParams& p, cudaStream_t s) {
@@ -879,11 +1005,11 @@ extern "C" dspark_status dspark_distill(int32_t N, int32_t V, int32_t K, int32_t
   int held;
   const int elem = dtype == DSPARK_BF16 ? 2 : 4;
   const int C = row_cluster(N, V, elem, sms, held);
-  // one byte a piece of this CTA, whole steps of the block
-  const int marks = ceil_div((long long)V * elem / 16, (long long)C * kRowThreads) * kRowThreads;
+  // one byte a piece of this CTA, whole steps of the block (for the entries that are left out of the rest)
+  const int marks = !teacher_lse ? 0 : ceil_div((long long)V * elem / 16, (long long)C * kRowThreads) * kRowThreads;
   const double k = 1.44269504088896340736 / (double)temperature;
   const int windows = std::max(1, ceil_div(ceil_div((long long)V * elem / 16, (long long)C * kRowThreads), kPieces));
-  const DistillParams p{N, V, K, C, windows, held, marks, logits, ids, teacher, teacher_lse, weight, 1.0 / (double)temperature,
+  const DistillParams p{N, V, K, C, windows, held, marks, logits, ids, teacher, teacher_lse, weight, (float)(1.0 / (double)temperature),
                         (float)k, (float)(k - (double)(float)k), loss, grad, static_cast<uint32_t*>(workspace)};
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = dtype == DSPARK_BF16 ? launch_distill<__nv_bfloat16>(p, s) : launch_distill<float>(p, s);
