@@ -169,28 +169,19 @@ __device__ __forceinline__ void store_piece(To* out, const float (&y)[E], bool w
   }
 }
 
-// Weights 2^((x - M) rate) of a row's entries. Where c = fl(M rate) is of an ordinary size the exponent is one fma,
-// x rate - c, rounded once at its own size; the weights are then 2^lost too large, lost what c's rounding cut off, and
-// `scale` takes that off a sum or a result. Else it is (x - M) rate as fma(x, h, -M h) (rate / h), with h = 1/2 for rates
-// so small that differences past float32's range count (scale 1).
+// Weights of a row's entries relative to its maximum M. Where M rate is of an ordinary size they are 2^(x rate - c), c the
+// whole number nearest to M rate: the exponent is one fma, rounded once at its own size, and sums relative to other maxima
+// differ by exact powers of two. Else they are 2^((x - M) rate), as fma(x, h, -M h) (rate / h), with h = 1/2 for rates so
+// small that differences past float32's range count.
 struct Rate {
   float h, rate;  // rate / h
 };
 __device__ __forceinline__ bool plain_exponent(const Rate& r, float M) { return r.h == 1.f && fabsf(M * r.rate) < 0x1p20f; }
+__device__ __forceinline__ float origin(const Rate& r, float M) { return rintf(__fmul_rn(M, r.rate)); }
 template <bool kPlain>
 struct Weigher {
-  float a, b, rate, scale;
-  __device__ __forceinline__ Weigher(const Rate& r, float M) : rate(r.rate) {
-    if constexpr (kPlain) {
-      a = r.rate;
-      b = -__fmul_rn(M, r.rate);
-      scale = ex2_approx(-__fmaf_rn(M, r.rate, b));
-    } else {
-      a = r.h;
-      b = -M * r.h;
-      scale = 1.f;
-    }
-  }
+  float a, b, rate;
+  __device__ __forceinline__ Weigher(const Rate& r, float M) : a(kPlain ? r.rate : r.h), b(kPlain ? -origin(r, M) : -M * r.h), rate(r.rate) {}
   __device__ __forceinline__ float operator()(float x) const {
     const float y = __fmaf_rn(x, a, b);
     return ex2_approx(kPlain ? y : __fmul_rn(y, rate));
@@ -203,8 +194,18 @@ struct Weigher {
     return f32x2_pack(ex2_approx(y0), ex2_approx(y1));
   }
 };
-// 2^((x - M) rate), what a sum relative to x is multiplied by to be one relative to M
-__device__ __forceinline__ float rescale(const Rate& r, float x, float M) { return Weigher<false>(r, M)(x); }
+// What a sum relative to x is multiplied by to be one relative to M >= x.
+__device__ __forceinline__ float rescale(const Rate& r, float x, float M) {
+  const bool plain_x = plain_exponent(r, x), plain_M = plain_exponent(r, M);
+  if (plain_x && plain_M) {
+    const float d = origin(r, x) - origin(r, M);
+    return d < -126.f ? 0.f : __int_as_float((int)(127.f + d) << 23);
+  }
+  float y = __fmul_rn(__fmaf_rn(x, r.h, -M * r.h), r.rate);
+  if (plain_x) y -= __fmaf_rn(x, r.rate, -origin(r, x));
+  if (plain_M) y += __fmaf_rn(M, r.rate, -origin(r, M));
+  return ex2_approx(y);
+}
 
 // (maximum, sum) of a thread's entries so far; `listed` the part of the sum that is marked.
 struct ThreadSum {
@@ -251,8 +252,8 @@ __device__ __forceinline__ void add_weights(ThreadSum& s, const uint4 (&q)[kGrou
     if (kMarks && bits(-1)) l += y;
     else a0 += y;
   }
-  s.z = __fmaf_rn((a0 + a1) + (b0 + b1), w.scale, s.z);
-  if (kMarks) s.listed = __fmaf_rn(l, w.scale, s.listed);
+  s.z += (a0 + a1) + (b0 + b1);
+  if (kMarks) s.listed += l;
 }
 template <class T, bool kMarks, class Bits>
 __device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, Bits bits) {
@@ -284,10 +285,35 @@ __device__ __forceinline__ void add_groups(ThreadSum& s, const uint4* mine, int 
   if constexpr (g + 1 < kGroups) add_groups<T, kMarks, kRefill, g + 1>(s, mine, m, loose, r, bits, after);
 }
 
+// A value as a float and what its rounding left.
+struct Split {
+  float hi, lo;
+};
+__device__ __forceinline__ Split two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
+}
+__device__ __forceinline__ Split product(float a, float b_hi, float b_lo) {
+  const float p = __fmul_rn(a, b_hi);
+  return {p, __fmaf_rn(a, b_lo, __fmaf_rn(a, b_hi, -p))};
+}
+__device__ __forceinline__ Split add(Split a, Split b) {
+  const Split s = two_sum(a.hi, b.hi);
+  const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
+  return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
+}
+__device__ __forceinline__ Split warp_add(Split v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = add(v, Split{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
 // The row's maximum and sums from those of all warps of the cluster, the same in every thread (a warp's lanes each
 // take every 32nd entry, then a fixed tree).
 struct RowSum {
   float M, z, listed;
+  float z_lo, listed_lo;  // kPair: what the sums' roundings left
 };
 template <bool kMarks>
 __device__ __forceinline__ void send(const ThreadSum& s, float4* all, int C, int rank, const Rate& rate) {
@@ -298,10 +324,10 @@ __device__ __forceinline__ void send(const ThreadSum& s, float4* all, int C, int
   if (lane < C) store_peer(peer_address(all + rank * kRowWarps + warp, lane), make_float4(m, zw, lw, 0.f));
   __syncwarp();
 }
-template <bool kMarks>
+template <bool kMarks, bool kPair>
 __device__ __forceinline__ RowSum combine(const float4* all, int C, const Rate& rate) {
   const int lane = threadIdx.x & 31;
-  RowSum r{-INFINITY, 0.f, 0.f};
+  RowSum r{-INFINITY, 0.f, 0.f, 0.f, 0.f};
   const int n = C * kRowWarps;
   constexpr int L = kMaxCluster * kRowWarps / 32;  // entries a lane
   float4 t[L];
@@ -312,14 +338,27 @@ __device__ __forceinline__ RowSum combine(const float4* all, int C, const Rate& 
   }
   r.M = warp_nan_max(r.M);
   if (r.M == -INFINITY) return r;
+  if constexpr (kPair) {
+    Split z{0.f, 0.f}, l = z;
 #pragma unroll
-  for (int i = 0; i < L; ++i) {
-    const float g = t[i].x == -INFINITY ? 0.f : rescale(rate, t[i].x, r.M);
-    r.z = __fmaf_rn(t[i].y, g, r.z);
-    if (kMarks) r.listed = __fmaf_rn(t[i].z, g, r.listed);
+    for (int i = 0; i < L; ++i) {
+      const float g = t[i].x == -INFINITY ? 0.f : rescale(rate, t[i].x, r.M);
+      z = add(z, product(t[i].y, g, 0.f));
+      if (kMarks) l = add(l, product(t[i].z, g, 0.f));
+    }
+    z = warp_add(z);
+    r.z = z.hi, r.z_lo = z.lo;
+    if (kMarks) l = warp_add(l), r.listed = l.hi, r.listed_lo = l.lo;
+  } else {
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      const float g = t[i].x == -INFINITY ? 0.f : rescale(rate, t[i].x, r.M);
+      r.z = __fmaf_rn(t[i].y, g, r.z);
+      if (kMarks) r.listed = __fmaf_rn(t[i].z, g, r.listed);
+    }
+    r.z = warp_sum(r.z);
+    if (kMarks) r.listed = warp_sum(r.listed);
   }
-  r.z = warp_sum(r.z);
-  if (kMarks) r.listed = warp_sum(r.listed);
   return r;
 }
 
@@ -327,7 +366,7 @@ template <bool kMarks>
 __device__ __forceinline__ RowSum receive(const float4* all, int C, const Rate& rate) {
   cluster_arrive();
   cluster_wait();
-  return combine<kMarks>(all, C, rate);
+  return combine<kMarks, false>(all, C, rate);
 }
 
 // ---------------------------------------------------------------------------
@@ -467,8 +506,7 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
     for (int i = lane; i < C * kRowWarps; i += 32) top = min(top, (int)first[i]);
     write_one(part, own, warp_min_i(top), out, wide, loose_at);
   } else if (plain_exponent(rate, sum.M)) {
-    const Weigher<true> w(rate, sum.M);
-    write_weights(part, held, own, windows, w, __fdiv_rn(w.scale, sum.z), out, wide, loose_at, loose, [](int) {});
+    write_weights(part, held, own, windows, Weigher<true>(rate, sum.M), __fdiv_rn(1.f, sum.z), out, wide, loose_at, loose, [](int) {});
   } else {
     write_weights(part, held, own, windows, Weigher<false>(rate, sum.M), __fdiv_rn(1.f, sum.z), out, wide, loose_at, loose, [](int) {});
   }
@@ -489,32 +527,9 @@ struct DistillParams {
   uint32_t* status;
 };
 
-// A value as a float and what its rounding left.
-struct Split {
-  float hi, lo;
-};
-__device__ __forceinline__ Split two_sum(float a, float b) {
-  const float s = __fadd_rn(a, b), v = __fsub_rn(s, a);
-  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, v)), __fsub_rn(b, v))};
-}
-__device__ __forceinline__ Split product(float a, float b_hi, float b_lo) {
-  const float p = __fmul_rn(a, b_hi);
-  return {p, __fmaf_rn(a, b_lo, __fmaf_rn(a, b_hi, -p))};
-}
-__device__ __forceinline__ Split add(Split a, Split b) {
-  const Split s = two_sum(a.hi, b.hi);
-  const float lo = __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)), hi = __fadd_rn(s.hi, lo);
-  return {hi, __fsub_rn(lo, __fsub_rn(hi, s.hi))};
-}
 __device__ __forceinline__ Split times(Split a, Split b) {
   const float p = __fmul_rn(a.hi, b.hi);
   return {p, __fmaf_rn(a.hi, b.lo, __fmaf_rn(a.lo, b.hi, __fmaf_rn(a.hi, b.hi, -p)))};
-}
-__device__ __forceinline__ Split warp_add(Split v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    v = add(v, Split{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
-  return v;
 }
 constexpr float kLn2 = 0.693147182f, kLn2Lo = -1.90465421e-9f;
 // 2^(a - b) within 2^-27 of it, whatever the size of a and b: float64 would do it on 1/64 of the lanes. With
@@ -674,8 +689,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
 #pragma unroll 1
           for (int g = 0; g < kGroups; ++g) after(g);
         } else if (plain_exponent(rate, sum.M)) {
-          const Weigher<true> w(rate, sum.M);
-          write_weights(part, held, own, p.windows, w, f.rest * w.scale, grad, wide, loose_at, loose, after);
+          write_weights(part, held, own, p.windows, Weigher<true>(rate, sum.M), f.rest, grad, wide, loose_at, loose, after);
         } else {
           write_weights(part, held, own, p.windows, Weigher<false>(rate, sum.M), f.rest, grad, wide, loose_at, loose, after);
         }
@@ -832,7 +846,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
     cluster_arrive();
     gather(min(r_next, p.N - 1), early);  // (past the last row: no ids)
     cluster_wait();
-    const RowSum sum = combine<kRest>(all[turn], C, rate);
+    const RowSum sum = combine<kRest, true>(all[turn], C, rate);
     const Factors f = factors<kRest>(teachers[turn], C, sum, p.weight ? __ldg(p.weight + r) : 1.f, p.per_tau);
     const RowPart<T> part = part_of(r);
     const Listed* list = list_of(turn, warp);
@@ -861,15 +875,18 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
         infinite |= of.e_x.hi == -INFINITY;
         x = add(x, of.e_x);
       }
-      // sum of e (log2 e - log2 of the drafter's weight), then ln 2 of it; the rate as the weights have it
-      a = add(a, negative(times(add(x, negative(times(share, Split{sum.M, 0.f}))), Split{rate.rate, 0.f})));
+      // sum of e (log2 e - log2 of the drafter's weight), then ln 2 of it; rate and origin as the weights have them
+      const bool plain = plain_exponent(rate, sum.M);
+      const Split from = times(share, Split{plain ? origin(rate, sum.M) : sum.M, 0.f});
+      const Split k{rate.rate, 0.f};
+      a = add(a, negative(plain ? add(times(x, k), negative(from)) : times(add(x, negative(from)), k)));
       a = times(a, Split{kLn2, kLn2Lo});
-      const Split z = two_sum(sum.z, sum.listed), ln_z = ln_of(z);
+      const Split z_rest{sum.z, sum.z_lo}, ln_z = ln_of(add(z_rest, Split{sum.listed, sum.listed_lo}));
       Split loss{0.f, 0.f};
       if (kRest) {
         const Split left = add(Split{1.f, 0.f}, negative(share));
         loss = add(a, times(share, ln_z));
-        if (f.some) loss = add(loss, times(left, add(add(ln_of(left), negative(ln_of(Split{sum.z, 0.f}))), ln_z)));
+        if (f.some) loss = add(loss, times(left, add(add(ln_of(left), negative(ln_of(z_rest))), ln_z)));
       } else if (share.hi > 0.f) {
         loss = add(add(quotient(a, share), ln_z), negative(ln_of(share)));
       }
@@ -891,13 +908,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
               if (list_of(turn, w)[i].id == list[k].id) e += list_of(turn, w)[i].e;
         }
         const float x = list[k].x;
-        float y;
-        if (plain) {
-          const Weigher<true> w(rate, sum.M);
-          y = w(x) * w.scale;
-        } else {
-          y = Weigher<false>(rate, sum.M)(x);
-        }
+        const float y = plain ? Weigher<true>(rate, sum.M)(x) : Weigher<false>(rate, sum.M)(x);
         store_elem(grad + list[k].id, __fmaf_rn(-f.teacher, e, y * f.listed));
       }
       named_sync<kListSync, kListThreads>();
