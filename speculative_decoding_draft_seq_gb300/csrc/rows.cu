@@ -555,13 +555,17 @@ __device__ __forceinline__ Split exp2_difference(Split a, Split b, Split& differ
   const float lo = __fadd_rn(__fadd_rn(t.lo, v.lo), __fadd_rn(w.lo, __fadd_rn(u_lo, 0.5f * s_lo)));
   return {ldexpf(__fadd_rn(t.hi, lo), (int)n), ldexpf(__fsub_rn(lo, __fsub_rn(__fadd_rn(t.hi, lo), t.hi)), (int)n)};
 }
-// ln v, v > 0: within 2^-24 whatever its size, since only the logarithm of v's fraction is rounded to float32
+// ln v, v > 0, within 2^-27 whatever its size: the logarithm of v's fraction to float32, and what its power leaves of the
+// fraction
 __device__ __forceinline__ Split ln_of(Split v) {
   int e;
   float m = frexpf(v.hi, &e);  // [1/2, 1)
   if (m < 0.70710678f) m *= 2.f, --e;
-  const Split whole = product((float)e, kLn2, kLn2Lo);
-  return add(whole, two_sum(logf(m), __fdiv_rn(v.lo, v.hi)));
+  const float y = logf(m);
+  Split unused;
+  const Split q = times(exp2_difference(Split{0.f, 0.f}, product(y, 1.44269502e+00f, 1.92596299e-08f), unused), Split{m, 0.f});  // m e^-y
+  const float left = __fadd_rn(add(q, Split{-1.f, 0.f}).hi, __fdiv_rn(v.lo, v.hi));
+  return add(product((float)e, kLn2, kLn2Lo), two_sum(y, left));
 }
 __device__ __forceinline__ Split negative(Split v) { return {-v.hi, -v.lo}; }
 __device__ __forceinline__ Split quotient(Split a, Split b) {
