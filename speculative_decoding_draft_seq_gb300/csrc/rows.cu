@@ -95,6 +95,9 @@ struct RowPart {
     local = (block >> shift) * kRowThreads + g % kRowThreads;
     return block & ((1 << shift) - 1);
   }
+  // the word of the map that holds the marks of a piece with this local number, and the piece's byte in it
+  static __device__ __forceinline__ int mark_word(int local) { return local / kRowThreads / kGroup * kRowThreads + local % kRowThreads; }
+  static __device__ __forceinline__ int mark_byte(int local) { return local / kRowThreads % kGroup; }
   // starts the copies of group g of this thread's pieces i0 .. i0 + m - 1
   __device__ __forceinline__ void fetch_group(uint4* held, int i0, int m, int g) const {
     const T* from = row + a0 + (size_t)piece(i0) * E;
@@ -211,10 +214,10 @@ __device__ __forceinline__ float rescale(const Rate& r, float x, float M) {
 struct ThreadSum {
   float m = -INFINITY, z = 0.f, listed = 0.f;
 };
-// Adds kGroup pieces and a loose element (-inf: none). bits(i): the marked entries of piece i, bits(-1): whether the
-// loose one is.
-template <class T, bool kMarks, bool kPlain, class Bits>
-__device__ __forceinline__ void add_weights(ThreadSum& s, const uint4 (&q)[kGroup], float loose, const Rate& r, Bits bits) {
+// Adds kGroup pieces and a loose element (-inf: none). marks: the marked entries of each piece, a byte each;
+// loose_mark: whether the loose one is.
+template <class T, bool kMarks, bool kPlain>
+__device__ __forceinline__ void add_weights(ThreadSum& s, const uint4 (&q)[kGroup], float loose, const Rate& r, uint32_t marks, bool loose_mark) {
   constexpr int W = 8 / sizeof(T);
   const Weigher<kPlain> w(r, s.m);
   unsigned long long a = 0, b = 0;
@@ -226,7 +229,7 @@ __device__ __forceinline__ void add_weights(ThreadSum& s, const uint4 (&q)[kGrou
 #pragma unroll
     for (int e = 0; e < W; ++e) x[e] = w.both(x[e]);
     if (kMarks) {
-      const uint32_t marked = bits(i);
+      const uint32_t marked = marks >> (8 * i) & 255u;
       if (marked) {
 #pragma unroll
         for (int e = 0; e < W; ++e) {
@@ -249,14 +252,15 @@ __device__ __forceinline__ void add_weights(ThreadSum& s, const uint4 (&q)[kGrou
   f32x2_unpack(b, b0, b1);
   if (loose != -INFINITY) {
     const float y = w(loose);
-    if (kMarks && bits(-1)) l += y;
+    if (kMarks && loose_mark) l += y;
     else a0 += y;
   }
   s.z += (a0 + a1) + (b0 + b1);
   if (kMarks) s.listed += l;
 }
-template <class T, bool kMarks, class Bits>
-__device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, Bits bits) {
+template <class T, bool kMarks>
+__device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, uint32_t marks, bool loose_mark) {
+  static_assert(kGroup == 4, "a byte a piece");
   uint4 q[kGroup];
 #pragma unroll
   for (int i = 0; i < kGroup; ++i) q[i] = i < m ? mine[i * kRowThreads] : empty_piece<T>();
@@ -270,19 +274,20 @@ __device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m
     }
     s.m = top;
   }
-  if (plain_exponent(r, top)) add_weights<T, kMarks, true>(s, q, loose, r, bits);
-  else add_weights<T, kMarks, false>(s, q, loose, r, bits);
+  if (plain_exponent(r, top)) add_weights<T, kMarks, true>(s, q, loose, r, marks, loose_mark);
+  else add_weights<T, kMarks, false>(s, q, loose, r, marks, loose_mark);
 }
-// A window's pieces, a group as soon as it has arrived; after(g) may start another group's copies over group g's
-// (kRefill).
-template <class T, bool kMarks, bool kRefill, int g, class Bits, class After>
-__device__ __forceinline__ void add_groups(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, Bits bits, After after) {
+// A window's pieces, a group as soon as it has arrived; marks(g): the marked entries of group g; after(g) may start another
+// group's copies over group g's (kRefill).
+template <class T, bool kMarks, bool kRefill, int g, class Marks, class After>
+__device__ __forceinline__ void add_groups(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, Marks marks, bool loose_mark,
+                                           After after) {
   copies_done<kRefill ? kGroups - 1 : kGroups - 1 - g>();
   if (g == 0 || m > g * kGroup)
-    add_group<T, kMarks>(s, mine + g * kGroup * kRowThreads, m - g * kGroup, g == 0 ? loose : -INFINITY, r,
-                         [&](int i) { return bits(i < 0 ? i : i + g * kGroup); });
+    add_group<T, kMarks>(s, mine + g * kGroup * kRowThreads, m - g * kGroup, g == 0 ? loose : -INFINITY, r, kMarks ? marks(g) : 0u,
+                         loose_mark);
   after(g);
-  if constexpr (g + 1 < kGroups) add_groups<T, kMarks, kRefill, g + 1>(s, mine, m, loose, r, bits, after);
+  if constexpr (g + 1 < kGroups) add_groups<T, kMarks, kRefill, g + 1>(s, mine, m, loose, r, marks, loose_mark, after);
 }
 
 // A value as a float and what its rounding left.
@@ -440,7 +445,7 @@ __device__ __forceinline__ void write_one(const RowPart<T>& part, int own, int t
 template <class T, class To>
 __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsParams p) {
   constexpr int E = 16 / sizeof(T), W = E / 2;
-  extern __shared__ __align__(16) uint4 held[];
+  extern __shared__ __align__(128) uint4 held[];  // (copies to unaligned lines take a tenth longer)
   __shared__ float4 all[kMaxCluster * kRowWarps];
   __shared__ uint32_t first[kMaxCluster * kRowWarps];
   const int rank = (int)cluster_rank(), C = p.C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -459,13 +464,12 @@ __global__ void __launch_bounds__(kRowThreads, 3) probabilities_kernel(ProbsPara
   const int loose_at = part.own_loose(p.V);
   const float loose = loose_at >= 0 ? row_elem(part.row + loose_at) : -INFINITY;
   const int windows = max(1, (part.steps() + kPieces - 1) / kPieces);
-  const auto unmarked = [](int) { return 0u; };
 
   ThreadSum s;
   for (int c = 0; c < windows; ++c) {
     const int m = min(own - c * kPieces, kPieces);
     if (c > 0) part.fetch(held, c * kPieces, m);
-    add_groups<T, false, false, 0>(s, held + threadIdx.x, m, c == 0 ? loose : -INFINITY, rate, unmarked, [](int) {});
+    add_groups<T, false, false, 0>(s, held + threadIdx.x, m, c == 0 ? loose : -INFINITY, rate, [](int) { return 0u; }, false, [](int) {});
   }
   cluster_wait();
   send<false>(s, all, C, rank, rate);
@@ -626,7 +630,7 @@ __device__ __forceinline__ Factors factors(const ListSums* of, int C, const RowS
 // meet once a row, at the cluster's exchange (with a rest also where the marks have to be ready).
 template <class T, bool kRest, bool kGrad>
 __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillParams p) {
-  extern __shared__ __align__(16) uint4 held[];
+  extern __shared__ __align__(128) uint4 held[];  // (copies to unaligned lines take a tenth longer)
   // two sets each: a CTA may write the next row's while another still reads this one's
   __shared__ float4 all[2][kMaxCluster * kRowWarps];
   __shared__ ListSums teachers[2][kMaxCluster];
@@ -661,21 +665,21 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
       const auto refill = [&](int g) { follow.fetch_group(held, 0, own_next, g); };
       if (kRest) named_sync<kMarksReady, kDistillThreads>();
       ThreadSum s;
-      const auto bits = [&](int i0, int i) -> uint32_t {
-        if (i < 0) return loose_marks >> tid & 1u;
-        const int local = (i0 + i) * kRowThreads + tid;
-        return local < p.marks ? s_marks[local >> 2] >> ((local & 3) * 8) & 255u : 0u;
-      };
+      const bool loose_mark = kRest && loose_at >= 0 && (loose_marks >> tid & 1u);
       if (p.windows == 1) {
-        const auto mark = [&](int i) { return bits(0, i); };
-        if constexpr (kGrad) add_groups<T, kRest, false, 0>(s, held + tid, own, loose, rate, mark, [](int) {});
-        else add_groups<T, kRest, true, 0>(s, held + tid, own, loose, rate, mark, refill);
+        const auto marks = [&](int g) { return g * kRowThreads + tid < p.marks / 4 ? s_marks[g * kRowThreads + tid] : 0u; };
+        if constexpr (kGrad) add_groups<T, kRest, false, 0>(s, held + tid, own, loose, rate, marks, loose_mark, [](int) {});
+        else add_groups<T, kRest, true, 0>(s, held + tid, own, loose, rate, marks, loose_mark, refill);
       } else {
         for (int c = 0; c < p.windows; ++c) {
           const int m = min(own - c * kPieces, kPieces);
           part.fetch(held, c * kPieces, m);
-          add_groups<T, kRest, false, 0>(s, held + tid, m, c == 0 ? loose : -INFINITY, rate, [&](int i) { return bits(c * kPieces, i); },
-                                         [](int) {});
+          add_groups<T, kRest, false, 0>(s, held + tid, m, c == 0 ? loose : -INFINITY, rate,
+                                         [&](int g) {
+                                           const int word = (c * kGroups + g) * kRowThreads + tid;
+                                           return word < p.marks / 4 ? s_marks[word] : 0u;
+                                         },
+                                         loose_mark, [](int) {});
         }
       }
       send<kRest>(s, all[turn], C, rank, rate);
@@ -781,8 +785,8 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
       if (kRest) {
         int local, at;
         part.owner(id, local, at);
-        uint32_t* word = local < 0 ? &loose_marks : s_marks + (local >> 2);
-        const uint32_t bit = local < 0 ? 1u << (-1 - local) : 1u << ((local & 3) * 8 + at);
+        uint32_t* word = local < 0 ? &loose_marks : s_marks + part.mark_word(local);
+        const uint32_t bit = local < 0 ? 1u << (-1 - local) : 1u << (part.mark_byte(local) * 8 + at);
         if (atomicOr(word, bit) & bit) twice[turn] = 1;
       } else {  // nobody else needs the map
         int same = 0;
@@ -860,7 +864,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
       for (int k = lane; k < now.n; k += 32) {
         int local, at;
         part.owner(list[k].id, local, at);
-        if (local >= 0) s_marks[local >> 2] = 0;
+        if (local >= 0) s_marks[part.mark_word(local)] = 0;
       }
       if (j0 == 0) loose_marks = 0;
       named_sync<kListSync, kListThreads>();
@@ -949,7 +953,7 @@ static cudaError_t launch_probs(const ProbsParams& p, int N, int held, cudaStrea
 }
 
 // the pieces, two rows' listed entries, and a byte for each piece of a row of 2^20 float32
-constexpr int kDistillSmem = kPieces * kRowThreads * 16 + kMaxTop * 2 * (int)sizeof(Listed) + (1 << 20) / 4 / kMaxCluster + kRowThreads;
+constexpr int kDistillSmem = kPieces * kRowThreads * 16 + kMaxTop * 2 * (int)sizeof(Listed) + (1 << 20) / 4 / kMaxCluster + kGroup * kRowThreads;
 
 // Rows are taken in equal turns by as many clusters as the GPU holds at once (more would begin when those end).
 template <class T, bool kRest, bool kGrad>
@@ -1020,10 +1024,11 @@ extern "C" dspark_status dspark_distill(int32_t N, int32_t V, int32_t K, int32_t
   int held;
   const int elem = dtype == DSPARK_BF16 ? 2 : 4;
   const int C = row_cluster(N, V, elem, sms, held);
-  // one byte a piece of this CTA, whole steps of the block (for the entries that are left out of the rest)
-  const int marks = !teacher_lse ? 0 : ceil_div((long long)V * elem / 16, (long long)C * kRowThreads) * kRowThreads;
+  // with a rest, the map of listed entries: a byte for each piece of this CTA, a word for a group of a thread's
+  const int steps = ceil_div((long long)V * elem / 16, (long long)C * kRowThreads);
+  const int marks = teacher_lse ? ceil_div(steps, kGroup) * kRowThreads * 4 : 0;
   const double k = 1.44269504088896340736 / (double)temperature;
-  const int windows = std::max(1, ceil_div(ceil_div((long long)V * elem / 16, (long long)C * kRowThreads), kPieces));
+  const int windows = std::max(1, ceil_div(steps, kPieces));
   const DistillParams p{N, V, K, C, windows, held, marks, logits, ids, teacher, teacher_lse, weight, (float)(1.0 / (double)temperature),
                         (float)k, (float)(k - (double)(float)k), loss, grad, static_cast<uint32_t*>(workspace)};
   cudaStream_t s = (cudaStream_t)stream;
