@@ -11,9 +11,18 @@
 // floor(min(w, 1) 2^40) and Z their sum: integer sums do not depend on an order.
 //
 // A cluster of CTAs takes a request. Every CTA walks the request's chain itself (a
-// warp, a lane a draft; three dependent loads), then sums a contiguous share of the one row
+// warp, a lane a draft; two dependent loads), then sums a contiguous share of the one row
 // that matters, warp by warp; the warps' sums go to all CTAs, and the warp whose
-// share holds the token reads that share once more to find it.
+// share holds the token reads a part of that share once more to find it. The rows come through
+// a ring of asynchronous copies a warp: they keep the loads going while a step is added up, and
+// let rows of any alignment be copied in whole pieces and put together in shared memory (with loads to registers an
+// odd row length took twice the time of an even one).
+//
+// Bound by bytes where requests fill the GPU, by its chain of dependent steps (row numbers, draft, probability,
+// row, exchange, token) where they do not. 128 requests over 129,280 float32 entries, up to 16 drafts: 28 to 31 us, 110
+// MB (0.55 of the measured copy bandwidth), odd row length 31, bf16 20; without rows of the drafter's 20; one request 8.5,
+// over 32,000 entries 6. CTAs a request: 8, 4, 2, 1 as the SMs hold them (16 requests: 9.6 us with 8,
+// 12.7 with 4; 512 over 32,000: 24 with 1, 31 with 2).
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -116,9 +125,10 @@ constexpr int kStretches = 4;  // parts of a warp's share whose masses its lanes
 
 constexpr int kLane = 2;       // pieces of a row that a lane takes in a step
 constexpr int kAhead = 2;      // steps of a warp that are on their way to shared memory
-// a step's pieces: the target's, and the drafter's with the one after the last
-struct StepBuffer {
-  uint4 p[32 * kLane], q[32 * kLane + 1];
+// a step's pieces: the target's, and the drafter's with the one after the last (whole lines: copies to unaligned ones are
+// slower)
+struct __align__(128) StepBuffer {
+  uint4 p[32 * kLane], q[32 * kLane + 8];
 };
 constexpr int kVpSmem = kVpWarps * kAhead * (int)sizeof(StepBuffer);
 
@@ -197,7 +207,7 @@ __device__ __forceinline__ void share_masses(const DrawRow<T>& row, int V, int v
 template <class T>
 __global__ void __launch_bounds__(kVpThreads, 4) verify_probs_kernel(VerifyProbsParams p) {
   constexpr int E = 16 / sizeof(T);
-  extern __shared__ __align__(16) StepBuffer rings[];
+  extern __shared__ __align__(128) StepBuffer rings[];
   __shared__ unsigned long long sums[2][kVpMaxCluster * kVpWarps];  // one set a pass
   __shared__ int s_start, s_n, s_accepted, s_token;
   const int rank = (int)cluster_rank(), C = p.C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

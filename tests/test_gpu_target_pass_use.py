@@ -159,6 +159,36 @@ def test_captured_and_replayed():
     assert dspark.device_status(ws) == dspark.OK and dspark.device_status(wsp) == dspark.OK
 
 
+def test_first_call_of_its_kind_captured():
+    """Nothing a call looks up or sets on its first use is forbidden in a capture."""
+    x, ids, t, _, _ = problem(6, 5, 70001, 13, torch.float32, 1.0)
+    loss, grad, ws = torch.zeros(5, device=DEV), torch.zeros_like(x), ws_small()
+    d_ids, d_t = i32(ids), on(t, torch.float32)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        dspark.distill(x, d_ids, d_t, 1.0, loss, ws, grad=grad)
+    graph.replay()
+    torch.cuda.synchronize()
+    want = run_distill(x, ids, t, 1.0)
+    assert np.array_equal(host(loss), want[0]) and np.array_equal(host(grad), want[1])
+
+
+@pytest.mark.parametrize("V", [1003, 300001])
+def test_probabilities_in_place(V):
+    g = torch.Generator(device=DEV).manual_seed(V)
+    x = torch.randn((4, V), generator=g, device=DEV)
+    T, ws, p = on(np.array([1.0, 0.0, 0.5, math.inf], dtype=np.float32), torch.float32), ws_small(), torch.empty((4, V), device=DEV)
+    dspark.probabilities(x, T, p, ws)
+    dspark.probabilities(x, T, x, ws)
+    assert torch.equal(x, p)
+
+
+def test_page_fork_of_a_row_longer_than_its_table():
+    table, got, ws = i32([[4, 2], [3, 1]]), [blank(2, 2)] + [blank(2) for _ in range(4)] + [blank(1)], dspark.new_page_workspace(10)
+    dspark.page_fork(table, i32([9, 4]), i32([0, 1]), None, 4, 10, i32([0]), *got, ws)
+    assert dspark.device_status(ws) == dspark.ERR_RANGE and got[0].tolist() == [[4, 2], [3, -1]] and got[1].tolist() == [8, 4]
+
+
 def test_two_streams_with_a_workspace_each():
     x, ids, t, lse, _ = problem(3, 300, 2000, 16, torch.float32, 1.0)
     b = block(4, 30, 4, 2000, torch.float32)
