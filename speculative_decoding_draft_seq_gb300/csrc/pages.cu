@@ -11,8 +11,8 @@
 //
 // Bound by the chain of phases: collecting the holders of 128 rows of up to 64 pages takes 7 us in one cluster (1.9 of them the
 // launch and its barriers) and 9 as four launches; 256 rows of 128 pages 9.4 either way; 8,192 rows of 128 pages (2.6 MB)
-// 15 us over the GPU and 105 in one cluster. page_copy_kernel is bound by bytes: 1,400 pages of 32 KB, four times (keys
-// and values of two layers), in 54 us (367 MB, 6.8 TB/s: some of it from L2); 4 units a thread in flight instead of 8: 64.
+// 15 us over the GPU and 105 in one cluster. page_copy_kernel is bound by bytes: 1,180 pages of 32 KB, four times (keys
+// and values of two layers, 308 MB read and written), in 54 us (5.7 TB/s); 4 units a thread in flight instead of 8: 64.
 #include <algorithm>
 
 #include "cluster.cuh"

@@ -19,8 +19,8 @@
 // odd row length took twice the time of an even one).
 //
 // Bound by bytes where requests fill the GPU, by its chain of dependent steps (row numbers, draft, probability,
-// row, exchange, token) where they do not. 128 requests over 129,280 float32 entries, up to 16 drafts: 28 to 31 us, 110
-// MB (0.55 of the measured copy bandwidth), odd row length 31, bf16 20; without rows of the drafter's 20; one request 8.5,
+// row, exchange, token) where they do not. 128 requests over 129,280 float32 entries, up to 16 drafts: 28 us, 117
+// MB (0.62 of the measured copy bandwidth), odd row length 31, bf16 20; without rows of the drafter's 20; one request 8.5,
 // over 32,000 entries 6. CTAs a request: 8, 4, 2, 1 as the SMs hold them (16 requests: 9.6 us with 8,
 // 12.7 with 4; 512 over 32,000: 24 with 1, 31 with 2).
 #include <algorithm>
