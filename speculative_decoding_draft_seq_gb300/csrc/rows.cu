@@ -746,10 +746,14 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
       }
     }
   };
+  const auto is_mine = [&](const RowPart<T>& part, int id) {
+    int local, at;
+    return id >= 0 && id < p.V && part.owner(id, local, at) == rank;
+  };
   const auto gather = [&](int r, Early& e) {
+    const RowPart<T> part = part_of(r);
 #pragma unroll
-    for (int i = 0; i < kEarly / 32; ++i)
-      e.x[i] = e.id[i] >= 0 && e.id[i] < p.V ? row_elem(logits + (size_t)r * p.V + e.id[i]) : -INFINITY;
+    for (int i = 0; i < kEarly / 32; ++i) e.x[i] = is_mine(part, e.id[i]) ? row_elem(part.row + e.id[i]) : -INFINITY;
   };
   const auto prepare = [&](int r, int turn, const Early& early) {
     Listed* list = list_of(turn, warp);
@@ -758,8 +762,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
     int n = 0;
     const auto keep = [&](int id, float t, float x) {
       if (id >= p.V) set_status(p.status, DSPARK_ERR_RANGE);
-      int local, at;
-      const bool valid = id >= 0 && id < p.V, mine = valid && part.owner(id, local, at) == rank;
+      const bool valid = id >= 0 && id < p.V, mine = is_mine(part, id);
       if (valid) t_max = nan_max(t_max, t);
       const uint32_t b = __ballot_sync(0xffffffffu, mine);
       if (mine) list[n + __popc(b & ((1u << lane) - 1u))] = Listed{t, x, id};
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
         t[i] = j < last ? __ldg(p.teacher + (size_t)r * p.K + j) : -INFINITY;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = id[i] >= 0 && id[i] < p.V ? row_elem(part.row + id[i]) : -INFINITY;
+      for (int i = 0; i < 4; ++i) x[i] = is_mine(part, id[i]) ? row_elem(part.row + id[i]) : -INFINITY;
 #pragma unroll
       for (int i = 0; i < 4; ++i) keep(id[i], t[i], x[i]);
     }
