@@ -543,6 +543,9 @@ dspark_status dspark_verify_probs(int32_t R, int32_t gamma, int32_t V, int32_t T
  * [0, max_pages * page_size] (clamped), sets DSPARK_ERR_RANGE; such an entry is
  * nobody's page and is carried along as it is.
  *
+ * Larger tables run as one cooperative launch whose CTAs wait for each other, each wait with a limit: DSPARK_ERR_TIMEOUT if
+ * one runs out (clear the workspace before its next use then).
+ *
  * dspark_page_collect: the holders of each page, and the free pages.
  *   block_table [R, max_pages] int32, kv_len [R] int32
  *   refs        [n_pages] int32 out   entries that hold the page

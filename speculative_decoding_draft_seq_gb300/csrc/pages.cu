@@ -4,15 +4,16 @@
 //
 // The block table is the only record of who holds a page: counts and lists are formed from
 // it anew, so that nothing can drift from it. Each call is a few phases over the table's entries and over the
-// pages, every phase done by all CTAs before the next begins: as the phases of one
-// cluster of CTAs (a barrier between two costs less than a launch), or, where there is more to read than one
-// cluster reads in the time of the launches, as a launch each over the whole GPU. Both run the same code with
-// another number of CTAs. Integers only, and every list in ascending order: results do not depend on which.
+// pages, every phase done by all CTAs before the next begins: in one cluster of CTAs, which meet at the
+// hardware's barrier, or, where there is more to read than one cluster reads in the time that saves, in a cooperative launch
+// over the GPU, whose CTAs meet at a counter. Both run the same code with another number of CTAs. Integers
+// only, and every list in ascending order: results do not depend on which.
 //
 // Bound by the chain of phases: collecting the holders of 128 rows of up to 64 pages takes 7 us in one cluster (1.9 of them the
-// launch and its barriers) and 9 as four launches; 256 rows of 128 pages 9.4 either way; 8,192 rows of 128 pages (2.6 MB)
-// 15 us over the GPU and 105 in one cluster. page_copy_kernel is bound by bytes: 1,180 pages of 32 KB, four times (keys
-// and values of two layers, 308 MB read and written), in 54 us (5.7 TB/s); 4 units a thread in flight instead of 8: 64.
+// launch and its barriers) and 8.4 over the GPU; 256 rows of 128 pages 9.6 either way, 1,024 19 and 9.6, 8,192 (5.8 MB)
+// 104 and 17. (A launch for each phase: 15 for the last, but 20 with the host's four launches.) page_copy_kernel is bound by
+// bytes: 1,180 pages of 32 KB, four times (keys and values of two layers, 308 MB read and written), in 54 us (5.7 TB/s); 4
+// units a thread in flight instead of 8: 64.
 #include <algorithm>
 
 #include "cluster.cuh"
@@ -24,7 +25,8 @@ namespace dspark {
 constexpr int kPgThreads = 1024;
 constexpr int kPgWarps = kPgThreads / 32;
 constexpr int kPgCluster = 8;
-constexpr int kPgGrid = 152;
+constexpr int kPgGrid = 128;      // a power of two, at most the SMs
+constexpr int kPgMeetWord = 40;   // of the status block: the CTAs' meetings so far
 
 // Workspace: status block, counts a CTA, and two words a page.
 constexpr size_t kPgCounts = 256;
@@ -394,14 +396,38 @@ __global__ void __launch_bounds__(kPgThreads) pages_cluster_kernel(PageParams p)
     __syncwarp();
   }
 }
-struct PhaseParams {
-  PageParams p;
-  int phase;
-};
+// All phases over the GPU: the CTAs of a cooperative launch (all resident) meet between two. The word counts on from call
+// to call: its number of CTAs divides 2^32, so a meeting is over when it reaches the next multiple. Bounded: a wait that runs
+// out records DSPARK_ERR_TIMEOUT, and its CTA returns (the workspace has to be cleared then).
+constexpr uint32_t kMeetLimit = 1u << 20;  // about 1 s of polls
+__device__ __forceinline__ bool meet(uint32_t* word, uint32_t* status, int* ok) {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    const uint32_t goal = (atomicAdd(word, 1u) / kPgGrid + 1u) * kPgGrid;
+    int there = 0;
+    for (uint32_t i = 0; i < kMeetLimit && !there; ++i) {
+      uint32_t v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(word) : "memory");
+      there = (int32_t)(v - goal) >= 0;
+      if (!there && i > 64) __nanosleep(32);
+    }
+    if (!there) set_status(status, DSPARK_ERR_TIMEOUT);
+    *ok = there;
+  }
+  __syncthreads();
+  return *ok != 0;
+}
 template <int kOp>
-__global__ void __launch_bounds__(kPgThreads) pages_phase_kernel(PhaseParams p) {
+__global__ void __launch_bounds__(kPgThreads) pages_grid_kernel(PageParams p) {
   __shared__ int sh[32];
-  run_phase<kOp>(p.p, Team{(int)blockIdx.x, (int)gridDim.x}, p.phase, sh);
+  __shared__ int ok;
+  const Team t{(int)blockIdx.x, kPgGrid};
+#pragma unroll
+  for (int phase = 0; phase < phases_of(kOp); ++phase) {
+    if (phase > 0 && !meet(p.status + kPgMeetWord, p.status, &ok)) return;
+    run_phase<kOp>(p, t, phase, sh);
+  }
 }
 
 template <int kOp>
@@ -412,10 +438,10 @@ static dspark_status launch_pages(const PageParams& p, cudaStream_t s) {
     e = launch_clusters(pages_cluster_kernel<kOp>, p, kPgCluster, kPgCluster, kPgThreads, 0, s);
     note_launches(1);
   } else {
-    for (int phase = 0; phase < phases_of(kOp); ++phase)
-      pages_phase_kernel<kOp><<<kPgGrid, kPgThreads, 0, s>>>(PhaseParams{p, phase});
-    e = cudaGetLastError();
-    note_launches(phases_of(kOp));
+    PageParams q = p;
+    void* args[] = {&q};
+    e = cudaLaunchCooperativeKernel((const void*)pages_grid_kernel<kOp>, dim3(kPgGrid), dim3(kPgThreads), args, 0, s);
+    note_launches(1);
   }
   return e == cudaSuccess ? DSPARK_OK : DSPARK_ERR_CUDA;
 }

@@ -235,6 +235,50 @@ def test_a_workspace_may_be_shared_by_later_calls_of_other_sizes():
     assert dspark.device_status(ws) == dspark.ERR_NONFINITE
 
 
+def test_large_page_calls_in_turn_on_one_workspace():
+    """Calls over the whole GPU, whose CTAs meet at a word of the workspace: one after the other, in a graph, between calls
+    of one cluster."""
+    rng = np.random.default_rng(12)
+    R, width, page, n_pages = 3000, 30, 16, 60000
+    table, kv_len, spare = table_of(rng, R, width, page, n_pages, 3)
+    parent, free = rng.integers(-1, R, R), spare
+    ws, small = dspark.new_page_workspace(n_pages), table_of(rng, 4, 3, 16, 50)
+    d = [i32(table), i32(kv_len), i32(parent), i32(free)]
+    refs, list_, n = blank(n_pages), blank(n_pages), blank(1)
+    new, new_len, pair, count, used = blank(R, width), blank(R), [blank(R), blank(R)], blank(R), blank(1)
+    moved, moves, live = blank(R, width), [blank(n_pages // 2), blank(n_pages // 2)], blank(1)
+
+    def step():
+        dspark.page_collect(d[0], d[1], page, refs, list_, n, ws)
+        dspark.page_fork(d[0], d[1], d[2], None, page, n_pages, d[3], new, new_len, *pair, count, used, ws)
+        dspark.page_compact(d[0], d[1], page, n_pages, moved, *moves, live, ws)
+
+    def check():
+        want = O.page_collect(table, kv_len, page, n_pages)
+        assert refs.tolist() == want[0] and list_.tolist() == want[1] and n.item() == want[2]
+        want = O.page_fork(table, kv_len, parent, None, page, n_pages, free)
+        assert new.tolist() == want["new_table"] and pair[0].tolist() == want["src"] and pair[1].tolist() == want["dst"]
+        want = O.page_compact(table, kv_len, page, n_pages)
+        assert moved.tolist() == want["new_table"] and moves[0].tolist() == want["src"] and live.item() == want["n_live"]
+        for t in (refs, list_, n, new, *pair, moved, *moves, live):
+            t.fill_(-9)
+
+    for _ in range(3):
+        step()
+        check()
+        small_refs, small_free = blank(50), blank(50)
+        dspark.page_collect(i32(small[0]), i32(small[1]), 16, small_refs, small_free, n, ws)
+        assert small_refs.tolist() == O.page_collect(small[0], small[1], 16, 50)[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        step()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        check()
+    assert dspark.device_status(ws) == dspark.OK
+
+
 def test_page_copy_past_2_32_elements():
     n_pages, page, H, D = 2 ** 17 + 3, 16, 16, 128  # 2^32 elements and more a cache
     k = torch.zeros((n_pages, page, H, D), dtype=torch.bfloat16, device=DEV)
