@@ -591,9 +591,10 @@ __device__ __forceinline__ Split quotient(Split a, Split b) {
 // and e x. As pairs of floats, since what the shares leave of 1, and differences of logarithms, may be small (a float64
 // instruction takes the SM 16 cycles a warp).
 enum { kNoList = 1, kBadList = 2 };  // (of the whole row) nothing listed has a share; a NaN or infinity among the teacher's numbers
+constexpr float kSmall = 0x1p-40f;
 struct __align__(16) ListSums {
   Split share, e_log_e;
-  Split e_x;
+  Split e_x;  // times kSmall: masked entries hold the type's lowest value, of which a sum would overflow
   int flags, unused;
 };
 // A listed entry as the gradient needs it.
@@ -824,7 +825,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
         a = add(a, e);
         b = add(b, times(e, y));
         const float x = list[k].x;
-        c = x == -INFINITY ? Split{-INFINITY, 0.f} : add(c, times(e, Split{x, 0.f}));
+        c = x == -INFINITY ? Split{-INFINITY, 0.f} : add(c, times(e, Split{x * kSmall, 0.f}));
       }
     }
     if (n > 0) {
@@ -898,19 +899,21 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
       }
       // sum of e (log2 e - log2 of the drafter's weight), then ln 2 of it; rate and origin as the weights have them
       const bool plain = plain_exponent(rate, sum.M);
-      const Split from = times(share, Split{plain ? origin(rate, sum.M) : sum.M, 0.f});
+      const Split from = times(share, Split{(plain ? origin(rate, sum.M) : sum.M) * kSmall, 0.f});
       const Split k{rate.rate, 0.f};
-      a = add(a, negative(plain ? add(times(x, k), negative(from)) : times(add(x, negative(from)), k)));
-      a = times(a, Split{kLn2, kLn2Lo});
+      const Split below = plain ? add(times(x, k), negative(from)) : times(add(x, negative(from)), k);
+      const auto small = [](Split v) { return Split{v.hi * kSmall, v.lo * kSmall}; };
+      a = times(add(small(a), negative(below)), Split{kLn2, kLn2Lo});
       const Split z_rest{sum.z, sum.z_lo}, ln_z = ln_of(add(z_rest, Split{sum.listed, sum.listed_lo}));
-      Split loss{0.f, 0.f};
+      Split loss{0.f, 0.f};  // times kSmall
       if (kRest) {
         const Split left = add(Split{1.f, 0.f}, negative(share));
-        loss = add(a, times(share, ln_z));
-        if (f.some) loss = add(loss, times(left, add(add(ln_of(left), negative(ln_of(z_rest))), ln_z)));
+        loss = add(a, small(times(share, ln_z)));
+        if (f.some) loss = add(loss, small(times(left, add(add(ln_of(left), negative(ln_of(z_rest))), ln_z))));
       } else if (share.hi > 0.f) {
-        loss = add(add(quotient(a, share), ln_z), negative(ln_of(share)));
+        loss = add(quotient(a, share), small(add(ln_z, negative(ln_of(share)))));
       }
+      loss.hi /= kSmall;
       if (infinite) loss.hi = INFINITY;
       p.loss[r] = f.bad ? NAN : loss.hi;
       if (f.bad) set_status(p.status, DSPARK_ERR_NONFINITE);

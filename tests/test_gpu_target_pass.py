@@ -498,6 +498,32 @@ def test_distill_masked_and_extreme_rows():
     assert loss[5] == 0 and not grad[5].any() and status == dspark.OK
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("tau", [0.5, 1.0, 4.0])
+def test_distill_lists_masked_entries(dtype, rest, tau):
+    """The teacher lists entries that the drafter's truncated row holds at the type's lowest value: their distance times
+    their share, which may be past float32's range (then infinite), and the gradient of an entry without probability."""
+    V, low = 600, float(torch.finfo(dtype).min)
+    x = torch.full((4, V), low, dtype=dtype, device=DEV)
+    x[:, 5:9] = torch.tensor([1.0, 2.0, -1.0, 0.5], dtype=dtype, device=DEV)
+    ids = np.array([[5, 6, 100], [100, 101, 102], [5, 100, 101], [5, 6, 7]])
+    t = np.array([[1.0, 2.0, 0.0], [3.0, 3.0, 3.0], [0.0, -9.0, 2.0], [1.0, 1.0, 1.0]])
+    lse = np.log(np.exp(t / tau).sum(1) + 0.7)
+    loss, grad, status = run_distill(x, ids, t, tau, lse if rest else None)
+    assert status == dspark.OK
+    for r in range(4):
+        L, G, _ = O.distill(host(x)[r], ids[r], np.float32(t[r]), tau, np.float32(lse[r]) if rest else None)
+        # the shares are within 2^-24 of the sum's terms, the logarithms within 2^-22. The largest float32 is 2^128 (1 - 2^-24),
+        # infinity what rounds past it: within 2^-20 of 2^128 a value may come out as either
+        if L > 2.0 ** 128 * (1 + 2.0 ** -20):
+            assert loss[r] == math.inf
+        else:
+            near = L > 2.0 ** 128 * (1 - 2.0 ** -20) and loss[r] == math.inf
+            assert near or abs(loss[r] - L) <= 2.0 ** -21 * (1 + abs(L)), (r, loss[r], L)
+        assert np.abs(grad[r] - G).max() <= (HALF_STEP[dtype] + 2.0 ** -19) * (np.abs(G).max() + 2.0 ** -3)
+
+
 def test_distill_bad_rows():
     x, ids, t, lse, _ = problem(3, 6, 500, 4, torch.float32, 1.0)
     good = run_distill(x, ids, t, 1.0, lse)
