@@ -163,7 +163,9 @@ def distill(x, ids, teacher, tau, lse=None):
         shift, p_rest = float(lse), 1.0
     else:
         top = max(listed, default=-math.inf)
-        shift = top + math.log(sum(math.exp(a - top) for a in listed)) if top > -math.inf else None
+        if top > -math.inf:
+            t = t - top  # (of masked entries a sum's logarithm would vanish beside the largest)
+        shift = math.log(sum(math.exp(a - top) for a in listed)) if top > -math.inf else None
     for j in keep if shift is not None else []:
         q = math.exp(t[j] - shift)
         if q > 0:

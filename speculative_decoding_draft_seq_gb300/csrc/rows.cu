@@ -591,6 +591,8 @@ __device__ __forceinline__ Split quotient(Split a, Split b) {
 // and e x. As pairs of floats, since what the shares leave of 1, and differences of logarithms, may be small (a float64
 // instruction takes the SM 16 cycles a warp).
 enum { kNoList = 1, kBadList = 2 };  // (of the whole row) nothing listed has a share; a NaN or infinity among the teacher's numbers
+constexpr float kFar = 1e32f;  // teacher's logits count up to here, so that none times log2(e) / tau overflows (masked ones do not differ)
+__device__ __forceinline__ float clamped(float t) { return fminf(fmaxf(t, -kFar), kFar); }
 constexpr float kSmall = 0x1p-40f;
 struct __align__(16) ListSums {
   Split share, e_log_e;
@@ -810,8 +812,8 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
       }
     }
     if (kRest) named_arrive<kMarksReady, kDistillThreads>();
-    const float lse = kRest ? __ldg(p.teacher_lse + r) : t_max;
-    const bool bad = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < INFINITY));
+    const float lse = kRest ? __ldg(p.teacher_lse + r) : clamped(t_max);
+    const bool bad = !(t_max < INFINITY) || (kRest && !(fabsf(lse) < kFar));
     const bool none = t_max == -INFINITY || bad;
     // an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum
     const Split ref = kRest ? product(lse, 1.44269502e+00f, 1.92596299e-08f) : product(lse, p.k_hi, p.k_lo);
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
     for (int k = lane; k < n; k += 32) {
       const float t = list[k].e;
       Split e{0.f, 0.f}, y = e;
-      if (t != -INFINITY && !none) e = exp2_difference(product(t, p.k_hi, p.k_lo), ref, y);
+      if (t != -INFINITY && !none) e = exp2_difference(product(clamped(t), p.k_hi, p.k_lo), ref, y);
       list[k].e = e.hi;
       if (e.hi > 0.f) {
         a = add(a, e);

@@ -524,6 +524,21 @@ def test_distill_lists_masked_entries(dtype, rest, tau):
         assert np.abs(grad[r] - G).max() <= (HALF_STEP[dtype] + 2.0 ** -19) * (np.abs(G).max() + 2.0 ** -3)
 
 
+@pytest.mark.parametrize("tau", [0.5, 2.0])
+def test_distill_masked_teachers(tau):
+    """Teachers' lists that hold the type's lowest value: no share beside an ordinary entry, equal shares among themselves."""
+    x, ids, t, lse, _ = problem(2, 3, 200, 4, torch.float32, tau)
+    low = float(np.finfo(np.float32).min)
+    t[0, 1:], t[1], t[2, 3] = low, low, low
+    assert check_distill(x, ids, t, tau)[2] == dspark.OK
+    t[1, 0] = 1.0
+    lse = np.log(np.exp(t / tau).sum(1) + 0.5)
+    assert check_distill(x, ids, t, tau, lse)[2] == dspark.OK
+    lse[2] = -3e38
+    loss, grad, status = run_distill(x, ids, t, tau, lse)
+    assert status == dspark.ERR_NONFINITE and math.isnan(loss[2]) and not grad[2].any() and np.isfinite(loss[:2]).all()
+
+
 def test_distill_bad_rows():
     x, ids, t, lse, _ = problem(3, 6, 500, 4, torch.float32, 1.0)
     good = run_distill(x, ids, t, 1.0, lse)
