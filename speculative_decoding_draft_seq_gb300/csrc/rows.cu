@@ -818,6 +818,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
     // an entry's share before it is scaled: relative to the largest entry, or to the teacher's sum
     const Split ref = kRest ? product(lse, 1.44269502e+00f, 1.92596299e-08f) : product(lse, p.k_hi, p.k_lo);
     Split a{0.f, 0.f}, b = a, c = a;
+    bool infinite = false;  // a listed entry to which the drafter gives nothing (apart from the sum: -inf less -inf is NaN)
     for (int k = lane; k < n; k += 32) {
       const float t = list[k].e;
       Split e{0.f, 0.f}, y = e;
@@ -827,14 +828,14 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
         a = add(a, e);
         b = add(b, times(e, y));
         const float x = list[k].x;
-        c = x == -INFINITY ? Split{-INFINITY, 0.f} : add(c, times(e, Split{x * kSmall, 0.f}));
+        if (x == -INFINITY) infinite = true;
+        else c = add(c, times(e, Split{x * kSmall, 0.f}));
       }
     }
     if (n > 0) {
       a = warp_add(a);
       b = warp_add(b);
-      const bool infinite = __any_sync(0xffffffffu, c.hi == -INFINITY);  // a listed entry to which the drafter gives nothing
-      c = infinite ? Split{-INFINITY, 0.f} : warp_add(c);
+      c = __any_sync(0xffffffffu, infinite) ? Split{-INFINITY, 0.f} : warp_add(c);
     }
     if (lane == 0) sums[warp][0] = a, sums[warp][1] = b, sums[warp][2] = c;
     named_sync<kListSync, kListThreads>();
