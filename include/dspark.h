@@ -625,7 +625,7 @@ dspark_status dspark_page_copy(int32_t n, int32_t n_layers, int32_t n_pages, int
  *   teacher_lse given: the natural log of sum e^(t / tau) over the teacher's whole
  *                      vocabulary; p_j = e^(t_j / tau - lse), p_R = 1 - sum_j p_j (at least 0), s_R =
  *                      the sum of s over all entries that are not listed, and the loss has the term
- *                      p_R (ln p_R - ln s_R) too (0 if either is 0)
+ *                      p_R (ln p_R - ln s_R) too, however small s_R is (0 if p_R is 0, or s_R: all of them at -inf)
  *   grad[r, v] = weight[r] d loss_r / d x_v
  *   logits      [N, V] dtype (V <= 2^20)
  *   ids         [N, K] int32   1 <= K <= 1024; a negative id pads a shorter list; of an id that comes

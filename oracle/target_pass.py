@@ -147,7 +147,8 @@ def page_compact(table, kv_len, page, n_pages, pinned=()):
 # distillation
 
 def distill(x, ids, teacher, tau, lse=None):
-    """(loss, d loss / d x, parts) of one row; parts: s, p over the vocabulary, p_rest, s_rest, octaves below the maximum."""
+    """(loss, d loss / d x, parts) of one row; parts: s, p over the vocabulary, p_rest, s_rest, octaves below the maximum.
+    The rest's logarithm and its entries' shares in it are formed from its own maximum: s_rest may be far below float64's range."""
     x, t = np.asarray(x, dtype=np.float64), np.asarray(teacher, dtype=np.float64) / tau
     V = len(x)
     keep = [j for j, v in enumerate(ids) if 0 <= v < V]
@@ -173,12 +174,15 @@ def distill(x, ids, teacher, tau, lse=None):
         p[ids[j]] += q
     if lse is not None:
         p_rest, s_rest = max(0.0, 1.0 - p.sum()), s[~named].sum()
-        if p_rest > 0 and s_rest > 0:
-            loss += p_rest * (math.log(p_rest) - math.log(s_rest))
+        x_out = np.where(named, -np.inf, x)
+        top = x_out.max()
+        if p_rest > 0 and top > -math.inf:
+            out = np.exp((x_out - top) / tau)
+            loss += p_rest * (math.log(p_rest) - ln_s[np.argmax(x_out)] - math.log(out.sum()))
         else:
             p_rest = 0.0
     grad = s * (p.sum() + p_rest) - p
     if p_rest > 0:
-        grad = grad - np.where(named, 0.0, s * (p_rest / s_rest))
+        grad = grad - p_rest * (out / out.sum())
     return loss, grad / tau, {"s": s, "p": p, "p_rest": p_rest, "s_rest": s_rest, "named": named,
                               "below": np.where(np.isneginf(x), 0.0, (M - x) / tau)}

@@ -17,7 +17,8 @@
 //
 // Measured (129,280 entries): 1,152 rows of bf16 to float32 probabilities 136 us (6.55 TB/s, 0.97 of the measured copy
 // bandwidth), to bf16 100 (5.95); 2,048 rows of bf16 distilled with 64 entries each 192 us (5.5 TB/s, 0.82), 1,024 of float32
-// 181 (0.87), the loss alone 116 (4.6 TB/s), with a rest 246 (the marks, and the weights' second sum); 256 entries a row 238.
+// 181 (0.87), the loss alone 116 (4.6 TB/s), with a rest 254 (the marks, and the weights' second sum; 247
+// without what far rests need); 256 entries a row 238.
 // One row of 32,000: probabilities 4.1 us. What holds the distillation below the copy rate: instructions (0.48 of the issue
 // slots, at 30 warps an SM) and the meeting of a row's CTAs, once a row.
 #include <algorithm>
@@ -141,6 +142,21 @@ template <class T>
 __device__ __forceinline__ uint4 empty_piece() {  // -inf throughout
   const uint32_t e = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
   return make_uint4(e, e, e, e);
+}
+// The piece with its marked entries at -inf.
+template <class T>
+__device__ __forceinline__ uint4 without_marked(const uint4& q, uint32_t marked) {
+  uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      if (marked >> i & 1) w[i] = 0xff800000u;
+    } else {
+      if (marked >> (2 * i) & 1) w[i] = (w[i] & 0xffff0000u) | 0xff80u;
+      if (marked >> (2 * i + 1) & 1) w[i] = (w[i] & 0xffffu) | 0xff800000u;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <class T>
 __device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b) {  // of one float32 or two bf16
@@ -269,11 +285,7 @@ __device__ __forceinline__ void add_weights(ThreadSum& s, const uint4 (&q)[kGrou
   if (kMarks) s.listed += l;
 }
 template <class T, bool kMarks>
-__device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, uint32_t marks, bool loose_mark) {
-  static_assert(kGroup == 4, "a byte a piece");
-  uint4 q[kGroup];
-#pragma unroll
-  for (int i = 0; i < kGroup; ++i) q[i] = i < m ? mine[i * kRowThreads] : empty_piece<T>();
+__device__ __forceinline__ void add_pieces(ThreadSum& s, const uint4 (&q)[kGroup], float loose, const Rate& r, uint32_t marks, bool loose_mark) {
   const float top = nan_max(nan_max(s.m, loose), pieces_max<T>(q));
   if (top == -INFINITY) return;
   if (top != s.m) {
@@ -286,6 +298,14 @@ __device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m
   }
   if (plain_exponent(r, top)) add_weights<T, kMarks, true>(s, q, loose, r, marks, loose_mark);
   else add_weights<T, kMarks, false>(s, q, loose, r, marks, loose_mark);
+}
+template <class T, bool kMarks>
+__device__ __forceinline__ void add_group(ThreadSum& s, const uint4* mine, int m, float loose, const Rate& r, uint32_t marks, bool loose_mark) {
+  static_assert(kGroup == 4, "a byte a piece");
+  uint4 q[kGroup];
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i) q[i] = i < m ? mine[i * kRowThreads] : empty_piece<T>();
+  add_pieces<T, kMarks>(s, q, loose, r, marks, loose_mark);
 }
 // A window's pieces, a group as soon as it has arrived; marks(g): the marked entries of group g; after(g) may start another
 // group's copies over group g's (kRefill).
@@ -324,10 +344,18 @@ __device__ __forceinline__ Split warp_add(Split v) {
   return v;
 }
 
+// Where every warp's part of the unlisted entries' sum, relative to the row's maximum, is below this, they are summed once more,
+// relative to their own maximum. Down to it what weights lose below 2^-126 is 2^-60 of the sum an entry, and no quotient
+// by the sum overflows; below, the sum would first lose entries and then be 0, where its logarithm and its entries' shares in it
+// are of an ordinary size. (Of parts, not of their sum: every thread of the cluster has to find the same, those that sum pairs of
+// floats too.)
+constexpr float kFarRest = 0x1p-66f;
+
 // The row's maximum and sums from those of all warps of the cluster, the same in every thread (a warp's lanes each
 // take every 32nd entry, then a fixed tree).
 struct RowSum {
   float M, z, listed;
+  bool far;  // kMarks: z is below kFarRest, all warps' parts of it are
   float z_lo, listed_lo;  // kPair: what the sums' roundings left
 };
 template <bool kMarks>
@@ -342,7 +370,7 @@ __device__ __forceinline__ void send(const ThreadSum& s, float4* all, int C, int
 template <bool kMarks, bool kPair>
 __device__ __forceinline__ RowSum combine(const float4* all, int C, const Rate& rate) {
   const int lane = threadIdx.x & 31;
-  RowSum r{-INFINITY, 0.f, 0.f, 0.f, 0.f};
+  RowSum r{-INFINITY, 0.f, 0.f, false, 0.f, 0.f};
   const int n = C * kRowWarps;
   constexpr int L = kMaxCluster * kRowWarps / 32;  // entries a lane
   float4 t[L];
@@ -353,11 +381,13 @@ __device__ __forceinline__ RowSum combine(const float4* all, int C, const Rate& 
   }
   r.M = warp_nan_max(r.M);
   if (r.M == -INFINITY) return r;
+  bool near = !(fabsf(r.M) < INFINITY);
   if constexpr (kPair) {
     Split z{0.f, 0.f}, l = z;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const float g = t[i].x == -INFINITY ? 0.f : rescale(rate, t[i].x, r.M);
+      near |= __fmul_rn(t[i].y, g) >= kFarRest;
       z = add(z, product(t[i].y, g, 0.f));
       if (kMarks) l = add(l, product(t[i].z, g, 0.f));
     }
@@ -368,12 +398,14 @@ __device__ __forceinline__ RowSum combine(const float4* all, int C, const Rate& 
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const float g = t[i].x == -INFINITY ? 0.f : rescale(rate, t[i].x, r.M);
+      near |= __fmul_rn(t[i].y, g) >= kFarRest;
       r.z = __fmaf_rn(t[i].y, g, r.z);
       if (kMarks) r.listed = __fmaf_rn(t[i].z, g, r.listed);
     }
     r.z = warp_sum(r.z);
     if (kMarks) r.listed = warp_sum(r.listed);
   }
+  if (kMarks) r.far = !__any_sync(0xffffffffu, near);
   return r;
 }
 
@@ -613,13 +645,59 @@ template <int kId, int kThreads>
 __device__ __forceinline__ void named_arrive() { asm volatile("barrier.cta.arrive %0, %1;" ::"n"(kId), "n"(kThreads) : "memory"); }
 enum { kMarksReady = 1, kRowWritten = 2, kListSync = 3 };  // named barriers
 
+// What a row with a far rest needs besides, as functions of their own: in line their registers cost the other rows time (the loss
+// alone of 2,048 rows 166 us for 162, with the gradient 255.6 for 255; without any of it 156 and 249).
+// The streaming threads' part: each one's unlisted entries, from the row itself (what held it may already hold the next one), then
+// the cluster's exchange. loose: the loose element (-inf: none, or listed).
+template <class T>
+__device__ __noinline__ RowSum unlisted_sum(RowPart<T> part, int own, float loose, Rate r, const uint32_t* s_marks, int words, float4* apart) {
+  ThreadSum s;
+#pragma unroll 1
+  for (int i0 = 0; i0 < own || i0 == 0; i0 += kGroup) {
+    const int word = i0 / kGroup * kRowThreads + (int)threadIdx.x;
+    const uint32_t marks = word < words ? s_marks[word] : 0u;
+    uint4 q[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      q[i] = empty_piece<T>();
+      if (i0 + i < own) q[i] = *reinterpret_cast<const uint4*>(part.row + part.a0 + (size_t)part.piece(i0 + i) * RowPart<T>::E);
+      q[i] = without_marked<T>(q[i], marks >> (8 * i) & 255u);
+    }
+    add_pieces<T, false>(s, q, i0 == 0 ? loose : -INFINITY, r, 0u, false);
+  }
+  const int C = 1 << part.shift;
+  send<false>(s, apart, C, part.rank, r);
+  return receive<false>(apart, C, r);
+}
+// The list's warps take part in that exchange: the sum.
+__device__ __noinline__ float unlisted_received(const float4* apart, int C, Rate r) {
+  cluster_arrive();
+  cluster_wait();
+  return combine<false, false>(apart, C, r).z;
+}
+// The same after it, with what its roundings left.
+__device__ __noinline__ RowSum unlisted_pair(const float4* apart, int C, Rate r) { return combine<false, true>(apart, C, r); }
+// p_R (ln p_R - ln s_R) times kSmall, with p_R = left, ln_z the logarithm of the row's sum relative to its maximum M. (One thread's.)
+__device__ __noinline__ Split far_term(RowSum rest, Rate r, float M, Split left, Split ln_z) {
+  const bool plain_rest = plain_exponent(r, rest.M), plain_M = plain_exponent(r, M);
+  const Split k{r.rate, 0.f};
+  // in octaves, times kSmall: what a weight of 1 relative to rest.M is relative to M
+  const auto level = [&](float x, bool plain) { return plain ? Split{origin(r, x) * kSmall, 0.f} : times(Split{x * kSmall, 0.f}, k); };
+  const Split octaves = plain_rest || plain_M ? add(level(rest.M, plain_rest), negative(level(M, plain_M)))
+                                              : times(two_sum(rest.M * kSmall, -M * kSmall), k);
+  const Split near = add(add(ln_of(left), negative(ln_of(Split{rest.z, rest.z_lo}))), ln_z);
+  return times(left, add(Split{near.hi * kSmall, near.lo * kSmall}, negative(times(octaves, Split{kLn2, kLn2Lo}))));
+}
+
 // What the weights of a row are multiplied by in its gradient: entries of the rest, listed ones; and the teacher's shares.
+// z_rest: the rest's sum, relative to an origin at which a weight of 1 is one of to_M relative to the row's maximum; the rest's
+// weights are to be relative to it too.
 struct Factors {
   float rest, listed, teacher;
   bool bad, some;  // some: a rest without mass on either side counts for nothing
 };
 template <bool kRest>
-__device__ __forceinline__ Factors factors(const ListSums* of, int C, const RowSum& sum, float weight, float per_tau) {
+__device__ __forceinline__ Factors factors(const ListSums* of, int C, const RowSum& sum, float z_rest, float to_M, float weight, float per_tau) {
   Split share{0.f, 0.f};
   for (int c = 0; c < C; ++c) share = add(share, of[c].share);
   const Split rest = two_sum(1.f, -share.hi);
@@ -627,11 +705,11 @@ __device__ __forceinline__ Factors factors(const ListSums* of, int C, const RowS
   const int flags = of[0].flags;
   Factors f;
   f.bad = !(fabsf(sum.M) < INFINITY) || flags & kBadList;
-  f.some = kRest && left > 0.f && sum.z > 0.f;
+  f.some = kRest && left > 0.f && z_rest > 0.f;
   const float scale = __fmul_rn(weight, per_tau);
   const float per_z = __fdiv_rn(kRest ? (f.some ? fmaxf(1.f, all) : all) : flags & kNoList ? 0.f : 1.f, sum.z + sum.listed);
   f.listed = scale * per_z;
-  f.rest = scale * (per_z - (f.some ? __fdiv_rn(left, sum.z) : 0.f));
+  f.rest = scale * (kRest ? __fmaf_rn(per_z, to_M, f.some ? -__fdiv_rn(left, z_rest) : 0.f) : per_z);
   f.teacher = kRest ? scale : flags & kNoList ? 0.f : scale * __fdiv_rn(1.f, all);
   return f;
 }
@@ -652,6 +730,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
   __shared__ float maxima[kListThreads / 32];
   __shared__ uint32_t loose_marks;
   __shared__ int twice[2];
+  __shared__ float4 apart[kRest ? kMaxCluster * kRowWarps : 1];  // of the unlisted entries, relative to their own maxima
   const int half = (p.K + 1) / 2;  // a warp's part of a list
   Listed* lists = reinterpret_cast<Listed*>(reinterpret_cast<char*>(held) + p.held);  // two rows' two parts
   uint32_t* s_marks = reinterpret_cast<uint32_t*>(lists + 4 * half);
@@ -697,9 +776,23 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
       }
       send<kRest>(s, all[turn], C, rank, rate);
       const RowSum sum = receive<kRest>(all[turn], C, rate);
+      float rest_M = sum.M;  // the entry that the rest's weights are relative to
+      const auto row_factors = [&](float z_rest, float to_M) {
+        return factors<kRest>(teachers[turn], C, sum, z_rest, to_M, p.weight ? __ldg(p.weight + r) : 1.f, p.per_tau);
+      };
+      Factors f{};
+      if constexpr (kGrad) f = row_factors(sum.z, 1.f);
+      if constexpr (kRest) {
+        if (sum.far) {
+          const RowSum unlisted = unlisted_sum(part, own, loose_mark ? -INFINITY : loose, rate, s_marks, p.marks / 4, apart);
+          if (kGrad && unlisted.M != -INFINITY) {
+            rest_M = unlisted.M;
+            f = row_factors(unlisted.z, rescale(rate, rest_M, sum.M));
+          }
+        }
+      }
       if constexpr (kGrad) {
         // d loss / d x_v = (1/tau) (s_v total - [rest] s_v p_rest / s_rest - p_v), here without the last term
-        const Factors f = factors<kRest>(teachers[turn], C, sum, p.weight ? __ldg(p.weight + r) : 1.f, p.per_tau);
         T* grad = static_cast<T*>(p.grad) + (size_t)r * p.V;
         const bool wide = (reinterpret_cast<uintptr_t>(grad + part.a0) & 15) == 0;
         const auto after = [&](int g) {
@@ -709,10 +802,10 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
           write_one(part, own, -1, grad, wide, loose_at);
 #pragma unroll 1
           for (int g = 0; g < kGroups; ++g) after(g);
-        } else if (plain_exponent(rate, sum.M)) {
-          write_weights(part, held, own, p.windows, Weigher<true>(rate, sum.M), f.rest, grad, wide, loose_at, loose, after);
+        } else if (plain_exponent(rate, rest_M)) {
+          write_weights(part, held, own, p.windows, Weigher<true>(rate, rest_M), f.rest, grad, wide, loose_at, loose, after);
         } else {
-          write_weights(part, held, own, p.windows, Weigher<false>(rate, sum.M), f.rest, grad, wide, loose_at, loose, after);
+          write_weights(part, held, own, p.windows, Weigher<false>(rate, rest_M), f.rest, grad, wide, loose_at, loose, after);
         }
         named_arrive<kRowWritten, kDistillThreads>();
       }
@@ -872,7 +965,9 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
     gather(min(r_next, p.N - 1), early);  // (past the last row: no ids)
     cluster_wait();
     const RowSum sum = combine<kRest, true>(all[turn], C, rate);
-    const Factors f = factors<kRest>(teachers[turn], C, sum, p.weight ? __ldg(p.weight + r) : 1.f, p.per_tau);
+    // (of a far rest the streaming threads read the marks before that)
+    const float z_rest = kRest && sum.far ? unlisted_received(apart, C, rate) : sum.z;
+    const Factors f = factors<kRest>(teachers[turn], C, sum, z_rest, 1.f, p.weight ? __ldg(p.weight + r) : 1.f, p.per_tau);
     const RowPart<T> part = part_of(r);
     const Listed* list = list_of(turn, warp);
 
@@ -889,6 +984,8 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
     Row next{0, 0};
     if (r_next < p.N) next = prepare(r_next, turn ^ 1, early);
 
+    RowSum rest = sum;  // its z: the unlisted entries', relative to its M
+    if (kRest && sum.far) rest = unlisted_pair(apart, C, rate);  // (by whole warps)
     // the loss: the last CTA's
     if (rank == C - 1 && j0 == 32) {
       Split share{0.f, 0.f}, a = share, x = share;
@@ -907,12 +1004,13 @@ __global__ void __launch_bounds__(kDistillThreads, 3) distill_kernel(DistillPara
       const Split below = plain ? add(times(x, k), negative(from)) : times(add(x, negative(from)), k);
       const auto small = [](Split v) { return Split{v.hi * kSmall, v.lo * kSmall}; };
       a = times(add(small(a), negative(below)), Split{kLn2, kLn2Lo});
-      const Split z_rest{sum.z, sum.z_lo}, ln_z = ln_of(add(z_rest, Split{sum.listed, sum.listed_lo}));
+      const Split z{sum.z, sum.z_lo}, ln_z = ln_of(add(z, Split{sum.listed, sum.listed_lo}));
       Split loss{0.f, 0.f};  // times kSmall
       if (kRest) {
         const Split left = add(Split{1.f, 0.f}, negative(share));
         loss = add(a, small(times(share, ln_z)));
-        if (f.some) loss = add(loss, small(times(left, add(add(ln_of(left), negative(ln_of(z_rest))), ln_z))));
+        if (f.some && sum.far) loss = add(loss, far_term(rest, rate, sum.M, left, ln_z));
+        else if (f.some) loss = add(loss, small(times(left, add(add(ln_of(left), negative(ln_of(z))), ln_z))));
       } else if (share.hi > 0.f) {
         loss = add(quotient(a, share), small(add(ln_z, negative(ln_of(share)))));
       }
