@@ -4,6 +4,7 @@ top logits. Plain numpy in float64 and Python integers, one row, request or page
 
 Pinned in tests/test_oracle_target_pass.py: the output law of a verified block by enumeration of its
 uniforms, the gradients by differences, the page lists by what each row reads through its table."""
+import itertools
 import math
 from fractions import Fraction
 
@@ -103,8 +104,9 @@ def page_collect(table, kv_len, page, n_pages, pinned=()):
 
 
 def page_fork(table, kv_len, parent, fork_len, page, n_pages, free, pinned=()):
-    """Dictionary of new_table, new_len, src, dst, tokens, used."""
+    """Dictionary of new_table, new_len, src, dst, tokens, used. The list of free pages ends at its first negative id."""
     width, rows, lens = len(table[0]), [], []
+    free = [int(x) for x in itertools.takewhile(lambda x: x >= 0, free)]
     for i, q in enumerate(parent):
         have = 0 if not 0 <= q < len(table) else min(max(int(kv_len[q]), 0), width * page)
         n = have if fork_len is None else min(max(int(fork_len[i]), 0), have)
@@ -121,7 +123,7 @@ def page_fork(table, kv_len, parent, fork_len, page, n_pages, free, pinned=()):
                 ended.add(row[-1])
             src.append(-1), dst.append(-1), tokens.append(0)
             continue
-        to = int(free[wanted]) if wanted < len(free) else -1
+        to = free[wanted] if wanted < len(free) else -1
         wanted += 1
         taken = min(wanted, len(free))
         src.append(row[-1] if to >= 0 else -1), dst.append(to), tokens.append(rest if to >= 0 else 0)

@@ -30,6 +30,7 @@ constexpr int kPgMeetWord = 40;   // of the status block: the CTAs' meetings so 
 
 // Workspace: status block, counts a CTA, and two words a page.
 constexpr size_t kPgCounts = 256;
+constexpr int kPgListEnd = kPgGrid;  // word behind the counts: where a fork's list of free pages ends
 constexpr size_t kPgMarks = 256 + 4 * 256;
 static size_t page_workspace(int n_pages) { return align256(kPgMarks + (size_t)n_pages * 8); }
 
@@ -182,7 +183,8 @@ __device__ __forceinline__ void collect_phase(const PageParams& p, const Team& t
 }
 
 // ---- fork: 0 clear, 1 mark, 2 copies a share of the rows, 3 lists and rows
-// mark0: the page is held in full by a new row, or pinned; mark1: the first new row that ends inside it.
+// mark0: the page is held in full by a new row, or pinned; mark1: the first new row that ends inside it. The list of free pages
+// ends at its first negative id: phase 1 looks for it among the R entries that could be asked for.
 struct Fork {
   int parent, whole, rest;  // full pages, tokens of the last one
 };
@@ -215,11 +217,13 @@ __device__ __forceinline__ void fork_phase(const PageParams& p, const Team& t, i
       p.mark0[i] = 0;
       p.mark1[i] = INT_MAX;
     }
+    if (t.first() == 0) p.counts[kPgListEnd] = INT_MAX;
     return;
   }
   bool bad = false;
   const int lane = threadIdx.x & 31;
   if (phase == 1) {
+    const int listed = min(p.R, p.free_count);
     for_stretches(p, t, [&](int i, int lo, int hi) {
       const Fork f = fork_of(p, i, bad);
       for (int c = lo + lane; c < hi; c += 32) {
@@ -239,6 +243,10 @@ __device__ __forceinline__ void fork_phase(const PageParams& p, const Team& t, i
       if (x >= 0 && x < p.n_pages) p.mark0[x] = 1;
       else bad = true;
     }
+    for (long long i = t.first(); i < listed; i += t.step()) {
+      // (the first of a run of negative ids is enough)
+      if (__ldg(p.free_list + i) < 0 && (i == 0 || __ldg(p.free_list + i - 1) >= 0)) atomicMin(p.counts + kPgListEnd, (int)i);
+    }
     if (bad) set_status(p.status, DSPARK_ERR_RANGE);
     return;
   }
@@ -251,6 +259,7 @@ __device__ __forceinline__ void fork_phase(const PageParams& p, const Team& t, i
     if (threadIdx.x == 0) p.counts[t.rank] = n;
     return;
   }
+  const int list_end = min(p.free_count, __ldcg(p.counts + kPgListEnd));
   int before = 0, all = 0;
   for (int i = threadIdx.x; i < t.n; i += kPgThreads) {
     const int n = __ldcg(p.counts + i);
@@ -273,7 +282,7 @@ __device__ __forceinline__ void fork_phase(const PageParams& p, const Team& t, i
     if (i >= hi) continue;
     int from = -1, to = -1;
     if (copies) {
-      if (k < p.free_count) to = __ldg(p.free_list + k);
+      if (k < list_end) to = __ldg(p.free_list + k);
       if (to < 0 || to >= p.n_pages) {
         set_status(p.status, to < p.n_pages ? DSPARK_ERR_CAPACITY : DSPARK_ERR_RANGE);
         to = -1;
@@ -286,7 +295,7 @@ __device__ __forceinline__ void fork_phase(const PageParams& p, const Team& t, i
     p.dst[i] = to;
     p.tokens[i] = to >= 0 ? f.rest : 0;
   }
-  if (t.rank == 0 && threadIdx.x == 0) p.used[0] = min(all, p.free_count);
+  if (t.rank == 0 && threadIdx.x == 0) p.used[0] = min(all, list_end);
 }
 
 // ---- compact: 0 clear, 1 mark, 2 live pages a share, 3 names and lists, 4 rows
