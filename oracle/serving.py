@@ -1,6 +1,7 @@
 """Oracle of the target's side of a round in a serving engine: cache pages and slots, attention over a
 shared prefix and private pages, and the sampling rule. Plain numpy in float64 (integers where the
 definition has integers), one request, row or token at a time."""
+import itertools
 import math
 
 import numpy as np
@@ -8,7 +9,8 @@ import numpy as np
 
 def page_plan(cached, new, free, page, table, capacity):
     """Block table, starts, lengths, positions, slots and pages used; short lists leave -1. Of the new tokens those that
-    fit the capacity are planned, in request order."""
+    fit the capacity are planned, in request order. The list of free pages ends at its first negative id."""
+    free = [int(x) for x in itertools.takewhile(lambda x: x >= 0, free)]
     table = np.array(table, dtype=np.int64)
     R, width = table.shape
     taken, tok, short = 0, 0, sum(max(0, int(n)) for n in new) > capacity
@@ -17,7 +19,7 @@ def page_plan(cached, new, free, page, table, capacity):
         q_start.append(tok)
         c, n = int(cached[r]), min(int(new[r]), capacity - tok)
         for col in range(-(-c // page), -(-(c + n) // page)):
-            page_id = int(free[taken]) if taken < len(free) else -1
+            page_id = free[taken] if taken < len(free) else -1
             short |= page_id < 0 or col >= width
             taken += 1
             if col < width:

@@ -9,13 +9,17 @@
 //   index the sum of n before it. A request that the token capacity cuts asks for
 //   what is left of it, the later ones for nothing. Each CTA plans kPlanReqs requests and forms
 //   both sums over all earlier requests itself: at 8,192 requests that reads at
-//   most 64 KB from L2 in a CTA, and no CTA waits for another. Bound by latency:
-//   128 requests, 1,144 tokens 8 us a call (the launch's host side), 8,192 requests,
-//   73,720 tokens 12 us (1.05 MB, 0.16 us of bandwidth).
+//   most 64 KB from L2 in a CTA, and no CTA waits for another. The list ends at its first
+//   negative id, which each CTA looks for among the entries that its requests and the
+//   earlier ones ask for (35 KB there). Bound by latency:
+//   128 requests, 1,144 tokens 8 us a call (the launch's host side; 5.9 on the GPU), 8,192 requests,
+//   73,720 tokens 12 us (1.05 MB, 0.16 us of bandwidth; 10.8 on the GPU, of which the list's end 0.9,
+//   looked for an entry at a time 1.8).
 // kv_append_kernel  one 16-byte piece of one token's key and value row a thread
 //   step; bound by bytes (each read once and written once): 15,904 tokens of 8 heads
 //   of 128 bf16 (130 MB) 23 us, 5.6 TB/s, 0.83 of the measured copy bandwidth.
 #include <algorithm>
+#include <climits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -56,8 +60,29 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
   __shared__ long long s_tok[kPlanReqs + 1], s_pg[kPlanReqs + 1];  // token / free-list starts of this CTA's requests
   __shared__ long long s_warp[kPlanReqs / 32];
   __shared__ int s_c[kPlanReqs], s_have[kPlanReqs];
+  __shared__ int s_end;  // where the list of free pages ends: at its first negative id
   const int tid = threadIdx.x, r0 = blockIdx.x * kPlanReqs, nr = min(kPlanReqs, p.R - r0);
   bool bad = false;
+  if (tid == 0) s_end = p.n_free;
+  // Every CTA looks for the list's end among the entries that its requests and the earlier ones ask for, four at a time: the
+  // first 4 kPlanThreads in flight with the lengths. (Entries past what is asked for do no harm.)
+  const int lead = (int)((16 - (reinterpret_cast<uintptr_t>(p.free_pages) & 15)) & 15) / 4;  // before the first 16-byte boundary
+  auto entries = [&](int i) {
+    const long long at = lead + 4ll * i;
+    if (at + 4 <= p.n_free) return __ldg(reinterpret_cast<const int4*>(p.free_pages + at));
+    auto one = [&](long long k) { return k < p.n_free ? __ldg(p.free_pages + k) : 0; };
+    return make_int4(one(at), one(at + 1), one(at + 2), one(at + 3));
+  };
+  auto first_negative = [&](const int4& ids, int i) {
+    const int at = ids.x < 0 ? 0 : ids.y < 0 ? 1 : ids.z < 0 ? 2 : 3;
+    return (ids.x | ids.y | ids.z | ids.w) < 0 ? lead + 4 * i + at : INT_MAX;
+  };
+  auto ends_at = [&](int at) {  // the lowest of a warp's
+    at = __reduce_min_sync(0xffffffffu, at);
+    if ((tid & 31) == 0 && at < INT_MAX) atomicMin(&s_end, at);
+  };
+  const int4 head = entries(tid);
+  const int loose = tid < min(lead, p.n_free) ? __ldg(p.free_pages + tid) : 0;
   auto lengths = [&](int r, int& c, int& n) {
     c = __ldg(p.cached + r);
     n = __ldg(p.fresh + r);
@@ -112,7 +137,17 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
     bad |= end > 0x7fffffffll;
     p.kv_len[r0 + tid] = (int)min(end, 0x7fffffffll);
   }
+  ends_at(loose < 0 ? tid : first_negative(head, tid));  // (s_end was set before the barriers of the first running sum)
   running(miss, pg, s_pg);
+  const int asked = (int)min(s_pg[nr], (long long)p.n_free);
+  if (asked > lead + 4 * kPlanThreads) {
+    int at = INT_MAX;
+#pragma unroll 4
+    for (int i = kPlanThreads + tid; lead + 4ll * i < asked; i += kPlanThreads) at = min(at, first_negative(entries(i), i));
+    ends_at(at);
+    __syncthreads();
+  }
+  const int list_end = s_end;
   // new entries of the block table: -1 where the list has run out
   bool full = false;
   const int warp = tid >> 5, lane = tid & 31;
@@ -122,7 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
     full |= have + n_new > p.max_pages;
     for (long long j = lane; j < n_new && have + j < p.max_pages; j += 32) {
       const long long at = s_pg[i] + j;
-      const int id = at < p.n_free ? __ldg(p.free_pages + at) : -1;  // (a list may end early: dspark_page_collect's do)
+      const int id = at < list_end ? __ldg(p.free_pages + at) : -1;  // (a list may end early: dspark_page_collect's do)
       full |= id < 0;
       p.table[(size_t)(r0 + i) * p.max_pages + have + j] = id;
     }
@@ -146,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
         id = __ldg(p.table + (size_t)(r0 + lo) * p.max_pages + col);
       } else {
         const long long at = s_pg[lo] + col - s_have[lo];
-        if (at < p.n_free) id = __ldg(p.free_pages + at);
+        if (at < list_end) id = __ldg(p.free_pages + at);
       }
     }
     p.positions[t] = (int)pos;
@@ -155,7 +190,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanParams p) {
   // pages are taken up to the CTA in which the capacity is reached (pg of the later ones is not their start: a request
   // that the capacity cuts counts in full there)
   if (tid == 0 && (r0 == 0 || s_tok[0] < p.capacity) && (t_end >= p.capacity || r0 + nr == p.R))
-    p.used[0] = (int)min(s_pg[nr], (long long)p.n_free);
+    p.used[0] = (int)min(s_pg[nr], (long long)list_end);
   if (r0 + nr == p.R) {
     if (tid == 0) p.q_start[p.R] = (int)min(t_end, (long long)p.capacity);
     for (long long t = t_end + tid; t < p.capacity; t += kPlanThreads) {
