@@ -541,7 +541,9 @@ dspark_status dspark_verify_probs(int32_t R, int32_t gamma, int32_t V, int32_t T
  * a page is freed by shortening or dropping the rows that hold it. An entry
  * outside [0, n_pages) within a row's length, or a length outside
  * [0, max_pages * page_size] (clamped), sets DSPARK_ERR_RANGE; such an entry is
- * nobody's page and is carried along as it is.
+ * nobody's page and is carried along as it is. Outputs share no memory with inputs
+ * or with each other, except where it is said (DSPARK_ERR_INVALID_ARG): the lengths that
+ * dspark_page_fork reads and those that it writes are two arrays.
  *
  * Larger tables run as one cooperative launch whose CTAs wait for each other, each wait with a limit: DSPARK_ERR_TIMEOUT if
  * one runs out (clear the workspace before its next use then).

@@ -542,7 +542,8 @@ def page_fork(block_table, kv_len, parent, fork_len, page_size, n_pages, free_pa
               used, ws, pinned=None, stream=None):
     """new_table [R, max_pages]: row i the first fork_len[i] tokens (None: all) of row parent[i] (-1: empty) of
     block_table [R_from, max_pages]; pages shared, those that a row writes next its own, from free_pages. Fills
-    new_len, and the copies to make: src, dst, tokens [R] (-1, -1, 0: none), used [1]. All int32."""
+    new_len, and the copies to make: src, dst, tokens [R] (-1, -1, 0: none), used [1]. All int32; the outputs are tensors
+    of their own (new_len is not kv_len)."""
     R_from, max_pages = block_table.shape
     R = parent.numel()
     if (new_table.shape != (R, max_pages) or kv_len.numel() != R_from or new_len.numel() != R or src.numel() != R or
