@@ -483,7 +483,8 @@ dspark_status dspark_truncate(int32_t N, int32_t V, int32_t dtype, const void* l
  * cache's pages follow that decision, and the rows' largest entries teach the
  * drafter. These calls take any workspace of at least 256 bytes for the device
  * status word; dspark_page_collect, _fork and _compact need the size that
- * dspark_page_workspace_bytes gives.
+ * dspark_page_workspace_bytes gives. Outputs share no memory with inputs or with each
+ * other, except where it is said (DSPARK_ERR_INVALID_ARG): inputs are read after the first outputs are written.
  *
  * dspark_probabilities: probs[r] = softmax(logits[r] / T_r), N rows [N, V]
  * (V <= 2^20), with the weights of dspark_sample: w = 2^((l - M) r), r =
@@ -493,7 +494,7 @@ dspark_status dspark_truncate(int32_t N, int32_t V, int32_t dtype, const void* l
  * (the type's lowest value) at any T below 1e36.
  *   logits      [N, V] dtype
  *   temperature [N] float
- *   probs       [N, V] probs_dtype out (not the logits' memory unless of the same type)
+ *   probs       [N, V] probs_dtype out (may be logits itself, of the same type)
  * A row with a NaN or +inf, or with nothing above -inf, sets
  * DSPARK_ERR_NONFINITE and gets zeros.
  */
@@ -541,9 +542,8 @@ dspark_status dspark_verify_probs(int32_t R, int32_t gamma, int32_t V, int32_t T
  * a page is freed by shortening or dropping the rows that hold it. An entry
  * outside [0, n_pages) within a row's length, or a length outside
  * [0, max_pages * page_size] (clamped), sets DSPARK_ERR_RANGE; such an entry is
- * nobody's page and is carried along as it is. Outputs share no memory with inputs
- * or with each other, except where it is said (DSPARK_ERR_INVALID_ARG): the lengths that
- * dspark_page_fork reads and those that it writes are two arrays.
+ * nobody's page and is carried along as it is. (The lengths that dspark_page_fork
+ * reads and those that it writes are two arrays.)
  *
  * Larger tables run as one cooperative launch whose CTAs wait for each other, each wait with a limit: DSPARK_ERR_TIMEOUT if
  * one runs out (clear the workspace before its next use then).

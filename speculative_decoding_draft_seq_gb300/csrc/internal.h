@@ -3,6 +3,7 @@
 
 #include <atomic>
 #include <cuda_runtime.h>
+#include <initializer_list>
 #include <stdint.h>
 
 #include "../../include/dspark.h"
@@ -112,5 +113,26 @@ cudaError_t launch_verify_tail(const VerifyArgs& a, cudaStream_t s, int& launche
 // Acceptance labels; `supported` is false (and nothing is launched) when the
 // sampled-mode shape is outside the tensor-core path.
 cudaError_t launch_labels(const LabelArgs& a, cudaStream_t s, int& launches, bool& supported);
+
+// Arrays of a call, whose kernels read inputs after the first outputs are written.
+struct Span {
+  uintptr_t at, bytes;
+};
+template <class T>
+inline Span span(const T* p, long long n) {
+  return {reinterpret_cast<uintptr_t>(p), p && n > 0 ? (uintptr_t)n * sizeof(T) : 0};
+}
+inline Span span(const void* p, long long n, int elem) { return {reinterpret_cast<uintptr_t>(p), p && n > 0 ? (uintptr_t)n * elem : 0}; }
+// No output shares memory with an input or with another output.
+inline bool separate(std::initializer_list<Span> inputs, std::initializer_list<Span> outputs) {
+  const auto overlap = [](const Span& a, const Span& b) { return a.bytes && b.bytes && a.at < b.at + b.bytes && b.at < a.at + a.bytes; };
+  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Span& i : inputs)
+      if (overlap(*o, i)) return false;
+    for (const Span* q = outputs.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return false;
+  }
+  return true;
+}
 
 }  // namespace dspark

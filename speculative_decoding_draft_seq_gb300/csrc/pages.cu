@@ -15,7 +15,6 @@
 // bytes: 1,180 pages of 32 KB, four times (keys and values of two layers, 308 MB read and written), in 54 us (5.7 TB/s); 4
 // units a thread in flight instead of 8: 64.
 #include <algorithm>
-#include <initializer_list>
 
 #include "cluster.cuh"
 #include "common.cuh"
@@ -521,24 +520,6 @@ static bool page_args(int R, int page, int max_pages, int n_pages, int n_pinned,
 static bool page_workspace_ok(const void* ws, size_t bytes, int n_pages) {
   return ws && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && bytes >= page_workspace(n_pages);
 }
-// The phases read inputs after outputs were written: they must not share memory. Neither must outputs, some of which are read again.
-struct Span {
-  const void* at;
-  long long n;  // int32 entries
-};
-static bool separate(std::initializer_list<Span> inputs, std::initializer_list<Span> outputs) {
-  const auto overlap = [](const Span& a, const Span& b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-    return a.at && b.at && x < y + 4 * (uintptr_t)b.n && y < x + 4 * (uintptr_t)a.n;
-  };
-  for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
-    for (const Span& i : inputs)
-      if (overlap(*o, i)) return false;
-    for (const Span* q = outputs.begin(); q != o; ++q)
-      if (overlap(*o, *q)) return false;
-  }
-  return true;
-}
 static void use_workspace(PageParams& p, void* ws) {
   p.status = static_cast<uint32_t*>(ws);
   p.counts = ws_at<int32_t>(ws, kPgCounts);
@@ -562,7 +543,8 @@ extern "C" dspark_status dspark_page_collect(int32_t R, int32_t page_size, int32
     return DSPARK_ERR_INVALID_ARG;
   if (!page_workspace_ok(workspace, workspace_bytes, n_pages)) return DSPARK_ERR_WORKSPACE;
   const long long entries = (long long)R * max_pages;
-  if (!separate({{block_table, entries}, {kv_len, R}, {pinned, n_pinned}}, {{refs, n_pages}, {free_pages, n_pages}, {n_free, 1}}))
+  if (!separate({span(block_table, entries), span(kv_len, R), span(pinned, n_pinned)},
+                {span(refs, n_pages), span(free_pages, n_pages), span(n_free, 1)}))
     return DSPARK_ERR_INVALID_ARG;
   PageParams p{};
   p.R = R; p.page = page_size; p.max_pages = max_pages; p.n_pages = n_pages; p.n_pinned = n_pinned;
@@ -584,8 +566,9 @@ extern "C" dspark_status dspark_page_fork(int32_t R_from, int32_t R, int32_t pag
       !tokens || !used || (long long)max_pages * page_size > 0x7fffffffll || new_table == block_table)
     return DSPARK_ERR_INVALID_ARG;
   if (!page_workspace_ok(workspace, workspace_bytes, n_pages)) return DSPARK_ERR_WORKSPACE;
-  if (!separate({{block_table, (long long)R_from * max_pages}, {kv_len, R_from}, {parent, R}, {fork_len, R}, {free_pages, n_free}, {pinned, n_pinned}},
-                {{new_table, (long long)R * max_pages}, {new_len, R}, {src, R}, {dst, R}, {tokens, R}, {used, 1}}))
+  if (!separate({span(block_table, (long long)R_from * max_pages), span(kv_len, R_from), span(parent, R), span(fork_len, R),
+                 span(free_pages, n_free), span(pinned, n_pinned)},
+                {span(new_table, (long long)R * max_pages), span(new_len, R), span(src, R), span(dst, R), span(tokens, R), span(used, 1)}))
     return DSPARK_ERR_INVALID_ARG;
   PageParams p{};
   p.R = R; p.from = R_from; p.page = page_size; p.max_pages = max_pages; p.n_pages = n_pages; p.n_pinned = n_pinned;
@@ -607,9 +590,9 @@ extern "C" dspark_status dspark_page_compact(int32_t R, int32_t page_size, int32
     return DSPARK_ERR_INVALID_ARG;
   if (!page_workspace_ok(workspace, workspace_bytes, n_pages)) return DSPARK_ERR_WORKSPACE;
   const long long entries = (long long)R * max_pages;
-  const Span table{block_table, new_table == block_table ? 0 : entries}, pins{pinned, new_pinned == pinned ? 0 : n_pinned};  // in place
-  if (!separate({table, {kv_len, R}, pins},
-                {{new_table, entries}, {new_pinned, n_pinned}, {src, n_pages / 2}, {dst, n_pages / 2}, {n_live, 1}}))
+  const Span table = span(block_table, new_table == block_table ? 0 : entries), pins = span(pinned, new_pinned == pinned ? 0 : n_pinned);
+  if (!separate({table, span(kv_len, R), pins},  // (those may be written in place)
+                {span(new_table, entries), span(new_pinned, n_pinned), span(src, n_pages / 2), span(dst, n_pages / 2), span(n_live, 1)}))
     return DSPARK_ERR_INVALID_ARG;
   PageParams p{};
   p.R = R; p.page = page_size; p.max_pages = max_pages; p.n_pages = n_pages; p.n_pinned = n_pinned;

@@ -1110,10 +1110,15 @@ extern "C" dspark_status dspark_probabilities(int32_t N, int32_t V, int32_t dtyp
   if (N > 0 && (!logits || !temperature || !probs)) return DSPARK_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes)) return DSPARK_ERR_WORKSPACE;
   if (N == 0) return DSPARK_OK;
+  const int elem = dtype == DSPARK_BF16 ? 2 : 4;
+  const long long entries = (long long)N * V;
+  const bool in_place = probs == logits && probs_dtype == dtype;
+  if (!separate({span(logits, in_place ? 0 : entries, elem), span(temperature, N)}, {span(probs, entries, probs_dtype == DSPARK_BF16 ? 2 : 4)}))
+    return DSPARK_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms == 0) return DSPARK_ERR_CUDA;
   int held;
-  const int C = row_cluster(N, V, dtype == DSPARK_BF16 ? 2 : 4, sms, held);
+  const int C = row_cluster(N, V, elem, sms, held);
   const ProbsParams p{V, C, logits, temperature, probs, static_cast<uint32_t*>(workspace)};
   cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
@@ -1136,10 +1141,14 @@ extern "C" dspark_status dspark_distill(int32_t N, int32_t V, int32_t K, int32_t
   if (N > 0 && (!logits || !ids || !teacher || !loss)) return DSPARK_ERR_INVALID_ARG;
   if (!workspace_ok(workspace, workspace_bytes)) return DSPARK_ERR_WORKSPACE;
   if (N == 0) return DSPARK_OK;
+  const int elem = dtype == DSPARK_BF16 ? 2 : 4;
+  const long long entries = (long long)N * V, listed = (long long)N * K;
+  if (!separate({span(logits, grad == logits ? 0 : entries, elem), span(ids, listed), span(teacher, listed), span(teacher_lse, N), span(weight, N)},
+                {span(loss, N), span(grad, entries, elem)}))
+    return DSPARK_ERR_INVALID_ARG;
   const int sms = sm_count();
   if (sms == 0) return DSPARK_ERR_CUDA;
   int held;
-  const int elem = dtype == DSPARK_BF16 ? 2 : 4;
   const int C = row_cluster(N, V, elem, sms, held);
   // with a rest, the map of listed entries: a byte for each piece of this CTA, a word for a group of a thread's
   const int steps = ceil_div((long long)V * elem / 16, (long long)C * kRowThreads);

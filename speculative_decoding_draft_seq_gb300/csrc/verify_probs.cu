@@ -391,6 +391,12 @@ extern "C" dspark_status dspark_verify_probs(int32_t R, int32_t gamma, int32_t V
     return DSPARK_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 || workspace_bytes < 256)
     return DSPARK_ERR_WORKSPACE;
+  const int elem = dtype == DSPARK_BF16 ? 2 : 4;
+  const long long drafts = (long long)R * gamma;
+  if (!separate({span(target_probs, (long long)T * V, elem), span(q_start, R + 1ll), span(draft_probs, drafts, V * elem),
+                 span(draft_tokens, drafts), span(u, drafts + R)},
+                {span(out_tokens, drafts + R), span(accepted_len, R), span(p_tok, drafts)}))
+    return DSPARK_ERR_INVALID_ARG;
   // CTAs a request: what the SMs hold at once, four each (more leave each warp too little to pay for its chain and exchange)
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return DSPARK_ERR_CUDA;
