@@ -643,7 +643,8 @@ dspark_status dspark_page_copy(int32_t n, int32_t n_layers, int32_t n_pages, int
  * (left out). DSPARK_ERR_NONFINITE: a row with a NaN or +inf, or with nothing above -inf, or whose listed teacher
  * logits or lse hold a NaN or infinity (other than a logit of -inf: probability 0; an lse past 1e32 is one, a logit
  * past it counts as 1e32): loss NaN, gradient 0.
- * Statistics and the listed entries' terms are summed in float32 or float64.
+ * Sums over a row are float32; the listed entries' shares, terms and logarithms, and the sums where they are joined, pairs of
+ * float32 (2^-27).
  */
 dspark_status dspark_distill(int32_t N, int32_t V, int32_t K, int32_t dtype, const void* logits,
                              const int32_t* ids, const float* teacher, const float* teacher_lse,

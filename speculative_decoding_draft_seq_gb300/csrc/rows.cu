@@ -11,16 +11,19 @@
 // independently of each other (held in registers, one CTA an SM, the same took 2.5 times as long). A row longer than a
 // cluster holds is taken in windows, which are read again for the results.
 //
-// Statistics are float32: a thread adds a group's weights in four chains, groups one by one, then trees. The loss of a distilled row is a small
+// Statistics are float32: a thread adds a group's weights in four chains (8 additions each for bf16, 4 for float32), joins these and a
+// loose entry (3), groups one by one, then trees (5 over a warp, 7 over the cluster): at most 27 roundings in a sum over a row that is
+// held at once (4 groups), 51 for 2^20 float32 (32). The loss of a distilled row is a small
 // difference of large terms, so what it is made of (the listed entries' shares and sums, the logarithms) is kept in pairs of
 // floats; float64, at 1/64 of the rate, took a third of the time.
 //
 // Measured (129,280 entries): 1,152 rows of bf16 to float32 probabilities 136 us (6.55 TB/s, 0.97 of the measured copy
-// bandwidth), to bf16 100 (5.95); 2,048 rows of bf16 distilled with 64 entries each 192 us (5.5 TB/s, 0.82), 1,024 of float32
-// 181 (0.87), the loss alone 116 (4.6 TB/s), with a rest 254 (the marks, and the weights' second sum; 247
-// without what far rests need); 256 entries a row 238.
+// bandwidth), to bf16 100 (5.95); 2,048 rows of bf16 distilled with 64 entries each 196 us (5.4 TB/s, 0.80), 1,024 of float32
+// 181 (0.87), the loss alone 117 (4.5 TB/s), with a rest 254 (the marks, the weights' second sum, and instructions that the cache
+// does not hold; 248 without what far rests need), its loss alone 162; 256 entries a row 239, with a rest 333. All rows' rests
+// far: 391, the loss alone 290. Lists of 1,024: 700, with a rest 513 (without one, repeated ids are found pairwise).
 // One row of 32,000: probabilities 4.1 us. What holds the distillation below the copy rate: instructions (0.48 of the issue
-// slots, at 30 warps an SM) and the meeting of a row's CTAs, once a row.
+// slots, at 30 warps an SM) and the meeting of a row's CTAs, once a row; the loss alone waits for the meetings most.
 #include <algorithm>
 
 #include "cluster.cuh"
